@@ -429,7 +429,7 @@ def exact(case, seed):
             x = x.float().to(torch.bfloat16).double()
         else:
             b = x[:, :LATENT].reshape(-1, 32)
-            unit = 2.0 ** (torch.floor(torch.log2(b.abs().amax(1, keepdim=True))) - 2)
+            unit = torch.ldexp(torch.ones_like(b[:, :1]), torch.frexp(b.abs().amax(1, keepdim=True))[1] - 3)  # a logarithm can fall below an exact power of two
             y = b / unit
             # the spacing of e2m1 at each magnitude: 1/2 below 2, 1 below 4, 2 above; round() takes ties to even
             step = torch.where(y.abs() < 2, 0.5, torch.where(y.abs() < 4, 1.0, 2.0))
