@@ -1,0 +1,308 @@
+"""Thin Python binding of the latent-cache operators of libcsa_index.so
+(include/csa_latent.h): block tables, the paged latent cache's writer and reader,
+and latent attention, absorbed (over the cache) and expanded (prompts).
+
+Argument marshalling only, as in `native`; there is no fallback. Every tensor is
+on the GPU; work goes to `stream`, or the current stream.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import native
+from .native import _check, _ptr, _stream
+
+LATENT_DIM, MAX_HEADS, TABLES_MAX_REQ = 512, 128, 16384
+PREFILL_NOPE, PREFILL_ROPE, PREFILL_V = 128, 64, 128
+FORMAT_BF16, FORMAT_MXFP4 = 0, 1
+FORMATS = {"bf16": FORMAT_BF16, "mxfp4": FORMAT_MXFP4, FORMAT_BF16: FORMAT_BF16, FORMAT_MXFP4: FORMAT_MXFP4}
+DEV_POOL, DEV_ROWS = 64, 128
+
+_vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float
+
+
+class CacheArgs(ctypes.Structure):
+    """Mirror of `csa_latent_cache`."""
+    _fields_ = [("pages", _vp), ("num_pages", _i64), ("page_stride_bytes", _i64), ("rope_dim", _i32),
+                ("record_format", _i32)]
+
+
+class TablesArgs(ctypes.Structure):
+    """Mirror of `csa_tables_args`."""
+    _fields_ = [("old_len", _vp), ("new_len", _vp), ("num_req", _i32), ("pt_stride", _i32), ("page_table", _vp),
+                ("free_pages", _vp), ("n_free", _i64), ("n_rows", _i64), ("row_req", _vp), ("row_pos", _vp),
+                ("row_len", _vp), ("row_slot", _vp), ("row_start", _vp), ("kv_start", _vp), ("taken", _vp),
+                ("dev_status", _vp)]
+
+
+class LatentWriteArgs(ctypes.Structure):
+    """Mirror of `csa_latent_write_args`."""
+    _fields_ = [("cache", CacheArgs), ("x", _vp), ("x_stride", _i64), ("dtype", _i32), ("reserved0", _i32),
+                ("n", _i64), ("slots", _vp), ("dev_status", _vp)]
+
+
+class LatentReadArgs(ctypes.Structure):
+    """Mirror of `csa_latent_read_args`."""
+    _fields_ = [("cache", CacheArgs), ("page_table", _vp), ("num_req", _i32), ("pt_stride", _i32),
+                ("kv_start", _vp), ("n_rows", _i64), ("out", _vp), ("dev_status", _vp)]
+
+
+class AttendArgs(ctypes.Structure):
+    """Mirror of `csa_latent_attend_args`."""
+    _fields_ = [("cache", CacheArgs), ("q", _vp), ("q_row_stride", _i64), ("q_head_stride", _i64), ("num_q", _i32),
+                ("num_heads", _i32), ("page_table", _vp), ("num_req", _i32), ("pt_stride", _i32), ("row_req", _vp),
+                ("row_len", _vp), ("idx", _vp), ("idx_stride", _i64), ("top", _i32), ("scale", _f32), ("out", _vp),
+                ("lse", _vp), ("dev_status", _vp)]
+
+
+class PrefillArgs(ctypes.Structure):
+    """Mirror of `csa_latent_prefill_args`."""
+    _fields_ = [("q", _vp), ("k_nope", _vp), ("k_rope", _vp), ("v", _vp), ("q_row_stride", _i64),
+                ("q_head_stride", _i64), ("k_row_stride", _i64), ("k_head_stride", _i64), ("rope_row_stride", _i64),
+                ("v_row_stride", _i64), ("v_head_stride", _i64), ("total_q", _i64), ("total_k", _i64),
+                ("q_start", _vp), ("kv_start", _vp), ("num_req", _i32), ("num_heads", _i32), ("causal", _i32),
+                ("scale", _f32), ("out", _vp), ("lse", _vp), ("dev_status", _vp)]
+
+
+_lib = None
+
+
+def load():
+    """The library with this module's entry points declared. Raises if it has not been built."""
+    global _lib
+    if _lib is None:
+        lib = native.load()
+        P = ctypes.POINTER
+        lib.csa_latent_abi_version.argtypes = []
+        lib.csa_latent_abi_version.restype = _i32
+        lib.csa_latent_record_bytes.argtypes = [_i32, _i32]
+        lib.csa_latent_record_bytes.restype = _i64
+        lib.csa_build_tables.argtypes = [P(TablesArgs), _vp]
+        lib.csa_build_tables.restype = ctypes.c_int
+        lib.csa_latent_write.argtypes = [P(LatentWriteArgs), _vp]
+        lib.csa_latent_write.restype = ctypes.c_int
+        lib.csa_latent_read.argtypes = [P(LatentReadArgs), _vp]
+        lib.csa_latent_read.restype = ctypes.c_int
+        lib.csa_latent_attend_workspace_bytes.argtypes = [P(AttendArgs)]
+        lib.csa_latent_attend_workspace_bytes.restype = ctypes.c_size_t
+        lib.csa_latent_attend.argtypes = [P(AttendArgs), _vp, ctypes.c_size_t, _vp]
+        lib.csa_latent_attend.restype = ctypes.c_int
+        lib.csa_latent_prefill.argtypes = [P(PrefillArgs), _vp]
+        lib.csa_latent_prefill.restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def record_bytes(record_format, rope_dim: int) -> int:
+    """Bytes of one record; raises for a format or rope_dim that the cache does not have."""
+    n = int(load().csa_latent_record_bytes(FORMATS.get(record_format, -1), int(rope_dim)))
+    if n == 0:
+        raise ValueError(f"no latent record of format {record_format!r} with rope_dim {rope_dim}")
+    return n
+
+
+def _want(t: torch.Tensor, dtype, dims: int, name: str, last: bool = True) -> torch.Tensor:
+    """Checks a tensor argument: on the GPU, of this type and rank, its last axis (or all of it) contiguous."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != dims:
+        raise ValueError(f"{name}: a {dims}-d {dtype} CUDA tensor, not {tuple(t.shape)} {t.dtype} on {t.device}")
+    if not (t.is_contiguous() or (last and (t.shape[-1] == 1 or t.stride(-1) == 1))):
+        raise ValueError(f"{name}: contiguous{' in its last axis' if last else ''}")
+    return t
+
+
+def _pick(out, shape, dtype, device, name):
+    """The caller's output tensor, checked, or a new one."""
+    if out is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    _want(out, dtype, len(shape), name, last=False)
+    if tuple(out.shape) != tuple(shape) or out.device != device:
+        raise ValueError(f"{name}: {tuple(shape)} on {device}, not {tuple(out.shape)} on {out.device}")
+    return out
+
+
+def _status(t):
+    return None if t is None else _want(t, torch.int32, 1, "dev_status").data_ptr()
+
+
+def _step(t: torch.Tensor, dim: int, width: int) -> int:
+    """The stride along `dim`; an axis of one element has none that matters."""
+    return t.stride(dim) if t.shape[dim] > 1 else width
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+class LatentCache:
+    """A paged latent cache: `pages` uint8 [num_pages, >= 64 * record bytes], rows page stride apart."""
+
+    def __init__(self, pages: torch.Tensor, rope_dim: int = 64, record_format="bf16"):
+        _want(pages, torch.uint8, 2, "pages")
+        self.record_format, self.rope_dim = FORMATS.get(record_format, -1), int(rope_dim)
+        self.record_bytes = record_bytes(record_format, rope_dim)
+        if pages.shape[1] < native.PAGE_RECORDS * self.record_bytes:
+            raise ValueError(f"pages hold at least {native.PAGE_RECORDS * self.record_bytes} bytes")
+        self.pages = pages
+        self.width = LATENT_DIM + self.rope_dim
+        self.args = CacheArgs(pages.data_ptr(), pages.shape[0], _step(pages, 0, pages.shape[1]), self.rope_dim, self.record_format)
+
+    @staticmethod
+    def empty(num_pages: int, rope_dim: int = 64, record_format="bf16", device="cuda") -> "LatentCache":
+        n = native.PAGE_RECORDS * record_bytes(record_format, rope_dim)
+        return LatentCache(torch.empty((num_pages, n), dtype=torch.uint8, device=device), rope_dim, record_format)
+
+
+class StepTables(NamedTuple):
+    """What csa_build_tables makes beside the page table."""
+    row_req: torch.Tensor    # [n_rows] int32
+    row_pos: torch.Tensor    # [n_rows] int32
+    row_len: torch.Tensor    # [n_rows] int32
+    row_slot: torch.Tensor   # [n_rows] int64
+    row_start: torch.Tensor  # [num_req + 1] int32
+    kv_start: torch.Tensor   # [num_req + 1] int32
+    taken: torch.Tensor      # [1] int32
+
+
+def empty_tables(num_req: int, n_rows: int, device="cuda") -> StepTables:
+    """Tables for csa_build_tables to fill, in one allocation."""
+    ints = 3 * n_rows + 2 * (num_req + 1) + 1
+    buf = torch.empty(2 * n_rows + ints, dtype=torch.int32, device=device)
+    slot = buf[:2 * n_rows].view(torch.int64)
+    req, pos, length, row_start, kv_start, taken = buf[2 * n_rows:].split([n_rows] * 3 + [num_req + 1] * 2 + [1])
+    return StepTables(req, pos, length, slot, row_start, kv_start, taken)
+
+
+def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
+                     n_rows: int, out: Optional[StepTables] = None, dev_status: Optional[torch.Tensor] = None,
+                     stream=None) -> StepTables:
+    """Block tables and slot maps of one step: request r holds old_len[r] records and gets new_len[r]
+    more. page_table [num_req, pt_stride] gets the new pages in place, out of free_pages; the maps of
+    the new records (n_rows of them, the rest padding) are returned."""
+    _want(old_len, torch.int32, 1, "old_len")
+    _want(new_len, torch.int32, 1, "new_len")
+    _want(page_table, torch.int32, 2, "page_table")
+    _want(free_pages, torch.int32, 1, "free_pages")
+    dev, n, n_rows = old_len.device, old_len.shape[0], int(n_rows)
+    _same_device(dev, new_len=new_len, page_table=page_table, free_pages=free_pages)
+    if new_len.shape[0] != n or page_table.shape[0] != n:
+        raise ValueError("old_len, new_len and page_table: one row a request")
+    if n > 0 and page_table.stride(0) != page_table.shape[1]:
+        raise ValueError("page_table: contiguous")
+    if out is None:
+        out = empty_tables(n, n_rows, dev)
+    else:
+        for t, (size, dtype), name in zip(out, [(n_rows, torch.int32)] * 3 + [(n_rows, torch.int64)] +
+                                          [(n + 1, torch.int32)] * 2 + [(1, torch.int32)], StepTables._fields):
+            _pick(t, (size,), dtype, dev, name)
+    a = TablesArgs(old_len.data_ptr(), new_len.data_ptr(), n, page_table.shape[1], page_table.data_ptr(),
+                   free_pages.data_ptr(), free_pages.shape[0], n_rows, out.row_req.data_ptr(), out.row_pos.data_ptr(),
+                   out.row_len.data_ptr(), out.row_slot.data_ptr(), out.row_start.data_ptr(), out.kv_start.data_ptr(),
+                   out.taken.data_ptr(), _status(dev_status))
+    _check(load().csa_build_tables(ctypes.byref(a), _stream(stream)), "csa_build_tables")
+    return out
+
+
+def csa_latent_write(x: torch.Tensor, slots: torch.Tensor, cache: LatentCache,
+                     dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Stores rows x [n, 512 + rope] (fp32 or bf16) as the cache's records at `slots` [n] (int64)."""
+    if x.dtype not in (torch.float32, torch.bfloat16):
+        raise TypeError("x must be float32 or bfloat16")
+    _want(x, x.dtype, 2, "x")
+    _want(slots, torch.int64, 1, "slots")
+    _same_device(cache.pages.device, x=x, slots=slots)
+    if x.shape[1] != cache.width or slots.shape[0] != x.shape[0]:
+        raise ValueError(f"x [n, {cache.width}] and slots [n]")
+    a = LatentWriteArgs(cache.args, x.data_ptr(), _step(x, 0, cache.width),
+                        native.KEYS_BF16 if x.dtype == torch.bfloat16 else native.KEYS_F32, 0, x.shape[0],
+                        slots.data_ptr(), _status(dev_status))
+    _check(load().csa_latent_write(ctypes.byref(a), _stream(stream)), "csa_latent_write")
+
+
+def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torch.Tensor, n_rows: int,
+                    out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
+                    stream=None) -> torch.Tensor:
+    """Histories as rows [n_rows, 512 + rope] in bf16: record j of request r at kv_start[r] + j."""
+    _want(page_table, torch.int32, 2, "page_table")
+    _want(kv_start, torch.int32, 1, "kv_start")
+    dev = cache.pages.device
+    _same_device(dev, page_table=page_table, kv_start=kv_start)
+    if kv_start.shape[0] != page_table.shape[0] + 1 or not page_table.is_contiguous():
+        raise ValueError("page_table [num_req, pt_stride], contiguous, and kv_start [num_req + 1]")
+    out = _pick(out, (int(n_rows), cache.width), torch.bfloat16, dev, "out")
+    a = LatentReadArgs(cache.args, page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
+                       kv_start.data_ptr(), int(n_rows), out.data_ptr(), _status(dev_status))
+    _check(load().csa_latent_read(ctypes.byref(a), _stream(stream)), "csa_latent_read")
+    return out
+
+
+def _attend_args(q, cache, page_table, row_len, scale, idx, row_req, out, lse, dev_status):
+    _want(q, torch.bfloat16, 3, "q")
+    _want(page_table, torch.int32, 2, "page_table")
+    _want(row_len, torch.int32, 1, "row_len")
+    dev = cache.pages.device
+    _same_device(dev, q=q, page_table=page_table, row_len=row_len, idx=idx, row_req=row_req)
+    n, heads = q.shape[0], q.shape[1]
+    if q.shape[2] != cache.width or row_len.shape[0] != n or not page_table.is_contiguous():
+        raise ValueError(f"q [num_q, heads, {cache.width}], row_len [num_q], page_table contiguous")
+    if idx is not None:
+        _want(idx, torch.int32, 2, "idx")
+        if idx.shape[0] != n:
+            raise ValueError("idx [num_q, top]")
+    if row_req is not None and _want(row_req, torch.int32, 1, "row_req").shape[0] != n:
+        raise ValueError("row_req [num_q]")
+    out = _pick(out, (n, heads, LATENT_DIM), torch.bfloat16, dev, "out")
+    lse = _pick(lse, (n, heads), torch.float32, dev, "lse")
+    a = AttendArgs(cache.args, q.data_ptr(), _step(q, 0, cache.width), _step(q, 1, cache.width), n, heads, page_table.data_ptr(),
+                   page_table.shape[0], page_table.shape[1], _ptr(row_req), row_len.data_ptr(), _ptr(idx),
+                   0 if idx is None else _step(idx, 0, idx.shape[1]), 0 if idx is None else idx.shape[1],
+                   float(scale), out.data_ptr(), lse.data_ptr(), _status(dev_status))
+    return a, out, lse
+
+
+def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Tensor, row_len: torch.Tensor, *,
+                      scale: float, idx: Optional[torch.Tensor] = None, row_req: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                      ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Latent attention, absorbed form: q [num_q, heads, 512 + rope] bf16 over the records below row_len[b]
+    of request row_req[b] (identity when None), or over the positions idx [num_q, top] (-1: none) among
+    them. Returns (out [num_q, heads, 512] bf16, lse [num_q, heads] fp32)."""
+    a, out, lse = _attend_args(q, cache, page_table, row_len, scale, idx, row_req, out, lse, dev_status)
+    lib = load()
+    if ws is None:
+        ws = torch.empty(max(int(lib.csa_latent_attend_workspace_bytes(ctypes.byref(a))), 16), dtype=torch.uint8,
+                         device=out.device)
+    _check(lib.csa_latent_attend(ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(stream)), "csa_latent_attend")
+    return out, lse
+
+
+def csa_latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
+                       q_start: torch.Tensor, kv_start: torch.Tensor, *, scale: float, causal: bool = True,
+                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                       dev_status: Optional[torch.Tensor] = None, stream=None):
+    """Latent attention, expanded form: q [total_q, heads, 192], k_nope and v [total_k, heads, 128], k_rope
+    [total_k, 64], all bf16; request r has rows q_start[r] .. q_start[r + 1] of q and kv_start[r] ..
+    kv_start[r + 1] of the keys. Returns (out [total_q, heads, 128] bf16, lse [total_q, heads] fp32)."""
+    for t, name, dims in ((q, "q", 3), (k_nope, "k_nope", 3), (v, "v", 3), (k_rope, "k_rope", 2)):
+        _want(t, torch.bfloat16, dims, name)
+    _want(q_start, torch.int32, 1, "q_start")
+    _want(kv_start, torch.int32, 1, "kv_start")
+    _same_device(q.device, k_nope=k_nope, k_rope=k_rope, v=v, q_start=q_start, kv_start=kv_start)
+    tq, heads, tk = q.shape[0], q.shape[1], k_nope.shape[0]
+    if (q.shape[2] != PREFILL_NOPE + PREFILL_ROPE or k_nope.shape[1:] != (heads, PREFILL_NOPE) or
+            v.shape != (tk, heads, PREFILL_V) or k_rope.shape != (tk, PREFILL_ROPE) or
+            q_start.shape != kv_start.shape or q_start.shape[0] < 1):
+        raise ValueError("q [tq, h, 192], k_nope and v [tk, h, 128], k_rope [tk, 64], q_start and kv_start [num_req + 1]")
+    out = _pick(out, (tq, heads, PREFILL_V), torch.bfloat16, q.device, "out")
+    lse = _pick(lse, (tq, heads), torch.float32, q.device, "lse")
+    a = PrefillArgs(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _step(q, 0, 192),
+                    _step(q, 1, 192), _step(k_nope, 0, 128), _step(k_nope, 1, 128), _step(k_rope, 0, 64),
+                    _step(v, 0, 128), _step(v, 1, 128), tq, tk,
+                    q_start.data_ptr(), kv_start.data_ptr(), q_start.shape[0] - 1, heads, int(bool(causal)),
+                    float(scale), out.data_ptr(), lse.data_ptr(), _status(dev_status))
+    _check(load().csa_latent_prefill(ctypes.byref(a), _stream(stream)), "csa_latent_prefill")
+    return out, lse
