@@ -1,42 +1,119 @@
 // csa_latent_attend.cu — latent attention, absorbed form (include/csa_latent.h).
-#include <cuda_fp4.h>
-
 #include "csa_latent_common.cuh"
+#include "csa_latent_ptx.cuh"
 
 namespace csa_latent {
 namespace {
 
-constexpr int kThreads = 128;
+using csa::mbar_arrive;
+using csa::mbar_wait;
+using csa::smem_u32;
+
+// The kernel. Per head h and visible record n, with S = q . c:
+//   p_n = 2^(S_n c - m c), c = scale log2 e,  O = sum p_n c_n[0:512],  l = sum p_n,
+// out = O / l, lse = ln 2 (m c + log2 l), for any reference m per head: m is the first tile's
+// maximum and moves only when a tile exceeds it by 2^8, so that O is rarely rescaled and
+// p stays below 2^8.
+//
+// A CTA takes 64 heads of one row and runs over tiles of 64 records. One tile in shared
+// memory is both operands of the tensor cores: K-major as the keys (S = Q C^T, 64 heads x 64
+// records over the record's 512 + rope values), MN-major as the values (O^T = C^T P^T, 512
+// values x 64 heads over the 64 records), so a record is fetched once. S is kept with a head a
+// TMEM lane, so that a softmax row belongs to one thread; O is kept transposed (128 values a
+// lane block, a head a column), because 64 heads x 512 values with the heads in the lanes
+// would fill all 512 columns of TMEM and leave S no room.
+//
+// Shared memory: Q (72 KB), two record tiles (72 KB each), P (8 KB): 224 KB, one CTA an SM.
+// Warps 0-3: softmax (S from TMEM, P to shared memory) and the output. Warps 4-11: loaders.
+// They hold one more tile in registers, so that its global loads are in flight while
+// both tiles in shared memory are in use; MXFP4 codes become bf16 values (exactly) on the
+// way. Warp 12: one thread issues the MMAs: S of tile i + 1 before O of tile i, so that the
+// tensor cores work during tile i's softmax.
+//
+// Work is split over a long axis: the tiles of all (row, head group) units, in order, are
+// cut into equal runs, one a CTA; a unit that is cut leaves unnormalised parts (O, m, l in
+// fp32) in the workspace, which a second kernel joins in the order of the runs, so results do not
+// depend on timing.
+constexpr int kTile = 64, kHeads = 64;            // records a tile, heads a unit
+constexpr int kColBytes = kTile * 128;            // 64 values of a tile's 64 records (or of Q's 64 heads)
+constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
+constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
+constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kMaxGrid = 160;                     // CTAs at most: sizes the workspace
+constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T in columns 0 .. 255, S in 256 .. 383
+constexpr float kGrow = 8.0f;                     // log2 of how far p may exceed 1
+constexpr int kBarSoftmax = 1;
+
+template <int kRope>
+struct Smem {
+  static constexpr int kCols = (kDim + kRope) / 64;
+  uint8_t q[kCols * kColBytes];
+  uint8_t c[2][kCols * kColBytes];
+  uint8_t p[kHeads * 128];
+  uint64_t bars[16];
+  uint8_t valid[2][kTile];  // 1 where the tile's record is visible
+  float alpha[kHeads];
+  int64_t total;
+  int32_t unit, off;
+  uint32_t tmem;
+  int abort;
+};
+enum { kBarCFull = 0, kBarCEmpty = 2, kBarSFull = 4, kBarSEmpty = 6, kBarQFull = 8, kBarQEmpty, kBarPFull, kBarPEmpty,
+       kBarOFull, kBarOEmpty, kBarDrain };
+
+// A part of a cut unit: O [64 heads][512], then m c and l of the 64 heads.
+constexpr size_t kPartFloats = static_cast<size_t>(kHeads) * (kDim + 2);
+
+struct Plan {  // of one CTA's run, for the join: where in its first unit it starts
+  int64_t total;
+  int32_t unit, off, tiles, pad;
+};
+
+struct Kernel {
+  csa_latent_attend_args A;
+  Plan* plans;
+  float* parts;
+  int32_t groups;  // head groups of 64
+};
 
 // What a query row sees: its request's page table row and its length.
 struct RowView {
-  const int32_t* table;  // null: an empty row
-  int32_t len;
+  const int32_t* table;
+  int32_t len;  // 0 for a row whose request is out of range
 };
 
 __device__ __forceinline__ RowView row_view(const csa_latent_attend_args& A, int b, int32_t* flags) {
   const int32_t req = A.row_req ? A.row_req[b] : b;
   if (req < 0 || req >= A.num_req) {
     *flags |= CSA_DEV_BAD_REQUEST;
-    return {nullptr, 0};
+    return {A.page_table, 0};
   }
   const int32_t n = A.row_len[b], cap = kPageRecs * A.pt_stride, len = min(max(n, 0), cap);
   if (len != n) *flags |= CSA_DEV_LEN_OOB;
   return {A.page_table + static_cast<int64_t>(req) * A.pt_stride, len};
 }
 
-// The record of the row's j-th entry (of the listed positions or of the history),
-// or null where nothing is visible.
+// Tiles of row b; an empty row still has one, which writes its output.
+__device__ __forceinline__ int tiles_of(const csa_latent_attend_args& A, int b) {
+  if (A.idx) return (A.top + kTile - 1) / kTile;
+  int32_t ignore = 0;
+  return max(1, (row_view(A, b, &ignore).len + kTile - 1) / kTile);
+}
+
+// The record of entry j of the row (of the listed positions, or of the history), or null.
 __device__ __forceinline__ const uint8_t* record_of(const csa_latent_attend_args& A, const RowView& R, int b, int j,
                                                     int rec_bytes, int32_t* flags) {
   int32_t pos = j;
   if (A.idx) {
+    if (j >= A.top) return nullptr;
     pos = A.idx[b * A.idx_stride + j];
     if (pos == -1) return nullptr;
     if (pos < 0 || pos >= R.len) {
       *flags |= CSA_DEV_LEN_OOB;
       return nullptr;
     }
+  } else if (j >= R.len) {
+    return nullptr;
   }
   const int32_t page = R.table[pos / kPageRecs];
   if (page < 0 || page >= A.cache.num_pages) {
@@ -46,88 +123,598 @@ __device__ __forceinline__ const uint8_t* record_of(const csa_latent_attend_args
   return A.cache.pages + page * A.cache.page_stride_bytes + static_cast<int64_t>(pos % kPageRecs) * rec_bytes;
 }
 
-// Lane l's 16 latent values (16 l ..) and 2 rope values (2 l, 2 l + 1) of a record.
-template <bool kFp4>
-__device__ __forceinline__ void lane_values(const uint8_t* rec, int lane, int rope, float (&v)[18]) {
-  if constexpr (kFp4) {
-    const uint2 c = reinterpret_cast<const uint2*>(rec)[lane];
-    const float s = ue8m0(rec[kCodeBytes + (lane >> 1)]);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const uint32_t byte = ((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 0xFFu;
-      const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h));
-      v[2 * k] = f.x * s;
-      v[2 * k + 1] = f.y * s;
-    }
-  } else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(rec) + 8 * lane;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      v[2 * k] = __uint_as_float(w[k] << 16);
-      v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
-    }
-  }
-  const uint32_t t = rope ? reinterpret_cast<const uint32_t*>(rec + record_bytes(kFp4, 0))[lane] : 0u;
-  v[16] = __uint_as_float(t << 16);
-  v[17] = __uint_as_float(t & 0xFFFF0000u);
-}
+__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int c, int grid) { return total * c / grid; }
 
-// One block per (row, head): each warp takes every fourth visible record, the dot
-// product split over its lanes, and keeps its own running maximum, sum and
-// weighted sum of values in registers; the warps are joined at the end.
-template <bool kFp4>
-__global__ void __launch_bounds__(kThreads) attend_kernel(const csa_latent_attend_args A) {
-  const int h = blockIdx.x % A.num_heads, b = blockIdx.x / A.num_heads;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int rope = A.cache.rope_dim, rec_bytes = record_bytes(kFp4, rope);
-  __shared__ float s_o[kThreads / 32][kDim];
-  __shared__ float s_m[kThreads / 32], s_l[kThreads / 32];
-  int32_t flags = 0;
-  const RowView R = row_view(A, b, &flags);
-  const __nv_bfloat16* qp =
-      static_cast<const __nv_bfloat16*>(A.q) + b * A.q_row_stride + static_cast<int64_t>(h) * A.q_head_stride;
-  float q[18], o[16] = {}, m = -INFINITY, l = 0.f;
-  lane_values<false>(reinterpret_cast<const uint8_t*>(qp), lane, rope, q);
-  const int n = R.table ? (A.idx ? A.top : R.len) : 0;
-  for (int j = warp; j < n; j += kThreads / 32) {
-    const uint8_t* rec = record_of(A, R, b, j, rec_bytes, &flags);
-    if (!rec) continue;
-    float v[18], s = 0.f;
-    lane_values<kFp4>(rec, lane, rope, v);
-#pragma unroll
-    for (int k = 0; k < 18; ++k) s = fmaf(q[k], v[k], s);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-    s *= A.scale;
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    m = top;
-    l = fmaf(l, keep, p);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = fmaf(o[k], keep, p * v[k]);
+// This CTA's run: the total of all units' tiles, and the unit and the tile in it where the run starts.
+template <int kRope>
+__device__ void make_plan(const Kernel& K, Smem<kRope>& S, int64_t* scan) {
+  const csa_latent_attend_args& A = K.A;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (A.idx) {
+    if (tid == 0) {
+      const int64_t per = tiles_of(A, 0);
+      S.total = per * A.num_q * K.groups;
+      const int64_t at = run_start(S.total, blockIdx.x, gridDim.x);
+      S.unit = static_cast<int32_t>(at / per);
+      S.off = static_cast<int32_t>(at % per);
+    }
+    __syncthreads();
+    return;
   }
+  const int per = (A.num_q + kThreads - 1) / kThreads;
+  const int b0 = min(tid * per, A.num_q), b1 = min(b0 + per, A.num_q);
+  int64_t mine = 0;
+  for (int b = b0; b < b1; ++b) mine += tiles_of(A, b);
+  int64_t incl = mine;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) s_o[warp][16 * lane + k] = o[k];
-  if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scan[w];
+    total += scan[w];
+  }
+  before *= K.groups;
+  total *= K.groups;
+  const int64_t at = run_start(total, blockIdx.x, gridDim.x);
+  if (tid == 0) S.total = total;
+  if (at >= before && at < before + mine * K.groups) {
+    for (int b = b0; b < b1; ++b) {
+      const int64_t n = tiles_of(A, b), all = n * K.groups;
+      if (at < before + all) {
+        S.unit = b * K.groups + static_cast<int32_t>((at - before) / n);
+        S.off = static_cast<int32_t>((at - before) % n);
+        break;
+      }
+      before += all;
+    }
   }
   __syncthreads();
-  float top = -INFINITY, sum = 0.f, w[kThreads / 32];
-  for (int k = 0; k < kThreads / 32; ++k) top = fmaxf(top, s_m[k]);
-  for (int k = 0; k < kThreads / 32; ++k) {
-    w[k] = s_m[k] == -INFINITY ? 0.f : expf(s_m[k] - top);
-    sum = fmaf(s_l[k], w[k], sum);
+}
+
+// Walks a run piece by piece: a piece is the run's part of one unit.
+struct Pieces {
+  int64_t left;
+  int unit, off, tiles, n;  // tiles of the unit, tiles of the piece
+  template <int kRope>
+  __device__ __forceinline__ Pieces(const Kernel& K, const Smem<kRope>& S) {
+    left = run_start(S.total, blockIdx.x + 1, gridDim.x) - run_start(S.total, blockIdx.x, gridDim.x);
+    unit = S.unit;
+    off = S.off;
+    size(K);
   }
-  const int64_t row = static_cast<int64_t>(b) * A.num_heads + h;
-  for (int d = threadIdx.x; d < kDim; d += kThreads) {
-    float a = 0.f;
-    for (int k = 0; k < kThreads / 32; ++k) a = fmaf(s_o[k][d], w[k], a);
-    static_cast<__nv_bfloat16*>(A.out)[row * kDim + d] = __float2bfloat16_rn(sum > 0.f ? a / sum : 0.f);
+  __device__ __forceinline__ void size(const Kernel& K) {
+    if (left <= 0) return;
+    tiles = tiles_of(K.A, unit / K.groups);
+    n = static_cast<int>(min(left, static_cast<int64_t>(tiles - off)));
   }
-  if (A.lse && threadIdx.x == 0) A.lse[row] = sum > 0.f ? top + logf(sum) : -INFINITY;
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const Kernel& K) {
+    left -= n;
+    ++unit;
+    off = 0;
+    size(K);
+  }
+};
+
+// The bytes of one tile in a loader thread's registers, and how they become the tile in
+// shared memory: value v of record r at column v / 64, row r, 16-byte chunk (v % 64) / 8 ^ (r % 8).
+template <bool kFp4, int kRope>
+struct TileRegs;
+
+// bf16: eight lanes a record (128 bytes of it at a time), records r and r + 32.
+template <int kRope>
+struct TileRegs<false, kRope> {
+  static constexpr int kCols = (kDim + kRope) / 64;
+  uint4 w[2][kCols];
+  bool live[2];
+  __device__ __forceinline__ void fetch(const csa_latent_attend_args& A, const RowView& R, int b, int tile, int t,
+                                        int32_t* flags) {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint8_t* rec = record_of(A, R, b, tile * kTile + (t >> 3) + 32 * k, record_bytes(false, kRope), flags);
+      live[k] = rec != nullptr;
+      const uint4* p = reinterpret_cast<const uint4*>(rec) + (t & 7);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) w[k][c] = rec ? __ldg(p + 8 * c) : make_uint4(0, 0, 0, 0);
+    }
+  }
+  __device__ __forceinline__ void store(uint32_t dst, uint8_t* valid, int t) const {
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int r = (t >> 3) + 32 * k;
+      const uint32_t at = dst + r * 128 + (((t & 7) ^ (r & 7)) << 4);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) csa::st_shared_v4(at + c * kColBytes, w[k][c].x, w[k][c].y, w[k][c].z, w[k][c].w);
+      if ((t & 7) == 0) valid[r] = live[k];
+    }
+  }
+};
+
+// MXFP4: four lanes a record; lane s takes its blocks of 32 values s, s + 4, s + 8, s + 12
+// (16 code bytes and one scale byte each) and a quarter of its rope values.
+template <int kRope>
+struct TileRegs<true, kRope> {
+  uint4 code[4], scale, rope[2];
+  bool live;
+  __device__ __forceinline__ void fetch(const csa_latent_attend_args& A, const RowView& R, int b, int tile, int t,
+                                        int32_t* flags) {
+    const uint8_t* rec = record_of(A, R, b, tile * kTile + (t >> 2), record_bytes(true, kRope), flags);
+    live = rec != nullptr;
+    const uint4* p = reinterpret_cast<const uint4*>(rec);
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) code[k] = rec ? __ldg(p + (t & 3) + 4 * k) : zero;
+    scale = rec ? __ldg(p + kCodeBytes / 16) : zero;
+#pragma unroll
+    for (int k = 0; k < 2; ++k)
+      rope[k] = kRope != 0 && rec ? __ldg(p + (kCodeBytes + kScaleBytes) / 16 + 2 * (t & 3) + k) : zero;
+  }
+  // Four e2m1 codes (the low 16 bits of `sel`) as bf16 values times `s2`. The magnitudes
+  // 0 1/2 1 3/2 2 3 4 6 are looked up as the two bytes of their bf16 by byte permutes; a permute
+  // in its sign-replicating mode spreads the codes' sign bits. The product with a power of two is
+  // exact.
+  static __device__ __forceinline__ void four(uint32_t sel, __nv_bfloat162 s2, uint32_t* lo, uint32_t* hi) {
+    const uint32_t mag = sel & 0x7777u;
+    const uint32_t h = __byte_perm(0x3F3F3F00u, 0x40404040u, mag), l = __byte_perm(0xC0800000u, 0xC0804000u, mag);
+    // bytes 0x80 where the sign bit is clear, 0xFF where it is set: bit 6 is the sign
+    uint32_t sg;
+    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(sel));
+    const uint32_t hs = h | ((sg << 1) & 0x80808080u);
+    uint32_t a = __byte_perm(l, hs, 0x5140), b = __byte_perm(l, hs, 0x7362);
+    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), s2);
+    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), s2);
+    *lo = *reinterpret_cast<const uint32_t*>(&x);
+    *hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+  __device__ __forceinline__ void store(uint32_t dst, uint8_t* valid, int t) const {
+    const int r = t >> 2, s = t & 3;
+    const bool swap = s >= 2;  // lanes 2, 3 store their words in another order: no two on one bank
+    const uint32_t row = dst + r * 128;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int blk = s + 4 * k;
+      const uint32_t sw = k == 0 ? scale.x : (k == 1 ? scale.y : (k == 2 ? scale.z : scale.w));
+      const uint32_t sb = (sw >> (8 * s)) & 0xFFu;
+      const uint32_t bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7);
+      const uint32_t two = bits | (bits << 16);
+      const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
+      const uint32_t word[4] = {swap ? code[k].z : code[k].x, swap ? code[k].w : code[k].y,
+                                swap ? code[k].x : code[k].z, swap ? code[k].y : code[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t v[4];
+        four(word[j], s2, &v[0], &v[1]);
+        four(word[j] >> 16, s2, &v[2], &v[3]);
+        const int chunk = 4 * (blk & 1) + (swap ? j ^ 2 : j);
+        csa::st_shared_v4(row + (blk >> 1) * kColBytes + ((chunk ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+      }
+    }
+    if constexpr (kRope != 0) {
+#pragma unroll
+      for (int k = 0; k < 2; ++k)
+        csa::st_shared_v4(row + (kDim / 64) * kColBytes + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y, rope[k].z,
+                          rope[k].w);
+    }
+    if (s == 0) valid[r] = live;
+  }
+};
+
+// A whole warp's bounded wait. The answer is the same for all lanes: a lane that left a role alone
+// would strand the others at their next warp barrier.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, stop));
+}
+
+template <bool kFp4, int kRope>
+__device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
+  constexpr int kCols = Smem<kRope>::kCols;
+  const csa_latent_attend_args& A = K.A;
+  const int t = threadIdx.x - 32 * kSoftmaxWarps, lane = t & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars);
+  Pieces run(K, S);
+  if (!run.more()) return;
+  RowView R = row_view(A, run.unit / K.groups, flags);
+  TileRegs<kFp4, kRope> x;
+  x.fetch(A, R, run.unit / K.groups, run.off, t, flags);
+  uint32_t g = 0, piece = 0;
+  while (run.more()) {
+    // Q of the piece: head h's 64-value columns at row h, swizzled as the records; zeros past the last head
+    const int b = run.unit / K.groups, h0 = (run.unit % K.groups) * kHeads;
+    if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int h = (t >> 3) + 32 * k;
+      const bool live = h0 + h < A.num_heads;
+      const uint8_t* q = static_cast<const uint8_t*>(A.q) +
+                         2 * (b * A.q_row_stride + (live ? h0 + h : 0) * A.q_head_stride) + 16 * (t & 7);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+        csa::cp_async16(smem_u32(S.q) + c * kColBytes + h * 128 + (((t & 7) ^ (h & 7)) << 4), q + 128 * c, live);
+    }
+    csa::cp_async_wait_all();
+    csa::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * kBarQFull);
+    const int n = run.n, off = run.off;
+    for (int i = 0; i < n; ++i) {
+      if (!warp_wait(bars + 8 * (kBarCEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop)) return;
+      x.store(smem_u32(S.c[g & 1]), S.valid[g & 1], t);
+      csa::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kBarCFull + (g & 1)));
+      ++g;
+      int nb = b, ntile = off + i + 1;
+      if (i + 1 == n) {
+        run.next(K);
+        if (!run.more()) break;
+        nb = run.unit / K.groups;
+        ntile = run.off;
+        R = row_view(A, nb, flags);
+      }
+      x.fetch(A, R, nb, ntile, t, flags);
+    }
+    ++piece;
+  }
+}
+
+template <int kRope>
+__device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
+  constexpr int kCols = Smem<kRope>::kCols;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem;
+  const int heads_left = K.A.num_heads;
+  constexpr uint32_t idesc_s = csa::idesc_bf16_f32(64, kTile);
+  const uint64_t q_desc = csa::sdesc_kmajor_sw128(smem_u32(S.q)), p_desc = csa::sdesc_kmajor_sw128(smem_u32(S.p));
+  uint32_t g = 0, piece = 0;
+  bool ok = true;
+  // O of tile g: the first of a piece overwrites
+  auto issue_o = [&](uint32_t tile, uint32_t pc, bool first, bool last, uint32_t idesc_o) {
+    ok = ok && mbar_wait(bars + 8 * kBarPFull, tile & 1, stop);
+    if (first) ok = ok && mbar_wait(bars + 8 * kBarOEmpty, (pc & 1) ^ 1, stop);
+    if (!ok) return;
+    csa::tc_fence_after();
+    const uint32_t c = smem_u32(S.c[tile & 1]);
+#pragma unroll
+    for (int d = 0; d < kDim / 128; ++d) {
+#pragma unroll
+      for (int k = 0; k < kTile / 16; ++k) {
+        const uint64_t a = csa::sdesc_mn_sw128_b16(c + 2 * d * kColBytes + k * 2048, kColBytes);
+        csa::mma_f16_ss(tmem + d * kHeads, a, p_desc + 2 * k, idesc_o, !first || k > 0);
+      }
+    }
+    csa::mma_commit(bars + 8 * (kBarCEmpty + (tile & 1)));
+    csa::mma_commit(bars + 8 * kBarPEmpty);
+    if (last) csa::mma_commit(bars + 8 * kBarOFull);
+  };
+  bool pending = false, pend_first = false, pend_last = false;
+  uint32_t pend_idesc = 0, pend_piece = 0;
+  for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
+    const int heads = min(heads_left - (run.unit % K.groups) * kHeads, kHeads);
+    const uint32_t idesc_o = csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor;
+    ok = ok && mbar_wait(bars + 8 * kBarQFull, piece & 1, stop);
+    for (int i = 0; ok && i < run.n; ++i, ++g) {
+      ok = ok && mbar_wait(bars + 8 * (kBarCFull + (g & 1)), (g >> 1) & 1, stop);
+      ok = ok && mbar_wait(bars + 8 * (kBarSEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop);
+      if (!ok) break;
+      csa::tc_fence_after();
+      const uint64_t c_desc = csa::sdesc_kmajor_sw128(smem_u32(S.c[g & 1]));
+#pragma unroll
+      for (int c = 0; c < kCols; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          csa::mma_f16_ss(tmem + kTmemS + (g & 1) * kTile, q_desc + c * (kColBytes >> 4) + 2 * k,
+                          c_desc + c * (kColBytes >> 4) + 2 * k, idesc_s, c > 0 || k > 0);
+      csa::mma_commit(bars + 8 * (kBarSFull + (g & 1)));
+      if (i + 1 == run.n) csa::mma_commit(bars + 8 * kBarQEmpty);
+      if (pending) issue_o(g - 1, pend_piece, pend_first, pend_last, pend_idesc);
+      pending = true;
+      pend_first = i == 0;
+      pend_last = i + 1 == run.n;
+      pend_idesc = idesc_o;
+      pend_piece = piece;
+    }
+  }
+  if (ok && pending) issue_o(g - 1, pend_piece, pend_first, pend_last, pend_idesc);
+  // nothing of this CTA's MMAs is in flight when it leaves
+  csa::mma_commit(bars + 8 * kBarDrain);
+  csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
+}
+
+// out (or a part) from O^T: a thread holds one value of 128 per column block, for every head.
+template <int kRope>
+__device__ void write_out(const Kernel& K, Smem<kRope>& S, int unit, int heads, int warp, int lane) {
+  const int b = unit / K.groups, h0 = (unit % K.groups) * kHeads;
+  __nv_bfloat16* out =
+      static_cast<__nv_bfloat16*>(K.A.out) + (static_cast<int64_t>(b) * K.A.num_heads + h0) * kDim + 32 * warp;
+  const int odd = lane & 1;
+#pragma unroll 1
+  for (int d = 0; d < kDim / 128; ++d) {
+#pragma unroll 1
+    for (int hh = 0; hh < heads; hh += 32) {
+      uint32_t v[32];
+      csa::tmem_ld32(S.tmem + d * kHeads + hh + (static_cast<uint32_t>(32 * warp) << 16), v);
+      csa::tmem_wait_ld();
+      // two heads at a time: even lanes end with values (lane, lane + 1) of the first, odd lanes with
+      // values (lane - 1, lane) of the second
+#pragma unroll
+      for (int j = 0; j < 32; j += 2) {
+        const float x0 = __uint_as_float(v[j]) * S.alpha[hh + j], x1 = __uint_as_float(v[j + 1]) * S.alpha[hh + j + 1];
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
+        const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(got, x1) : __floats2bfloat162_rn(x0, got);
+        if (hh + j + odd < heads)
+          *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(hh + j + odd) * kDim + 128 * d + (lane & ~1)) = two;
+      }
+    }
+  }
+}
+
+template <int kRope>
+__device__ void write_part(const Kernel& K, Smem<kRope>& S, float* part, int heads, int warp, int lane) {
+#pragma unroll 1
+  for (int d = 0; d < kDim / 128; ++d) {
+#pragma unroll 1
+    for (int hh = 0; hh < heads; hh += 32) {
+      uint32_t v[32];
+      csa::tmem_ld32(S.tmem + d * kHeads + hh + (static_cast<uint32_t>(32 * warp) << 16), v);
+      csa::tmem_wait_ld();
+#pragma unroll
+      for (int j = 0; j < 32; ++j) part[(hh + j) * kDim + 128 * d + 32 * warp + lane] = __uint_as_float(v[j]);
+    }
+  }
+}
+
+template <int kRope>
+__device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
+  const csa_latent_attend_args& A = K.A;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars);
+  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;  // this warp's TMEM lanes
+  // S of 64 rows lies in lanes 0 .. 15 of each warp's 32: head 16 warp + lane
+  const bool mine = lane < 16;
+  const int head = 16 * warp + (lane & 15);
+  const uint32_t p_row = smem_u32(S.p) + head * 128;
+  const float c = A.scale * 1.4426950408889634f;
+  const float grow = kGrow / c;
+  uint32_t g = 0, piece = 0;
+  bool ok = true;  // once a wait has run out, the rest runs through without waiting: all warps meet at every barrier
+  for (Pieces run(K, S); run.more(); run.next(K), ++piece) {
+    const int heads = min(A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < run.n; ++i, ++g) {
+      ok = ok && warp_wait(bars + 8 * (kBarSFull + (g & 1)), (g >> 1) & 1, stop);
+      ok = ok && warp_wait(bars + 8 * (kBarCFull + (g & 1)), (g >> 1) & 1, stop);  // complete: for `valid`
+      csa::tc_fence_after();
+      uint32_t raw[2][32];
+      csa::tmem_ld32(S.tmem + kTmemS + (g & 1) * kTile + lanes, raw[0]);
+      csa::tmem_ld32(S.tmem + kTmemS + (g & 1) * kTile + 32 + lanes, raw[1]);
+      csa::tmem_wait_ld();
+      csa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * (kBarSEmpty + (g & 1)));
+      float s[kTile];
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) s[j] = __uint_as_float(raw[j >> 5][j & 31]);
+      const uint32_t* vw = reinterpret_cast<const uint32_t*>(S.valid[g & 1]);
+      uint32_t all = 0x01010101u;
+#pragma unroll
+      for (int k = 0; k < kTile / 4; ++k) all &= vw[k];
+      if (all != 0x01010101u) {
+#pragma unroll
+        for (int k = 0; k < kTile / 4; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!((vw[k] >> (8 * j)) & 1u)) s[4 * k + j] = -INFINITY;
+      }
+      float top = s[0];
+#pragma unroll
+      for (int j = 1; j < kTile; ++j) top = fmaxf(top, s[j]);
+      float keep = 1.f;
+      const bool up = mine && top > m + grow;
+      if (up) {
+        keep = csa::ex2((m - top) * c);  // 0 when there was nothing
+        m = top;
+        l *= keep;
+      }
+      if (i > 0 && csa::named_bar_any(kBarSoftmax, 32 * kSoftmaxWarps, up)) {
+        if (mine) S.alpha[head] = keep;
+        csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+        ok = ok && warp_wait(bars + 8 * kBarPEmpty, (g & 1) ^ 1, stop);  // O of the tile before is complete
+        csa::tc_fence_after();
+#pragma unroll 1
+        for (int col = 0; col < kDim / 128 * kHeads; col += 32) {
+          uint32_t v[32];
+          csa::tmem_ld32(S.tmem + col + lanes, v);
+          csa::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * S.alpha[(col & (kHeads - 1)) + j]);
+          csa::tmem_st32(S.tmem + col + lanes, v);
+        }
+        csa::tmem_wait_st();
+        csa::tc_fence_before();
+        csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);  // alpha is free again
+      }
+      const float mc = m == -INFINITY ? 0.f : m * c;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < kTile; ++j) {
+        s[j] = csa::ex2(fmaf(s[j], c, -mc));
+        sum += s[j];
+      }
+      l += sum;
+      ok = ok && warp_wait(bars + 8 * kBarPEmpty, (g & 1) ^ 1, stop);
+      if (mine) {
+#pragma unroll
+        for (int k = 0; k < kTile / 8; ++k) {
+          // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const __nv_bfloat162 two = __floats2bfloat162_rn(s[8 * k + 2 * j], s[8 * k + 2 * j + 1]);
+            w[j] = *reinterpret_cast<const uint32_t*>(&two);
+          }
+          csa::st_shared_v4(p_row + ((k ^ (head & 7)) << 4), w[0], w[1], w[2], w[3]);
+        }
+      }
+      csa::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bars + 8 * kBarPFull);
+    }
+    // the piece's output
+    ok = ok && warp_wait(bars + 8 * kBarOFull, piece & 1, stop);
+    csa::tc_fence_after();
+    const float mc = m == -INFINITY ? -INFINITY : m * c;
+    if (run.n == run.tiles) {
+      csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      if (mine) {
+        S.alpha[head] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
+        if (A.lse && head < heads)
+          A.lse[static_cast<int64_t>(run.unit / K.groups) * A.num_heads + (run.unit % K.groups) * kHeads + head] =
+              l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
+      }
+      csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
+      write_out(K, S, run.unit, heads, warp, lane);
+    } else {
+      float* part = K.parts + (2 * blockIdx.x + (run.off == 0)) * kPartFloats;
+      if (mine && head < heads) {
+        part[kHeads * kDim + head] = mc;
+        part[kHeads * (kDim + 1) + head] = l;
+      }
+      write_part(K, S, part, heads, warp, lane);
+    }
+    csa::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bars + 8 * kBarOEmpty);
+  }
+}
+
+template <bool kFp4, int kRope>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem<kRope>& S = *reinterpret_cast<Smem<kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int64_t scan[kThreads / 32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bars = smem_u32(S.bars);
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < 2; ++k) {
+      csa::mbar_init(bars + 8 * (kBarCFull + k), kLoadWarps);
+      csa::mbar_init(bars + 8 * (kBarCEmpty + k), 1);
+      csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarSEmpty + k), kSoftmaxWarps);
+    }
+    csa::mbar_init(bars + 8 * kBarQFull, kLoadWarps);
+    csa::mbar_init(bars + 8 * kBarQEmpty, 1);
+    csa::mbar_init(bars + 8 * kBarPFull, kSoftmaxWarps);
+    csa::mbar_init(bars + 8 * kBarPEmpty, 1);
+    csa::mbar_init(bars + 8 * kBarOFull, 1);
+    csa::mbar_init(bars + 8 * kBarOEmpty, kSoftmaxWarps);
+    csa::mbar_init(bars + 8 * kBarDrain, 1);
+    csa::mbar_init_fence();
+    S.abort = 0;
+  }
+  if (warp == kMmaWarp) {
+    csa::tmem_alloc(smem_u32(&S.tmem), kTmemCols);
+    csa::tmem_relinquish();
+  }
+  csa::tc_fence_before();
+  make_plan(K, S, scan);  // ends with a block barrier
+  csa::tc_fence_after();
+  int32_t flags = 0;
+  if (warp < kSoftmaxWarps) {
+    role_softmax(K, S);
+  } else if (warp < kMmaWarp) {
+    role_load<kFp4, kRope>(K, S, &flags);
+  } else {
+    if (lane == 0) {
+      if (K.plans) K.plans[blockIdx.x] = {S.total, S.unit, S.off, tiles_of(K.A, S.unit / K.groups), 0};
+      role_mma(K, S);
+    }
+    __syncwarp();
+  }
+  csa::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    csa::tc_fence_after();
+    csa::tmem_dealloc(S.tmem, kTmemCols);
+  }
+  if (threadIdx.x == 0 && S.abort) flags |= CSA_DEV_TIMEOUT;
   flags = static_cast<int32_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(flags)));
-  if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
+  if (flags && K.A.dev_status && lane == 0) atomicOr(K.A.dev_status, flags);
+}
+
+// Joins a cut unit: block (c - 1, head) does the unit that run c starts inside of, if c is the first
+// such run. Its parts are run c - 1's (from the unit's first tile on) and those of runs c, c + 1, ...
+// up to the unit's end, added in that order.
+constexpr int kJoinThreads = kDim / 4;
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Kernel K, int grid) {
+  const csa_latent_attend_args& A = K.A;
+  const int c = blockIdx.x + 1, head = blockIdx.y;
+  const Plan p = K.plans[c];
+  if (p.off == 0) return;
+  const int64_t begin = run_start(p.total, c, grid) - p.off, end = begin + p.tiles;
+  if (run_start(p.total, c - 1, grid) > begin) return;
+  const int h = (p.unit % K.groups) * kHeads + head;
+  if (h >= A.num_heads) return;
+  auto part_of = [&](int r) { return K.parts + (2 * static_cast<int64_t>(r) + (r == c - 1)) * kPartFloats; };
+  int last = c;
+  while (last + 1 < grid && run_start(p.total, last + 1, grid) < end) ++last;
+  float top = -INFINITY;
+  auto empty = [&](int r) { return run_start(p.total, r, grid) == run_start(p.total, r + 1, grid); };
+  for (int r = c - 1; r <= last; ++r)
+    if (!empty(r)) top = fmaxf(top, part_of(r)[kHeads * kDim + head]);
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int r = c - 1; r <= last; ++r) {
+    if (empty(r)) continue;
+    const float* part = part_of(r);
+    const float m = part[kHeads * kDim + head], w = m == -INFINITY ? 0.f : csa::ex2(m - top);
+    const float4 v = reinterpret_cast<const float4*>(part + head * kDim)[threadIdx.x];
+    l = fmaf(part[kHeads * (kDim + 1) + head], w, l);
+    o.x = fmaf(v.x, w, o.x);
+    o.y = fmaf(v.y, w, o.y);
+    o.z = fmaf(v.z, w, o.z);
+    o.w = fmaf(v.w, w, o.w);
+  }
+  const float inv = l > 0.f ? 1.f / l : l;
+  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), d = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+  const int64_t row = static_cast<int64_t>(p.unit / K.groups) * A.num_heads + h;
+  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + row * kDim)[threadIdx.x] =
+      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&d));
+  if (A.lse && threadIdx.x == 0) A.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+// CTAs of the call: one an SM, fewer when there cannot be as many tiles.
+int grid_cap(const csa_latent_attend_args* a) {
+  const int64_t groups = (a->num_heads + kHeads - 1) / kHeads;
+  const int64_t per = a->idx ? (a->top + kTile - 1) / kTile : (a->pt_stride > 0 ? a->pt_stride : 1);
+  const int64_t units = a->num_q * groups;
+  return static_cast<int>(units > kMaxGrid || per > kMaxGrid || units * per > kMaxGrid ? kMaxGrid : units * per);
+}
+
+constexpr size_t kPlanBytes = (kMaxGrid * sizeof(Plan) + 255) / 256 * 256;
+
+template <bool kFp4, int kRope>
+csa_status launch(const Kernel& K, int grid, cudaStream_t stream) {
+  static bool ready[64];  // the kernel's shared memory size is set on each device once
+  constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
+  static_assert(smem + 256 <= 232448, "shared memory of one CTA");
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA_ERR_CUDA;
+  if (!ready[dev]) {
+    if (cudaFuncSetAttribute(attend_kernel<kFp4, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem)) != cudaSuccess)
+      return CSA_ERR_CUDA;
+    ready[dev] = true;
+  }
+  attend_kernel<kFp4, kRope><<<grid, kThreads, smem, stream>>>(K);
+  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 csa_status check_args(const csa_latent_attend_args* a) {
@@ -158,7 +745,8 @@ csa_status check_args(const csa_latent_attend_args* a) {
 using namespace csa_latent;
 
 extern "C" size_t csa_latent_attend_workspace_bytes(const csa_latent_attend_args* a) {
-  return a && a->num_q >= 0 && a->num_heads >= 1 && a->num_heads <= CSA_LATENT_MAX_HEADS ? 16 : 0;
+  if (!a || a->num_q < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
+  return kPlanBytes + 2 * static_cast<size_t>(grid_cap(a)) * kPartFloats * sizeof(float);
 }
 
 extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -167,9 +755,21 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   if (a->num_q == 0) return CSA_OK;
   if (!ws || ws_bytes < csa_latent_attend_workspace_bytes(a)) return CSA_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return CSA_ERR_ALIGNMENT;
-  const int64_t blocks = static_cast<int64_t>(a->num_q) * a->num_heads;
-  if (blocks > INT32_MAX) return CSA_ERR_INVALID_ARG;
-  const auto kernel = a->cache.record_format == CSA_LATENT_MXFP4 ? attend_kernel<true> : attend_kernel<false>;
-  kernel<<<static_cast<unsigned>(blocks), kThreads, 0, static_cast<cudaStream_t>(stream)>>>(*a);
+  const int groups = (a->num_heads + kHeads - 1) / kHeads;
+  if (static_cast<int64_t>(a->num_q) * groups > INT32_MAX) return CSA_ERR_INVALID_ARG;
+  int sms = 0;
+  if (sm_count(&sms) != CSA_OK) return CSA_ERR_CUDA;
+  const int cap = grid_cap(a), grid = cap < sms ? cap : sms;
+  Kernel K;
+  K.A = *a;
+  K.groups = groups;
+  K.plans = static_cast<Plan*>(ws);
+  K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPlanBytes);
+  const auto s = static_cast<cudaStream_t>(stream);
+  const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
+  const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, s) : launch<true, 0>(K, grid, s))
+                            : (rope ? launch<false, 64>(K, grid, s) : launch<false, 0>(K, grid, s));
+  if (ls != CSA_OK || grid == 1) return ls;
+  join_kernel<<<dim3(grid - 1, a->num_heads < kHeads ? a->num_heads : kHeads), kJoinThreads, 0, s>>>(K, grid);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
