@@ -27,8 +27,9 @@ using csa::smem_u32;
 // Warps 0-3: softmax (S from TMEM, P to shared memory) and the output. Warps 4-11: loaders.
 // They hold one more tile in registers, so that its global loads are in flight while
 // both tiles in shared memory are in use; MXFP4 codes become bf16 values (exactly) on the
-// way. Warp 12: one thread issues the MMAs: S of tile i + 1 before O of tile i, so that the
-// tensor cores work during tile i's softmax.
+// way. Warps 12, 13: one thread issues the MMAs of S, another those of O, so that neither waits for the
+// other's operands and S of tile i + 1 runs during tile i's softmax. A tile is filled and freed 128
+// values at a time: the next one moves in while O still reads the rest.
 //
 // Work is split over a long axis: the tiles of all (row, head group) units, in order, are
 // cut into equal runs, one a CTA; a unit that is cut leaves unnormalised parts (O, m, l in
@@ -38,7 +39,7 @@ constexpr int kTile = 64, kHeads = 64;            // records a tile, heads a uni
 constexpr int kColBytes = kTile * 128;            // 64 values of a tile's 64 records (or of Q's 64 heads)
 constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
 constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 1);
+constexpr int kThreads = 32 * (kMmaWarp + 2);
 constexpr int kMaxGrid = 160;                     // CTAs at most: sizes the workspace
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T in columns 0 .. 255, S in 256 .. 383
 constexpr float kGrow = 8.0f;                     // log2 of how far p may exceed 1
@@ -50,7 +51,7 @@ struct Smem {
   uint8_t q[kCols * kColBytes];
   uint8_t c[2][kCols * kColBytes];
   uint8_t p[kHeads * 128];
-  uint64_t bars[16];
+  uint64_t bars[18];
   uint8_t valid[2][kTile];  // 1 where the tile's record is visible
   float alpha[kHeads];
   int64_t total;
@@ -58,8 +59,10 @@ struct Smem {
   uint32_t tmem;
   int abort;
 };
-enum { kBarCFull = 0, kBarCEmpty = 2, kBarSFull = 4, kBarSEmpty = 6, kBarQFull = 8, kBarQEmpty, kBarPFull, kBarPEmpty,
-       kBarOFull, kBarOEmpty, kBarDrain };
+constexpr int kPairs = kDim / 128;  // a tile moves in 128 values at a time
+// A tile is handed over in two halves of 256 values: barriers 2 * stage + half.
+enum { kBarCFull = 0, kBarCEmpty = 4, kBarSFull = 8, kBarSEmpty = 10, kBarQFull = 12, kBarQEmpty, kBarPFull,
+       kBarOEmpty, kBarDrainS, kBarDrainO };
 
 // A part of a cut unit: O [64 heads][512], then m c and l of the 64 heads.
 constexpr size_t kPartFloats = static_cast<size_t>(kHeads) * (kDim + 2);
@@ -201,58 +204,63 @@ struct Pieces {
   }
 };
 
-// The bytes of one tile in a loader thread's registers, and how they become the tile in
-// shared memory: value v of record r at column v / 64, row r, 16-byte chunk (v % 64) / 8 ^ (r % 8).
+// The bytes of one tile in a loader thread's registers, 128 values of its records at a time, and how
+// they become the tile in shared memory: value v of record r at column v / 64, row r, 16-byte
+// chunk (v % 64) / 8 ^ (r % 8). The rope values travel with the first 128.
 template <bool kFp4, int kRope>
 struct TileRegs;
 
 // bf16: eight lanes a record (128 bytes of it at a time), records r and r + 32.
 template <int kRope>
 struct TileRegs<false, kRope> {
-  static constexpr int kCols = (kDim + kRope) / 64;
-  uint4 w[2][kCols];
-  bool live[2];
-  __device__ __forceinline__ void fetch(const csa_latent_attend_args& A, const RowView& R, int b, int tile, int t,
-                                        int32_t* flags) {
+  static constexpr int kRecords = 2;  // records a thread has a share in
+  uint4 w[kRecords][kDim / 64], rope[kRecords];
+  static __device__ __forceinline__ int record(int t, int k) { return (t >> 3) + 32 * k; }
+  static __device__ __forceinline__ bool leads(int t) { return (t & 7) == 0; }
+  __device__ __forceinline__ void convert(int, int) {}
+  __device__ __forceinline__ void fetch(const uint8_t* const (&rec)[kRecords], int pair, int t) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint8_t* rec = record_of(A, R, b, tile * kTile + (t >> 3) + 32 * k, record_bytes(false, kRope), flags);
-      live[k] = rec != nullptr;
-      const uint4* p = reinterpret_cast<const uint4*>(rec) + (t & 7);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) w[k][c] = rec ? __ldg(p + 8 * c) : make_uint4(0, 0, 0, 0);
+    for (int k = 0; k < kRecords; ++k) {
+      const uint4* p = reinterpret_cast<const uint4*>(rec[k]) + (t & 7);
+      const uint4 zero = make_uint4(0, 0, 0, 0);
+      w[k][2 * pair] = rec[k] ? __ldg(p + 16 * pair) : zero;
+      w[k][2 * pair + 1] = rec[k] ? __ldg(p + 16 * pair + 8) : zero;
+      if (kRope != 0 && pair == 0) rope[k] = rec[k] ? __ldg(p + kDim / 8) : zero;
     }
   }
-  __device__ __forceinline__ void store(uint32_t dst, uint8_t* valid, int t) const {
+  __device__ __forceinline__ void store(uint32_t dst, int pair, int t) const {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const int r = (t >> 3) + 32 * k;
+    for (int k = 0; k < kRecords; ++k) {
+      const int r = record(t, k);
       const uint32_t at = dst + r * 128 + (((t & 7) ^ (r & 7)) << 4);
 #pragma unroll
-      for (int c = 0; c < kCols; ++c) csa::st_shared_v4(at + c * kColBytes, w[k][c].x, w[k][c].y, w[k][c].z, w[k][c].w);
-      if ((t & 7) == 0) valid[r] = live[k];
+      for (int c = 2 * pair; c < 2 * pair + 2; ++c)
+        csa::st_shared_v4(at + c * kColBytes, w[k][c].x, w[k][c].y, w[k][c].z, w[k][c].w);
+      if (kRope != 0 && pair == 0)
+        csa::st_shared_v4(at + kDim / 64 * kColBytes, rope[k].x, rope[k].y, rope[k].z, rope[k].w);
     }
   }
 };
 
-// MXFP4: four lanes a record; lane s takes its blocks of 32 values s, s + 4, s + 8, s + 12
-// (16 code bytes and one scale byte each) and a quarter of its rope values.
+// MXFP4: four lanes a record; of each 128 values (four blocks of 32: 16 code bytes and one scale
+// byte) lane s takes block s, and a quarter of the rope values.
 template <int kRope>
 struct TileRegs<true, kRope> {
-  uint4 code[4], scale, rope[2];
-  bool live;
-  __device__ __forceinline__ void fetch(const csa_latent_attend_args& A, const RowView& R, int b, int tile, int t,
-                                        int32_t* flags) {
-    const uint8_t* rec = record_of(A, R, b, tile * kTile + (t >> 2), record_bytes(true, kRope), flags);
-    live = rec != nullptr;
-    const uint4* p = reinterpret_cast<const uint4*>(rec);
+  static constexpr int kRecords = 1;
+  uint4 code[kPairs], rope[2];
+  uint32_t scale[kPairs], value[2][16];
+  static __device__ __forceinline__ int record(int t, int) { return t >> 2; }
+  static __device__ __forceinline__ bool leads(int t) { return (t & 3) == 0; }
+  __device__ __forceinline__ void fetch(const uint8_t* const (&rec)[kRecords], int pair, int t) {
+    const uint4* p = reinterpret_cast<const uint4*>(rec[0]);
     const uint4 zero = make_uint4(0, 0, 0, 0);
+    code[pair] = p ? __ldg(p + 4 * pair + (t & 3)) : zero;
+    scale[pair] = p ? __ldg(rec[0] + kCodeBytes + 4 * pair + (t & 3)) : 0u;
+    if (pair == 0) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) code[k] = rec ? __ldg(p + (t & 3) + 4 * k) : zero;
-    scale = rec ? __ldg(p + kCodeBytes / 16) : zero;
-#pragma unroll
-    for (int k = 0; k < 2; ++k)
-      rope[k] = kRope != 0 && rec ? __ldg(p + (kCodeBytes + kScaleBytes) / 16 + 2 * (t & 3) + k) : zero;
+      for (int k = 0; k < 2; ++k)
+        rope[k] = kRope != 0 && p ? __ldg(p + (kCodeBytes + kScaleBytes) / 16 + 2 * (t & 3) + k) : zero;
+    }
   }
   // Four e2m1 codes (the low 16 bits of `sel`) as bf16 values times `s2`. The magnitudes
   // 0 1/2 1 3/2 2 3 4 6 are looked up as the two bytes of their bf16 by byte permutes; a permute
@@ -271,36 +279,37 @@ struct TileRegs<true, kRope> {
     *lo = *reinterpret_cast<const uint32_t*>(&x);
     *hi = *reinterpret_cast<const uint32_t*>(&y);
   }
-  __device__ __forceinline__ void store(uint32_t dst, uint8_t* valid, int t) const {
+  // The codes fetched become the values to store, ahead of the tile's turn.
+  __device__ __forceinline__ void convert(int pair, int t) {
+    const bool swap = (t & 3) >= 2;  // lanes 2, 3 store their words in another order: no two on one bank
+    const uint32_t sb = scale[pair];
+    const uint32_t bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7);
+    const uint32_t two = bits | (bits << 16);
+    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
+    const uint4 c = code[pair];
+    const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t* v = value[pair & 1] + 4 * j;
+      four(word[j], s2, &v[0], &v[1]);
+      four(word[j] >> 16, s2, &v[2], &v[3]);
+    }
+  }
+  __device__ __forceinline__ void store(uint32_t dst, int pair, int t) const {
     const int r = t >> 2, s = t & 3;
-    const bool swap = s >= 2;  // lanes 2, 3 store their words in another order: no two on one bank
     const uint32_t row = dst + r * 128;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int blk = s + 4 * k;
-      const uint32_t sw = k == 0 ? scale.x : (k == 1 ? scale.y : (k == 2 ? scale.z : scale.w));
-      const uint32_t sb = (sw >> (8 * s)) & 0xFFu;
-      const uint32_t bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7);
-      const uint32_t two = bits | (bits << 16);
-      const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
-      const uint32_t word[4] = {swap ? code[k].z : code[k].x, swap ? code[k].w : code[k].y,
-                                swap ? code[k].x : code[k].z, swap ? code[k].y : code[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        uint32_t v[4];
-        four(word[j], s2, &v[0], &v[1]);
-        four(word[j] >> 16, s2, &v[2], &v[3]);
-        const int chunk = 4 * (blk & 1) + (swap ? j ^ 2 : j);
-        csa::st_shared_v4(row + (blk >> 1) * kColBytes + ((chunk ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
-      }
+    for (int j = 0; j < 4; ++j) {
+      const int chunk = 4 * (s & 1) + (s >= 2 ? j ^ 2 : j);
+      const uint32_t* v = value[pair & 1] + 4 * j;
+      csa::st_shared_v4(row + (2 * pair + (s >> 1)) * kColBytes + ((chunk ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
     }
-    if constexpr (kRope != 0) {
+    if (kRope != 0 && pair == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        csa::st_shared_v4(row + (kDim / 64) * kColBytes + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y, rope[k].z,
-                          rope[k].w);
+        csa::st_shared_v4(row + kDim / 64 * kColBytes + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y,
+                          rope[k].z, rope[k].w);
     }
-    if (s == 0) valid[r] = live;
   }
 };
 
@@ -313,117 +322,166 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 template <bool kFp4, int kRope>
 __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   constexpr int kCols = Smem<kRope>::kCols;
+  using Regs = TileRegs<kFp4, kRope>;
   const csa_latent_attend_args& A = K.A;
   const int t = threadIdx.x - 32 * kSoftmaxWarps, lane = t & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
-  Pieces run(K, S);
+  Pieces run(K, S), ahead = run;  // `ahead` resolves the tile after the one that is stored
   if (!run.more()) return;
-  RowView R = row_view(A, run.unit / K.groups, flags);
-  TileRegs<kFp4, kRope> x;
-  x.fetch(A, R, run.unit / K.groups, run.off, t, flags);
+  RowView R = row_view(A, ahead.unit / K.groups, flags);
+  int tile = ahead.off, piece_end = ahead.off + ahead.n;
+  const uint8_t* rec[Regs::kRecords];
+  // The records of the next tile of the run, null past its end.
+  auto resolve = [&]() {
+    if (ahead.more() && tile == piece_end) {
+      ahead.next(K);
+      if (ahead.more()) {
+        R = row_view(A, ahead.unit / K.groups, flags);
+        tile = ahead.off;
+        piece_end = ahead.off + ahead.n;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < Regs::kRecords; ++k)
+      rec[k] = ahead.more() ? record_of(A, R, ahead.unit / K.groups, tile * kTile + Regs::record(t, k),
+                                        record_bytes(kFp4, kRope), flags)
+                            : nullptr;
+    ++tile;
+  };
+  Regs x;
+  bool live[Regs::kRecords];
+  resolve();
+#pragma unroll
+  for (int pair = 0; pair < kPairs; ++pair) x.fetch(rec, pair, t);
   uint32_t g = 0, piece = 0;
-  while (run.more()) {
+  for (; run.more(); run.next(K), ++piece) {
     // Q of the piece: head h's 64-value columns at row h, swizzled as the records; zeros past the last head
     const int b = run.unit / K.groups, h0 = (run.unit % K.groups) * kHeads;
     if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
       const int h = (t >> 3) + 32 * k;
-      const bool live = h0 + h < A.num_heads;
+      const bool on = h0 + h < A.num_heads;
       const uint8_t* q = static_cast<const uint8_t*>(A.q) +
-                         2 * (b * A.q_row_stride + (live ? h0 + h : 0) * A.q_head_stride) + 16 * (t & 7);
+                         2 * (b * A.q_row_stride + (on ? h0 + h : 0) * A.q_head_stride) + 16 * (t & 7);
 #pragma unroll
       for (int c = 0; c < kCols; ++c)
-        csa::cp_async16(smem_u32(S.q) + c * kColBytes + h * 128 + (((t & 7) ^ (h & 7)) << 4), q + 128 * c, live);
+        csa::cp_async16(smem_u32(S.q) + c * kColBytes + h * 128 + (((t & 7) ^ (h & 7)) << 4), q + 128 * c, on);
     }
     csa::cp_async_wait_all();
     csa::fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * kBarQFull);
-    const int n = run.n, off = run.off;
-    for (int i = 0; i < n; ++i) {
-      if (!warp_wait(bars + 8 * (kBarCEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop)) return;
-      x.store(smem_u32(S.c[g & 1]), S.valid[g & 1], t);
-      csa::fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bars + 8 * (kBarCFull + (g & 1)));
-      ++g;
-      int nb = b, ntile = off + i + 1;
-      if (i + 1 == n) {
-        run.next(K);
-        if (!run.more()) break;
-        nb = run.unit / K.groups;
-        ntile = run.off;
-        R = row_view(A, nb, flags);
+    for (int i = 0; i < run.n; ++i, ++g) {
+      const uint32_t stage = g & 1;
+#pragma unroll
+      for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
+      resolve();
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        x.convert(2 * half, t);  // before the tile's turn, where that is not yet come
+        x.convert(2 * half + 1, t);
+        if (!warp_wait(bars + 8 * (kBarCEmpty + 2 * stage + half), ((g >> 1) & 1) ^ 1, stop)) return;
+        x.store(smem_u32(S.c[stage]), 2 * half, t);
+        x.store(smem_u32(S.c[stage]), 2 * half + 1, t);
+        if (half == 0 && Regs::leads(t)) {
+#pragma unroll
+          for (int k = 0; k < Regs::kRecords; ++k) S.valid[stage][Regs::record(t, k)] = live[k];
+        }
+        csa::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bars + 8 * (kBarCFull + 2 * stage + half));
+        x.fetch(rec, 2 * half, t);  // of the next tile: in flight until this half's turn comes again
+        x.fetch(rec, 2 * half + 1, t);
       }
-      x.fetch(A, R, nb, ntile, t, flags);
     }
-    ++piece;
   }
 }
 
+// Nothing of this thread's MMAs is in flight when it leaves its role.
+__device__ __forceinline__ void drain(uint32_t bar) {
+  csa::mma_commit(bar);
+  csa::mbar_wait_drain(bar, 0);
+}
+
 template <int kRope>
-__device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
-  constexpr int kCols = Smem<kRope>::kCols;
+__device__ void role_mma_s(const Kernel& K, Smem<kRope>& S) {
   volatile int* stop = &S.abort;
-  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem;
-  const int heads_left = K.A.num_heads;
-  constexpr uint32_t idesc_s = csa::idesc_bf16_f32(64, kTile);
-  const uint64_t q_desc = csa::sdesc_kmajor_sw128(smem_u32(S.q)), p_desc = csa::sdesc_kmajor_sw128(smem_u32(S.p));
+  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem + kTmemS;
+  constexpr uint32_t idesc = csa::idesc_bf16_f32(64, kTile);
+  const csa::Desc q_desc(csa::sdesc_kmajor_sw128(smem_u32(S.q)));
+  const csa::Desc c_descs[2] = {csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.c[0]))),
+                                csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.c[1])))};
   uint32_t g = 0, piece = 0;
   bool ok = true;
-  // O of tile g: the first of a piece overwrites
-  auto issue_o = [&](uint32_t tile, uint32_t pc, bool first, bool last, uint32_t idesc_o) {
-    ok = ok && mbar_wait(bars + 8 * kBarPFull, tile & 1, stop);
-    if (first) ok = ok && mbar_wait(bars + 8 * kBarOEmpty, (pc & 1) ^ 1, stop);
-    if (!ok) return;
-    csa::tc_fence_after();
-    const uint32_t c = smem_u32(S.c[tile & 1]);
-#pragma unroll
-    for (int d = 0; d < kDim / 128; ++d) {
-#pragma unroll
-      for (int k = 0; k < kTile / 16; ++k) {
-        const uint64_t a = csa::sdesc_mn_sw128_b16(c + 2 * d * kColBytes + k * 2048, kColBytes);
-        csa::mma_f16_ss(tmem + d * kHeads, a, p_desc + 2 * k, idesc_o, !first || k > 0);
-      }
-    }
-    csa::mma_commit(bars + 8 * (kBarCEmpty + (tile & 1)));
-    csa::mma_commit(bars + 8 * kBarPEmpty);
-    if (last) csa::mma_commit(bars + 8 * kBarOFull);
-  };
-  bool pending = false, pend_first = false, pend_last = false;
-  uint32_t pend_idesc = 0, pend_piece = 0;
   for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
-    const int heads = min(heads_left - (run.unit % K.groups) * kHeads, kHeads);
-    const uint32_t idesc_o = csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor;
-    ok = ok && mbar_wait(bars + 8 * kBarQFull, piece & 1, stop);
+    ok = mbar_wait(bars + 8 * kBarQFull, piece & 1, stop);
     for (int i = 0; ok && i < run.n; ++i, ++g) {
-      ok = ok && mbar_wait(bars + 8 * (kBarCFull + (g & 1)), (g >> 1) & 1, stop);
-      ok = ok && mbar_wait(bars + 8 * (kBarSEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop);
+      ok = mbar_wait(bars + 8 * (kBarSEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop);
+      const csa::Desc c_desc = c_descs[g & 1];
+      const uint32_t d = tmem + (g & 1) * kTile;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {  // as the tile is filled
+        ok = ok && mbar_wait(bars + 8 * (kBarCFull + 2 * (g & 1) + half), (g >> 1) & 1, stop);
+        if (!ok) break;
+        csa::tc_fence_after();
+#pragma unroll
+        for (int at = kDim / 2 * half; at < kDim / 2 * (half + 1); at += 16) {
+          const uint32_t bytes = at / 64 * kColBytes + at % 64 * 2;
+          if (at == 0)
+            csa::mma_f16_ss<false>(d, q_desc, bytes, c_desc, bytes, idesc);
+          else
+            csa::mma_f16_ss<true>(d, q_desc, bytes, c_desc, bytes, idesc);
+        }
+        if (kRope != 0 && half == 0) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            csa::mma_f16_ss<true>(d, q_desc, kDim / 64 * kColBytes + 32 * k, c_desc, kDim / 64 * kColBytes + 32 * k, idesc);
+        }
+      }
       if (!ok) break;
-      csa::tc_fence_after();
-      const uint64_t c_desc = csa::sdesc_kmajor_sw128(smem_u32(S.c[g & 1]));
-#pragma unroll
-      for (int c = 0; c < kCols; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          csa::mma_f16_ss(tmem + kTmemS + (g & 1) * kTile, q_desc + c * (kColBytes >> 4) + 2 * k,
-                          c_desc + c * (kColBytes >> 4) + 2 * k, idesc_s, c > 0 || k > 0);
       csa::mma_commit(bars + 8 * (kBarSFull + (g & 1)));
       if (i + 1 == run.n) csa::mma_commit(bars + 8 * kBarQEmpty);
-      if (pending) issue_o(g - 1, pend_piece, pend_first, pend_last, pend_idesc);
-      pending = true;
-      pend_first = i == 0;
-      pend_last = i + 1 == run.n;
-      pend_idesc = idesc_o;
-      pend_piece = piece;
     }
   }
-  if (ok && pending) issue_o(g - 1, pend_piece, pend_first, pend_last, pend_idesc);
-  // nothing of this CTA's MMAs is in flight when it leaves
-  csa::mma_commit(bars + 8 * kBarDrain);
-  csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
+  drain(bars + 8 * kBarDrainS);
+}
+
+template <int kRope>
+__device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem;
+  const csa::Desc p_desc(csa::sdesc_kmajor_sw128(smem_u32(S.p)));
+  const csa::Desc c_descs[2] = {csa::Desc(csa::sdesc_mn_sw128_b16(smem_u32(S.c[0]), kColBytes)),
+                                csa::Desc(csa::sdesc_mn_sw128_b16(smem_u32(S.c[1]), kColBytes))};
+  uint32_t g = 0, piece = 0;
+  bool ok = true;
+  for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
+    const int heads = min(K.A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
+    const uint32_t idesc = csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor;
+    ok = mbar_wait(bars + 8 * kBarOEmpty, (piece & 1) ^ 1, stop);
+    for (int i = 0; ok && i < run.n; ++i, ++g) {
+      ok = mbar_wait(bars + 8 * kBarPFull, g & 1, stop);
+      if (!ok) break;
+      csa::tc_fence_after();
+      // the tile's records are complete and read by S: the softmax waited for both
+      const csa::Desc c_desc = c_descs[g & 1];
+#pragma unroll
+      for (int d = 0; d < kDim / 128; ++d) {
+#pragma unroll
+        for (int k = 0; k < kTile / 16; ++k) {
+          const uint32_t c_bytes = 2 * d * kColBytes + k * 2048;
+          if (i == 0 && k == 0)  // the piece's first tile overwrites
+            csa::mma_f16_ss<false>(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc);
+          else
+            csa::mma_f16_ss<true>(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc);
+        }
+        if (d & 1) csa::mma_commit(bars + 8 * (kBarCEmpty + 2 * (g & 1) + (d >> 1)));
+      }
+    }
+  }
+  drain(bars + 8 * kBarDrainO);
 }
 
 // out (or a part) from O^T: a thread holds one value of 128 per column block, for every head.
@@ -476,115 +534,136 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
   const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;  // this warp's TMEM lanes
-  // S of 64 rows lies in lanes 0 .. 15 of each warp's 32: head 16 warp + lane
-  const bool mine = lane < 16;
-  const int head = 16 * warp + (lane & 15);
-  const uint32_t p_row = smem_u32(S.p) + head * 128;
+  // S of 64 rows lies in lanes 0 .. 15 of each warp's 32: heads 16 warp .. 16 warp + 15. A thread holds
+  // two heads' scores (head[0], head[0] + 8), a quarter of the tile's records each.
+  const int head[2] = {16 * warp + (lane >> 2), 16 * warp + (lane >> 2) + 8};
+  const int col = 2 * (lane & 3);  // its records: 8 i + col, 8 i + col + 1
+  // where this lane's row of a group of four 8 x 8 matrices of P goes: matrices 0, 1 the heads' halves at
+  // records 8 i, 2, 3 at records 8 (i + 1)
+  const int p_head = 16 * warp + (lane & 15);
+  const uint32_t p_row = smem_u32(S.p) + p_head * 128;
   const float c = A.scale * 1.4426950408889634f;
   const float grow = kGrow / c;
-  uint32_t g = 0, piece = 0;
+  // O of the tile before tile g is complete: its second half is free (there is nothing before tile 0)
+  auto o_done = [&](uint32_t tile) {
+    return tile == 0 || warp_wait(bars + 8 * (kBarCEmpty + 2 * ((tile - 1) & 1) + 1), ((tile - 1) >> 1) & 1, stop);
+  };
+  uint32_t g = 0;
   bool ok = true;  // once a wait has run out, the rest runs through without waiting: all warps meet at every barrier
-  for (Pieces run(K, S); run.more(); run.next(K), ++piece) {
+  for (Pieces run(K, S); run.more(); run.next(K)) {
     const int heads = min(A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
-    float m = -INFINITY, l = 0.f;
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's share of the sum
     for (int i = 0; i < run.n; ++i, ++g) {
+      ok = ok && warp_wait(bars + 8 * (kBarCFull + 2 * (g & 1)), (g >> 1) & 1, stop);
+      const bool all = __all_sync(0xFFFFFFFFu, reinterpret_cast<const uint16_t*>(S.valid[g & 1])[lane] == 0x0101u);
       ok = ok && warp_wait(bars + 8 * (kBarSFull + (g & 1)), (g >> 1) & 1, stop);
-      ok = ok && warp_wait(bars + 8 * (kBarCFull + (g & 1)), (g >> 1) & 1, stop);  // complete: for `valid`
       csa::tc_fence_after();
-      uint32_t raw[2][32];
-      csa::tmem_ld32(S.tmem + kTmemS + (g & 1) * kTile + lanes, raw[0]);
-      csa::tmem_ld32(S.tmem + kTmemS + (g & 1) * kTile + 32 + lanes, raw[1]);
+      uint32_t raw[32];
+      csa::tmem_ld_16x64(S.tmem + kTmemS + (g & 1) * kTile + lanes, raw);
       csa::tmem_wait_ld();
       csa::tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * (kBarSEmpty + (g & 1)));
-      float s[kTile];
+      float s[2][16];
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) s[j] = __uint_as_float(raw[j >> 5][j & 31]);
-      const uint32_t* vw = reinterpret_cast<const uint32_t*>(S.valid[g & 1]);
-      uint32_t all = 0x01010101u;
+      for (int j = 0; j < 32; ++j) s[(j >> 1) & 1][2 * (j >> 2) + (j & 1)] = __uint_as_float(raw[j]);
+      if (!all) {
 #pragma unroll
-      for (int k = 0; k < kTile / 4; ++k) all &= vw[k];
-      if (all != 0x01010101u) {
-#pragma unroll
-        for (int k = 0; k < kTile / 4; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!((vw[k] >> (8 * j)) & 1u)) s[4 * k + j] = -INFINITY;
+        for (int j = 0; j < 16; ++j)
+          if (!S.valid[g & 1][8 * (j >> 1) + col + (j & 1)]) s[0][j] = s[1][j] = -INFINITY;
       }
-      float top = s[0];
+      float keep[2];
+      bool up = false;
 #pragma unroll
-      for (int j = 1; j < kTile; ++j) top = fmaxf(top, s[j]);
-      float keep = 1.f;
-      const bool up = mine && top > m + grow;
-      if (up) {
-        keep = csa::ex2((m - top) * c);  // 0 when there was nothing
-        m = top;
-        l *= keep;
+      for (int r = 0; r < 2; ++r) {
+        float top = s[r][0];
+#pragma unroll
+        for (int j = 1; j < 16; ++j) top = fmaxf(top, s[r][j]);
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+        keep[r] = 1.f;
+        if (top > m[r] + grow) {
+          up = true;
+          keep[r] = csa::ex2((m[r] - top) * c);  // 0 when there was nothing
+          m[r] = top;
+          l[r] *= keep[r];
+        }
       }
       if (i > 0 && csa::named_bar_any(kBarSoftmax, 32 * kSoftmaxWarps, up)) {
-        if (mine) S.alpha[head] = keep;
+        if ((lane & 3) == 0) {
+          S.alpha[head[0]] = keep[0];
+          S.alpha[head[1]] = keep[1];
+        }
         csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
-        ok = ok && warp_wait(bars + 8 * kBarPEmpty, (g & 1) ^ 1, stop);  // O of the tile before is complete
+        ok = ok && o_done(g);  // O of the tile before is complete
         csa::tc_fence_after();
 #pragma unroll 1
-        for (int col = 0; col < kDim / 128 * kHeads; col += 32) {
+        for (int at = 0; at < kDim / 128 * kHeads; at += 32) {
           uint32_t v[32];
-          csa::tmem_ld32(S.tmem + col + lanes, v);
+          csa::tmem_ld32(S.tmem + at + lanes, v);
           csa::tmem_wait_ld();
 #pragma unroll
-          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * S.alpha[(col & (kHeads - 1)) + j]);
-          csa::tmem_st32(S.tmem + col + lanes, v);
+          for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * S.alpha[(at & (kHeads - 1)) + j]);
+          csa::tmem_st32(S.tmem + at + lanes, v);
         }
         csa::tmem_wait_st();
         csa::tc_fence_before();
         csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);  // alpha is free again
       }
-      const float mc = m == -INFINITY ? 0.f : m * c;
-      float sum = 0.f;
+      // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
+      uint32_t w[2][8];
 #pragma unroll
-      for (int j = 0; j < kTile; ++j) {
-        s[j] = csa::ex2(fmaf(s[j], c, -mc));
-        sum += s[j];
-      }
-      l += sum;
-      ok = ok && warp_wait(bars + 8 * kBarPEmpty, (g & 1) ^ 1, stop);
-      if (mine) {
+      for (int r = 0; r < 2; ++r) {
+        const float mc = m[r] == -INFINITY ? 0.f : m[r] * c;
+        float sum = 0.f;
 #pragma unroll
-        for (int k = 0; k < kTile / 8; ++k) {
-          // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
-          uint32_t w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const __nv_bfloat162 two = __floats2bfloat162_rn(s[8 * k + 2 * j], s[8 * k + 2 * j + 1]);
-            w[j] = *reinterpret_cast<const uint32_t*>(&two);
-          }
-          csa::st_shared_v4(p_row + ((k ^ (head & 7)) << 4), w[0], w[1], w[2], w[3]);
+        for (int j = 0; j < 16; j += 2) {
+          const float p0 = csa::ex2(fmaf(s[r][j], c, -mc)), p1 = csa::ex2(fmaf(s[r][j + 1], c, -mc));
+          sum += p0 + p1;
+          const __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+          w[r][j >> 1] = *reinterpret_cast<const uint32_t*>(&two);
         }
+        l[r] += sum;
       }
+      ok = ok && o_done(g);
+#pragma unroll
+      for (int k = 0; k < 8; k += 2)
+        csa::stmatrix_x4(p_row + (((k + (lane >> 4)) ^ (p_head & 7)) << 4), w[0][k], w[1][k], w[0][k + 1], w[1][k + 1]);
       csa::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(bars + 8 * kBarPFull);
     }
     // the piece's output
-    ok = ok && warp_wait(bars + 8 * kBarOFull, piece & 1, stop);
+    ok = ok && o_done(g);
     csa::tc_fence_after();
-    const float mc = m == -INFINITY ? -INFINITY : m * c;
+    float mc[2];
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 1);
+      l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
+      mc[r] = m[r] == -INFINITY ? -INFINITY : m[r] * c;
+    }
     if (run.n == run.tiles) {
       csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
-      if (mine) {
-        S.alpha[head] = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);  // a NaN stays one
-        if (A.lse && head < heads)
-          A.lse[static_cast<int64_t>(run.unit / K.groups) * A.num_heads + (run.unit % K.groups) * kHeads + head] =
-              l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          S.alpha[head[r]] = l[r] > 0.f ? 1.f / l[r] : l[r];  // 0 for an empty row; a NaN stays one
+          if (A.lse && head[r] < heads)
+            A.lse[static_cast<int64_t>(run.unit / K.groups) * A.num_heads + (run.unit % K.groups) * kHeads + head[r]] =
+                l[r] == 0.f ? -INFINITY : (mc[r] + log2f(l[r])) * 0.6931471805599453f;
+        }
       }
       csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
       write_out(K, S, run.unit, heads, warp, lane);
     } else {
       float* part = K.parts + (2 * blockIdx.x + (run.off == 0)) * kPartFloats;
-      if (mine && head < heads) {
-        part[kHeads * kDim + head] = mc;
-        part[kHeads * (kDim + 1) + head] = l;
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          part[kHeads * kDim + head[r]] = mc[r];
+          part[kHeads * (kDim + 1) + head[r]] = l[r];
+        }
       }
       write_part(K, S, part, heads, warp, lane);
     }
@@ -602,19 +681,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t bars = smem_u32(S.bars);
   if (threadIdx.x == 0) {
-    for (int k = 0; k < 2; ++k) {
+    for (int k = 0; k < 4; ++k) {
       csa::mbar_init(bars + 8 * (kBarCFull + k), kLoadWarps);
       csa::mbar_init(bars + 8 * (kBarCEmpty + k), 1);
+    }
+    for (int k = 0; k < 2; ++k) {
       csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarSEmpty + k), kSoftmaxWarps);
     }
     csa::mbar_init(bars + 8 * kBarQFull, kLoadWarps);
     csa::mbar_init(bars + 8 * kBarQEmpty, 1);
     csa::mbar_init(bars + 8 * kBarPFull, kSoftmaxWarps);
-    csa::mbar_init(bars + 8 * kBarPEmpty, 1);
-    csa::mbar_init(bars + 8 * kBarOFull, 1);
     csa::mbar_init(bars + 8 * kBarOEmpty, kSoftmaxWarps);
-    csa::mbar_init(bars + 8 * kBarDrain, 1);
+    csa::mbar_init(bars + 8 * kBarDrainS, 1);
+    csa::mbar_init(bars + 8 * kBarDrainO, 1);
     csa::mbar_init_fence();
     S.abort = 0;
   }
@@ -632,8 +712,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
     role_load<kFp4, kRope>(K, S, &flags);
   } else {
     if (lane == 0) {
-      if (K.plans) K.plans[blockIdx.x] = {S.total, S.unit, S.off, tiles_of(K.A, S.unit / K.groups), 0};
-      role_mma(K, S);
+      if (warp == kMmaWarp) {
+        K.plans[blockIdx.x] = {S.total, S.unit, S.off, tiles_of(K.A, S.unit / K.groups), 0};
+        role_mma_s(K, S);
+      } else {
+        role_mma_o(K, S);
+      }
     }
     __syncwarp();
   }

@@ -35,15 +35,32 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128_b16(uint32_t saddr, uint32_t 
   return d;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, one CTA, kind::f16 (K = 16 per call).
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                           uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// D[tmem] (+)= A[smem] * B[smem]^T, one CTA, kind::f16 (K = 16 per call). The descriptors' low
+// words (where the address is) and high words are apart, so that stepping through an operand is one
+// addition: the issuing thread's own instructions take as long as a small MMA (measured: 66 clocks a
+// 128 x 64 MMA with descriptors built for each, 48 with them stepped).
+struct Desc {
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+};
+
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_bytes, Desc b, uint32_t b_bytes,
+                                           uint32_t idesc) {
+  if constexpr (kAccumulate)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.eq.u32 p, 0, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.u32 p, 0, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc)
+        : "memory");
 }
 
 // 2^x: 2^-22 relative error, subnormal results become 0, 2^-infinity is 0.
@@ -69,6 +86,29 @@ __device__ __forceinline__ bool named_bar_any(int id, int nthreads, bool p) {
 
 __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+// 16 lanes x 64 consecutive 32-bit columns over a whole warp: registers 4 i, 4 i + 1 hold row
+// lane / 4, columns 8 i + 2 (lane % 4) and the next; 4 i + 2, 4 i + 3 the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, "
+      "%14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+        "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]),
+        "=r"(v[15]), "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]),
+        "=r"(v[22]), "=r"(v[23]), "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]),
+        "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements to shared memory: lanes 8 k .. 8 k + 7 give the row
+// addresses of matrix k; a lane holds row lane / 4, columns 2 (lane % 4) and the next of each.
+__device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c),
+               "r"(d)
+               : "memory");
 }
 
 // 16 bytes global -> shared without a register, or zeros when !live (src is not read then).
