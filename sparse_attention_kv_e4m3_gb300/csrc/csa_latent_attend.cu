@@ -67,16 +67,19 @@ enum { kBarCFull = 0, kBarCEmpty = 4, kBarSFull = 8, kBarSEmpty = 10, kBarQFull 
 // A part of a cut unit: O [64 heads][512], then m c and l of the 64 heads.
 constexpr size_t kPartFloats = static_cast<size_t>(kHeads) * (kDim + 2);
 
-struct Plan {  // of one CTA's run, for the join: where in its first unit it starts
-  int64_t total;
-  int32_t unit, off, tiles, pad;
+// Where a unit begins, for the join: written by the run that holds its first tile, at the unit's index
+// where there are at most as many units as runs, else at the run's (a run opens one cut unit at most).
+struct Open {
+  int64_t begin, total;  // the unit's first tile and all units' tiles, in the order of the runs
+  int32_t unit, run, tiles, cut;
 };
 
 struct Kernel {
   csa_latent_attend_args A;
-  Plan* plans;
+  Open* opens;
   float* parts;
   int32_t groups;  // head groups of 64
+  int32_t by_unit;  // opens are indexed by unit
 };
 
 // What a query row sees: its request's page table row and its length.
@@ -203,6 +206,19 @@ struct Pieces {
     size(K);
   }
 };
+
+// The units that begin in this run.
+template <int kRope>
+__device__ void write_opens(const Kernel& K, const Smem<kRope>& S) {
+  int64_t at = run_start(S.total, blockIdx.x, gridDim.x);
+  if (!K.by_unit) K.opens[blockIdx.x].cut = 0;
+  for (Pieces run(K, S); run.more(); run.next(K)) {
+    const bool cut = run.n < run.tiles;
+    if (run.off == 0 && (cut || K.by_unit))
+      K.opens[K.by_unit ? run.unit : blockIdx.x] = {at, S.total, run.unit, static_cast<int32_t>(blockIdx.x), run.tiles, cut};
+    at += run.n;
+  }
+}
 
 // The bytes of one tile in a loader thread's registers, 128 values of its records at a time, and how
 // they become the tile in shared memory: value v of record r at column v / 64, row r, 16-byte
@@ -712,12 +728,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
     role_load<kFp4, kRope>(K, S, &flags);
   } else {
     if (lane == 0) {
-      if (warp == kMmaWarp) {
-        K.plans[blockIdx.x] = {S.total, S.unit, S.off, tiles_of(K.A, S.unit / K.groups), 0};
-        role_mma_s(K, S);
-      } else {
-        role_mma_o(K, S);
-      }
+      if (warp == kMmaWarp) role_mma_s(K, S);
+      else role_mma_o(K, S);
+    } else if (lane == 1 && warp != kMmaWarp) {
+      write_opens(K, S);
     }
     __syncwarp();
   }
@@ -732,45 +746,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   if (flags && K.A.dev_status && lane == 0) atomicOr(K.A.dev_status, flags);
 }
 
-// Joins a cut unit: block (c - 1, head) does the unit that run c starts inside of, if c is the first
-// such run. Its parts are run c - 1's (from the unit's first tile on) and those of runs c, c + 1, ...
-// up to the unit's end, added in that order.
-constexpr int kJoinThreads = kDim / 4;
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const Kernel K, int grid) {
+// Joins a cut unit: one block a (possibly cut) unit and head. Its parts are those of run `o.run` (which
+// ends inside the unit) and of the runs after it up to the unit's end. Each warp adds every eighth
+// part, the warps' sums are added in their order, so the result does not depend on timing. Launched as a
+// programmatic dependent of the attention kernel: its blocks are in place when that one ends.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, int grid) {
   const csa_latent_attend_args& A = K.A;
-  const int c = blockIdx.x + 1, head = blockIdx.y;
-  const Plan p = K.plans[c];
-  if (p.off == 0) return;
-  const int64_t begin = run_start(p.total, c, grid) - p.off, end = begin + p.tiles;
-  if (run_start(p.total, c - 1, grid) > begin) return;
-  const int h = (p.unit % K.groups) * kHeads + head;
+  __shared__ float s_o[kJoinWarps][kDim], s_l[kJoinWarps];
+  const int head = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Open o = K.opens[blockIdx.x];
+  if (!o.cut) return;
+  const int h = (o.unit % K.groups) * kHeads + head;
   if (h >= A.num_heads) return;
-  auto part_of = [&](int r) { return K.parts + (2 * static_cast<int64_t>(r) + (r == c - 1)) * kPartFloats; };
-  int last = c;
-  while (last + 1 < grid && run_start(p.total, last + 1, grid) < end) ++last;
+  // runs o.run .. last; a run without tiles has no part
+  const int64_t end = o.begin + o.tiles;
+  int last = static_cast<int>(min((end * grid - 1) / o.total, static_cast<int64_t>(grid) - 1)) + 1;
+  while (last >= grid || run_start(o.total, last, grid) >= end) --last;
+  auto part_of = [&](int r) { return K.parts + (2 * static_cast<int64_t>(r) + (r == o.run)) * kPartFloats; };
+  auto there = [&](int r) { return r <= last && run_start(o.total, r, grid) < run_start(o.total, r + 1, grid); };
   float top = -INFINITY;
-  auto empty = [&](int r) { return run_start(p.total, r, grid) == run_start(p.total, r + 1, grid); };
-  for (int r = c - 1; r <= last; ++r)
-    if (!empty(r)) top = fmaxf(top, part_of(r)[kHeads * kDim + head]);
+  for (int r = o.run + lane; r <= last; r += 32)
+    if (there(r)) top = fmaxf(top, part_of(r)[kHeads * kDim + head]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
   float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int r = c - 1; r <= last; ++r) {
-    if (empty(r)) continue;
+  float4 v[4] = {};
+  const float ref = top == -INFINITY ? 0.f : top;
+#pragma unroll 2
+  for (int r = o.run + warp; r <= last; r += kJoinWarps) {
+    if (!there(r)) continue;
     const float* part = part_of(r);
-    const float m = part[kHeads * kDim + head], w = m == -INFINITY ? 0.f : csa::ex2(m - top);
-    const float4 v = reinterpret_cast<const float4*>(part + head * kDim)[threadIdx.x];
+    const float4* x = reinterpret_cast<const float4*>(part + head * kDim);
+    const float w = csa::ex2(part[kHeads * kDim + head] - ref);
     l = fmaf(part[kHeads * (kDim + 1) + head], w, l);
-    o.x = fmaf(v.x, w, o.x);
-    o.y = fmaf(v.y, w, o.y);
-    o.z = fmaf(v.z, w, o.z);
-    o.w = fmaf(v.w, w, o.w);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 y = x[lane + 32 * k];
+      v[k] = make_float4(fmaf(y.x, w, v[k].x), fmaf(y.y, w, v[k].y), fmaf(y.z, w, v[k].z), fmaf(y.w, w, v[k].w));
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(s_o[warp])[lane + 32 * k] = v[k];
+  if (lane == 0) s_l[warp] = l;
+  __syncthreads();
+  l = 0.f;
+  float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) {
+    const float2 y = reinterpret_cast<const float2*>(s_o[w])[threadIdx.x];
+    sum.x += y.x;
+    sum.y += y.y;
+    l += s_l[w];
   }
   const float inv = l > 0.f ? 1.f / l : l;
-  const __nv_bfloat162 a = __floats2bfloat162_rn(o.x * inv, o.y * inv), d = __floats2bfloat162_rn(o.z * inv, o.w * inv);
-  const int64_t row = static_cast<int64_t>(p.unit / K.groups) * A.num_heads + h;
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + row * kDim)[threadIdx.x] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&d));
+  const int64_t row = static_cast<int64_t>(o.unit / K.groups) * A.num_heads + h;
+  reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(A.out) + row * kDim)[threadIdx.x] =
+      __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
   if (A.lse && threadIdx.x == 0) A.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
@@ -782,7 +815,7 @@ int grid_cap(const csa_latent_attend_args* a) {
   return static_cast<int>(units > kMaxGrid || per > kMaxGrid || units * per > kMaxGrid ? kMaxGrid : units * per);
 }
 
-constexpr size_t kPlanBytes = (kMaxGrid * sizeof(Plan) + 255) / 256 * 256;
+constexpr size_t kOpenBytes = (kMaxGrid * sizeof(Open) + 255) / 256 * 256;
 
 template <bool kFp4, int kRope>
 csa_status launch(const Kernel& K, int grid, cudaStream_t stream) {
@@ -830,7 +863,7 @@ using namespace csa_latent;
 
 extern "C" size_t csa_latent_attend_workspace_bytes(const csa_latent_attend_args* a) {
   if (!a || a->num_q < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
-  return kPlanBytes + 2 * static_cast<size_t>(grid_cap(a)) * kPartFloats * sizeof(float);
+  return kOpenBytes + 2 * static_cast<size_t>(grid_cap(a)) * kPartFloats * sizeof(float);
 }
 
 extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -840,20 +873,30 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   if (!ws || ws_bytes < csa_latent_attend_workspace_bytes(a)) return CSA_ERR_WORKSPACE;
   if (!aligned(ws, 16)) return CSA_ERR_ALIGNMENT;
   const int groups = (a->num_heads + kHeads - 1) / kHeads;
-  if (static_cast<int64_t>(a->num_q) * groups > INT32_MAX) return CSA_ERR_INVALID_ARG;
+  const int64_t units = static_cast<int64_t>(a->num_q) * groups;
+  if (units > INT32_MAX) return CSA_ERR_INVALID_ARG;
   int sms = 0;
   if (sm_count(&sms) != CSA_OK) return CSA_ERR_CUDA;
   const int cap = grid_cap(a), grid = cap < sms ? cap : sms;
   Kernel K;
   K.A = *a;
   K.groups = groups;
-  K.plans = static_cast<Plan*>(ws);
-  K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPlanBytes);
+  K.by_unit = units <= grid;
+  K.opens = static_cast<Open*>(ws);
+  K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kOpenBytes);
   const auto s = static_cast<cudaStream_t>(stream);
   const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
   const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, s) : launch<true, 0>(K, grid, s))
                             : (rope ? launch<false, 64>(K, grid, s) : launch<false, 0>(K, grid, s));
   if (ls != CSA_OK || grid == 1) return ls;
-  join_kernel<<<dim3(grid - 1, a->num_heads < kHeads ? a->num_heads : kHeads), kJoinThreads, 0, s>>>(K, grid);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, a->num_heads < kHeads ? a->num_heads : kHeads);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, K, grid) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
