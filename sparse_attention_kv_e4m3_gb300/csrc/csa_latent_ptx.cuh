@@ -63,6 +63,34 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_b
         : "memory");
 }
 
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's 16 values of a step are 8 columns, two bf16 a column.
+template <bool kAccumulate>
+__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t b_bytes, uint32_t idesc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      : "memory");
+}
+
+// Tiled tensor copies global -> this CTA's shared memory (see tma_load_3d), without a cache policy.
+__device__ __forceinline__ void tma_tile_3d(uint32_t dst, const void* tmap, int32_t x, int32_t y, int32_t z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void tma_tile_2d(uint32_t dst, const void* tmap, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          dst),
+      "l"(tmap), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 // 2^x: 2^-22 relative error, subnormal results become 0, 2^-infinity is 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
