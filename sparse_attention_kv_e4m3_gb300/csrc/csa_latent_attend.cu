@@ -54,6 +54,7 @@ struct Smem {
   uint64_t bars[18];
   uint8_t valid[2][kTile];  // 1 where the tile's record is visible
   float alpha[kHeads];
+  float mc[kHeads], l[kHeads];  // cluster: this CTA's reference and sum per head
   int64_t total;
   int32_t unit, off;
   uint32_t tmem;
@@ -80,6 +81,7 @@ struct Kernel {
   float* parts;
   int32_t groups;  // head groups of 64
   int32_t by_unit;  // opens are indexed by unit
+  int32_t cluster;  // CTAs that share a unit and join it among themselves; 0: runs over all units
 };
 
 // What a query row sees: its request's page table row and its length.
@@ -136,6 +138,16 @@ template <int kRope>
 __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int64_t* scan) {
   const csa_latent_attend_args& A = K.A;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (K.cluster) {
+    if (tid == 0) {
+      S.unit = blockIdx.x / K.cluster;
+      const int n = tiles_of(A, S.unit / K.groups), rank = blockIdx.x % K.cluster;
+      S.off = n * rank / K.cluster;
+      S.total = n * (rank + 1) / K.cluster - S.off;  // this CTA's tiles, maybe none
+    }
+    __syncthreads();
+    return;
+  }
   if (A.idx) {
     if (tid == 0) {
       const int64_t per = tiles_of(A, 0);
@@ -188,7 +200,7 @@ struct Pieces {
   int unit, off, tiles, n;  // tiles of the unit, tiles of the piece
   template <int kRope>
   __device__ __forceinline__ Pieces(const Kernel& K, const Smem<kRope>& S) {
-    left = run_start(S.total, blockIdx.x + 1, gridDim.x) - run_start(S.total, blockIdx.x, gridDim.x);
+    left = K.cluster ? S.total : run_start(S.total, blockIdx.x + 1, gridDim.x) - run_start(S.total, blockIdx.x, gridDim.x);
     unit = S.unit;
     off = S.off;
     size(K);
@@ -442,13 +454,14 @@ __device__ void role_mma_s(const Kernel& K, Smem<kRope>& S) {
         ok = ok && mbar_wait(bars + 8 * (kBarCFull + 2 * (g & 1) + half), (g >> 1) & 1, stop);
         if (!ok) break;
         csa::tc_fence_after();
+#pragma unroll 1
+        for (int c = kDim / 128 * half; c < kDim / 128 * (half + 1); ++c) {  // 64 values; rolled: code that runs once is fetched once
 #pragma unroll
-        for (int at = kDim / 2 * half; at < kDim / 2 * (half + 1); at += 16) {
-          const uint32_t bytes = at / 64 * kColBytes + at % 64 * 2;
-          if (at == 0)
-            csa::mma_f16_ss<false>(d, q_desc, bytes, c_desc, bytes, idesc);
-          else
-            csa::mma_f16_ss<true>(d, q_desc, bytes, c_desc, bytes, idesc);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bytes = c * kColBytes + 32 * k;
+            if (k == 0) csa::mma_f16_ss(d, q_desc, bytes, c_desc, bytes, idesc, c > 0);
+            else csa::mma_f16_ss<true>(d, q_desc, bytes, c_desc, bytes, idesc);
+          }
         }
         if (kRope != 0 && half == 0) {
 #pragma unroll
@@ -483,13 +496,13 @@ __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
       csa::tc_fence_after();
       // the tile's records are complete and read by S: the softmax waited for both
       const csa::Desc c_desc = c_descs[g & 1];
-#pragma unroll
+#pragma unroll 1
       for (int d = 0; d < kDim / 128; ++d) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k) {
           const uint32_t c_bytes = 2 * d * kColBytes + k * 2048;
-          if (i == 0 && k == 0)  // the piece's first tile overwrites
-            csa::mma_f16_ss<false>(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc);
+          if (k == 0)  // the piece's first tile overwrites
+            csa::mma_f16_ss(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc, i > 0);
           else
             csa::mma_f16_ss<true>(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc);
         }
@@ -659,6 +672,16 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
       l[r] += __shfl_xor_sync(0xFFFFFFFFu, l[r], 2);
       mc[r] = m[r] == -INFINITY ? -INFINITY : m[r] * c;
     }
+    if (K.cluster) {  // joined by cluster_join, once all CTAs of the unit are here
+      if ((lane & 3) == 0) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          S.mc[head[r]] = mc[r];
+          S.l[head[r]] = l[r];
+        }
+      }
+      return;
+    }
     if (run.n == run.tiles) {
       csa::named_bar_sync(kBarSoftmax, 32 * kSoftmaxWarps);
       if ((lane & 3) == 0) {
@@ -689,6 +712,95 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
   }
 }
 
+// A part's weight 2^x, x <= 0: as a square, so that it becomes subnormal before it becomes 0 and how a
+// row is split does not decide at which size its smallest terms vanish.
+__device__ __forceinline__ float weight(float x) {
+  const float h = csa::ex2(0.5f * x);
+  return h * h;
+}
+
+// Joins a unit among its cluster's CTAs, each of which has seen a part of the tiles: CTA r finishes values
+// 512 r / size .. of all heads (of 32 heads where size is 8). Everyone scales its O by its share of the
+// softmax, 2^(m c - M c) / L, and writes the others' slices into their record tiles, which are free by
+// now; sums go in the order of the ranks. Needs no workspace and no second launch.
+template <int kRope>
+__device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t size = K.cluster, rank = blockIdx.x % size;
+  const int heads = min(K.A.num_heads - (S.unit % K.groups) * kHeads, kHeads);
+  const int64_t row = static_cast<int64_t>(S.unit / K.groups) * K.A.num_heads + (S.unit % K.groups) * kHeads;
+  const int64_t tiles = S.total;
+  csa::cluster_arrive();
+  csa::cluster_wait();  // every CTA's m, l are there and its MMAs are done
+  if (threadIdx.x < kHeads) {
+    const int h = threadIdx.x;
+    float top = -INFINITY, sum = 0.f;
+    for (uint32_t r = 0; r < size; ++r) top = fmaxf(top, csa::ld_peer_f32(csa::peer_smem(smem_u32(&S.mc[h]), r)));
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (uint32_t r = 0; r < size; ++r)
+      sum = fmaf(csa::ld_peer_f32(csa::peer_smem(smem_u32(&S.l[h]), r)),
+                 weight(csa::ld_peer_f32(csa::peer_smem(smem_u32(&S.mc[h]), r)) - ref), sum);
+    S.alpha[h] = (sum > 0.f ? 1.f / sum : sum) * weight(S.mc[h] - ref);
+    if (rank == 0 && K.A.lse && h < heads) K.A.lse[row + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+  }
+  __syncthreads();
+  // A step is 4 heads of a block of 128 values; step s of the unit belongs to CTA s / per
+  constexpr int kSteps = kDim / 128 * (kHeads / 4), kStepBytes = 4 * 128 * 4;
+  const int per = kSteps / size;
+  auto slice_at = [&](uint32_t from, int s) {  // where CTA `from` puts its part of step s at the step's owner
+    return smem_u32(S.c[0]) + static_cast<uint32_t>(from * per + s % per) * kStepBytes;
+  };
+  const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+  auto mine = [&](int s, float (&v)[4]) {
+    const int d = s / (kHeads / 4), h = s % (kHeads / 4) * 4;
+    uint32_t raw[4];
+    csa::tmem_ld4(S.tmem + d * kHeads + h + lanes, raw);
+    csa::tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = tiles > 0 ? __uint_as_float(raw[j]) * S.alpha[h + j] : 0.f;
+  };
+  if (warp < kMmaWarp) {  // three warps a lane quarter
+    for (int s = warp >> 2; s < kSteps; s += kMmaWarp / 4) {
+      const uint32_t owner = s / per;
+      if (owner == rank || s % (kHeads / 4) * 4 >= heads) continue;
+      float v[4];
+      mine(s, v);
+      csa::st_peer_v4(csa::peer_smem(slice_at(rank, s), owner) + 16 * (32 * (warp & 3) + lane), v[0], v[1], v[2], v[3]);
+    }
+  }
+  csa::cluster_arrive();
+  csa::cluster_wait();
+  if (warp < kMmaWarp) {
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(K.A.out) + row * kDim + 32 * (warp & 3);
+    const int odd = lane & 1;
+    for (int s = static_cast<int>(rank) * per + (warp >> 2); s < static_cast<int>(rank + 1) * per; s += kMmaWarp / 4) {
+      const int d = s / (kHeads / 4), h = s % (kHeads / 4) * 4;
+      if (h >= heads) continue;
+      float own[4], v[4] = {};
+      mine(s, own);
+      for (uint32_t r = 0; r < size; ++r) {
+        float4 x = make_float4(own[0], own[1], own[2], own[3]);
+        if (r != rank)
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(slice_at(r, s) + 16 * (32 * (warp & 3) + lane))
+                       : "memory");
+        v[0] += x.x;
+        v[1] += x.y;
+        v[2] += x.z;
+        v[3] += x.w;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; j += 2) {  // as in write_out
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
+        if (h + j + odd < heads)
+          *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(h + j + odd) * kDim + 128 * d + (lane & ~1)) = two;
+      }
+    }
+  }
+}
+
 template <bool kFp4, int kRope>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   extern __shared__ uint8_t smem_raw[];
@@ -714,6 +826,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
     csa::mbar_init_fence();
     S.abort = 0;
   }
+  if (threadIdx.x < kHeads) {  // of a CTA without tiles
+    S.mc[threadIdx.x] = -INFINITY;
+    S.l[threadIdx.x] = 0.f;
+  }
   if (warp == kMmaWarp) {
     csa::tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     csa::tmem_relinquish();
@@ -730,13 +846,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
     if (lane == 0) {
       if (warp == kMmaWarp) role_mma_s(K, S);
       else role_mma_o(K, S);
-    } else if (lane == 1 && warp != kMmaWarp) {
+    } else if (lane == 1 && warp != kMmaWarp && !K.cluster) {
       write_opens(K, S);
     }
     __syncwarp();
   }
   csa::tc_fence_before();
   __syncthreads();
+  if (K.cluster) {
+    csa::tc_fence_after();
+    cluster_join(K, S);
+    csa::tc_fence_before();
+    __syncthreads();
+  }
   if (warp == kMmaWarp) {
     csa::tc_fence_after();
     csa::tmem_dealloc(S.tmem, kTmemCols);
@@ -779,7 +901,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, i
     if (!there(r)) continue;
     const float* part = part_of(r);
     const float4* x = reinterpret_cast<const float4*>(part + head * kDim);
-    const float w = csa::ex2(part[kHeads * kDim + head] - ref);
+    const float w = weight(part[kHeads * kDim + head] - ref);
     l = fmaf(part[kHeads * (kDim + 1) + head], w, l);
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -817,6 +939,18 @@ int grid_cap(const csa_latent_attend_args* a) {
 
 constexpr size_t kOpenBytes = (kMaxGrid * sizeof(Open) + 255) / 256 * 256;
 
+// CTAs that share a unit: where every unit is short (8 tiles a CTA at most) and there are fewer units than
+// SMs, the largest power of two up to 8 that still fits the SMs; else 0, the runs. Measured on 64 rows of
+// 8 tiles: see the note at cluster_join's call.
+int cluster_of(const csa_latent_attend_args* a, int sms) {
+  const int64_t units = static_cast<int64_t>(a->num_q) * ((a->num_heads + kHeads - 1) / kHeads);
+  const int64_t per = a->idx ? (a->top + kTile - 1) / kTile : a->pt_stride;
+  if (units > sms) return 0;
+  int size = 1;
+  while (size < 8 && 2 * size * units <= sms && size < per) size *= 2;
+  return per <= 8 * size ? size : 0;
+}
+
 template <bool kFp4, int kRope>
 csa_status launch(const Kernel& K, int grid, cudaStream_t stream) {
   static bool ready[64];  // the kernel's shared memory size is set on each device once
@@ -830,8 +964,17 @@ csa_status launch(const Kernel& K, int grid, cudaStream_t stream) {
       return CSA_ERR_CUDA;
     ready[dev] = true;
   }
-  attend_kernel<kFp4, kRope><<<grid, kThreads, smem, stream>>>(K);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim = {static_cast<unsigned>(K.cluster ? K.cluster : 1), 1, 1};
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<kFp4, kRope>, K) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 csa_status check_args(const csa_latent_attend_args* a) {
@@ -877,9 +1020,11 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   if (units > INT32_MAX) return CSA_ERR_INVALID_ARG;
   int sms = 0;
   if (sm_count(&sms) != CSA_OK) return CSA_ERR_CUDA;
-  const int cap = grid_cap(a), grid = cap < sms ? cap : sms;
   Kernel K;
   K.A = *a;
+  K.cluster = cluster_of(a, sms);
+  const int cap = K.cluster ? static_cast<int>(units) * K.cluster : grid_cap(a);
+  const int grid = cap < sms ? cap : sms;
   K.groups = groups;
   K.by_unit = units <= grid;
   K.opens = static_cast<Open*>(ws);
@@ -888,7 +1033,7 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
   const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, s) : launch<true, 0>(K, grid, s))
                             : (rope ? launch<false, 64>(K, grid, s) : launch<false, 0>(K, grid, s));
-  if (ls != CSA_OK || grid == 1) return ls;
+  if (ls != CSA_OK || grid == 1 || K.cluster) return ls;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, a->num_heads < kHeads ? a->num_heads : kHeads);
   cfg.blockDim = dim3(32 * kJoinWarps);

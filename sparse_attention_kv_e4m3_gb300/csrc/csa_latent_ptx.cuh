@@ -63,6 +63,17 @@ __device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_b
         : "memory");
 }
 
+__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_bytes, Desc b, uint32_t b_bytes,
+                                           uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc),
+      "r"(static_cast<uint32_t>(accumulate))
+      : "memory");
+}
+
 // D[tmem] (+)= A[tmem] * B[smem]^T: A's 16 values of a step are 8 columns, two bf16 a column.
 template <bool kAccumulate>
 __device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t b_bytes, uint32_t idesc) {
@@ -89,6 +100,28 @@ __device__ __forceinline__ void tma_tile_2d(uint32_t dst, const void* tmap, int3
           dst),
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// ----------------------------------------------------------------- clusters
+
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+
+// The address in the shared memory of the cluster's CTA `rank` of what lies at `addr` in this CTA's.
+__device__ __forceinline__ uint32_t peer_smem(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+
+__device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+__device__ __forceinline__ void st_peer_v4(uint32_t addr, float a, float b, float c, float d) {
+  asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
 }
 
 // 2^x: 2^-22 relative error, subnormal results become 0, 2^-infinity is 0.
@@ -129,6 +162,14 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32])
         "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
       : "r"(taddr)
       : "memory");
+}
+
+// 32 lanes x 32 bits, 4 consecutive columns: thread t reads lane (base + t).
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+               : "r"(taddr)
+               : "memory");
 }
 
 // Four 8 x 8 matrices of 16-bit elements to shared memory: lanes 8 k .. 8 k + 7 give the row

@@ -13,7 +13,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import native
-from .native import _check, _ptr, _stream
+from .native import CSA_OK, _check
 
 LATENT_DIM, MAX_HEADS, TABLES_MAX_REQ = 512, 128, 16384
 PREFILL_NOPE, PREFILL_ROPE, PREFILL_V = 128, 64, 128
@@ -104,12 +104,12 @@ def record_bytes(record_format, rope_dim: int) -> int:
     return n
 
 
-def _want(t: torch.Tensor, dtype, dims: int, name: str, last: bool = True) -> torch.Tensor:
-    """Checks a tensor argument: on the GPU, of this type and rank, its last axis (or all of it) contiguous."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != dims:
+def _want(t: torch.Tensor, dtype, dims: int, name: str, whole: bool = False) -> torch.Tensor:
+    """Checks a tensor argument: on the GPU, of this type and rank, contiguous in its last axis (or `whole`)."""
+    if not (t.is_cuda and t.dtype == dtype and t.dim() == dims):
         raise ValueError(f"{name}: a {dims}-d {dtype} CUDA tensor, not {tuple(t.shape)} {t.dtype} on {t.device}")
-    if not (t.is_contiguous() or (last and (t.shape[-1] == 1 or t.stride(-1) == 1))):
-        raise ValueError(f"{name}: contiguous{' in its last axis' if last else ''}")
+    if not t.is_contiguous() and (whole or (t.stride(-1) != 1 and t.shape[-1] != 1)):
+        raise ValueError(f"{name}: contiguous{'' if whole else ' in its last axis'}")
     return t
 
 
@@ -117,14 +117,28 @@ def _pick(out, shape, dtype, device, name):
     """The caller's output tensor, checked, or a new one."""
     if out is None:
         return torch.empty(shape, dtype=dtype, device=device)
-    _want(out, dtype, len(shape), name, last=False)
-    if tuple(out.shape) != tuple(shape) or out.device != device:
+    _want(out, dtype, len(shape), name, whole=True)
+    if out.shape != shape or out.device != device:
         raise ValueError(f"{name}: {tuple(shape)} on {device}, not {tuple(out.shape)} on {out.device}")
     return out
 
 
-def _status(t):
-    return None if t is None else _want(t, torch.int32, 1, "dev_status").data_ptr()
+def _status(t, device):
+    if t is None:
+        return None
+    if _want(t, torch.int32, 1, "dev_status").device != device or t.shape[0] < 1:
+        raise ValueError(f"dev_status: one int32 on {device}")
+    return t.data_ptr()
+
+
+def _stream(stream, device) -> int:
+    """The given stream, or the current one of the tensors' device, as an address."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
+def _done(st: int, what: str) -> None:
+    if st != CSA_OK:
+        _check(st, what)
 
 
 def _step(t: torch.Tensor, dim: int, width: int) -> int:
@@ -132,10 +146,10 @@ def _step(t: torch.Tensor, dim: int, width: int) -> int:
     return t.stride(dim) if t.shape[dim] > 1 else width
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
+def _same_device(device, *tensors):
+    for t in tensors:
         if t is not None and t.device != device:
-            raise ValueError(f"{name} is on {t.device}, not on {device}")
+            raise ValueError(f"every tensor is on {device}, not on {t.device}")
 
 
 class LatentCache:
@@ -147,7 +161,7 @@ class LatentCache:
         self.record_bytes = record_bytes(record_format, rope_dim)
         if pages.shape[1] < native.PAGE_RECORDS * self.record_bytes:
             raise ValueError(f"pages hold at least {native.PAGE_RECORDS * self.record_bytes} bytes")
-        self.pages = pages
+        self.pages, self.device = pages, pages.device
         self.width = LATENT_DIM + self.rope_dim
         self.args = CacheArgs(pages.data_ptr(), pages.shape[0], _step(pages, 0, pages.shape[1]), self.rope_dim, self.record_format)
 
@@ -170,11 +184,10 @@ class StepTables(NamedTuple):
 
 def empty_tables(num_req: int, n_rows: int, device="cuda") -> StepTables:
     """Tables for csa_build_tables to fill, in one allocation."""
-    ints = 3 * n_rows + 2 * (num_req + 1) + 1
-    buf = torch.empty(2 * n_rows + ints, dtype=torch.int32, device=device)
-    slot = buf[:2 * n_rows].view(torch.int64)
-    req, pos, length, row_start, kv_start, taken = buf[2 * n_rows:].split([n_rows] * 3 + [num_req + 1] * 2 + [1])
-    return StepTables(req, pos, length, slot, row_start, kv_start, taken)
+    buf = torch.empty(5 * n_rows + 2 * num_req + 3, dtype=torch.int32, device=device)
+    slot, req, pos, length, row_start, kv_start, taken = buf.split_with_sizes(
+        (2 * n_rows, n_rows, n_rows, n_rows, num_req + 1, num_req + 1, 1))
+    return StepTables(req, pos, length, slot.view(torch.int64), row_start, kv_start, taken)
 
 
 def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: torch.Tensor, free_pages: torch.Tensor,
@@ -185,83 +198,79 @@ def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: t
     the new records (n_rows of them, the rest padding) are returned."""
     _want(old_len, torch.int32, 1, "old_len")
     _want(new_len, torch.int32, 1, "new_len")
-    _want(page_table, torch.int32, 2, "page_table")
+    _want(page_table, torch.int32, 2, "page_table", whole=True)
     _want(free_pages, torch.int32, 1, "free_pages")
     dev, n, n_rows = old_len.device, old_len.shape[0], int(n_rows)
-    _same_device(dev, new_len=new_len, page_table=page_table, free_pages=free_pages)
-    if new_len.shape[0] != n or page_table.shape[0] != n:
-        raise ValueError("old_len, new_len and page_table: one row a request")
-    if n > 0 and page_table.stride(0) != page_table.shape[1]:
-        raise ValueError("page_table: contiguous")
+    _same_device(dev, new_len, page_table, free_pages)
+    if new_len.shape[0] != n or page_table.shape[0] != n or n_rows < 0:
+        raise ValueError("old_len, new_len and page_table: one row a request; n_rows at least 0")
     if out is None:
         out = empty_tables(n, n_rows, dev)
+        at = out.row_slot.data_ptr()  # one allocation: slots, three maps, two running sums, the count
+        req, pos, length = at + 8 * n_rows, at + 12 * n_rows, at + 16 * n_rows
+        start = at + 20 * n_rows
+        ptrs = (req, pos, length, at, start, start + 4 * (n + 1), start + 8 * (n + 1))
     else:
         for t, (size, dtype), name in zip(out, [(n_rows, torch.int32)] * 3 + [(n_rows, torch.int64)] +
                                           [(n + 1, torch.int32)] * 2 + [(1, torch.int32)], StepTables._fields):
             _pick(t, (size,), dtype, dev, name)
+        ptrs = tuple(t.data_ptr() for t in out)
     a = TablesArgs(old_len.data_ptr(), new_len.data_ptr(), n, page_table.shape[1], page_table.data_ptr(),
-                   free_pages.data_ptr(), free_pages.shape[0], n_rows, out.row_req.data_ptr(), out.row_pos.data_ptr(),
-                   out.row_len.data_ptr(), out.row_slot.data_ptr(), out.row_start.data_ptr(), out.kv_start.data_ptr(),
-                   out.taken.data_ptr(), _status(dev_status))
-    _check(load().csa_build_tables(ctypes.byref(a), _stream(stream)), "csa_build_tables")
+                   free_pages.data_ptr(), free_pages.shape[0], n_rows, *ptrs, _status(dev_status, dev))
+    _done(load().csa_build_tables(ctypes.byref(a), _stream(stream, dev)), "csa_build_tables")
     return out
 
 
 def csa_latent_write(x: torch.Tensor, slots: torch.Tensor, cache: LatentCache,
                      dev_status: Optional[torch.Tensor] = None, stream=None) -> None:
     """Stores rows x [n, 512 + rope] (fp32 or bf16) as the cache's records at `slots` [n] (int64)."""
-    if x.dtype not in (torch.float32, torch.bfloat16):
+    dtype, dev = x.dtype, cache.device
+    if dtype != torch.bfloat16 and dtype != torch.float32:
         raise TypeError("x must be float32 or bfloat16")
-    _want(x, x.dtype, 2, "x")
+    _want(x, dtype, 2, "x")
     _want(slots, torch.int64, 1, "slots")
-    _same_device(cache.pages.device, x=x, slots=slots)
-    if x.shape[1] != cache.width or slots.shape[0] != x.shape[0]:
+    _same_device(dev, x, slots)
+    n, width = x.shape
+    if width != cache.width or slots.shape[0] != n:
         raise ValueError(f"x [n, {cache.width}] and slots [n]")
-    a = LatentWriteArgs(cache.args, x.data_ptr(), _step(x, 0, cache.width),
-                        native.KEYS_BF16 if x.dtype == torch.bfloat16 else native.KEYS_F32, 0, x.shape[0],
-                        slots.data_ptr(), _status(dev_status))
-    _check(load().csa_latent_write(ctypes.byref(a), _stream(stream)), "csa_latent_write")
+    a = LatentWriteArgs(cache.args, x.data_ptr(), _step(x, 0, width),
+                        native.KEYS_BF16 if dtype == torch.bfloat16 else native.KEYS_F32, 0, n, slots.data_ptr(),
+                        _status(dev_status, dev))
+    _done(load().csa_latent_write(ctypes.byref(a), _stream(stream, dev)), "csa_latent_write")
 
 
 def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torch.Tensor, n_rows: int,
                     out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
     """Histories as rows [n_rows, 512 + rope] in bf16: record j of request r at kv_start[r] + j."""
-    _want(page_table, torch.int32, 2, "page_table")
+    _want(page_table, torch.int32, 2, "page_table", whole=True)
     _want(kv_start, torch.int32, 1, "kv_start")
-    dev = cache.pages.device
-    _same_device(dev, page_table=page_table, kv_start=kv_start)
-    if kv_start.shape[0] != page_table.shape[0] + 1 or not page_table.is_contiguous():
-        raise ValueError("page_table [num_req, pt_stride], contiguous, and kv_start [num_req + 1]")
-    out = _pick(out, (int(n_rows), cache.width), torch.bfloat16, dev, "out")
-    a = LatentReadArgs(cache.args, page_table.data_ptr(), page_table.shape[0], page_table.shape[1],
-                       kv_start.data_ptr(), int(n_rows), out.data_ptr(), _status(dev_status))
-    _check(load().csa_latent_read(ctypes.byref(a), _stream(stream)), "csa_latent_read")
+    dev, n_rows = cache.device, int(n_rows)
+    _same_device(dev, page_table, kv_start)
+    num_req, width = page_table.shape
+    if kv_start.shape[0] != num_req + 1 or n_rows < 0:
+        raise ValueError("page_table [num_req, pt_stride], kv_start [num_req + 1], n_rows at least 0")
+    out = _pick(out, (n_rows, cache.width), torch.bfloat16, dev, "out")
+    a = LatentReadArgs(cache.args, page_table.data_ptr(), num_req, width, kv_start.data_ptr(), n_rows, out.data_ptr(),
+                       _status(dev_status, dev))
+    _done(load().csa_latent_read(ctypes.byref(a), _stream(stream, dev)), "csa_latent_read")
     return out
 
 
-def _attend_args(q, cache, page_table, row_len, scale, idx, row_req, out, lse, dev_status):
-    _want(q, torch.bfloat16, 3, "q")
-    _want(page_table, torch.int32, 2, "page_table")
-    _want(row_len, torch.int32, 1, "row_len")
-    dev = cache.pages.device
-    _same_device(dev, q=q, page_table=page_table, row_len=row_len, idx=idx, row_req=row_req)
-    n, heads = q.shape[0], q.shape[1]
-    if q.shape[2] != cache.width or row_len.shape[0] != n or not page_table.is_contiguous():
-        raise ValueError(f"q [num_q, heads, {cache.width}], row_len [num_q], page_table contiguous")
-    if idx is not None:
-        _want(idx, torch.int32, 2, "idx")
-        if idx.shape[0] != n:
-            raise ValueError("idx [num_q, top]")
-    if row_req is not None and _want(row_req, torch.int32, 1, "row_req").shape[0] != n:
-        raise ValueError("row_req [num_q]")
-    out = _pick(out, (n, heads, LATENT_DIM), torch.bfloat16, dev, "out")
-    lse = _pick(lse, (n, heads), torch.float32, dev, "lse")
-    a = AttendArgs(cache.args, q.data_ptr(), _step(q, 0, cache.width), _step(q, 1, cache.width), n, heads, page_table.data_ptr(),
-                   page_table.shape[0], page_table.shape[1], _ptr(row_req), row_len.data_ptr(), _ptr(idx),
-                   0 if idx is None else _step(idx, 0, idx.shape[1]), 0 if idx is None else idx.shape[1],
-                   float(scale), out.data_ptr(), lse.data_ptr(), _status(dev_status))
-    return a, out, lse
+_workspaces = {}  # (device index, stream): the workspace of calls on that stream, which run one after the other
+
+
+def _workspace(device, stream_address: int, stream, size: int) -> torch.Tensor:
+    """A stream's workspace of at least `size` bytes. A captured call gets one of its own: its graph may be
+    replayed on any stream, beside eager calls on this one."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    ws = _workspaces.get((device.index, stream_address))
+    if ws is None or ws.shape[0] < size:
+        on = stream if stream is not None else torch.cuda.current_stream(device)
+        with torch.cuda.stream(on):  # the allocator reuses its memory in that stream's order
+            ws = _workspaces[device.index, stream_address] = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    return ws
 
 
 def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Tensor, row_len: torch.Tensor, *,
@@ -270,14 +279,46 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
                       ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """Latent attention, absorbed form: q [num_q, heads, 512 + rope] bf16 over the records below row_len[b]
     of request row_req[b] (identity when None), or over the positions idx [num_q, top] (-1: none) among
-    them. Returns (out [num_q, heads, 512] bf16, lse [num_q, heads] fp32)."""
-    a, out, lse = _attend_args(q, cache, page_table, row_len, scale, idx, row_req, out, lse, dev_status)
-    lib = load()
+    them. `ws` is a uint8 workspace of attend_workspace_bytes(...) or more; None takes one that is kept for
+    the stream (42 MB at most), or a new one while a graph is captured.
+    Returns (out [num_q, heads, 512] bf16, lse [num_q, heads] fp32)."""
+    _want(q, torch.bfloat16, 3, "q")
+    _want(page_table, torch.int32, 2, "page_table", whole=True)
+    _want(row_len, torch.int32, 1, "row_len")
+    dev = cache.device
+    _same_device(dev, q, page_table, row_len, idx, row_req)
+    n, heads, width = q.shape
+    num_req, pt_stride = page_table.shape
+    if width != cache.width or row_len.shape[0] != n:
+        raise ValueError(f"q [num_q, heads, {cache.width}], row_len [num_q]")
+    idx_ptr, idx_step, top, req_ptr = None, 0, 0, None
+    if idx is not None:
+        if _want(idx, torch.int32, 2, "idx").shape[0] != n:
+            raise ValueError("idx [num_q, top]")
+        top = idx.shape[1]
+        idx_ptr, idx_step = idx.data_ptr(), _step(idx, 0, top)
+    if row_req is not None:
+        if _want(row_req, torch.int32, 1, "row_req").shape[0] != n:
+            raise ValueError("row_req [num_q]")
+        req_ptr = row_req.data_ptr()
+    out = _pick(out, (n, heads, LATENT_DIM), torch.bfloat16, dev, "out")
+    lse = _pick(lse, (n, heads), torch.float32, dev, "lse")
+    a = AttendArgs(cache.args, q.data_ptr(), _step(q, 0, width), _step(q, 1, width), n, heads, page_table.data_ptr(),
+                   num_req, pt_stride, req_ptr, row_len.data_ptr(), idx_ptr, idx_step, top, float(scale),
+                   out.data_ptr(), lse.data_ptr(), _status(dev_status, dev))
+    lib, ref, st = load(), ctypes.byref(a), _stream(stream, dev)
     if ws is None:
-        ws = torch.empty(max(int(lib.csa_latent_attend_workspace_bytes(ctypes.byref(a))), 16), dtype=torch.uint8,
-                         device=out.device)
-    _check(lib.csa_latent_attend(ctypes.byref(a), ws.data_ptr(), ws.numel(), _stream(stream)), "csa_latent_attend")
+        ws = _workspace(dev, st, stream, lib.csa_latent_attend_workspace_bytes(ref))
+    elif _want(ws, torch.uint8, 1, "ws").device != dev:
+        raise ValueError(f"ws is on {ws.device}, not on {dev}")
+    _done(lib.csa_latent_attend(ref, ws.data_ptr(), ws.shape[0], st), "csa_latent_attend")
     return out, lse
+
+
+def attend_workspace_bytes(num_q: int, heads: int, pt_stride: int, top: int = 0) -> int:
+    """Workspace of csa_latent_attend for these sizes (top: positions a row, 0 for whole histories)."""
+    a = AttendArgs(num_q=int(num_q), num_heads=int(heads), pt_stride=int(pt_stride), top=int(top), idx=16 if top else None)
+    return int(load().csa_latent_attend_workspace_bytes(ctypes.byref(a)))
 
 
 def csa_latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tensor, v: torch.Tensor,
@@ -287,22 +328,26 @@ def csa_latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tens
     """Latent attention, expanded form: q [total_q, heads, 192], k_nope and v [total_k, heads, 128], k_rope
     [total_k, 64], all bf16; request r has rows q_start[r] .. q_start[r + 1] of q and kv_start[r] ..
     kv_start[r + 1] of the keys. Returns (out [total_q, heads, 128] bf16, lse [total_q, heads] fp32)."""
-    for t, name, dims in ((q, "q", 3), (k_nope, "k_nope", 3), (v, "v", 3), (k_rope, "k_rope", 2)):
-        _want(t, torch.bfloat16, dims, name)
+    _want(q, torch.bfloat16, 3, "q")
+    _want(k_nope, torch.bfloat16, 3, "k_nope")
+    _want(v, torch.bfloat16, 3, "v")
+    _want(k_rope, torch.bfloat16, 2, "k_rope")
     _want(q_start, torch.int32, 1, "q_start")
     _want(kv_start, torch.int32, 1, "kv_start")
-    _same_device(q.device, k_nope=k_nope, k_rope=k_rope, v=v, q_start=q_start, kv_start=kv_start)
-    tq, heads, tk = q.shape[0], q.shape[1], k_nope.shape[0]
-    if (q.shape[2] != PREFILL_NOPE + PREFILL_ROPE or k_nope.shape[1:] != (heads, PREFILL_NOPE) or
+    dev = q.device
+    _same_device(dev, k_nope, k_rope, v, q_start, kv_start)
+    tq, heads, width = q.shape
+    tk = k_nope.shape[0]
+    if (width != PREFILL_NOPE + PREFILL_ROPE or k_nope.shape != (tk, heads, PREFILL_NOPE) or
             v.shape != (tk, heads, PREFILL_V) or k_rope.shape != (tk, PREFILL_ROPE) or
             q_start.shape != kv_start.shape or q_start.shape[0] < 1):
         raise ValueError("q [tq, h, 192], k_nope and v [tk, h, 128], k_rope [tk, 64], q_start and kv_start [num_req + 1]")
-    out = _pick(out, (tq, heads, PREFILL_V), torch.bfloat16, q.device, "out")
-    lse = _pick(lse, (tq, heads), torch.float32, q.device, "lse")
-    a = PrefillArgs(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _step(q, 0, 192),
-                    _step(q, 1, 192), _step(k_nope, 0, 128), _step(k_nope, 1, 128), _step(k_rope, 0, 64),
-                    _step(v, 0, 128), _step(v, 1, 128), tq, tk,
-                    q_start.data_ptr(), kv_start.data_ptr(), q_start.shape[0] - 1, heads, int(bool(causal)),
-                    float(scale), out.data_ptr(), lse.data_ptr(), _status(dev_status))
-    _check(load().csa_latent_prefill(ctypes.byref(a), _stream(stream)), "csa_latent_prefill")
+    out = _pick(out, (tq, heads, PREFILL_V), torch.bfloat16, dev, "out")
+    lse = _pick(lse, (tq, heads), torch.float32, dev, "lse")
+    a = PrefillArgs(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _step(q, 0, width),
+                    _step(q, 1, width), _step(k_nope, 0, 128), _step(k_nope, 1, 128), _step(k_rope, 0, 64),
+                    _step(v, 0, 128), _step(v, 1, 128), tq, tk, q_start.data_ptr(), kv_start.data_ptr(),
+                    q_start.shape[0] - 1, heads, 1 if causal else 0, float(scale), out.data_ptr(), lse.data_ptr(),
+                    _status(dev_status, dev))
+    _done(load().csa_latent_prefill(ctypes.byref(a), _stream(stream, dev)), "csa_latent_prefill")
     return out, lse
