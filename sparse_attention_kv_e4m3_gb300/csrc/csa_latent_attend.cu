@@ -53,7 +53,7 @@ struct Smem {
   uint8_t p[kHeads * 128];
   uint64_t bars[18];
   uint8_t valid[2][kTile];  // 1 where the tile's record is visible
-  float alpha[kHeads];
+  alignas(16) float alpha[kHeads];
   float mc[kHeads], l[kHeads];  // cluster: this CTA's reference and sum per head
   int64_t total;
   int32_t unit, off;
@@ -108,22 +108,21 @@ __device__ __forceinline__ int tiles_of(const csa_latent_attend_args& A, int b) 
   return max(1, (row_view(A, b, &ignore).len + kTile - 1) / kTile);
 }
 
-// The record of entry j of the row (of the listed positions, or of the history), or null.
-__device__ __forceinline__ const uint8_t* record_of(const csa_latent_attend_args& A, const RowView& R, int b, int j,
+// The position of entry j of the row (of the listed positions, or of the history); -1 for none.
+__device__ __forceinline__ int32_t position_of(const csa_latent_attend_args& A, const RowView& R, int b, int j) {
+  if (A.idx) return j < A.top ? __ldg(A.idx + b * A.idx_stride + j) : -1;
+  return j < R.len ? j : -1;
+}
+
+// The record at a position, or null.
+__device__ __forceinline__ const uint8_t* record_at(const csa_latent_attend_args& A, const RowView& R, int32_t pos,
                                                     int rec_bytes, int32_t* flags) {
-  int32_t pos = j;
-  if (A.idx) {
-    if (j >= A.top) return nullptr;
-    pos = A.idx[b * A.idx_stride + j];
-    if (pos == -1) return nullptr;
-    if (pos < 0 || pos >= R.len) {
-      *flags |= CSA_DEV_LEN_OOB;
-      return nullptr;
-    }
-  } else if (j >= R.len) {
+  if (pos == -1) return nullptr;
+  if (pos < 0 || pos >= R.len) {
+    *flags |= CSA_DEV_LEN_OOB;
     return nullptr;
   }
-  const int32_t page = R.table[pos / kPageRecs];
+  const int32_t page = __ldg(R.table + pos / kPageRecs);
   if (page < 0 || page >= A.cache.num_pages) {
     *flags |= CSA_DEV_PAGE_OOB;
     return nullptr;
@@ -355,13 +354,16 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   const int t = threadIdx.x - 32 * kSoftmaxWarps, lane = t & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
-  Pieces run(K, S), ahead = run;  // `ahead` resolves the tile after the one that is stored
+  Pieces run(K, S);
   if (!run.more()) return;
-  RowView R = row_view(A, ahead.unit / K.groups, flags);
+  // A tile's records are found in two steps, one tile apart, so that no load waits for another one just
+  // issued: the entries' positions, then their pages.
+  Pieces ahead = run;
   int tile = ahead.off, piece_end = ahead.off + ahead.n;
+  RowView R = row_view(A, ahead.unit / K.groups, flags), R_found = R;
+  int32_t pos[Regs::kRecords];
   const uint8_t* rec[Regs::kRecords];
-  // The records of the next tile of the run, null past its end.
-  auto resolve = [&]() {
+  auto find = [&]() {  // the positions of the next tile of the run, -1 past its end
     if (ahead.more() && tile == piece_end) {
       ahead.next(K);
       if (ahead.more()) {
@@ -372,14 +374,19 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
     }
 #pragma unroll
     for (int k = 0; k < Regs::kRecords; ++k)
-      rec[k] = ahead.more() ? record_of(A, R, ahead.unit / K.groups, tile * kTile + Regs::record(t, k),
-                                        record_bytes(kFp4, kRope), flags)
-                            : nullptr;
+      pos[k] = ahead.more() ? position_of(A, R, ahead.unit / K.groups, tile * kTile + Regs::record(t, k)) : -1;
+    R_found = R;
     ++tile;
+  };
+  auto locate = [&]() {  // the records at the positions found
+#pragma unroll
+    for (int k = 0; k < Regs::kRecords; ++k) rec[k] = record_at(A, R_found, pos[k], record_bytes(kFp4, kRope), flags);
   };
   Regs x;
   bool live[Regs::kRecords];
-  resolve();
+  find();
+  locate();
+  find();
 #pragma unroll
   for (int pair = 0; pair < kPairs; ++pair) x.fetch(rec, pair, t);
   uint32_t g = 0, piece = 0;
@@ -397,6 +404,17 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
       for (int c = 0; c < kCols; ++c)
         csa::cp_async16(smem_u32(S.q) + c * kColBytes + h * 128 + (((t & 7) ^ (h & 7)) << 4), q + 128 * c, on);
     }
+    if (run.left > run.n) {  // the next unit's Q on its way to L2: its own copy can only start when this one's last S is done
+      const int nb = (run.unit + 1) / K.groups, n0 = (run.unit + 1) % K.groups * kHeads;
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int h = (t >> 3) + 32 * k;
+        if (n0 + h < A.num_heads && (t & 7) == 0)
+#pragma unroll
+          for (int c = 0; c < kCols; ++c)
+            csa::prefetch_l2(static_cast<const uint8_t*>(A.q) + 2 * (nb * A.q_row_stride + (n0 + h) * A.q_head_stride) + 128 * c);
+      }
+    }
     csa::cp_async_wait_all();
     csa::fence_proxy_async_smem();
     __syncwarp();
@@ -405,7 +423,8 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
       const uint32_t stage = g & 1;
 #pragma unroll
       for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
-      resolve();
+      locate();
+      find();
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         x.convert(2 * half, t);  // before the tile's turn, where that is not yet come
@@ -454,8 +473,8 @@ __device__ void role_mma_s(const Kernel& K, Smem<kRope>& S) {
         ok = ok && mbar_wait(bars + 8 * (kBarCFull + 2 * (g & 1) + half), (g >> 1) & 1, stop);
         if (!ok) break;
         csa::tc_fence_after();
-#pragma unroll 1
-        for (int c = kDim / 128 * half; c < kDim / 128 * (half + 1); ++c) {  // 64 values; rolled: code that runs once is fetched once
+#pragma unroll
+        for (int c = kDim / 128 * half; c < kDim / 128 * (half + 1); ++c) {
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const uint32_t bytes = c * kColBytes + 32 * k;
@@ -496,7 +515,7 @@ __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
       csa::tc_fence_after();
       // the tile's records are complete and read by S: the softmax waited for both
       const csa::Desc c_desc = c_descs[g & 1];
-#pragma unroll 1
+#pragma unroll
       for (int d = 0; d < kDim / 128; ++d) {
 #pragma unroll
         for (int k = 0; k < kTile / 16; ++k) {
@@ -517,27 +536,46 @@ __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
 template <int kRope>
 __device__ void write_out(const Kernel& K, Smem<kRope>& S, int unit, int heads, int warp, int lane) {
   const int b = unit / K.groups, h0 = (unit % K.groups) * kHeads;
-  __nv_bfloat16* out =
-      static_cast<__nv_bfloat16*>(K.A.out) + (static_cast<int64_t>(b) * K.A.num_heads + h0) * kDim + 32 * warp;
   const int odd = lane & 1;
-#pragma unroll 1
-  for (int d = 0; d < kDim / 128; ++d) {
-#pragma unroll 1
-    for (int hh = 0; hh < heads; hh += 32) {
-      uint32_t v[32];
-      csa::tmem_ld32(S.tmem + d * kHeads + hh + (static_cast<uint32_t>(32 * warp) << 16), v);
-      csa::tmem_wait_ld();
-      // two heads at a time: even lanes end with values (lane, lane + 1) of the first, odd lanes with
-      // values (lane - 1, lane) of the second
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(K.A.out) +
+                       (static_cast<int64_t>(b) * K.A.num_heads + h0 + odd) * kDim + 32 * warp + (lane & ~1);
+  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
+  // 32 heads of 128 values a step; the next step's O is on its way while this one's is written
+  const int halves = heads > 32 ? 2 : 1, steps = kDim / 128 * halves;
+  auto o_at = [&](int step) { return S.tmem + step / halves * kHeads + step % halves * 32 + lanes; };
+  auto write = [&](int step, const uint32_t (&v)[32]) {
+    const int hh = step % halves * 32;
+    const float4* alpha = reinterpret_cast<const float4*>(S.alpha + hh);
+    __nv_bfloat16* at = out + hh * kDim + 128 * (step / halves);
+    const int left = heads - hh - odd;  // of the heads from hh + odd on
+    // two heads at a time: even lanes end with values (lane, lane + 1) of the first, odd lanes with
+    // values (lane - 1, lane) of the second
+    uint32_t two[16];
 #pragma unroll
-      for (int j = 0; j < 32; j += 2) {
-        const float x0 = __uint_as_float(v[j]) * S.alpha[hh + j], x1 = __uint_as_float(v[j + 1]) * S.alpha[hh + j + 1];
+    for (int j = 0; j < 32; j += 4) {
+      const float4 a = alpha[j / 4];
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const float x0 = __uint_as_float(v[j + k]) * (k ? a.z : a.x), x1 = __uint_as_float(v[j + k + 1]) * (k ? a.w : a.y);
         const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
-        const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(got, x1) : __floats2bfloat162_rn(x0, got);
-        if (hh + j + odd < heads)
-          *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(hh + j + odd) * kDim + 128 * d + (lane & ~1)) = two;
+        const __nv_bfloat162 pair = __floats2bfloat162_rn(odd ? got : x0, odd ? x1 : got);
+        two[(j + k) / 2] = *reinterpret_cast<const uint32_t*>(&pair);
       }
     }
+    // the stores apart from the exchanges, which would wait for one another in between
+#pragma unroll
+    for (int j = 0; j < 32; j += 2) csa::st_global_if(j < left, at + j * kDim, two[j / 2]);
+  };
+  uint32_t va[32], vb[32];
+  csa::tmem_ld32(o_at(0), va);
+#pragma unroll 1
+  for (int step = 0; step < steps; step += 2) {  // steps is even
+    csa::tmem_wait_ld();
+    csa::tmem_ld32(o_at(step + 1), vb);
+    write(step, va);
+    csa::tmem_wait_ld();
+    if (step + 2 < steps) csa::tmem_ld32(o_at(step + 2), va);
+    write(step + 1, vb);
   }
 }
 

@@ -172,6 +172,15 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
                : "memory");
 }
 
+// A predicated 32-bit store: no branch around it.
+__device__ __forceinline__ void st_global_if(bool on, void* p, uint32_t v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p st.global.b32 [%0], %1;\n\t}" ::"l"(p), "r"(v),
+               "r"(static_cast<uint32_t>(on))
+               : "memory");
+}
+
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // Four 8 x 8 matrices of 16-bit elements to shared memory: lanes 8 k .. 8 k + 7 give the row
 // addresses of matrix k; a lane holds row lane / 4, columns 2 (lane % 4) and the next of each.
 __device__ __forceinline__ void stmatrix_x4(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
