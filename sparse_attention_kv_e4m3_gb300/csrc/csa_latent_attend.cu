@@ -27,7 +27,7 @@ using csa::smem_u32;
 // Warps 0-3: softmax (S from TMEM, P to shared memory) and the output. Warps 4-11: loaders.
 // They hold one more tile in registers, so that its global loads are in flight while
 // both tiles in shared memory are in use; MXFP4 codes become bf16 values (exactly) on the
-// way. Warps 12, 13: one thread issues the MMAs of S, another those of O, so that neither waits for the
+// way. Warp 12 issues the MMAs of S, warp 13 those of O, so that neither waits for the
 // other's operands and S of tile i + 1 runs during tile i's softmax. A tile is filled and freed 128
 // values at a time: the next one moves in while O still reads the rest.
 //
@@ -446,90 +446,79 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   }
 }
 
-// Nothing of this thread's MMAs is in flight when it leaves its role.
-__device__ __forceinline__ void drain(uint32_t bar) {
-  csa::mma_commit(bar);
-  csa::mbar_wait_drain(bar, 0);
-}
-
 template <int kRope>
 __device__ void role_mma_s(const Kernel& K, Smem<kRope>& S) {
   volatile int* stop = &S.abort;
-  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem + kTmemS;
+  const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem) + kTmemS, lead = csa::elect_lane();
   constexpr uint32_t idesc = csa::idesc_bf16_f32(64, kTile);
-  const csa::Desc q_desc(csa::sdesc_kmajor_sw128(smem_u32(S.q)));
-  const csa::Desc c_descs[2] = {csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.c[0]))),
-                                csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.c[1])))};
+  const csa::Desc q_desc(csa::sdesc_kmajor_sw128(smem_u32(S.q))), c_descs(csa::sdesc_kmajor_sw128(smem_u32(S.c[0])));
   uint32_t g = 0, piece = 0;
   bool ok = true;
   for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
-    ok = mbar_wait(bars + 8 * kBarQFull, piece & 1, stop);
-    for (int i = 0; ok && i < run.n; ++i, ++g) {
-      ok = mbar_wait(bars + 8 * (kBarSEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop);
-      const csa::Desc c_desc = c_descs[g & 1];
+    ok = warp_wait(bars + 8 * kBarQFull, piece & 1, stop);
+    const int n = csa::uniform(run.n);
+    for (int i = 0; ok && i < n; ++i, ++g) {
+      ok = warp_wait(bars + 8 * (kBarSEmpty + (g & 1)), ((g >> 1) & 1) ^ 1, stop);
+      const csa::Desc c_desc = c_descs.at((g & 1) * sizeof(S.c[0]));
       const uint32_t d = tmem + (g & 1) * kTile;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {  // as the tile is filled
-        ok = ok && mbar_wait(bars + 8 * (kBarCFull + 2 * (g & 1) + half), (g >> 1) & 1, stop);
+        ok = ok && warp_wait(bars + 8 * (kBarCFull + 2 * (g & 1) + half), (g >> 1) & 1, stop);
         if (!ok) break;
         csa::tc_fence_after();
 #pragma unroll
-        for (int c = kDim / 128 * half; c < kDim / 128 * (half + 1); ++c) {
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t bytes = c * kColBytes + 32 * k;
-            if (k == 0) csa::mma_f16_ss(d, q_desc, bytes, c_desc, bytes, idesc, c > 0);
-            else csa::mma_f16_ss<true>(d, q_desc, bytes, c_desc, bytes, idesc);
-          }
+        for (int at = kDim / 2 * half; at < kDim / 2 * (half + 1); at += 16) {
+          const uint32_t bytes = at / 64 * kColBytes + at % 64 * 2;
+          csa::mma_f16_ss(lead, d, q_desc.at(bytes), c_desc.at(bytes), idesc, at > 0);
         }
         if (kRope != 0 && half == 0) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            csa::mma_f16_ss<true>(d, q_desc, kDim / 64 * kColBytes + 32 * k, c_desc, kDim / 64 * kColBytes + 32 * k, idesc);
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t bytes = kDim / 64 * kColBytes + 32 * k;
+            csa::mma_f16_ss(lead, d, q_desc.at(bytes), c_desc.at(bytes), idesc, true);
+          }
         }
       }
       if (!ok) break;
-      csa::mma_commit(bars + 8 * (kBarSFull + (g & 1)));
-      if (i + 1 == run.n) csa::mma_commit(bars + 8 * kBarQEmpty);
+      csa::mma_commit_if(lead, bars + 8 * (kBarSFull + (g & 1)));
+      if (i + 1 == n) csa::mma_commit_if(lead, bars + 8 * kBarQEmpty);
     }
   }
-  drain(bars + 8 * kBarDrainS);
+  csa::mma_commit_if(lead, bars + 8 * kBarDrainS);  // nothing of this warp's MMAs is in flight when it leaves
+  csa::mbar_wait_drain(bars + 8 * kBarDrainS, 0);
+  __syncwarp();
 }
 
 template <int kRope>
 __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
   volatile int* stop = &S.abort;
-  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem;
-  const csa::Desc p_desc(csa::sdesc_kmajor_sw128(smem_u32(S.p)));
-  const csa::Desc c_descs[2] = {csa::Desc(csa::sdesc_mn_sw128_b16(smem_u32(S.c[0]), kColBytes)),
-                                csa::Desc(csa::sdesc_mn_sw128_b16(smem_u32(S.c[1]), kColBytes))};
+  const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem), lead = csa::elect_lane();
+  const csa::Desc p_desc(csa::sdesc_kmajor_sw128(smem_u32(S.p))), c_descs(csa::sdesc_mn_sw128_b16(smem_u32(S.c[0]), kColBytes));
   uint32_t g = 0, piece = 0;
   bool ok = true;
   for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
     const int heads = min(K.A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
-    const uint32_t idesc = csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor;
-    ok = mbar_wait(bars + 8 * kBarOEmpty, (piece & 1) ^ 1, stop);
-    for (int i = 0; ok && i < run.n; ++i, ++g) {
-      ok = mbar_wait(bars + 8 * kBarPFull, g & 1, stop);
+    const uint32_t idesc = csa::uniform(csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor);
+    ok = warp_wait(bars + 8 * kBarOEmpty, (piece & 1) ^ 1, stop);
+    const int n = csa::uniform(run.n);
+    for (int i = 0; ok && i < n; ++i, ++g) {
+      ok = warp_wait(bars + 8 * kBarPFull, g & 1, stop);
       if (!ok) break;
       csa::tc_fence_after();
       // the tile's records are complete and read by S: the softmax waited for both
-      const csa::Desc c_desc = c_descs[g & 1];
+      const csa::Desc c_desc = c_descs.at((g & 1) * sizeof(S.c[0]));
 #pragma unroll
       for (int d = 0; d < kDim / 128; ++d) {
 #pragma unroll
-        for (int k = 0; k < kTile / 16; ++k) {
-          const uint32_t c_bytes = 2 * d * kColBytes + k * 2048;
-          if (k == 0)  // the piece's first tile overwrites
-            csa::mma_f16_ss(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc, i > 0);
-          else
-            csa::mma_f16_ss<true>(tmem + d * kHeads, c_desc, c_bytes, p_desc, 32 * k, idesc);
-        }
-        if (d & 1) csa::mma_commit(bars + 8 * (kBarCEmpty + 2 * (g & 1) + (d >> 1)));
+        for (int k = 0; k < kTile / 16; ++k)  // the piece's first tile overwrites
+          csa::mma_f16_ss(lead, tmem + d * kHeads, c_desc.at(2 * d * kColBytes + k * 2048), p_desc.at(32 * k), idesc, i > 0 || k > 0);
+        if (d & 1) csa::mma_commit_if(lead, bars + 8 * (kBarCEmpty + 2 * (g & 1) + (d >> 1)));
       }
     }
   }
-  drain(bars + 8 * kBarDrainO);
+  csa::mma_commit_if(lead, bars + 8 * kBarDrainO);
+  csa::mbar_wait_drain(bars + 8 * kBarDrainO, 0);
+  __syncwarp();
 }
 
 // out (or a part) from O^T: a thread holds one value of 128 per column block, for every head.
@@ -881,13 +870,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   } else if (warp < kMmaWarp) {
     role_load<kFp4, kRope>(K, S, &flags);
   } else {
-    if (lane == 0) {
-      if (warp == kMmaWarp) role_mma_s(K, S);
-      else role_mma_o(K, S);
-    } else if (lane == 1 && warp != kMmaWarp && !K.cluster) {
-      write_opens(K, S);
+    if (warp == kMmaWarp) {
+      role_mma_s(K, S);
+    } else {
+      if (lane == 0 && !K.cluster) write_opens(K, S);
+      __syncwarp();
+      role_mma_o(K, S);
     }
-    __syncwarp();
   }
   csa::tc_fence_before();
   __syncthreads();

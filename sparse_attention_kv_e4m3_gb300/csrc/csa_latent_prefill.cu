@@ -1,6 +1,8 @@
 // csa_latent_prefill.cu — latent attention, expanded form (include/csa_latent.h).
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "csa_latent_common.cuh"
 #include "csa_latent_ptx.cuh"
 
@@ -18,20 +20,22 @@ using csa::smem_u32;
 // right; a stale one only scales O and l alike), so that O is rarely rescaled.
 //
 // Bound by the tensor cores (20 MMAs of 64 clocks a tile pair) while the exponentials of one query
-// tile run under the MMAs of the other: the order of issue is S0(j), O1(j - 1), S1(j), O0(j), so
-// each softmax has 1280 clocks. A row of S is a TMEM lane and belongs to one thread, P goes back over
+// tile run under the MMAs of the other. A row of S is a TMEM lane and belongs to one thread, P goes back over
 // S in TMEM as the A operand of O, V is read from shared memory as it lies (N-major).
 //
-// Shared memory: Q 2 x 48 KB, K 2 x 48 KB, V 32 KB (in two halves of 64 keys, each handed back as soon as
-// the last query tile has read it): 224 KB, one CTA an SM. TMEM: S0, S1, O0, O1, all 512 columns.
-// Warps 0-3 and 4-7: softmax and output of the two tiles. Warp 8: one thread issues the MMAs.
+// Shared memory: Q 2 x 48 KB and a ring of eight 16 KB chunks through which K(0), V(0), K(1), V(1), ... go in
+// turn (K(j) takes the place of K(j - 2)'s end and V(j - 2), V(j) that of K(j - 1)'s beginning), so that V has two
+// and a half of the MMAs' rounds to arrive and K one: 224 KB, one CTA an SM. TMEM: S0, S1, O0, O1, all 512 columns.
+// Warps 0-3 and 4-7: softmax and output of the two tiles. Warp 8 issues the MMAs.
 // Warp 9: TMA; it also zeroes the value rows past a request's last key, which belong to
 // others and may hold NaN (P is 0 there, but 0 x NaN is not).
 constexpr int kNope = CSA_PREFILL_NOPE, kRope = CSA_PREFILL_ROPE, kV = CSA_PREFILL_V;
 constexpr int kTile = 128;                            // query rows, keys
 constexpr int kColBytes = kTile * 128;                // 64 values of 128 rows
-constexpr int kQCols = (kNope + kRope) / 64, kVCols = kV / 64;
-constexpr int kQBytes = kQCols * kColBytes, kVBytes = kVCols * kColBytes;
+constexpr int kQCols = (kNope + kRope) / 64;
+constexpr int kQBytes = kQCols * kColBytes;
+constexpr int kRing = 8;                              // chunks of 16 KB: K is 3 (64 values of 128 keys each), V 2 (64 keys each)
+constexpr int kTileChunks = kQCols + 2;
 constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
 constexpr int kThreads = 32 * 10;
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;     // S of tile t at 128 t, O at 256 + 128 t
@@ -43,16 +47,19 @@ struct Maps {
 
 struct Smem {
   uint8_t q[2][kQBytes];
-  uint8_t k[2][kQBytes];
-  uint8_t v[kVBytes];
-  uint64_t bars[20];
+  uint8_t ring[kRing][kColBytes];
+  uint64_t bars[24];
   int32_t warp_pairs[kThreads / 32];
   int32_t total, request, first;  // of the item: its request and its first query row there
   uint32_t tmem;
   int abort;
 };
-enum { kBarQFull = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarVLand = 9, kBarSFull = 10,
-       kBarPFull = 12, kBarOFull = 14, kBarDrain = 16 };
+// K, V: by the key tile's parity (V also by half: 2 * parity + half); S, P, O, Q: by query tile
+enum { kBarQFull = 0, kBarKFull = 2, kBarKEmpty = 4, kBarVFull = 6, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14,
+       kBarOFull = 16, kBarVLand = 18, kBarDrain };
+
+// Where chunk i of key tile j lies: K 0 .. 2, V 3, 4.
+__device__ __forceinline__ uint32_t ring_slot(int j, int i) { return static_cast<uint32_t>(kTileChunks * j + i) % kRing; }
 
 // Bounds of request r, false where they descend or leave the tensors.
 struct Request {
@@ -130,128 +137,186 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
   const int lane = threadIdx.x & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
-  const int n = max(key_tiles(A, R, first, 0), key_tiles(A, R, first, 1));
+  const int nt[2] = {key_tiles(A, R, first, 0), key_tiles(A, R, first, 1)}, n = max(nt[0], nt[1]);
   if (n == 0) return;
-  if (lane == 0) {
-    csa::mbar_arrive_expect_tx(bars + 8 * kBarQFull, 2 * kQBytes);
-    for (int t = 0; t < 2; ++t)
-      for (int c = 0; c < kQCols; ++c)
-        csa::tma_tile_3d(smem_u32(S.q[t]) + c * kColBytes, &M.q, 64 * c, head, R.q0 + first + t * kTile, bars + 8 * kBarQFull);
-  }
+  auto load_q = [&](int t) {
+    if (lane != 0 || nt[t] == 0) return;
+    csa::mbar_arrive_expect_tx(bars + 8 * (kBarQFull + t), kQBytes);
+    for (int c = 0; c < kQCols; ++c)
+      csa::tma_tile_3d(smem_u32(S.q[t]) + c * kColBytes, &M.q, 64 * c, head, R.q0 + first + t * kTile, bars + 8 * (kBarQFull + t));
+  };
   bool ok = true;
   int k_done = 0, v_done = 0, landed = 0;
+  const uint32_t ring = smem_u32(S.ring[0]);
+  auto freed = [&](int bar, int j) {  // what tile j held there has been read (nothing held it where j < 0)
+    ok = ok && (j < 0 || warp_wait(bars + 8 * (bar + (j & 1)), (j >> 1) & 1, stop));
+    return ok;
+  };
   auto load_k = [&](int j) {
-    const uint32_t s = j & 1;
-    ok = ok && warp_wait(bars + 8 * (kBarKEmpty + s), ((j >> 1) & 1) ^ 1, stop);
-    if (!ok) return;
+    if (!freed(kBarKEmpty, j - 2)) return;
+    const uint32_t bar = bars + 8 * (kBarKFull + (j & 1));
+    const int row = R.k0 + j * kTile;
     if (lane == 0) {
-      const uint32_t bar = bars + 8 * (kBarKFull + s), dst = smem_u32(S.k[s]);
       csa::mbar_arrive_expect_tx(bar, kQBytes);
-      for (int c = 0; c < kNope / 64; ++c) csa::tma_tile_3d(dst + c * kColBytes, &M.k, 64 * c, head, R.k0 + j * kTile, bar);
-      csa::tma_tile_2d(dst + kNope / 64 * kColBytes, &M.rope, 0, R.k0 + j * kTile, bar);
+      csa::tma_tile_3d(ring + ring_slot(j, 0) * kColBytes, &M.k, 0, head, row, bar);
     }
     k_done = j + 1;
+    if (!freed(kBarVEmpty, j - 2)) return;
+    if (lane == 0) {
+      csa::tma_tile_3d(ring + ring_slot(j, 1) * kColBytes, &M.k, 64, head, row, bar);
+      csa::tma_tile_2d(ring + ring_slot(j, 2) * kColBytes, &M.rope, 0, row, bar);
+    }
   };
   auto load_v = [&](int j) {
+    if (!freed(kBarKEmpty, j - 1)) return;
     for (int half = 0; half < 2; ++half) {
-      ok = ok && warp_wait(bars + 8 * (kBarVEmpty + half), (j & 1) ^ 1, stop);
-      if (!ok) return;
       // rows of the half that are this request's; the others become zeros before the half is handed over
       const int rows = min(64, R.nk - j * kTile - 64 * half);
       const bool whole = rows == 64;
-      const uint32_t full = bars + 8 * (kBarVFull + half), land = whole ? full : bars + 8 * kBarVLand;
+      const uint32_t full = bars + 8 * (kBarVFull + 2 * (j & 1) + half), land = whole ? full : bars + 8 * kBarVLand;
+      const uint32_t dst = ring + ring_slot(j, kQCols + half) * kColBytes;
       if (rows > 0 && lane == 0) {
-        csa::mbar_arrive_expect_tx(land, kVBytes / 2);
-        for (int c = 0; c < kVCols; ++c)
-          csa::tma_tile_3d(smem_u32(S.v) + c * kColBytes + half * (kColBytes / 2), &M.v, 64 * c, head,
-                           R.k0 + j * kTile + 64 * half, land);
+        csa::mbar_arrive_expect_tx(land, kColBytes);
+        for (int c = 0; c < kV / 64; ++c)
+          csa::tma_tile_3d(dst + c * (kColBytes / 2), &M.v, 64 * c, head, R.k0 + j * kTile + 64 * half, land);
       }
       if (whole) continue;
       if (rows > 0) {
         ok = ok && warp_wait(land, landed & 1, stop);
         ++landed;
       }
-      for (int c = 0; c < kVCols; ++c)
-        for (int b = max(rows, 0) * 128 + 16 * lane; b < kColBytes / 2; b += 512)
-          csa::st_shared_v4(smem_u32(S.v) + c * kColBytes + half * (kColBytes / 2) + b, 0, 0, 0, 0);
+      for (int c = 0; c < kV / 64; ++c)
+        for (int b = max(rows, 0) * 128 + 16 * lane; b < kColBytes / 2; b += 512) csa::st_shared_v4(dst + c * (kColBytes / 2) + b, 0, 0, 0, 0);
       csa::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
     }
     v_done = j + 1;
   };
-  // in the order in which the MMAs give the buffers back
+  // in the order in which the MMAs give the chunks back
+  load_q(0);
   load_k(0);
+  load_q(1);
   load_v(0);
   if (n > 1) load_k(1);
   for (int j = 1; ok && j < n; ++j) {
-    if (j + 1 < n) load_k(j + 1);
-    if (ok) load_v(j);
+    load_v(j);
+    if (ok && j + 1 < n) load_k(j + 1);
   }
-  // no copy of this CTA is in flight when it leaves
+  // no copy of this CTA is in flight when it leaves (the last waits of each barrier; after a wait that ran out, some of
+  // them end by their time limit)
   if (lane == 0) {
-    csa::mbar_wait_drain(bars + 8 * kBarQFull, 0);
+    for (int t = 0; t < 2; ++t)
+      if (nt[t] > 0) csa::mbar_wait_drain(bars + 8 * (kBarQFull + t), 0);
     for (int j = max(k_done - 2, 0); j < k_done; ++j) csa::mbar_wait_drain(bars + 8 * (kBarKFull + (j & 1)), (j >> 1) & 1);
-    if (ok) {
-      for (int half = 0; half < 2; ++half) csa::mbar_wait_drain(bars + 8 * (kBarVFull + half), (v_done - 1) & 1);
-    } else {  // gave up: whatever was begun for V lands within the time limit
-      for (int half = 0; half < 2; ++half) csa::mbar_wait_drain(bars + 8 * (kBarVFull + half), v_done & 1);
-      csa::mbar_wait_drain(bars + 8 * kBarVLand, landed & 1);
-    }
+    for (int j = max(v_done - 2, 0); j < v_done; ++j)
+      for (int half = 0; half < 2; ++half) csa::mbar_wait_drain(bars + 8 * (kBarVFull + 2 * (j & 1) + half), (j >> 1) & 1);
+    if (!ok) csa::mbar_wait_drain(bars + 8 * kBarVLand, landed & 1);
   }
   __syncwarp();
 }
 
+// One warp issues all MMAs, S0(j), O1(j - 1), S1(j), O0(j) in turn, with as few waits and commits in
+// between as the buffers need: each costs the tensor cores some 80 clocks, and a thread of its own for
+// each query tile costs more (their MMAs interleave, and every softmax waits longer for its S).
 __device__ void role_mma(const csa_latent_prefill_args& A, Smem& S, const Request& R, int first) {
   volatile int* stop = &S.abort;
-  const uint32_t bars = smem_u32(S.bars), tmem = S.tmem;
-  const int n[2] = {key_tiles(A, R, first, 0), key_tiles(A, R, first, 1)}, most = max(n[0], n[1]);
+  const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem), lead = csa::elect_lane();
+  const int n[2] = {static_cast<int>(csa::uniform(key_tiles(A, R, first, 0))), static_cast<int>(csa::uniform(key_tiles(A, R, first, 1)))};
+  const int most = max(n[0], n[1]);
   constexpr uint32_t idesc_s = csa::idesc_bf16_f32(kTile, kTile);
   constexpr uint32_t idesc_o = csa::idesc_bf16_f32(kTile, kV) | csa::kIdescBMnMajor;
   const csa::Desc q[2] = {csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.q[0]))), csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.q[1])))};
-  const csa::Desc k[2] = {csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.k[0]))), csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.k[1])))};
-  const csa::Desc v(csa::sdesc_mn_sw128_b16(smem_u32(S.v), kColBytes));
-  bool ok = most == 0 || mbar_wait(bars + 8 * kBarQFull, 0, stop);
-  auto issue_s = [&](int t, int j) {
-    const csa::Desc a = t ? q[1] : q[0], b = (j & 1) ? k[1] : k[0];
-#pragma unroll
-    for (int x = 0; x < kNope + kRope; x += 16) {
-      const uint32_t bytes = x / 64 * kColBytes + x % 64 * 2;
-      if (x == 0) csa::mma_f16_ss<false>(tmem + t * kTile, a, bytes, b, bytes, idesc_s);
-      else csa::mma_f16_ss<true>(tmem + t * kTile, a, bytes, b, bytes, idesc_s);
-    }
-    csa::mma_commit(bars + 8 * (kBarSFull + t));
+  const csa::Desc k_ring(csa::sdesc_kmajor_sw128(smem_u32(S.ring[0])));
+  const csa::Desc v_ring(csa::sdesc_mn_sw128_b16(smem_u32(S.ring[0]), kColBytes / 2));
+  bool ok = true;
+  auto need = [&](int bar, uint32_t parity) {
+    ok = ok && warp_wait(bars + 8 * bar, parity, stop);
+    csa::tc_fence_after();
   };
-  // O of tile t over key tile j; `frees`: the last to read V
-  auto issue_o = [&](int t, int j, bool frees) {
-    ok = ok && mbar_wait(bars + 8 * (kBarPFull + t), j & 1, stop);
+  // S of tile t over key tile j. `ahead` looks, while these MMAs run, whether what comes after is there.
+  auto issue_s = [&](auto tile, int j, auto ahead) {
+    constexpr int t = decltype(tile)::value;
+    if (!ok) return;
+#pragma unroll
+    for (int c = 0; c < kQCols; ++c) {
+      const csa::Desc b = k_ring.at(ring_slot(j, c) * kColBytes);
+#pragma unroll
+      for (int x = 0; x < 4; ++x)
+        csa::mma_f16_ss(lead, tmem + t * kTile, q[t].at(c * kColBytes + 32 * x), b.at(32 * x), idesc_s, c > 0 || x > 0);
+      if (c == 1) ahead();
+    }
+    csa::mma_commit_if(lead, bars + 8 * (kBarSFull + t));
+  };
+  // O of tile t over key tile j. `last_reader`: V is free afterwards
+  auto issue_o = [&](auto tile, int j, bool last_reader, auto ahead) {
+    constexpr int t = decltype(tile)::value;
+    if (!ok) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      ok = ok && mbar_wait(bars + 8 * (kBarVFull + half), j & 1, stop);
-      if (!ok) return;
-      csa::tc_fence_after();
+      const csa::Desc b = v_ring.at(ring_slot(j, kQCols + half) * kColBytes);
 #pragma unroll
-      for (int x = 64 * half; x < 64 * half + 64; x += 16) {
-        if (j == 0 && x == 0) csa::mma_f16_ts<false>(tmem + kTmemO + t * kTile, tmem + t * kTile + x / 2, v, x * 128, idesc_o);
-        else csa::mma_f16_ts<true>(tmem + kTmemO + t * kTile, tmem + t * kTile + x / 2, v, x * 128, idesc_o);
-      }
-      if (frees) csa::mma_commit(bars + 8 * (kBarVEmpty + half));
+      for (int x = 0; x < 4; ++x)
+        csa::mma_f16_ts(lead, tmem + kTmemO + t * kTile, tmem + t * kTile + 32 * half + 8 * x, b.at(2048 * x), idesc_o,
+                        j > 0 || half > 0 || x > 0);
+      if (half == 0) ahead();
     }
-    if (j + 1 == n[t]) csa::mma_commit(bars + 8 * (kBarOFull + t));
+    if (last_reader) csa::mma_commit_if(lead, bars + 8 * (kBarVEmpty + (j & 1)));
+    if (j + 1 == n[t]) csa::mma_commit_if(lead, bars + 8 * (kBarOFull + t));
   };
-  for (int j = 0; ok && j < most; ++j) {
-    ok = mbar_wait(bars + 8 * (kBarKFull + (j & 1)), (j >> 1) & 1, stop);
-    if (!ok) break;
+  const std::integral_constant<int, 0> t0;
+  const std::integral_constant<int, 1> t1;
+  const auto nothing = [] {};
+  // What O of tile t over key tile j needs. A first look that finds it costs nothing: MMAs are still queued.
+  auto there = [&](int bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xFFFFFFFFu, csa::mbar_test(bars + 8 * bar, parity))); };
+  auto look_o = [&](int t, int j) {
+    const bool all = there(kBarPFull + t, j & 1) && there(kBarVFull + 2 * (j & 1), (j >> 1) & 1) && there(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
     csa::tc_fence_after();
-    if (j < n[0]) issue_s(0, j);
-    if (j > 0 && j - 1 < n[1]) issue_o(1, j - 1, true);
-    if (!ok) break;
-    if (j < n[1]) issue_s(1, j);
-    csa::mma_commit(bars + 8 * (kBarKEmpty + (j & 1)));
-    if (j < n[0]) issue_o(0, j, j >= n[1]);
+    return all;
+  };
+  auto need_o = [&](int t, int j, bool seen) {
+    if (seen) return;
+    need(kBarVFull + 2 * (j & 1), (j >> 1) & 1);
+    need(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
+    need(kBarPFull + t, j & 1);
+  };
+  if (most > 0) need(kBarKFull, 0);
+  if (n[0] > 0) need(kBarQFull, 0);
+  for (int j = 0; ok && j < most; ++j) {
+    const bool s0 = j < n[0], s1 = j < n[1], o1 = j > 0 && j - 1 < n[1];
+    bool seen1 = false, seen0 = false, seen_k = false;
+    if (s0)
+      issue_s(t0, j, [&] {
+        if (o1) seen1 = look_o(1, j - 1);
+      });
+    if (o1) {
+      need_o(1, j - 1, seen1);
+      issue_o(t1, j - 1, true, nothing);
+    }
+    if (j == 0 && s1) need(kBarQFull + 1, 0);
+    if (s1)
+      issue_s(t1, j, [&] {
+        if (s0) seen0 = look_o(0, j);
+      });
+    csa::mma_commit_if(lead, bars + 8 * (kBarKEmpty + (j & 1)));
+    const int k_bar = kBarKFull + ((j + 1) & 1);
+    const uint32_t k_parity = ((j + 1) >> 1) & 1;
+    if (s0) {
+      need_o(0, j, seen0);
+      issue_o(t0, j, !s1, [&] {
+        if (j + 1 < most) {
+          seen_k = there(k_bar, k_parity);
+          csa::tc_fence_after();
+        }
+      });
+    }
+    if (j + 1 < most && !seen_k) need(k_bar, k_parity);
   }
-  if (ok && n[1] == most && most > 0) issue_o(1, most - 1, true);
-  csa::mma_commit(bars + 8 * kBarDrain);
+  if (ok && n[1] == most && most > 0) {
+    need_o(1, most - 1, false);
+    issue_o(t1, most - 1, true, nothing);
+  }
+  csa::mma_commit_if(lead, bars + 8 * kBarDrain);  // nothing of this thread's is in flight when it leaves
   csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
 }
 
@@ -312,22 +377,34 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
       }
     }
     const float mc = m == -INFINITY ? 0.f : m * c;
-    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    const csa::F2 c2(c, c), mc2(-mc, -mc);
+    csa::F2 sum[4];
+    // the exponentials of 32 keys ahead of the rounding of the 32 before them
+    auto exps = [&](int k) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      uint32_t w[32];
+      for (int x = 0; x < 32; x += 2) {
+        csa::fma2(csa::F2(s[k][x], s[k][x + 1]), c2, mc2).get(s[k][x], s[k][x + 1]);
+        s[k][x] = csa::ex2(s[k][x]);
+        s[k][x + 1] = csa::ex2(s[k][x + 1]);
+      }
+    };
+    exps(0);
 #pragma unroll
-      for (int x = 0; x < 64; x += 2) {
-        const float p0 = csa::ex2(fmaf(s[2 * k + x / 32][x % 32], c, -mc));
-        const float p1 = csa::ex2(fmaf(s[2 * k + x / 32][x % 32 + 1], c, -mc));
-        sum[x / 2 % 4] += p0 + p1;
+    for (int k = 0; k < 4; ++k) {
+      if (k < 3) exps(k + 1);
+      uint32_t w[16];
+#pragma unroll
+      for (int x = 0; x < 32; x += 2) {
+        sum[x / 2 % 4] = csa::add2(sum[x / 2 % 4], csa::F2(s[k][x], s[k][x + 1]));
         // rounded to bf16 here, the tensor cores' operand type; l sums p unrounded
-        const __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
+        const __nv_bfloat162 two = __floats2bfloat162_rn(s[k][x], s[k][x + 1]);
         w[x / 2] = *reinterpret_cast<const uint32_t*>(&two);
       }
-      csa::tmem_st32(s_at + 32 * k, w);
+      csa::tmem_st16(s_at + 16 * k, w);
     }
-    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+    float l0, l1;
+    csa::add2(csa::add2(sum[0], sum[1]), csa::add2(sum[2], sum[3])).get(l0, l1);
+    l += l0 + l1;
     csa::tmem_wait_st();
     csa::tc_fence_before();
     __syncwarp();
@@ -339,7 +416,9 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
   const bool there = row < R.nq;
   const int64_t at = static_cast<int64_t>(R.q0 + row) * A.num_heads + head;
   if (there && A.lse) A.lse[at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(A.out) + (there ? at : 0) * kV);
+  // through this tile's Q (its last S is done), so that a row is written as 256 contiguous bytes: row r of the warp at 256 r, its
+  // 16-byte chunks exchanged by r so that neither side has lanes on one bank
+  const uint32_t stage = smem_u32(S.q[t]) + warp * 32 * 256;
 #pragma unroll 1
   for (int k = 0; k < kV; k += 32) {
     uint32_t v[32] = {};
@@ -347,19 +426,29 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
       csa::tmem_ld32(o_at + k, v);
       csa::tmem_wait_ld();
     }
-    if (there) {
 #pragma unroll
-      for (int x = 0; x < 32; x += 8) {
-        uint32_t w[4];
+    for (int x = 0; x < 32; x += 8) {
+      uint32_t w[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const __nv_bfloat162 two =
-              __floats2bfloat162_rn(__uint_as_float(v[x + 2 * y]) * inv, __uint_as_float(v[x + 2 * y + 1]) * inv);
-          w[y] = *reinterpret_cast<const uint32_t*>(&two);
-        }
-        out[(k + x) / 8] = make_uint4(w[0], w[1], w[2], w[3]);
+      for (int y = 0; y < 4; ++y) {
+        const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(v[x + 2 * y]) * inv, __uint_as_float(v[x + 2 * y + 1]) * inv);
+        w[y] = *reinterpret_cast<const uint32_t*>(&two);
       }
+      csa::st_shared_v4(stage + lane * 256 + ((((k + x) / 8) ^ (lane & 15)) << 4), w[0], w[1], w[2], w[3]);
     }
+  }
+  __syncwarp();
+  const int rows = min(32, R.nq - (first + t * kTile + 32 * warp));  // of this warp's
+  uint8_t* out = static_cast<uint8_t*>(A.out) +
+                 2 * ((static_cast<int64_t>(R.q0 + first + t * kTile + 32 * warp) * A.num_heads + head) * kV) + 16 * (lane & 15);
+#pragma unroll 4
+  for (int r = lane >> 4; r < rows; r += 2) {
+    uint4 x;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                 : "r"(stage + r * 256 + (((lane & 15) ^ (r & 15)) << 4))
+                 : "memory");
+    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * A.num_heads * (2 * kV)) = x;
   }
 }
 
@@ -378,13 +467,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   request_of(A, S.request, &R);
   const int first = S.first;
   if (threadIdx.x == 0) {
-    csa::mbar_init(bars + 8 * kBarQFull, 1);
     csa::mbar_init(bars + 8 * kBarVLand, 1);
     csa::mbar_init(bars + 8 * kBarDrain, 1);
     for (int k = 0; k < 2; ++k) {
+      csa::mbar_init(bars + 8 * (kBarQFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarKFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarKEmpty + k), 1);
-      csa::mbar_init(bars + 8 * (kBarVFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarVFull + 2 * k), 1);
+      csa::mbar_init(bars + 8 * (kBarVFull + 2 * k + 1), 1);
       csa::mbar_init(bars + 8 * (kBarVEmpty + k), 1);
       csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarPFull + k), 4);
@@ -403,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < kSoftmaxWarps) {
     role_softmax(A, S, R, first, head);
   } else if (warp == kMmaWarp) {
-    if (lane == 0) role_mma(A, S, R, first);
+    role_mma(A, S, R, first);
     __syncwarp();
   } else {
     role_load(A, M, S, R, first, head);

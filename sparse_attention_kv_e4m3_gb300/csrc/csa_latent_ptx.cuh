@@ -35,53 +35,61 @@ __device__ __forceinline__ uint64_t sdesc_mn_sw128_b16(uint32_t saddr, uint32_t 
   return d;
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, one CTA, kind::f16 (K = 16 per call). The descriptors' low
-// words (where the address is) and high words are apart, so that stepping through an operand is one
-// addition: the issuing thread's own instructions take as long as a small MMA (measured: 66 clocks a
-// 128 x 64 MMA with descriptors built for each, 48 with them stepped).
-struct Desc {
-  uint32_t lo, hi;
-  __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
-};
-
-template <bool kAccumulate>
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_bytes, Desc b, uint32_t b_bytes,
-                                           uint32_t idesc) {
-  if constexpr (kAccumulate)
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.eq.u32 p, 0, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc)
-        : "memory");
-  else
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-        "setp.ne.u32 p, 0, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-        "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc)
-        : "memory");
+// One lane of the warp (always the same while the warp is whole).
+__device__ __forceinline__ uint32_t elect_lane() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xFFFFFFFF;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r;
 }
 
-__device__ __forceinline__ void mma_f16_ss(uint32_t d_tmem, Desc a, uint32_t a_bytes, Desc b, uint32_t b_bytes,
-                                           uint32_t idesc, bool accumulate) {
+// What the compiler is to know is the same in all lanes.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xFFFFFFFFu, x, 0); }
+
+// MMAs are issued by whole warps with only the instruction itself predicated on one lane (`lead`), so that
+// addresses and descriptors stay in the warp's uniform registers, where the instruction takes them from: in
+// a branch that one lane takes alone each MMA costs several register moves, and with busy warps beside
+// it the thread took 90 clocks a 128 x 128 x 16 MMA, of which the tensor core needs 64.
+struct Desc {  // an operand's descriptor, its low word (where the address is) apart
+  uint32_t lo, hi;
+  __device__ __forceinline__ explicit Desc(uint64_t d) : lo(static_cast<uint32_t>(d)), hi(static_cast<uint32_t>(d >> 32)) {}
+  __device__ __forceinline__ Desc at(uint32_t bytes) const {
+    Desc r = *this;
+    r.lo += bytes >> 4;
+    return r;
+  }
+};
+
+// D[tmem] (+)= A[smem] * B[smem]^T, one CTA, kind::f16 (K = 16 per call).
+__device__ __forceinline__ void mma_f16_ss(uint32_t lead, uint32_t d_tmem, Desc a, Desc b, uint32_t idesc, bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
-      "r"(a.lo + (a_bytes >> 4)), "r"(a.hi), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc),
-      "r"(static_cast<uint32_t>(accumulate))
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 q, %7, 0;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d_tmem),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead)
       : "memory");
 }
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: A's 16 values of a step are 8 columns, two bf16 a column.
-template <bool kAccumulate>
-__device__ __forceinline__ void mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t b_bytes, uint32_t idesc) {
+__device__ __forceinline__ void mma_f16_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, Desc b, uint32_t idesc,
+                                           bool accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "setp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "r"(b.lo + (b_bytes >> 4)), "r"(b.hi), "r"(idesc), "n"(kAccumulate ? 1 : 0)
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.u32 q, %6, 0;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead)
+      : "memory");
+}
+
+// mma_commit by the lane that issued the MMAs.
+__device__ __forceinline__ void mma_commit_if(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+      "r"(lead)
       : "memory");
 }
 
@@ -100,6 +108,19 @@ __device__ __forceinline__ void tma_tile_2d(uint32_t dst, const void* tmap, int3
           dst),
       "l"(tmap), "r"(x), "r"(y), "r"(bar)
       : "memory");
+}
+
+// Whether the phase is complete now, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
 }
 
 // ----------------------------------------------------------------- clusters
@@ -122,6 +143,25 @@ __device__ __forceinline__ float ld_peer_f32(uint32_t addr) {
 
 __device__ __forceinline__ void st_peer_v4(uint32_t addr, float a, float b, float c, float d) {
   asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(a), "f"(b), "f"(c), "f"(d) : "memory");
+}
+
+// ----------------------------------------------------------------- pairs of fp32
+
+struct F2 {
+  uint64_t v;
+  __device__ __forceinline__ F2() : v(0) {}
+  __device__ __forceinline__ F2(float a, float b) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(a), "f"(b)); }
+  __device__ __forceinline__ void get(float& a, float& b) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+};
+__device__ __forceinline__ F2 fma2(F2 a, F2 b, F2 c) {
+  F2 r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
+__device__ __forceinline__ F2 add2(F2 a, F2 b) {
+  F2 r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
 }
 
 // 2^x: 2^-22 relative error, subnormal results become 0, 2^-infinity is 0.
@@ -180,6 +220,16 @@ __device__ __forceinline__ void st_global_if(bool on, void* p, uint32_t v) {
 }
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
+// 32 lanes x 32 bits, 16 consecutive columns: thread t writes lane (base + t).
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16};" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+      "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+      : "memory");
+}
 
 // Four 8 x 8 matrices of 16-bit elements to shared memory: lanes 8 k .. 8 k + 7 give the row
 // addresses of matrix k; a lane holds row lane / 4, columns 2 (lane % 4) and the next of each.
