@@ -979,12 +979,10 @@ int cluster_of(const csa_latent_attend_args* a, int sms) {
 }
 
 template <bool kFp4, int kRope>
-csa_status launch(const Kernel& K, int grid, cudaStream_t stream) {
-  static bool ready[64];  // the kernel's shared memory size is set on each device once
+csa_status launch(const Kernel& K, int grid, int dev, cudaStream_t stream) {
+  static bool ready[kMaxDevices];  // the kernel's shared memory size is set on each device once
   constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
   static_assert(smem + 256 <= 232448, "shared memory of one CTA");
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA_ERR_CUDA;
   if (!ready[dev]) {
     if (cudaFuncSetAttribute(attend_kernel<kFp4, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
@@ -1045,8 +1043,8 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   const int groups = (a->num_heads + kHeads - 1) / kHeads;
   const int64_t units = static_cast<int64_t>(a->num_q) * groups;
   if (units > INT32_MAX) return CSA_ERR_INVALID_ARG;
-  int sms = 0;
-  if (sm_count(&sms) != CSA_OK) return CSA_ERR_CUDA;
+  int sms = 0, dev = 0;
+  if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
   Kernel K;
   K.A = *a;
   K.cluster = cluster_of(a, sms);
@@ -1058,8 +1056,8 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kOpenBytes);
   const auto s = static_cast<cudaStream_t>(stream);
   const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
-  const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, s) : launch<true, 0>(K, grid, s))
-                            : (rope ? launch<false, 64>(K, grid, s) : launch<false, 0>(K, grid, s));
+  const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, dev, s) : launch<true, 0>(K, grid, dev, s))
+                            : (rope ? launch<false, 64>(K, grid, dev, s) : launch<false, 0>(K, grid, dev, s));
   if (ls != CSA_OK || grid == 1 || K.cluster) return ls;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, a->num_heads < kHeads ? a->num_heads : kHeads);

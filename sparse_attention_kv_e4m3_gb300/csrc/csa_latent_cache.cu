@@ -153,9 +153,9 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
 
 // ------------------------------------------------------------- writer
 //
-// A warp stores a row: lane l holds the 16 latent values 16 l .. 16 l + 15 (half a
-// 32-value block, so a block's amax takes one exchange with the neighbour lane)
-// and the rope values 2 l, 2 l + 1. Rows are read once, coalesced; bound by HBM.
+// A warp stores kRowsInFlight rows at a time, their loads all issued first: lane l holds the 16 latent
+// values 16 l .. 16 l + 15 (half a 32-value block, so a block's amax takes one exchange with the
+// neighbour lane) and the rope values 2 l, 2 l + 1. Rows are read once, coalesced. Bound by HBM.
 
 constexpr int kCopyThreads = 256;
 
@@ -210,140 +210,219 @@ __device__ __forceinline__ uint32_t nonfinite_bf16x2(uint32_t w) {
 }
 
 template <bool kBf16In, bool kFp4>
+__device__ __forceinline__ int32_t store_row(const csa_latent_write_args& A, const RowIn<kBf16In>& x, int64_t slot, int lane) {
+  if (slot == -1) return 0;
+  if (slot < 0 || slot >= A.cache.num_pages * kPageRecs) return CSA_DEV_PAGE_OOB;
+  const int rope = A.cache.rope_dim, rec_bytes = record_bytes(kFp4, rope);
+  uint8_t* rec = A.cache.pages + (slot / kPageRecs) * A.cache.page_stride_bytes + (slot % kPageRecs) * rec_bytes;
+  const uint32_t rope_word = pack_bf16(x.r[0], x.r[1]);
+  uint32_t bad = nonfinite_bf16x2(rope_word);
+  if constexpr (!kFp4) {
+    uint32_t w[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      w[k] = pack_bf16(x.v[2 * k], x.v[2 * k + 1]);
+      bad |= nonfinite_bf16x2(w[k]);
+    }
+    if (__any_sync(0xFFFFFFFFu, bad)) return CSA_DEV_RANGE;
+    uint4* p = reinterpret_cast<uint4*>(rec) + 2 * lane;
+    p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  } else {
+    uint32_t amax = 0;  // magnitude bits order like the magnitudes
+#pragma unroll
+    for (int k = 0; k < 16; ++k) amax = max(amax, __float_as_uint(x.v[k]) & 0x7FFFFFFFu);
+    bad |= amax >= 0x7F800000u;
+    if (__any_sync(0xFFFFFFFFu, bad)) return CSA_DEV_RANGE;
+    amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
+    // floor(log2 amax) - 2, held at -127: a subnormal amax (below 2^-126) lands there too
+    const int e = max(static_cast<int>(amax >> 23) - 129, -127);
+    // 2^-e is 2^-125 .. 2^127, a normal number; x 2^-e is exact where it can reach a nonzero code
+    const float up = __uint_as_float(static_cast<uint32_t>(min(-e, 127) + 127) << 23);
+    uint32_t code[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      code[h] = 0;
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        code[h] |= e2m1_pair(x.v[8 * h + 2 * k] * up, x.v[8 * h + 2 * k + 1] * up) << (8 * k);
+    }
+    reinterpret_cast<uint2*>(rec)[lane] = make_uint2(code[0], code[1]);
+    // four blocks' scale bytes gathered into one word by lanes 0, 8, 16, 24
+    uint32_t sb = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 1) & 3));
+    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
+    sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 4);
+    if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(rec + kCodeBytes)[lane >> 3] = sb;
+  }
+  if (rope) reinterpret_cast<uint32_t*>(rec + rec_bytes - 2 * rope)[lane] = rope_word;
+  return 0;
+}
+
+template <bool kBf16In, bool kFp4>
 __global__ void __launch_bounds__(kCopyThreads) latent_write_kernel(const csa_latent_write_args A) {
-  const int lane = threadIdx.x & 31, rope = A.cache.rope_dim;
+  constexpr int kRowsInFlight = kBf16In ? 4 : 2;
+  const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32);
-  const int64_t slots = A.cache.num_pages * kPageRecs;
-  const int rec_bytes = record_bytes(kFp4, rope);
   int32_t flags = 0;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; i < A.n; i += warps) {
-    const int64_t slot = A.slots[i];
-    RowIn<kBf16In> x;
-    x.load(static_cast<const uint8_t*>(A.x) + i * A.x_stride * (kBf16In ? 2 : 4), lane, rope);
-    if (slot == -1) continue;
-    if (slot < 0 || slot >= slots) {
-      flags |= CSA_DEV_PAGE_OOB;
-      continue;
+  // rows warp, warp + warps, ...: a small call spreads over the SMs
+  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; i < A.n; i += kRowsInFlight * warps) {
+    int64_t slot[kRowsInFlight];
+    RowIn<kBf16In> x[kRowsInFlight];
+#pragma unroll
+    for (int k = 0; k < kRowsInFlight; ++k) {
+      const int64_t r = i + k * warps, at = r < A.n ? r : i;
+      slot[k] = r < A.n ? A.slots[r] : -1;
+      x[k].load(static_cast<const uint8_t*>(A.x) + at * A.x_stride * (kBf16In ? 2 : 4), lane, A.cache.rope_dim);
     }
-    uint8_t* rec = A.cache.pages + (slot / kPageRecs) * A.cache.page_stride_bytes + (slot % kPageRecs) * rec_bytes;
-    const uint32_t rope_word = pack_bf16(x.r[0], x.r[1]);
-    uint32_t bad = nonfinite_bf16x2(rope_word);
-    if constexpr (!kFp4) {
-      uint32_t w[8];
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        w[k] = pack_bf16(x.v[2 * k], x.v[2 * k + 1]);
-        bad |= nonfinite_bf16x2(w[k]);
-      }
-      if (__any_sync(0xFFFFFFFFu, bad)) {
-        flags |= CSA_DEV_RANGE;
-        continue;
-      }
-      uint4* p = reinterpret_cast<uint4*>(rec) + 2 * lane;
-      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-    } else {
-      uint32_t amax = 0;  // magnitude bits order like the magnitudes
-#pragma unroll
-      for (int k = 0; k < 16; ++k) amax = max(amax, __float_as_uint(x.v[k]) & 0x7FFFFFFFu);
-      bad |= amax >= 0x7F800000u;
-      if (__any_sync(0xFFFFFFFFu, bad)) {
-        flags |= CSA_DEV_RANGE;
-        continue;
-      }
-      amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      // floor(log2 amax) - 2, held at -127: a subnormal amax (below 2^-126) lands there too
-      const int e = max(static_cast<int>(amax >> 23) - 129, -127);
-      // 2^-e is 2^-125 .. 2^127, a normal number; x 2^-e is exact where it can reach a nonzero code
-      const float up = __uint_as_float(static_cast<uint32_t>(min(-e, 127) + 127) << 23);
-      uint32_t code[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        code[h] = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          code[h] |= e2m1_pair(x.v[8 * h + 2 * k] * up, x.v[8 * h + 2 * k + 1] * up) << (8 * k);
-      }
-      reinterpret_cast<uint2*>(rec)[lane] = make_uint2(code[0], code[1]);
-      // four blocks' scale bytes gathered into one word by lanes 0, 8, 16, 24
-      uint32_t sb = static_cast<uint32_t>(e + 127) << (8 * ((lane >> 1) & 3));
-      sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 2);
-      sb |= __shfl_xor_sync(0xFFFFFFFFu, sb, 4);
-      if ((lane & 7) == 0) reinterpret_cast<uint32_t*>(rec + kCodeBytes)[lane >> 3] = sb;
-    }
-    if (rope) reinterpret_cast<uint32_t*>(rec + rec_bytes - 2 * rope)[lane] = rope_word;
+    for (int k = 0; k < kRowsInFlight; ++k) flags |= store_row<kBf16In, kFp4>(A, x[k], slot[k], lane);
   }
   if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
 }
 
 // ------------------------------------------------------------- reader
+//
+// A warp reads kReadRows neighbouring rows at a time: lane r < kReadRows finds row r's record (its request by
+// bisection, its page), then all lanes copy, many 16-byte pieces in flight. Bound by HBM.
 
-template <bool kFp4>
+constexpr int kReadRows = 8;
+
+// Row i's record: 0 where no request covers the row, 1 where the row becomes zeros.
+__device__ __forceinline__ uintptr_t record_of_row(const csa_latent_read_args& A, int64_t i, int rec_bytes, int32_t* flags) {
+  if (i >= A.n_rows) return 0;
+  int lo = 0, hi = A.num_req;  // the last request that starts at or before row i
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (A.kv_start[mid] <= i) lo = mid;
+    else hi = mid;
+  }
+  const int64_t begin = A.kv_start[lo], end = A.kv_start[lo + 1], pos = i - begin;
+  if (begin < 0 || i < begin || i >= end) return 0;
+  if (pos >= static_cast<int64_t>(kPageRecs) * A.pt_stride) {
+    *flags |= CSA_DEV_LEN_OOB;
+    return 1;
+  }
+  const int32_t page = A.page_table[static_cast<int64_t>(lo) * A.pt_stride + pos / kPageRecs];
+  if (page < 0 || page >= A.cache.num_pages) {
+    *flags |= CSA_DEV_PAGE_OOB;
+    return 1;
+  }
+  return reinterpret_cast<uintptr_t>(A.cache.pages + page * A.cache.page_stride_bytes + (pos % kPageRecs) * rec_bytes);
+}
+
+// bf16 records: 16 bytes to 16 bytes.
+template <int kRope>
+__device__ __forceinline__ void copy_rows(uintptr_t mine, uint8_t* out, int lane) {
+  constexpr int kChunks = 2 * (kDim + kRope) / 16, kAll = kReadRows * kChunks / 32, kBatch = kAll / 2;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uint4 w[kBatch];
+    uintptr_t rec[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int at = 32 * (kBatch * b + k) + lane;
+      rec[k] = __shfl_sync(0xFFFFFFFFu, mine, at / kChunks);
+      w[k] = rec[k] > 1 ? __ldg(reinterpret_cast<const uint4*>(rec[k]) + at % kChunks) : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k)
+      if (rec[k]) reinterpret_cast<uint4*>(out)[32 * (kBatch * b + k) + lane] = w[k];
+  }
+}
+
+// MXFP4 records: lane l decodes values 16 l .. 16 l + 15 and rope values 2 l, 2 l + 1.
+template <int kRope>
+__device__ __forceinline__ void decode_rows(uintptr_t mine, uint8_t* out, int lane) {
+  constexpr int kBatch = kReadRows / 2;
+#pragma unroll
+  for (int b = 0; b < 2; ++b) {
+    uintptr_t rec[kBatch];
+    uint2 code[kBatch];
+    uint32_t scale[kBatch], rope[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      rec[k] = __shfl_sync(0xFFFFFFFFu, mine, kBatch * b + k);
+      const uint8_t* p = reinterpret_cast<const uint8_t*>(rec[k]);
+      const bool live = rec[k] > 1;
+      code[k] = live ? __ldg(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0, 0);
+      scale[k] = live ? __ldg(p + kCodeBytes + (lane >> 1)) : 0u;
+      rope[k] = live && kRope != 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + kCodeBytes + kScaleBytes) + lane) : 0u;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (!rec[k]) continue;
+      const float s = ue8m0(scale[k]);
+      uint32_t w[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const uint32_t byte = ((j < 4 ? code[k].x : code[k].y) >> (8 * (j & 3))) & 0xFFu;
+        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+        w[j] = pack_bf16(v.x * s, v.y * s);  // exact: two significant bits times a power of two
+      }
+      uint8_t* row = out + (kBatch * b + k) * (2 * (kDim + kRope));
+      uint4* p = reinterpret_cast<uint4*>(row) + 2 * lane;
+      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
+      if (kRope != 0) reinterpret_cast<uint32_t*>(row)[kDim / 2 + lane] = rope[k];
+    }
+  }
+}
+
+template <bool kFp4, int kRope>
 __global__ void __launch_bounds__(kCopyThreads) latent_read_kernel(const csa_latent_read_args A) {
-  const int lane = threadIdx.x & 31, rope = A.cache.rope_dim;
-  const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32);
-  const int rec_bytes = record_bytes(kFp4, rope), row_bytes = 2 * (kDim + rope);
+  const int lane = threadIdx.x & 31;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32) * kReadRows;
   int32_t flags = 0;
   for (int64_t r = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; r < A.num_req;
        r += static_cast<int64_t>(gridDim.x) * kCopyThreads)
     if (A.kv_start[r] < 0 || A.kv_start[r + 1] < A.kv_start[r]) flags |= CSA_DEV_LEN_OOB;
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; i < A.n_rows; i += warps) {
-    int lo = 0, hi = A.num_req;  // the last request that starts at or before row i
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (A.kv_start[mid] <= i) lo = mid;
-      else hi = mid;
-    }
-    const int64_t begin = A.kv_start[lo], end = A.kv_start[lo + 1];
-    if (begin < 0 || i < begin || i >= end) continue;
-    const int64_t pos = i - begin;
-    const uint8_t* rec = nullptr;
-    if (pos >= static_cast<int64_t>(kPageRecs) * A.pt_stride) {
-      flags |= CSA_DEV_LEN_OOB;
-    } else {
-      const int32_t page = A.page_table[static_cast<int64_t>(lo) * A.pt_stride + pos / kPageRecs];
-      if (page < 0 || page >= A.cache.num_pages) flags |= CSA_DEV_PAGE_OOB;
-      else rec = A.cache.pages + page * A.cache.page_stride_bytes + (pos % kPageRecs) * rec_bytes;
-    }
-    uint8_t* out = static_cast<uint8_t*>(A.out) + i * row_bytes;
-    if constexpr (!kFp4) {
-      for (int k = lane; k < row_bytes / 16; k += 32)
-        reinterpret_cast<uint4*>(out)[k] = rec ? reinterpret_cast<const uint4*>(rec)[k] : make_uint4(0, 0, 0, 0);
-    } else {
-      uint32_t w[8] = {};
-      uint32_t rope_word = 0;
-      if (rec) {
-        const uint2 c = reinterpret_cast<const uint2*>(rec)[lane];
-        const float s = ue8m0(rec[kCodeBytes + (lane >> 1)]);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-          const uint32_t byte = ((k < 4 ? c.x : c.y) >> (8 * (k & 3))) & 0xFFu;
-          const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
-          w[k] = pack_bf16(v.x * s, v.y * s);  // exact: two significant bits times a power of two
-        }
-        if (rope) rope_word = reinterpret_cast<const uint32_t*>(rec + kCodeBytes + kScaleBytes)[lane];
-      }
-      uint4* p = reinterpret_cast<uint4*>(out) + 2 * lane;
-      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      if (rope) reinterpret_cast<uint32_t*>(out)[kDim / 2 + lane] = rope_word;
-    }
+  for (int64_t i = ((static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5) * kReadRows; i < A.n_rows; i += step) {
+    const uintptr_t mine = lane < kReadRows ? record_of_row(A, i + lane, record_bytes(kFp4, kRope), &flags) : 0;
+    uint8_t* out = static_cast<uint8_t*>(A.out) + i * (2 * (kDim + kRope));
+    if constexpr (kFp4) decode_rows<kRope>(mine, out, lane);
+    else copy_rows<kRope>(mine, out, lane);
   }
   flags = static_cast<int32_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(flags)));
   if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
 }
 
-// One full wave of blocks at most, each taking `per_block` rows at a time.
+// At most one full wave of blocks, each taking `per_block` rows at a time. `kept` (or null): the kernel's resident
+// blocks an SM on each device, asked for once.
 template <typename K>
-csa_status wave_grid(K kernel, int threads, size_t smem, int64_t rows, int64_t per_block, unsigned* grid) {
-  int sms = 0, per_sm = 0;
-  if (sm_count(&sms) != CSA_OK ||
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
-    return CSA_ERR_CUDA;
+csa_status wave_grid(K kernel, int threads, size_t smem, int* kept, int64_t rows, int64_t per_block, unsigned* grid) {
+  int sms = 0, dev = 0;
+  if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
+  int per_sm = kept ? kept[dev] : 0;
+  if (per_sm == 0) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
+      return CSA_ERR_CUDA;
+    if (kept) kept[dev] = per_sm;
+  }
   const int64_t want = (rows + per_block - 1) / per_block, cap = static_cast<int64_t>(sms) * per_sm;
   *grid = static_cast<unsigned>(want < 1 ? 1 : (want < cap ? want : cap));
   return CSA_OK;
+}
+
+template <bool kBf16In, bool kFp4>
+csa_status launch_write(const csa_latent_write_args& a, cudaStream_t stream) {
+  static int kept[kMaxDevices];
+  unsigned grid = 1;
+  const csa_status st = wave_grid(latent_write_kernel<kBf16In, kFp4>, kCopyThreads, 0, kept, a.n, kCopyThreads / 32, &grid);
+  if (st != CSA_OK) return st;
+  latent_write_kernel<kBf16In, kFp4><<<grid, kCopyThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+template <bool kFp4, int kRope>
+csa_status launch_read(const csa_latent_read_args& a, cudaStream_t stream) {
+  static int kept[kMaxDevices];
+  unsigned grid = 1;
+  const csa_status st =
+      wave_grid(latent_read_kernel<kFp4, kRope>, kCopyThreads, 0, kept, a.n_rows, kCopyThreads / 32 * kReadRows, &grid);
+  if (st != CSA_OK) return st;
+  latent_read_kernel<kFp4, kRope><<<grid, kCopyThreads, 0, stream>>>(a);
+  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
 }  // namespace
@@ -376,9 +455,10 @@ extern "C" csa_status csa_build_tables(const csa_tables_args* a, void* stream) {
   if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess)
     return CSA_ERR_CUDA;
+  static int kept[kMaxDevices];  // of calls of up to about 1000 requests
   unsigned grid = 1;
-  const csa_status st =
-      wave_grid(build_tables_kernel, kTabThreads, smem, a->n_rows + a->num_req, kTabRowsPerBlock, &grid);
+  const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 8192 ? 8192 : smem, smem <= 8192 ? kept : nullptr,
+                                  a->n_rows + a->num_req, kTabRowsPerBlock, &grid);
   if (st != CSA_OK) return st;
   build_tables_kernel<<<grid, kTabThreads, smem, static_cast<cudaStream_t>(stream)>>>(*a);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
@@ -395,13 +475,9 @@ extern "C" csa_status csa_latent_write(const csa_latent_write_args* a, void* str
   if (!aligned(a->x, 16) || a->x_stride % (bf16 ? 8 : 4) != 0 || !aligned(a->slots, 8) || !aligned(a->dev_status, 4))
     return CSA_ERR_ALIGNMENT;
   const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4;
-  const auto kernel = bf16 ? (fp4 ? latent_write_kernel<true, true> : latent_write_kernel<true, false>)
-                           : (fp4 ? latent_write_kernel<false, true> : latent_write_kernel<false, false>);
-  unsigned grid = 1;
-  const csa_status gs = wave_grid(kernel, kCopyThreads, 0, a->n, kCopyThreads / 32, &grid);
-  if (gs != CSA_OK) return gs;
-  kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  const auto s = static_cast<cudaStream_t>(stream);
+  if (bf16) return fp4 ? launch_write<true, true>(*a, s) : launch_write<true, false>(*a, s);
+  return fp4 ? launch_write<false, true>(*a, s) : launch_write<false, false>(*a, s);
 }
 
 extern "C" csa_status csa_latent_read(const csa_latent_read_args* a, void* stream) {
@@ -414,10 +490,8 @@ extern "C" csa_status csa_latent_read(const csa_latent_read_args* a, void* strea
     return CSA_ERR_INVALID_ARG;
   if (!aligned(a->page_table, 4) || !aligned(a->kv_start, 4) || !aligned(a->out, 16) || !aligned(a->dev_status, 4))
     return CSA_ERR_ALIGNMENT;
-  const auto kernel = a->cache.record_format == CSA_LATENT_MXFP4 ? latent_read_kernel<true> : latent_read_kernel<false>;
-  unsigned grid = 1;
-  const csa_status gs = wave_grid(kernel, kCopyThreads, 0, a->n_rows, kCopyThreads / 32, &grid);
-  if (gs != CSA_OK) return gs;
-  kernel<<<grid, kCopyThreads, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  const auto s = static_cast<cudaStream_t>(stream);
+  if (a->cache.record_format == CSA_LATENT_MXFP4)
+    return a->cache.rope_dim ? launch_read<true, 64>(*a, s) : launch_read<true, 0>(*a, s);
+  return a->cache.rope_dim ? launch_read<false, 64>(*a, s) : launch_read<false, 0>(*a, s);
 }

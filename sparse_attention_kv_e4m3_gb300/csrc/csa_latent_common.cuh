@@ -38,11 +38,21 @@ inline csa_status check_cache(const csa_latent_cache& c) {
   return CSA_OK;
 }
 
-inline csa_status sm_count(int* sms) {
+// The current device and its SM count (which is asked for once a device and kept, like a kernel's occupancy:
+// each query costs about a microsecond of a small call).
+constexpr int kMaxDevices = 64;
+
+inline csa_status sm_count(int* sms, int* device = nullptr) {
+  static int kept[kMaxDevices];  // 0: not asked yet; two threads may both ask, with the same answer
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || *sms < 1)
-    return CSA_ERR_CUDA;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return CSA_ERR_CUDA;
+  int n = kept[dev];
+  if (n == 0) {
+    if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return CSA_ERR_CUDA;
+    kept[dev] = n;
+  }
+  *sms = n;
+  if (device) *device = dev;
   return CSA_OK;
 }
 

@@ -270,21 +270,22 @@ __device__ void role_mma(const csa_latent_prefill_args& A, Smem& S, const Reques
   // What O of tile t over key tile j needs. A first look that finds it costs nothing: MMAs are still queued.
   auto there = [&](int bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xFFFFFFFFu, csa::mbar_test(bars + 8 * bar, parity))); };
   auto look_o = [&](int t, int j) {
-    const bool all = there(kBarPFull + t, j & 1) && there(kBarVFull + 2 * (j & 1), (j >> 1) & 1) && there(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
+    const int seen = there(kBarPFull + t, j & 1) + 2 * there(kBarVFull + 2 * (j & 1), (j >> 1) & 1) +
+                     4 * there(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
     csa::tc_fence_after();
-    return all;
+    return seen;
   };
-  auto need_o = [&](int t, int j, bool seen) {
-    if (seen) return;
-    need(kBarVFull + 2 * (j & 1), (j >> 1) & 1);
-    need(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
-    need(kBarPFull + t, j & 1);
+  auto need_o = [&](int t, int j, int seen) {
+    if (!(seen & 2)) need(kBarVFull + 2 * (j & 1), (j >> 1) & 1);
+    if (!(seen & 4)) need(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
+    if (!(seen & 1)) need(kBarPFull + t, j & 1);
   };
   if (most > 0) need(kBarKFull, 0);
   if (n[0] > 0) need(kBarQFull, 0);
   for (int j = 0; ok && j < most; ++j) {
     const bool s0 = j < n[0], s1 = j < n[1], o1 = j > 0 && j - 1 < n[1];
-    bool seen1 = false, seen0 = false, seen_k = false;
+    int seen1 = 0, seen0 = 0;
+    bool seen_k = false;
     if (s0)
       issue_s(t0, j, [&] {
         if (o1) seen1 = look_o(1, j - 1);
@@ -313,7 +314,7 @@ __device__ void role_mma(const csa_latent_prefill_args& A, Smem& S, const Reques
     if (j + 1 < most && !seen_k) need(k_bar, k_parity);
   }
   if (ok && n[1] == most && most > 0) {
-    need_o(1, most - 1, false);
+    need_o(1, most - 1, 0);
     issue_o(t1, most - 1, true, nothing);
   }
   csa::mma_commit_if(lead, bars + 8 * kBarDrain);  // nothing of this thread's is in flight when it leaves
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ csa_latent_prefill_args A, const __grid_constant__ Maps M) {
   extern __shared__ uint8_t smem_raw[];
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = threadIdx.x >> 5;
   const uint32_t bars = smem_u32(S.bars);
   const int head = blockIdx.x % A.num_heads;
   bool bad = false;
@@ -576,9 +577,9 @@ extern "C" csa_status csa_latent_prefill(const csa_latent_prefill_args* a, void*
   // pairs of query tiles: at most one a request beyond the whole ones
   const int64_t pairs = a->total_q / (2 * kTile) + (a->num_req < a->total_q ? a->num_req : a->total_q);
   if (pairs * a->num_heads > INT32_MAX) return CSA_ERR_INVALID_ARG;
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return CSA_ERR_CUDA;
-  static bool ready[64];  // the kernel's shared memory size is set on each device once
+  int sms = 0, dev = 0;
+  if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
+  static bool ready[kMaxDevices];  // the kernel's shared memory size is set on each device once
   constexpr size_t smem = sizeof(Smem) + 1024;
   static_assert(smem <= 232448, "shared memory of one CTA");
   if (!ready[dev]) {

@@ -185,8 +185,8 @@ class StepTables(NamedTuple):
 def empty_tables(num_req: int, n_rows: int, device="cuda") -> StepTables:
     """Tables for csa_build_tables to fill, in one allocation."""
     buf = torch.empty(5 * n_rows + 2 * num_req + 3, dtype=torch.int32, device=device)
-    slot, req, pos, length, row_start, kv_start, taken = buf.split_with_sizes(
-        (2 * n_rows, n_rows, n_rows, n_rows, num_req + 1, num_req + 1, 1))
+    slot, req, pos, length, row_start, kv_start, taken = torch.unsafe_split_with_sizes(
+        buf, (2 * n_rows, n_rows, n_rows, n_rows, num_req + 1, num_req + 1, 1))
     return StepTables(req, pos, length, slot.view(torch.int64), row_start, kv_start, taken)
 
 
