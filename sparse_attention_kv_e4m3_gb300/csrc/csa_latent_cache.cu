@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(kCopyThreads) latent_write_kernel(const csa_la
 // A warp reads kReadRows neighbouring rows at a time: lane r < kReadRows finds row r's record (its request by
 // bisection, its page), then all lanes copy, many 16-byte pieces in flight. Bound by HBM.
 
-constexpr int kReadRows = 8;
+constexpr int kReadRows = 4;  // with 8, a 16384-row history is 1.2 waves of blocks
 
 // Row i's record: 0 where no request covers the row, 1 where the row becomes zeros.
 __device__ __forceinline__ uintptr_t record_of_row(const csa_latent_read_args& A, int64_t i, int rec_bytes, int32_t* flags) {
@@ -313,59 +313,55 @@ __device__ __forceinline__ uintptr_t record_of_row(const csa_latent_read_args& A
 // bf16 records: 16 bytes to 16 bytes.
 template <int kRope>
 __device__ __forceinline__ void copy_rows(uintptr_t mine, uint8_t* out, int lane) {
-  constexpr int kChunks = 2 * (kDim + kRope) / 16, kAll = kReadRows * kChunks / 32, kBatch = kAll / 2;
+  constexpr int kChunks = 2 * (kDim + kRope) / 16, kAll = kReadRows * kChunks / 32;
+  uint4 w[kAll];
+  uintptr_t rec[kAll];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uint4 w[kBatch];
-    uintptr_t rec[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int at = 32 * (kBatch * b + k) + lane;
-      rec[k] = __shfl_sync(0xFFFFFFFFu, mine, at / kChunks);
-      w[k] = rec[k] > 1 ? __ldg(reinterpret_cast<const uint4*>(rec[k]) + at % kChunks) : make_uint4(0, 0, 0, 0);
-    }
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k)
-      if (rec[k]) reinterpret_cast<uint4*>(out)[32 * (kBatch * b + k) + lane] = w[k];
+  for (int k = 0; k < kAll; ++k) {
+    const int at = 32 * k + lane;
+    rec[k] = __shfl_sync(0xFFFFFFFFu, mine, at / kChunks);
+    w[k] = rec[k] > 1 ? __ldg(reinterpret_cast<const uint4*>(rec[k]) + at % kChunks) : make_uint4(0, 0, 0, 0);
   }
+#pragma unroll
+  for (int k = 0; k < kAll; ++k)
+    if (rec[k]) reinterpret_cast<uint4*>(out)[32 * k + lane] = w[k];
 }
 
-// MXFP4 records: lane l decodes values 16 l .. 16 l + 15 and rope values 2 l, 2 l + 1.
+// MXFP4 records: lane l decodes values 8 l .. 8 l + 7 and the same of the second half (4 code bytes to 16 each), and
+// copies rope values 2 l, 2 l + 1, so that every load and store of the warp is one contiguous piece.
 template <int kRope>
 __device__ __forceinline__ void decode_rows(uintptr_t mine, uint8_t* out, int lane) {
-  constexpr int kBatch = kReadRows / 2;
+  uintptr_t rec[kReadRows];
+  uint32_t code[kReadRows][2], scale[kReadRows][2], rope[kReadRows];
 #pragma unroll
-  for (int b = 0; b < 2; ++b) {
-    uintptr_t rec[kBatch];
-    uint2 code[kBatch];
-    uint32_t scale[kBatch], rope[kBatch];
+  for (int k = 0; k < kReadRows; ++k) {
+    rec[k] = __shfl_sync(0xFFFFFFFFu, mine, k);
+    const uint8_t* p = reinterpret_cast<const uint8_t*>(rec[k]);
+    const bool live = rec[k] > 1;
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      rec[k] = __shfl_sync(0xFFFFFFFFu, mine, kBatch * b + k);
-      const uint8_t* p = reinterpret_cast<const uint8_t*>(rec[k]);
-      const bool live = rec[k] > 1;
-      code[k] = live ? __ldg(reinterpret_cast<const uint2*>(p) + lane) : make_uint2(0, 0);
-      scale[k] = live ? __ldg(p + kCodeBytes + (lane >> 1)) : 0u;
-      rope[k] = live && kRope != 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + kCodeBytes + kScaleBytes) + lane) : 0u;
+    for (int h = 0; h < 2; ++h) {
+      code[k][h] = live ? __ldg(reinterpret_cast<const uint32_t*>(p) + 32 * h + lane) : 0u;
+      scale[k][h] = live ? __ldg(p + kCodeBytes + 8 * h + (lane >> 2)) : 0u;
     }
+    rope[k] = live && kRope != 0 ? __ldg(reinterpret_cast<const uint32_t*>(p + kCodeBytes + kScaleBytes) + lane) : 0u;
+  }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      if (!rec[k]) continue;
-      const float s = ue8m0(scale[k]);
-      uint32_t w[8];
+  for (int k = 0; k < kReadRows; ++k) {
+    if (!rec[k]) continue;
+    uint8_t* row = out + k * (2 * (kDim + kRope));
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t byte = ((j < 4 ? code[k].x : code[k].y) >> (8 * (j & 3))) & 0xFFu;
-        const __half2_raw h = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>(byte), __NV_E2M1);
-        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    for (int h = 0; h < 2; ++h) {
+      const float s = ue8m0(scale[k][h]);
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const __half2_raw r = __nv_cvt_fp4x2_to_halfraw2(static_cast<__nv_fp4x2_storage_t>((code[k][h] >> (8 * j)) & 0xFFu), __NV_E2M1);
+        const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&r));
         w[j] = pack_bf16(v.x * s, v.y * s);  // exact: two significant bits times a power of two
       }
-      uint8_t* row = out + (kBatch * b + k) * (2 * (kDim + kRope));
-      uint4* p = reinterpret_cast<uint4*>(row) + 2 * lane;
-      p[0] = make_uint4(w[0], w[1], w[2], w[3]);
-      p[1] = make_uint4(w[4], w[5], w[6], w[7]);
-      if (kRope != 0) reinterpret_cast<uint32_t*>(row)[kDim / 2 + lane] = rope[k];
+      reinterpret_cast<uint4*>(row)[32 * h + lane] = make_uint4(w[0], w[1], w[2], w[3]);
     }
+    if (kRope != 0) reinterpret_cast<uint32_t*>(row)[kDim / 2 + lane] = rope[k];
   }
 }
 
