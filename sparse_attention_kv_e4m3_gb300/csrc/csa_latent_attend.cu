@@ -245,6 +245,14 @@ struct TileRegs<false, kRope> {
   static __device__ __forceinline__ int record(int t, int k) { return (t >> 3) + 32 * k; }
   static __device__ __forceinline__ bool leads(int t) { return (t & 7) == 0; }
   __device__ __forceinline__ void convert(int, int) {}
+  static __device__ __forceinline__ void prefetch(const uint8_t* const (&rec)[kRecords], int t) {
+#pragma unroll
+    for (int k = 0; k < kRecords; ++k) {
+      if (!rec[k]) continue;
+      csa::prefetch_l2(rec[k] + 128 * (t & 7));
+      if (kRope != 0 && (t & 7) == 0) csa::prefetch_l2(rec[k] + 2 * kDim);
+    }
+  }
   __device__ __forceinline__ void fetch(const uint8_t* const (&rec)[kRecords], int pair, int t) {
 #pragma unroll
     for (int k = 0; k < kRecords; ++k) {
@@ -274,7 +282,7 @@ struct TileRegs<false, kRope> {
 template <int kRope>
 struct TileRegs<true, kRope> {
   static constexpr int kRecords = 1;
-  uint4 code[kPairs], rope[2];
+  uint4 code[kPairs], rope[2], rope_now[2];
   uint32_t scale[kPairs], value[2][16];
   static __device__ __forceinline__ int record(int t, int) { return t >> 2; }
   static __device__ __forceinline__ bool leads(int t) { return (t & 3) == 0; }
@@ -306,6 +314,9 @@ struct TileRegs<true, kRope> {
     *lo = *reinterpret_cast<const uint32_t*>(&x);
     *hi = *reinterpret_cast<const uint32_t*>(&y);
   }
+  static __device__ __forceinline__ void prefetch(const uint8_t* const (&rec)[kRecords], int t) {
+    if (rec[0]) csa::prefetch_l2(rec[0] + min(128 * (t & 3), record_bytes(true, kRope) - 1));
+  }
   // The codes fetched become the values to store, ahead of the tile's turn.
   __device__ __forceinline__ void convert(int pair, int t) {
     const bool swap = (t & 3) >= 2;  // lanes 2, 3 store their words in another order: no two on one bank
@@ -321,6 +332,10 @@ struct TileRegs<true, kRope> {
       four(word[j], s2, &v[0], &v[1]);
       four(word[j] >> 16, s2, &v[2], &v[3]);
     }
+    if (kRope != 0 && pair == 0) {
+      rope_now[0] = rope[0];
+      rope_now[1] = rope[1];
+    }
   }
   __device__ __forceinline__ void store(uint32_t dst, int pair, int t) const {
     const int r = t >> 2, s = t & 3;
@@ -334,8 +349,8 @@ struct TileRegs<true, kRope> {
     if (kRope != 0 && pair == 0) {
 #pragma unroll
       for (int k = 0; k < 2; ++k)
-        csa::st_shared_v4(row + kDim / 64 * kColBytes + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y,
-                          rope[k].z, rope[k].w);
+        csa::st_shared_v4(row + kDim / 64 * kColBytes + (((2 * s + k) ^ (r & 7)) << 4), rope_now[k].x, rope_now[k].y,
+                          rope_now[k].z, rope_now[k].w);
     }
   }
 };
@@ -384,11 +399,16 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   };
   Regs x;
   bool live[Regs::kRecords];
+  // `rec` are the records of the tile after the one in the registers
   find();
   locate();
   find();
 #pragma unroll
   for (int pair = 0; pair < kPairs; ++pair) x.fetch(rec, pair, t);
+#pragma unroll
+  for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
+  locate();
+  find();
   uint32_t g = 0, piece = 0;
   for (; run.more(); run.next(K), ++piece) {
     // Q of the piece: head h's 64-value columns at row h, swizzled as the records; zeros past the last head
@@ -422,13 +442,13 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
     for (int i = 0; i < run.n; ++i, ++g) {
       const uint32_t stage = g & 1;
 #pragma unroll
-      for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
-      locate();
-      find();
-#pragma unroll
       for (int half = 0; half < 2; ++half) {
         x.convert(2 * half, t);  // before the tile's turn, where that is not yet come
         x.convert(2 * half + 1, t);
+        if constexpr (kFp4) {  // the codes' registers are free: the next tile's have all of this one's time to arrive
+          x.fetch(rec, 2 * half, t);
+          x.fetch(rec, 2 * half + 1, t);
+        }
         if (!warp_wait(bars + 8 * (kBarCEmpty + 2 * stage + half), ((g >> 1) & 1) ^ 1, stop)) return;
         x.store(smem_u32(S.c[stage]), 2 * half, t);
         x.store(smem_u32(S.c[stage]), 2 * half + 1, t);
@@ -439,9 +459,19 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
         csa::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bars + 8 * (kBarCFull + 2 * stage + half));
-        x.fetch(rec, 2 * half, t);  // of the next tile: in flight until this half's turn comes again
-        x.fetch(rec, 2 * half + 1, t);
+        if constexpr (!kFp4) {  // in flight until this half's turn comes again
+          x.fetch(rec, 2 * half, t);
+          x.fetch(rec, 2 * half + 1, t);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
+      // While the tile's turn has not come: the records of the one after it, on their way to L2. Not where many
+      // rows list positions: such rows are a prompt chunk's, whose request's records are in L2 already (1024 rows
+      // of 512 positions: 333 us with it, 322 without).
+      locate();
+      find();
+      if (!A.idx || K.cluster) x.prefetch(rec, t);
     }
   }
 }
