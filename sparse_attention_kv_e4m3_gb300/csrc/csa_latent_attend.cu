@@ -79,10 +79,13 @@ struct Kernel {
   csa_latent_attend_args A;
   Open* opens;
   float* parts;
-  int32_t groups;  // head groups of 64
+  int32_t groups;  // head groups of 64: 1 or 2
   int32_t by_unit;  // opens are indexed by unit
   int32_t cluster;  // CTAs that share a unit and join it among themselves; 0: runs over all units
 };
+
+__device__ __forceinline__ int row_of(const Kernel& K, int unit) { return unit >> (K.groups - 1); }
+__device__ __forceinline__ int group_of(const Kernel& K, int unit) { return unit & (K.groups - 1); }
 
 // What a query row sees: its request's page table row and its length.
 struct RowView {
@@ -140,7 +143,7 @@ __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int64_t* scan) {
   if (K.cluster) {
     if (tid == 0) {
       S.unit = blockIdx.x / K.cluster;
-      const int n = tiles_of(A, S.unit / K.groups), rank = blockIdx.x % K.cluster;
+      const int n = tiles_of(A, row_of(K, S.unit)), rank = blockIdx.x % K.cluster;
       S.off = n * rank / K.cluster;
       S.total = n * (rank + 1) / K.cluster - S.off;  // this CTA's tiles, maybe none
     }
@@ -206,7 +209,7 @@ struct Pieces {
   }
   __device__ __forceinline__ void size(const Kernel& K) {
     if (left <= 0) return;
-    tiles = tiles_of(K.A, unit / K.groups);
+    tiles = tiles_of(K.A, row_of(K, unit));
     n = static_cast<int>(min(left, static_cast<int64_t>(tiles - off)));
   }
   __device__ __forceinline__ bool more() const { return left > 0; }
@@ -375,21 +378,21 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   // issued: the entries' positions, then their pages.
   Pieces ahead = run;
   int tile = ahead.off, piece_end = ahead.off + ahead.n;
-  RowView R = row_view(A, ahead.unit / K.groups, flags), R_found = R;
+  RowView R = row_view(A, row_of(K, ahead.unit), flags), R_found = R;
   int32_t pos[Regs::kRecords];
   const uint8_t* rec[Regs::kRecords];
   auto find = [&]() {  // the positions of the next tile of the run, -1 past its end
     if (ahead.more() && tile == piece_end) {
       ahead.next(K);
       if (ahead.more()) {
-        R = row_view(A, ahead.unit / K.groups, flags);
+        R = row_view(A, row_of(K, ahead.unit), flags);
         tile = ahead.off;
         piece_end = ahead.off + ahead.n;
       }
     }
 #pragma unroll
     for (int k = 0; k < Regs::kRecords; ++k)
-      pos[k] = ahead.more() ? position_of(A, R, ahead.unit / K.groups, tile * kTile + Regs::record(t, k)) : -1;
+      pos[k] = ahead.more() ? position_of(A, R, row_of(K, ahead.unit), tile * kTile + Regs::record(t, k)) : -1;
     R_found = R;
     ++tile;
   };
@@ -412,7 +415,7 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   uint32_t g = 0, piece = 0;
   for (; run.more(); run.next(K), ++piece) {
     // Q of the piece: head h's 64-value columns at row h, swizzled as the records; zeros past the last head
-    const int b = run.unit / K.groups, h0 = (run.unit % K.groups) * kHeads;
+    const int b = row_of(K, run.unit), h0 = group_of(K, run.unit) * kHeads;
     if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
@@ -425,7 +428,7 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
         csa::cp_async16(smem_u32(S.q) + c * kColBytes + h * 128 + (((t & 7) ^ (h & 7)) << 4), q + 128 * c, on);
     }
     if (run.left > run.n) {  // the next unit's Q on its way to L2: its own copy can only start when this one's last S is done
-      const int nb = (run.unit + 1) / K.groups, n0 = (run.unit + 1) % K.groups * kHeads;
+      const int nb = row_of(K, run.unit + 1), n0 = group_of(K, run.unit + 1) * kHeads;
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int h = (t >> 3) + 32 * k;
@@ -527,7 +530,7 @@ __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
   uint32_t g = 0, piece = 0;
   bool ok = true;
   for (Pieces run(K, S); ok && run.more(); run.next(K), ++piece) {
-    const int heads = min(K.A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
+    const int heads = min(K.A.num_heads - group_of(K, run.unit) * kHeads, kHeads);
     const uint32_t idesc = csa::uniform(csa::idesc_bf16_f32(128, (heads + 15) / 16 * 16) | csa::kIdescAMnMajor);
     ok = warp_wait(bars + 8 * kBarOEmpty, (piece & 1) ^ 1, stop);
     const int n = csa::uniform(run.n);
@@ -551,50 +554,56 @@ __device__ void role_mma_o(const Kernel& K, Smem<kRope>& S) {
   __syncwarp();
 }
 
-// out (or a part) from O^T: a thread holds one value of 128 per column block, for every head.
+// out from O^T: 32 heads x 128 values a step, a warp its 32 values (32 lanes of TMEM). They are read as 8 x 8
+// matrices (values x heads), scaled and rounded, transposed on the way to shared memory (2 KB a warp of P's, which
+// is not in use between a unit's last O and the next one's first P: head h at 64 h, its four 16-byte chunks
+// exchanged by h / 2 so that neither side has two lanes on one bank), and written as 64 contiguous bytes a head.
+// 7.5 k clocks a unit when the transposition was done by lane exchanges and 4-byte stores.
 template <int kRope>
 __device__ void write_out(const Kernel& K, Smem<kRope>& S, int unit, int heads, int warp, int lane) {
-  const int b = unit / K.groups, h0 = (unit % K.groups) * kHeads;
-  const int odd = lane & 1;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(K.A.out) +
-                       (static_cast<int64_t>(b) * K.A.num_heads + h0 + odd) * kDim + 32 * warp + (lane & ~1);
-  const uint32_t lanes = static_cast<uint32_t>(32 * warp) << 16;
-  // 32 heads of 128 values a step; the next step's O is on its way while this one's is written
-  const int halves = heads > 32 ? 2 : 1, steps = kDim / 128 * halves;
-  auto o_at = [&](int step) { return S.tmem + step / halves * kHeads + step % halves * 32 + lanes; };
-  auto write = [&](int step, const uint32_t (&v)[32]) {
-    const int hh = step % halves * 32;
-    const float4* alpha = reinterpret_cast<const float4*>(S.alpha + hh);
-    __nv_bfloat16* at = out + hh * kDim + 128 * (step / halves);
-    const int left = heads - hh - odd;  // of the heads from hh + odd on
-    // two heads at a time: even lanes end with values (lane, lane + 1) of the first, odd lanes with
-    // values (lane - 1, lane) of the second
-    uint32_t two[16];
+  const int b = row_of(K, unit), h0 = group_of(K, unit) * kHeads;
+  const uint32_t stage = smem_u32(S.p) + 2048 * warp, lanes = static_cast<uint32_t>(32 * warp) << 16;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(K.A.out) +
+                                        (static_cast<int64_t>(b) * K.A.num_heads + h0) * kDim + 32 * warp + 8 * (lane & 3));
+  const int row = lane & 7, chunk = lane >> 3;  // this lane's row of a matrix, and which of the four
+#pragma unroll 1
+  for (int hh = 0; hh < heads; hh += 32) {
+    float2 alpha[4];
 #pragma unroll
-    for (int j = 0; j < 32; j += 4) {
-      const float4 a = alpha[j / 4];
+    for (int i = 0; i < 4; ++i) alpha[i] = *reinterpret_cast<const float2*>(S.alpha + hh + 8 * i + 2 * (lane & 3));
+#pragma unroll 1
+    for (int d = 0; d < kDim / 128; ++d) {
+      uint32_t v[2][16];  // values 0 .. 15 and 16 .. 31 of the warp's
+      const uint32_t at = S.tmem + d * kHeads + hh + lanes;
+      csa::tmem_ld_16x32(at, v[0]);
+      csa::tmem_ld_16x32(at + (16u << 16), v[1]);
+      csa::tmem_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 4; k += 2) {
-        const float x0 = __uint_as_float(v[j + k]) * (k ? a.z : a.x), x1 = __uint_as_float(v[j + k + 1]) * (k ? a.w : a.y);
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? x0 : x1, 1);
-        const __nv_bfloat162 pair = __floats2bfloat162_rn(odd ? got : x0, odd ? x1 : got);
-        two[(j + k) / 2] = *reinterpret_cast<const uint32_t*>(&pair);
+      for (int i = 0; i < 4; ++i) {  // heads hh + 8 i ..
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {  // values 8 k ..
+          const uint32_t* x = v[k >> 1] + 4 * i + 2 * (k & 1);
+          const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(x[0]) * alpha[i].x, __uint_as_float(x[1]) * alpha[i].y);
+          w[k] = *reinterpret_cast<const uint32_t*>(&two);
+        }
+        const int h = 8 * i + row;
+        csa::stmatrix_x4_trans(stage + 64 * h + ((chunk ^ ((h >> 1) & 3)) << 4), w[0], w[1], w[2], w[3]);
+      }
+      __syncwarp();
+      uint4 x[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = 8 * i + (lane >> 2);
+        x[i] = csa::ld_shared_v4(stage + 64 * h + (((lane & 3) ^ ((h >> 1) & 3)) << 4));
+      }
+      __syncwarp();
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int h = hh + 8 * i + (lane >> 2);
+        if (h < heads) out[(h * kDim + 128 * d) / 8] = x[i];
       }
     }
-    // the stores apart from the exchanges, which would wait for one another in between
-#pragma unroll
-    for (int j = 0; j < 32; j += 2) csa::st_global_if(j < left, at + j * kDim, two[j / 2]);
-  };
-  uint32_t va[32], vb[32];
-  csa::tmem_ld32(o_at(0), va);
-#pragma unroll 1
-  for (int step = 0; step < steps; step += 2) {  // steps is even
-    csa::tmem_wait_ld();
-    csa::tmem_ld32(o_at(step + 1), vb);
-    write(step, va);
-    csa::tmem_wait_ld();
-    if (step + 2 < steps) csa::tmem_ld32(o_at(step + 2), va);
-    write(step + 1, vb);
   }
 }
 
@@ -637,7 +646,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
   uint32_t g = 0;
   bool ok = true;  // once a wait has run out, the rest runs through without waiting: all warps meet at every barrier
   for (Pieces run(K, S); run.more(); run.next(K)) {
-    const int heads = min(A.num_heads - (run.unit % K.groups) * kHeads, kHeads);
+    const int heads = min(A.num_heads - group_of(K, run.unit) * kHeads, kHeads);
     float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};  // l: this thread's share of the sum
     for (int i = 0; i < run.n; ++i, ++g) {
       ok = ok && warp_wait(bars + 8 * (kBarCFull + 2 * (g & 1)), (g >> 1) & 1, stop);
@@ -746,7 +755,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
         for (int r = 0; r < 2; ++r) {
           S.alpha[head[r]] = l[r] > 0.f ? 1.f / l[r] : l[r];  // 0 for an empty row; a NaN stays one
           if (A.lse && head[r] < heads)
-            A.lse[static_cast<int64_t>(run.unit / K.groups) * A.num_heads + (run.unit % K.groups) * kHeads + head[r]] =
+            A.lse[static_cast<int64_t>(row_of(K, run.unit)) * A.num_heads + group_of(K, run.unit) * kHeads + head[r]] =
                 l[r] == 0.f ? -INFINITY : (mc[r] + log2f(l[r])) * 0.6931471805599453f;
         }
       }
@@ -784,8 +793,8 @@ template <int kRope>
 __device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t size = K.cluster, rank = blockIdx.x % size;
-  const int heads = min(K.A.num_heads - (S.unit % K.groups) * kHeads, kHeads);
-  const int64_t row = static_cast<int64_t>(S.unit / K.groups) * K.A.num_heads + (S.unit % K.groups) * kHeads;
+  const int heads = min(K.A.num_heads - group_of(K, S.unit) * kHeads, kHeads);
+  const int64_t row = static_cast<int64_t>(row_of(K, S.unit)) * K.A.num_heads + group_of(K, S.unit) * kHeads;
   const int64_t tiles = S.total;
   csa::cluster_arrive();
   csa::cluster_wait();  // every CTA's m, l are there and its MMAs are done
@@ -937,7 +946,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, i
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Open o = K.opens[blockIdx.x];
   if (!o.cut) return;
-  const int h = (o.unit % K.groups) * kHeads + head;
+  const int h = group_of(K, o.unit) * kHeads + head;
   if (h >= A.num_heads) return;
   // runs o.run .. last; a run without tiles has no part
   const int64_t end = o.begin + o.tiles;
@@ -980,7 +989,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, i
     l += s_l[w];
   }
   const float inv = l > 0.f ? 1.f / l : l;
-  const int64_t row = static_cast<int64_t>(o.unit / K.groups) * A.num_heads + h;
+  const int64_t row = static_cast<int64_t>(row_of(K, o.unit)) * A.num_heads + h;
   reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(A.out) + row * kDim)[threadIdx.x] =
       __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
   if (A.lse && threadIdx.x == 0) A.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
