@@ -13,7 +13,8 @@ LIB_PATH = os.path.join(PKG, "libcsa_index.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("csa_index.cu", "csa_writer.cu", "csa_recall.cu", "csa_latent_cache.cu",
                                                "csa_latent_attend.cu", "csa_latent_prefill.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("csa_ptx.cuh", "csa_select.cuh", "csa_score64.cuh",
-                                                  "csa_internal.h", "csa_latent_common.cuh", "csa_latent_ptx.cuh")] + [
+                                                  "csa_internal.h", "csa_latent_common.cuh", "csa_latent_maps.h",
+                                                  "csa_latent_ptx.cuh")] + [
     os.path.join(INCLUDE, f) for f in ("csa_index.h", "csa_latent.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 

@@ -1,5 +1,6 @@
 // csa_latent_attend.cu — latent attention, absorbed form (include/csa_latent.h).
 #include "csa_latent_common.cuh"
+#include "csa_latent_maps.h"
 #include "csa_latent_ptx.cuh"
 
 namespace csa_latent {
@@ -37,9 +38,14 @@ using csa::smem_u32;
 // depend on timing.
 constexpr int kTile = 64, kHeads = 64;            // records a tile, heads a unit
 constexpr int kColBytes = kTile * 128;            // 64 values of a tile's 64 records (or of Q's 64 heads)
-constexpr int kSoftmaxWarps = 4, kLoadWarps = 8;
-constexpr int kMmaWarp = kSoftmaxWarps + kLoadWarps;
-constexpr int kThreads = 32 * (kMmaWarp + 2);
+constexpr int kSoftmaxWarps = 4;
+// How records get to shared memory.
+enum { kLoadTma = 0, kLoadFp4 = 1, kLoadBf16 = 2 };
+template <int kLoad>
+struct Warps {  // the softmax's, the loaders' (of which TMA uses one; all help in a cluster's join), S's and O's MMAs'
+  static constexpr int kLoaders = kLoad == kLoadTma ? 4 : 8, kMma = kSoftmaxWarps + kLoaders, kThreads = 32 * (kMma + 2);
+  static constexpr int kFills = kLoad == kLoadTma ? 1 : kLoaders;  // arrivals that make a buffer full
+};
 constexpr int kMaxGrid = 160;                     // CTAs at most: sizes the workspace
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O^T in columns 0 .. 255, S in 256 .. 383
 constexpr float kGrow = 8.0f;                     // log2 of how far p may exceed 1
@@ -51,7 +57,7 @@ struct Smem {
   uint8_t q[kCols * kColBytes];
   uint8_t c[2][kCols * kColBytes];
   uint8_t p[kHeads * 128];
-  uint64_t bars[18];
+  uint64_t bars[20];
   uint8_t valid[2][kTile];  // 1 where the tile's record is visible
   alignas(16) float alpha[kHeads];
   float mc[kHeads], l[kHeads];  // cluster: this CTA's reference and sum per head
@@ -63,7 +69,7 @@ struct Smem {
 constexpr int kPairs = kDim / 128;  // a tile moves in 128 values at a time
 // A tile is handed over in two halves of 256 values: barriers 2 * stage + half.
 enum { kBarCFull = 0, kBarCEmpty = 4, kBarSFull = 8, kBarSEmpty = 10, kBarQFull = 12, kBarQEmpty, kBarPFull,
-       kBarOEmpty, kBarDrainS, kBarDrainO };
+       kBarOEmpty, kBarDrainS, kBarDrainO, kBarLand };
 
 // A part of a cut unit: O [64 heads][512], then m c and l of the 64 heads.
 constexpr size_t kPartFloats = static_cast<size_t>(kHeads) * (kDim + 2);
@@ -136,7 +142,7 @@ __device__ __forceinline__ const uint8_t* record_at(const csa_latent_attend_args
 __host__ __device__ __forceinline__ int64_t run_start(int64_t total, int c, int grid) { return total * c / grid; }
 
 // This CTA's run: the total of all units' tiles, and the unit and the tile in it where the run starts.
-template <int kRope>
+template <int kThreads, int kRope>
 __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int64_t* scan) {
   const csa_latent_attend_args& A = K.A;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -365,7 +371,7 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 template <bool kFp4, int kRope>
-__device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
+__device__ void role_load_regs(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   constexpr int kCols = Smem<kRope>::kCols;
   using Regs = TileRegs<kFp4, kRope>;
   const csa_latent_attend_args& A = K.A;
@@ -477,6 +483,105 @@ __device__ void role_load(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
       if (!A.idx || K.cluster) x.prefetch(rec, t);
     }
   }
+}
+
+struct Maps {  // tensor maps of the TMA loader
+  CUtensorMap q;      // [row][head][value], boxes of 64 values of 64 heads
+  CUtensorMap pages;  // [page][record][column of 64 values][value], boxes of one column of a page: a tile
+};
+
+// The TMA loader: one warp, for whole histories, where a tile is a page and nine (or eight) copies fill it. Where a
+// page's end is not visible, its rows become zeros before the tile is handed over (they may hold NaN, and 0 x NaN is
+// not 0).
+template <int kRope>
+__device__ void role_load_tma(const Kernel& K, const Maps& M, Smem<kRope>& S, int32_t* flags) {
+  constexpr int kCols = Smem<kRope>::kCols, kRec = record_bytes(false, kRope);
+  const csa_latent_attend_args& A = K.A;
+  const int lane = threadIdx.x & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars);
+  Pieces run(K, S), ahead = run;
+  if (!run.more()) return;
+  struct Tile {
+    int32_t page, rows;  // -1, 0: nothing of it is visible
+  };
+  int tile = ahead.off, piece_end = ahead.off + ahead.n;
+  RowView R = row_view(A, row_of(K, ahead.unit), flags);
+  auto next_tile = [&]() {  // of the run, its page on the way to L2
+    if (ahead.more() && tile == piece_end) {
+      ahead.next(K);
+      if (ahead.more()) {
+        R = row_view(A, row_of(K, ahead.unit), flags);
+        tile = ahead.off;
+        piece_end = ahead.off + ahead.n;
+      }
+    }
+    Tile T = {-1, 0};
+    if (ahead.more() && tile * kTile < R.len) {
+      const int32_t page = __ldg(R.table + tile);
+      if (page < 0 || page >= A.cache.num_pages) *flags |= CSA_DEV_PAGE_OOB;
+      else T = {page, min(kTile, R.len - tile * kTile)};
+    }
+    if (lane == 0 && T.rows > 0) csa::bulk_prefetch_l2(A.cache.pages + T.page * A.cache.page_stride_bytes, T.rows * kRec);
+    ++tile;
+    return T;
+  };
+  static_assert(kTile == kPageRecs, "a tile is a page");
+  Tile now = next_tile(), next = next_tile();
+  uint32_t g = 0, piece = 0, landed = 0;
+  bool ok = true;
+  for (; ok && run.more(); run.next(K), ++piece) {
+    ok = warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop);
+    if (!ok) break;
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * kBarQFull;
+      csa::mbar_arrive_expect_tx(bar, sizeof(S.q));
+      for (int c = 0; c < kCols; ++c)
+        csa::tma_tile_3d(smem_u32(S.q) + c * kColBytes, &M.q, 64 * c, group_of(K, run.unit) * kHeads, row_of(K, run.unit), bar);
+    }
+    for (int i = 0; i < run.n; ++i, ++g) {
+      const uint32_t stage = g & 1, dst = smem_u32(S.c[stage]);
+      const bool whole = now.rows == kTile;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        ok = ok && warp_wait(bars + 8 * (kBarCEmpty + 2 * stage + half), ((g >> 1) & 1) ^ 1, stop);
+        if (!ok) break;
+        const uint32_t full = bars + 8 * (kBarCFull + 2 * stage + half), bar = whole ? full : bars + 8 * kBarLand;
+        if (half == 0) {
+          S.valid[stage][lane] = lane < now.rows;
+          S.valid[stage][lane + 32] = lane + 32 < now.rows;
+          __syncwarp();
+        }
+        const int columns = kDim / 128 + (kRope != 0 && half == 0);  // of the half: 4 half .. 4 half + 3, and rope with the first
+        auto column = [&](int c) { return c < kDim / 128 ? kDim / 128 * half + c : kDim / 64; };
+        if (now.rows > 0 && lane == 0) {
+          csa::mbar_arrive_expect_tx(bar, columns * kColBytes);
+          for (int c = 0; c < columns; ++c) csa::tma_tile_4d(dst + column(c) * kColBytes, &M.pages, 0, column(c), 0, now.page, bar);
+        }
+        if (whole) continue;
+        if (now.rows > 0) {
+          ok = ok && warp_wait(bar, landed & 1, stop);
+          ++landed;
+          if (!ok) break;
+        }
+        for (int c = 0; c < columns; ++c)
+          for (int b = now.rows * 128 + 16 * lane; b < kColBytes; b += 512) csa::st_shared_v4(dst + column(c) * kColBytes + b, 0, 0, 0, 0);
+        csa::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(full);
+      }
+      if (!ok) break;
+      now = next;
+      next = next_tile();
+    }
+  }
+  // No copy of this CTA is in flight when it leaves. Where a wait has run out, those begun land within the limit.
+  if (!ok && lane == 0) {
+    csa::mbar_wait_drain(bars + 8 * kBarQFull, piece & 1);
+    csa::mbar_wait_drain(bars + 8 * kBarLand, landed & 1);
+    for (uint32_t k = 0; k < 4; ++k) csa::mbar_wait_drain(bars + 8 * (kBarCFull + k), ((k >> 1) == (g & 1) ? g >> 1 : (g - 1) >> 1) & 1);
+  }
+  __syncwarp();
 }
 
 template <int kRope>
@@ -789,7 +894,7 @@ __device__ __forceinline__ float weight(float x) {
 // 512 r / size .. of all heads (of 32 heads where size is 8). Everyone scales its O by its share of the
 // softmax, 2^(m c - M c) / L, and writes the others' slices into their record tiles, which are free by
 // now; sums go in the order of the ranks. Needs no workspace and no second launch.
-template <int kRope>
+template <int kMmaWarp, int kRope>
 __device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t size = K.cluster, rank = blockIdx.x % size;
@@ -825,7 +930,7 @@ __device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) v[j] = tiles > 0 ? __uint_as_float(raw[j]) * S.alpha[h + j] : 0.f;
   };
-  if (warp < kMmaWarp) {  // three warps a lane quarter
+  if (warp < kMmaWarp) {  // two or three warps a lane quarter
     for (int s = warp >> 2; s < kSteps; s += kMmaWarp / 4) {
       const uint32_t owner = s / per;
       if (owner == rank || s % (kHeads / 4) * 4 >= heads) continue;
@@ -867,8 +972,21 @@ __device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
   }
 }
 
-template <bool kFp4, int kRope>
-__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
+template <int kLoad>
+struct MapsFor {
+  using type = int;  // none
+};
+template <>
+struct MapsFor<kLoadTma> {
+  using type = Maps;
+};
+template <int kLoad>
+using MapsOf = typename MapsFor<kLoad>::type;
+
+template <int kLoad, int kRope>
+__global__ void __launch_bounds__(Warps<kLoad>::kThreads, 1)
+    attend_kernel(const __grid_constant__ Kernel K, const __grid_constant__ MapsOf<kLoad> M) {
+  constexpr int kMmaWarp = Warps<kLoad>::kMma, kFills = Warps<kLoad>::kFills, kThreads = Warps<kLoad>::kThreads;
   extern __shared__ uint8_t smem_raw[];
   Smem<kRope>& S = *reinterpret_cast<Smem<kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ int64_t scan[kThreads / 32];
@@ -876,14 +994,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   const uint32_t bars = smem_u32(S.bars);
   if (threadIdx.x == 0) {
     for (int k = 0; k < 4; ++k) {
-      csa::mbar_init(bars + 8 * (kBarCFull + k), kLoadWarps);
+      csa::mbar_init(bars + 8 * (kBarCFull + k), kFills);
       csa::mbar_init(bars + 8 * (kBarCEmpty + k), 1);
     }
     for (int k = 0; k < 2; ++k) {
       csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarSEmpty + k), kSoftmaxWarps);
     }
-    csa::mbar_init(bars + 8 * kBarQFull, kLoadWarps);
+    csa::mbar_init(bars + 8 * kBarQFull, kFills);
+    csa::mbar_init(bars + 8 * kBarLand, 1);
     csa::mbar_init(bars + 8 * kBarQEmpty, 1);
     csa::mbar_init(bars + 8 * kBarPFull, kSoftmaxWarps);
     csa::mbar_init(bars + 8 * kBarOEmpty, kSoftmaxWarps);
@@ -901,13 +1020,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
     csa::tmem_relinquish();
   }
   csa::tc_fence_before();
-  make_plan(K, S, scan);  // ends with a block barrier
+  make_plan<kThreads>(K, S, scan);  // ends with a block barrier
   csa::tc_fence_after();
   int32_t flags = 0;
   if (warp < kSoftmaxWarps) {
     role_softmax(K, S);
   } else if (warp < kMmaWarp) {
-    role_load<kFp4, kRope>(K, S, &flags);
+    if constexpr (kLoad != kLoadTma) role_load_regs<kLoad == kLoadFp4, kRope>(K, S, &flags);
+    else if (warp == kSoftmaxWarps) role_load_tma(K, M, S, &flags);
   } else {
     if (warp == kMmaWarp) {
       role_mma_s(K, S);
@@ -921,7 +1041,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const Kernel K) {
   __syncthreads();
   if (K.cluster) {
     csa::tc_fence_after();
-    cluster_join(K, S);
+    cluster_join<kMmaWarp>(K, S);
     csa::tc_fence_before();
     __syncthreads();
   }
@@ -1017,20 +1137,20 @@ int cluster_of(const csa_latent_attend_args* a, int sms) {
   return per <= 8 * size ? size : 0;
 }
 
-template <bool kFp4, int kRope>
-csa_status launch(const Kernel& K, int grid, int dev, cudaStream_t stream) {
+template <int kLoad, int kRope>
+csa_status launch(const Kernel& K, const MapsOf<kLoad>& M, int grid, int dev, cudaStream_t stream) {
   static bool ready[kMaxDevices];  // the kernel's shared memory size is set on each device once
   constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
   static_assert(smem + 256 <= 232448, "shared memory of one CTA");
   if (!ready[dev]) {
-    if (cudaFuncSetAttribute(attend_kernel<kFp4, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(attend_kernel<kLoad, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return CSA_ERR_CUDA;
     ready[dev] = true;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(kThreads);
+  cfg.blockDim = dim3(Warps<kLoad>::kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
@@ -1038,7 +1158,27 @@ csa_status launch(const Kernel& K, int grid, int dev, cudaStream_t stream) {
   attr[0].val.clusterDim = {static_cast<unsigned>(K.cluster ? K.cluster : 1), 1, 1};
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, attend_kernel<kFp4, kRope>, K) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, attend_kernel<kLoad, kRope>, K, M) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
+// Whole histories of bf16 records go through TMA where the cache's pages are a tensor of 128-byte columns (pages that
+// are not padded, or by such columns): long rows 102 us, 108 through registers. Listed positions do not (gathered four
+// rows a copy, 64 rows of 512 positions took 47 us, through registers 28), nor do short units in a cluster, whose few
+// tiles do not pay for the maps (one row of 1000 records: 20.8 us, 17.4).
+template <int kRope>
+csa_status launch_bf16(const Kernel& K, int grid, int dev, cudaStream_t stream) {
+  const csa_latent_attend_args& a = K.A;
+  constexpr int64_t kRec = record_bytes(false, kRope);
+  const int64_t stride = a.cache.page_stride_bytes;
+  if (a.idx || K.cluster || stride % 128 != 0) return launch<kLoadBf16, kRope>(K, 0, grid, dev, stream);
+  Maps M;
+  const cuuint64_t page_dims[4] = {64, static_cast<cuuint64_t>(kRec / 128), kPageRecs, static_cast<cuuint64_t>(a.cache.num_pages)};
+  const cuuint64_t page_strides[3] = {128, static_cast<cuuint64_t>(kRec), static_cast<cuuint64_t>(stride)};
+  const cuuint32_t page_boxes[4] = {64, 1, kPageRecs, 1};
+  if (!encode_bf16(&M.q, a.q, kDim + kRope, a.num_heads, a.num_q, a.q_head_stride, a.q_row_stride, kHeads, 1) ||
+      !encode_map(&M.pages, a.cache.pages, 4, page_dims, page_strides, page_boxes))
+    return CSA_ERR_INVALID_ARG;
+  return launch<kLoadTma, kRope>(K, M, grid, dev, stream);
 }
 
 csa_status check_args(const csa_latent_attend_args* a) {
@@ -1095,8 +1235,8 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kOpenBytes);
   const auto s = static_cast<cudaStream_t>(stream);
   const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
-  const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, grid, dev, s) : launch<true, 0>(K, grid, dev, s))
-                            : (rope ? launch<false, 64>(K, grid, dev, s) : launch<false, 0>(K, grid, dev, s));
+  const csa_status ls = fp4 ? (rope ? launch<kLoadFp4, 64>(K, 0, grid, dev, s) : launch<kLoadFp4, 0>(K, 0, grid, dev, s))
+                            : (rope ? launch_bf16<64>(K, grid, dev, s) : launch_bf16<0>(K, grid, dev, s));
   if (ls != CSA_OK || grid == 1 || K.cluster) return ls;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, a->num_heads < kHeads ? a->num_heads : kHeads);

@@ -1,9 +1,8 @@
 // csa_latent_prefill.cu — latent attention, expanded form (include/csa_latent.h).
-#include <cuda.h>
-
 #include <type_traits>
 
 #include "csa_latent_common.cuh"
+#include "csa_latent_maps.h"
 #include "csa_latent_ptx.cuh"
 
 namespace csa_latent {
@@ -535,36 +534,6 @@ csa_status check_args(const csa_latent_prefill_args* a) {
   return CSA_OK;
 }
 
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                                 const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                 CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encode_tiled() {
-  static const EncodeTiled fn = [] {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult got;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &got) != cudaSuccess ||
-        got != cudaDriverEntryPointSuccess)
-      p = nullptr;
-    return reinterpret_cast<EncodeTiled>(p);
-  }();
-  return fn;
-}
-
-// bf16 [rows][heads][width] in boxes of 64 values of one head and `box` rows, 128-byte swizzle.
-bool encode(CUtensorMap* map, const void* base, int64_t width, int64_t heads, int64_t rows, int64_t head_stride,
-            int64_t row_stride, uint32_t box) {
-  const bool flat = heads == 0;  // [rows][width]
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(width), static_cast<cuuint64_t>(flat ? rows : heads),
-                              static_cast<cuuint64_t>(rows)};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(2 * (flat ? row_stride : head_stride)),
-                                 static_cast<cuuint64_t>(2 * row_stride)};
-  const cuuint32_t boxes[3] = {64, flat ? box : 1, box}, steps[3] = {1, 1, 1};
-  return encode_tiled()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, flat ? 2 : 3, const_cast<void*>(base), dims, strides, boxes,
-                        steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 }  // namespace
 }  // namespace csa_latent
 
@@ -591,12 +560,12 @@ extern "C" csa_status csa_latent_prefill(const csa_latent_prefill_args* a, void*
   Maps M;
   const bool keys = a->total_k > 0;  // without keys no map of theirs is used: any valid one does
   const int64_t rows = keys ? a->total_k : a->total_q, heads = a->num_heads;
-  if (!encode(&M.q, a->q, kNope + kRope, heads, a->total_q, a->q_head_stride, a->q_row_stride, kTile) ||
-      !encode(&M.k, keys ? a->k_nope : a->q, kNope, heads, rows, keys ? a->k_head_stride : a->q_head_stride,
-              keys ? a->k_row_stride : a->q_row_stride, kTile) ||
-      !encode(&M.rope, keys ? a->k_rope : a->q, kRope, 0, rows, 0, keys ? a->rope_row_stride : a->q_row_stride, kTile) ||
-      !encode(&M.v, keys ? a->v : a->q, kV, heads, rows, keys ? a->v_head_stride : a->q_head_stride,
-              keys ? a->v_row_stride : a->q_row_stride, kTile / 2))
+  if (!encode_bf16(&M.q, a->q, kNope + kRope, heads, a->total_q, a->q_head_stride, a->q_row_stride, 1, kTile) ||
+      !encode_bf16(&M.k, keys ? a->k_nope : a->q, kNope, heads, rows, keys ? a->k_head_stride : a->q_head_stride,
+                   keys ? a->k_row_stride : a->q_row_stride, 1, kTile) ||
+      !encode_bf16(&M.rope, keys ? a->k_rope : a->q, kRope, 0, rows, 0, keys ? a->rope_row_stride : a->q_row_stride, 1, kTile) ||
+      !encode_bf16(&M.v, keys ? a->v : a->q, kV, heads, rows, keys ? a->v_head_stride : a->q_head_stride,
+                   keys ? a->v_row_stride : a->q_row_stride, 1, kTile / 2))
     return CSA_ERR_INVALID_ARG;
   prefill_kernel<<<static_cast<unsigned>(pairs * heads), kThreads, smem, static_cast<cudaStream_t>(stream)>>>(*a, M);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
