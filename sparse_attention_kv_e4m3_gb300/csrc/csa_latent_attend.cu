@@ -915,59 +915,69 @@ __device__ void cluster_join(const Kernel& K, Smem<kRope>& S) {
     if (rank == 0 && K.A.lse && h < heads) K.A.lse[row + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
   __syncthreads();
-  // A step is 4 heads of a block of 128 values; step s of the unit belongs to CTA s / per
-  constexpr int kSteps = kDim / 128 * (kHeads / 4), kStepBytes = 4 * 128 * 4;
+  // A step is 16 heads of a block of 128 values (as four by four heads in a CTA's inbox, a float4 a lane); step s of the
+  // unit belongs to CTA s / per
+  constexpr int kSteps = kDim / 128 * (kHeads / 16), kStepBytes = 16 * 128 * 4;
   const int per = kSteps / size;
-  auto slice_at = [&](uint32_t from, int s) {  // where CTA `from` puts its part of step s at the step's owner
-    return smem_u32(S.c[0]) + static_cast<uint32_t>(from * per + s % per) * kStepBytes;
+  auto inbox = [&](uint32_t from, int s) {  // where CTA `from` puts its part of step s at the step's owner
+    return smem_u32(S.c[0]) + static_cast<uint32_t>(from * per + s % per) * kStepBytes + 16 * (32 * (warp & 3) + lane);
   };
   const uint32_t lanes = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-  auto mine = [&](int s, float (&v)[4]) {
-    const int d = s / (kHeads / 4), h = s % (kHeads / 4) * 4;
-    uint32_t raw[4];
-    csa::tmem_ld4(S.tmem + d * kHeads + h + lanes, raw);
+  auto mine = [&](int s, float (&v)[16]) {
+    const int d = s / (kHeads / 16), h = s % (kHeads / 16) * 16;
+    uint32_t raw[16];
+    csa::tmem_ld16(S.tmem + d * kHeads + h + lanes, raw);
     csa::tmem_wait_ld();
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = tiles > 0 ? __uint_as_float(raw[j]) * S.alpha[h + j] : 0.f;
+    for (int j = 0; j < 16; ++j) v[j] = tiles > 0 ? __uint_as_float(raw[j]) * S.alpha[h + j] : 0.f;
   };
   if (warp < kMmaWarp) {  // two or three warps a lane quarter
     for (int s = warp >> 2; s < kSteps; s += kMmaWarp / 4) {
       const uint32_t owner = s / per;
-      if (owner == rank || s % (kHeads / 4) * 4 >= heads) continue;
-      float v[4];
+      if (owner == rank || s % (kHeads / 16) * 16 >= heads) continue;
+      float v[16];
       mine(s, v);
-      csa::st_peer_v4(csa::peer_smem(slice_at(rank, s), owner) + 16 * (32 * (warp & 3) + lane), v[0], v[1], v[2], v[3]);
+      const uint32_t at = csa::peer_smem(inbox(rank, s), owner);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) csa::st_peer_v4(at + 2048 * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
     }
   }
   csa::cluster_arrive();
   csa::cluster_wait();
   if (warp < kMmaWarp) {
-    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(K.A.out) + row * kDim + 32 * (warp & 3);
     const int odd = lane & 1;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(K.A.out) + (row + odd) * kDim + 32 * (warp & 3) + (lane & ~1);
     for (int s = static_cast<int>(rank) * per + (warp >> 2); s < static_cast<int>(rank + 1) * per; s += kMmaWarp / 4) {
-      const int d = s / (kHeads / 4), h = s % (kHeads / 4) * 4;
+      const int d = s / (kHeads / 16), h = s % (kHeads / 16) * 16;
       if (h >= heads) continue;
-      float own[4], v[4] = {};
+      float own[16], v[16] = {};
       mine(s, own);
       for (uint32_t r = 0; r < size; ++r) {
-        float4 x = make_float4(own[0], own[1], own[2], own[3]);
-        if (r != rank)
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                       : "r"(slice_at(r, s) + 16 * (32 * (warp & 3) + lane))
-                       : "memory");
-        v[0] += x.x;
-        v[1] += x.y;
-        v[2] += x.z;
-        v[3] += x.w;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float4 x = make_float4(own[4 * j], own[4 * j + 1], own[4 * j + 2], own[4 * j + 3]);
+          if (r != rank) {
+            const uint4 y = csa::ld_shared_v4(inbox(r, s) + 2048 * j);
+            x = make_float4(__uint_as_float(y.x), __uint_as_float(y.y), __uint_as_float(y.z), __uint_as_float(y.w));
+          }
+          v[4 * j] += x.x;
+          v[4 * j + 1] += x.y;
+          v[4 * j + 2] += x.z;
+          v[4 * j + 3] += x.w;
+        }
+      }
+      // two heads at a time: even lanes end with values (lane, lane + 1) of the first, odd lanes with values
+      // (lane - 1, lane) of the second
+      uint32_t two[8];
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
+        const __nv_bfloat162 pair = __floats2bfloat162_rn(odd ? got : v[j], odd ? v[j + 1] : got);
+        two[j / 2] = *reinterpret_cast<const uint32_t*>(&pair);
       }
 #pragma unroll
-      for (int j = 0; j < 4; j += 2) {  // as in write_out
-        const float got = __shfl_xor_sync(0xFFFFFFFFu, odd ? v[j] : v[j + 1], 1);
-        const __nv_bfloat162 two = odd ? __floats2bfloat162_rn(got, v[j + 1]) : __floats2bfloat162_rn(v[j], got);
-        if (h + j + odd < heads)
-          *reinterpret_cast<__nv_bfloat162*>(out + static_cast<int64_t>(h + j + odd) * kDim + 128 * d + (lane & ~1)) = two;
-      }
+      for (int j = 0; j < 16; j += 2)
+        if (h + j + odd < heads) *reinterpret_cast<uint32_t*>(out + static_cast<int64_t>(h + j) * kDim + 128 * d) = two[j / 2];
     }
   }
 }

@@ -217,14 +217,6 @@ __device__ __forceinline__ void tmem_ld_16x64(uint32_t taddr, uint32_t (&v)[32])
       : "memory");
 }
 
-// 32 lanes x 32 bits, 4 consecutive columns: thread t reads lane (base + t).
-__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&v)[4]) {
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
-               : "r"(taddr)
-               : "memory");
-}
-
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // 32 lanes x 32 bits, 16 consecutive columns: thread t writes lane (base + t).
