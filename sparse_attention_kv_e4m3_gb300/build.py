@@ -55,7 +55,8 @@ def build(force: bool = False, verbose: bool = False) -> str:
 # (for example a short pipeline wait limit and a delayed producer, to exercise
 # the bounded-wait path). Each goes to its own file next to the product library.
 TEST_VARIANTS = {
-    "timeout": ["-DCSA_TEST_WAIT_LIMIT_NS=20000ull", "-DCSA_TEST_WALKER_DELAY_NS=200000ull"],
+    "timeout": ["-DCSA_TEST_WAIT_LIMIT_NS=20000ull", "-DCSA_TEST_WALKER_DELAY_NS=200000ull",
+                "-DCSA_TEST_LOADER_DELAY_NS=200000ull"],
 }
 
 

@@ -378,6 +378,7 @@ __device__ void role_load_regs(const Kernel& K, Smem<kRope>& S, int32_t* flags) 
   const int t = threadIdx.x - 32 * kSoftmaxWarps, lane = t & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
+  csa::test_delay();
   Pieces run(K, S);
   if (!run.more()) return;
   // A tile's records are found in two steps, one tile apart, so that no load waits for another one just
@@ -500,6 +501,7 @@ __device__ void role_load_tma(const Kernel& K, const Maps& M, Smem<kRope>& S, in
   const int lane = threadIdx.x & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
+  csa::test_delay();
   Pieces run(K, S), ahead = run;
   if (!run.more()) return;
   struct Tile {
@@ -528,11 +530,12 @@ __device__ void role_load_tma(const Kernel& K, const Maps& M, Smem<kRope>& S, in
   };
   static_assert(kTile == kPageRecs, "a tile is a page");
   Tile now = next_tile(), next = next_tile();
-  uint32_t g = 0, piece = 0, landed = 0;
-  bool ok = true;
-  for (; ok && run.more(); run.next(K), ++piece) {
-    ok = warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop);
+  uint32_t g = 0, piece = 0, landed = 0, filled[2] = {0, 0};  // tiles whose halves were begun (or handed over)
+  bool ok = true, landing = false;                            // landing: copies to kBarLand are in flight
+  for (; run.more(); run.next(K)) {
+    ok = ok && warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop);
     if (!ok) break;
+    ++piece;
     if (lane == 0) {
       const uint32_t bar = bars + 8 * kBarQFull;
       csa::mbar_arrive_expect_tx(bar, sizeof(S.q));
@@ -558,28 +561,34 @@ __device__ void role_load_tma(const Kernel& K, const Maps& M, Smem<kRope>& S, in
           csa::mbar_arrive_expect_tx(bar, columns * kColBytes);
           for (int c = 0; c < columns; ++c) csa::tma_tile_4d(dst + column(c) * kColBytes, &M.pages, 0, column(c), 0, now.page, bar);
         }
+        if (whole) filled[half] = g + 1;
         if (whole) continue;
         if (now.rows > 0) {
-          ok = ok && warp_wait(bar, landed & 1, stop);
-          ++landed;
+          landing = true;
+          ok = warp_wait(bar, landed & 1, stop);
           if (!ok) break;
+          landing = false;
+          ++landed;
         }
         for (int c = 0; c < columns; ++c)
           for (int b = now.rows * 128 + 16 * lane; b < kColBytes; b += 512) csa::st_shared_v4(dst + column(c) * kColBytes + b, 0, 0, 0, 0);
         csa::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(full);
+        filled[half] = g + 1;
       }
       if (!ok) break;
       now = next;
       next = next_tile();
     }
   }
-  // No copy of this CTA is in flight when it leaves. Where a wait has run out, those begun land within the limit.
-  if (!ok && lane == 0) {
-    csa::mbar_wait_drain(bars + 8 * kBarQFull, piece & 1);
-    csa::mbar_wait_drain(bars + 8 * kBarLand, landed & 1);
-    for (uint32_t k = 0; k < 4; ++k) csa::mbar_wait_drain(bars + 8 * (kBarCFull + k), ((k >> 1) == (g & 1) ? g >> 1 : (g - 1) >> 1) & 1);
+  // no copy of this CTA is in flight when it leaves
+  if (lane == 0) {
+    if (piece > 0) csa::mbar_wait_drain(bars + 8 * kBarQFull, (piece - 1) & 1);
+    for (int half = 0; half < 2; ++half)
+      for (uint32_t k = filled[half] > 2 ? filled[half] - 2 : 0; k < filled[half]; ++k)
+        csa::mbar_wait_drain(bars + 8 * (kBarCFull + 2 * (k & 1) + half), (k >> 1) & 1);
+    if (landing) csa::mbar_wait_drain(bars + 8 * kBarLand, landed & 1);
   }
   __syncwarp();
 }

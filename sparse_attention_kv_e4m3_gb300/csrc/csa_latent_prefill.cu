@@ -144,8 +144,9 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
     for (int c = 0; c < kQCols; ++c)
       csa::tma_tile_3d(smem_u32(S.q[t]) + c * kColBytes, &M.q, 64 * c, head, R.q0 + first + t * kTile, bars + 8 * (kBarQFull + t));
   };
-  bool ok = true;
-  int k_done = 0, v_done = 0, landed = 0;
+  csa::test_delay();
+  bool ok = true, landing = false;  // landing: a copy to kBarVLand is in flight
+  int k_done = 0, v_done[2] = {0, 0}, landed = 0;  // tiles loaded, of V by halves
   const uint32_t ring = smem_u32(S.ring[0]);
   auto freed = [&](int bar, int j) {  // what tile j held there has been read (nothing held it where j < 0)
     ok = ok && (j < 0 || warp_wait(bars + 8 * (bar + (j & 1)), (j >> 1) & 1, stop));
@@ -156,12 +157,16 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
     const uint32_t bar = bars + 8 * (kBarKFull + (j & 1));
     const int row = R.k0 + j * kTile;
     if (lane == 0) {
-      csa::mbar_arrive_expect_tx(bar, kQBytes);
+      csa::mbar_arrive_expect_tx(bar, kColBytes);
       csa::tma_tile_3d(ring + ring_slot(j, 0) * kColBytes, &M.k, 0, head, row, bar);
     }
     k_done = j + 1;
-    if (!freed(kBarVEmpty, j - 2)) return;
+    if (!freed(kBarVEmpty, j - 2)) {
+      if (lane == 0) mbar_arrive(bar);  // no more is coming: the first chunk's landing can be waited for
+      return;
+    }
     if (lane == 0) {
+      csa::mbar_arrive_expect_tx(bar, 2 * kColBytes);
       csa::tma_tile_3d(ring + ring_slot(j, 1) * kColBytes, &M.k, 64, head, row, bar);
       csa::tma_tile_2d(ring + ring_slot(j, 2) * kColBytes, &M.rope, 0, row, bar);
     }
@@ -179,9 +184,13 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
         for (int c = 0; c < kV / 64; ++c)
           csa::tma_tile_3d(dst + c * (kColBytes / 2), &M.v, 64 * c, head, R.k0 + j * kTile + 64 * half, land);
       }
+      if (whole) v_done[half] = j + 1;
       if (whole) continue;
       if (rows > 0) {
+        landing = true;
         ok = ok && warp_wait(land, landed & 1, stop);
+        if (!ok) return;
+        landing = false;
         ++landed;
       }
       for (int c = 0; c < kV / 64; ++c)
@@ -189,8 +198,8 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
       csa::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
+      v_done[half] = j + 1;
     }
-    v_done = j + 1;
   };
   // in the order in which the MMAs give the chunks back
   load_q(0);
@@ -202,15 +211,15 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
     load_v(j);
     if (ok && j + 1 < n) load_k(j + 1);
   }
-  // no copy of this CTA is in flight when it leaves (the last waits of each barrier; after a wait that ran out, some of
-  // them end by their time limit)
+  // no copy of this CTA is in flight when it leaves
   if (lane == 0) {
     for (int t = 0; t < 2; ++t)
       if (nt[t] > 0) csa::mbar_wait_drain(bars + 8 * (kBarQFull + t), 0);
     for (int j = max(k_done - 2, 0); j < k_done; ++j) csa::mbar_wait_drain(bars + 8 * (kBarKFull + (j & 1)), (j >> 1) & 1);
-    for (int j = max(v_done - 2, 0); j < v_done; ++j)
-      for (int half = 0; half < 2; ++half) csa::mbar_wait_drain(bars + 8 * (kBarVFull + 2 * (j & 1) + half), (j >> 1) & 1);
-    if (!ok) csa::mbar_wait_drain(bars + 8 * kBarVLand, landed & 1);
+    for (int half = 0; half < 2; ++half)
+      for (int j = max(v_done[half] - 2, 0); j < v_done[half]; ++j)
+        csa::mbar_wait_drain(bars + 8 * (kBarVFull + 2 * (j & 1) + half), (j >> 1) & 1);
+    if (landing) csa::mbar_wait_drain(bars + 8 * kBarVLand, landed & 1);
   }
   __syncwarp();
 }
@@ -471,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     csa::mbar_init(bars + 8 * kBarDrain, 1);
     for (int k = 0; k < 2; ++k) {
       csa::mbar_init(bars + 8 * (kBarQFull + k), 1);
-      csa::mbar_init(bars + 8 * (kBarKFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarKFull + k), 2);  // K comes in two parts
       csa::mbar_init(bars + 8 * (kBarKEmpty + k), 1);
       csa::mbar_init(bars + 8 * (kBarVFull + 2 * k), 1);
       csa::mbar_init(bars + 8 * (kBarVFull + 2 * k + 1), 1);

@@ -136,6 +136,16 @@ __device__ __forceinline__ void bulk_prefetch_l2(const void* p, uint32_t bytes) 
   asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// A test build of the library holds the loaders back by this much, so that the other roles' waits run out.
+#ifdef CSA_TEST_LOADER_DELAY_NS
+__device__ __forceinline__ void test_delay() {
+  const uint64_t t0 = globaltimer_ns();
+  while (globaltimer_ns() - t0 < CSA_TEST_LOADER_DELAY_NS) __nanosleep(1000);
+}
+#else
+__device__ __forceinline__ void test_delay() {}
+#endif
+
 // ----------------------------------------------------------------- clusters
 
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
