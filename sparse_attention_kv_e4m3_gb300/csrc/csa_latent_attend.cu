@@ -1073,24 +1073,26 @@ __global__ void __launch_bounds__(Warps<kLoad>::kThreads, 1)
   if (flags && K.A.dev_status && lane == 0) atomicOr(K.A.dev_status, flags);
 }
 
-// Joins a cut unit: one block a (possibly cut) unit and head. Its parts are those of run `o.run` (which
-// ends inside the unit) and of the runs after it up to the unit's end. Each warp adds every eighth
-// part, the warps' sums are added in their order, so the result does not depend on timing. Launched as a
-// programmatic dependent of the attention kernel: its blocks are in place when that one ends.
+// Joins a cut unit. Its parts are those of run `o.run` (which ends inside the unit) and of the runs after it up to the
+// unit's end, added in that order (by eight warps: each every eighth, then the warps' sums in their order), so the
+// result does not depend on timing. Launched as a programmatic dependent of the attention kernel: its blocks are in
+// place when that one ends. kJoinWarps a head where a unit has many parts; one a head where it has a few (2048
+// units of 8 tiles: 39 us with eight, most of them idle).
 constexpr int kJoinWarps = 8;
+template <bool kMany>
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, int grid) {
   const csa_latent_attend_args& A = K.A;
-  __shared__ float s_o[kJoinWarps][kDim], s_l[kJoinWarps];
-  const int head = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int head = kMany ? blockIdx.y : blockIdx.y * kJoinWarps + warp;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Open o = K.opens[blockIdx.x];
-  if (!o.cut) return;
   const int h = group_of(K, o.unit) * kHeads + head;
-  if (h >= A.num_heads) return;
+  if (!o.cut || (kMany && h >= A.num_heads)) return;
   // runs o.run .. last; a run without tiles has no part
   const int64_t end = o.begin + o.tiles;
   int last = static_cast<int>(min((end * grid - 1) / o.total, static_cast<int64_t>(grid) - 1)) + 1;
   while (last >= grid || run_start(o.total, last, grid) >= end) --last;
+  if (h >= A.num_heads) return;
   auto part_of = [&](int r) { return K.parts + (2 * static_cast<int64_t>(r) + (r == o.run)) * kPartFloats; };
   auto there = [&](int r) { return r <= last && run_start(o.total, r, grid) < run_start(o.total, r + 1, grid); };
   float top = -INFINITY;
@@ -1102,7 +1104,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, i
   float4 v[4] = {};
   const float ref = top == -INFINITY ? 0.f : top;
 #pragma unroll 2
-  for (int r = o.run + warp; r <= last; r += kJoinWarps) {
+  for (int r = o.run + (kMany ? warp : 0); r <= last; r += kMany ? kJoinWarps : 1) {
     if (!there(r)) continue;
     const float* part = part_of(r);
     const float4* x = reinterpret_cast<const float4*>(part + head * kDim);
@@ -1114,24 +1116,34 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K, i
       v[k] = make_float4(fmaf(y.x, w, v[k].x), fmaf(y.y, w, v[k].y), fmaf(y.z, w, v[k].z), fmaf(y.w, w, v[k].w));
     }
   }
-#pragma unroll
-  for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(s_o[warp])[lane + 32 * k] = v[k];
-  if (lane == 0) s_l[warp] = l;
-  __syncthreads();
-  l = 0.f;
-  float2 sum = make_float2(0.f, 0.f);
-#pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) {
-    const float2 y = reinterpret_cast<const float2*>(s_o[w])[threadIdx.x];
-    sum.x += y.x;
-    sum.y += y.y;
-    l += s_l[w];
-  }
-  const float inv = l > 0.f ? 1.f / l : l;
   const int64_t row = static_cast<int64_t>(row_of(K, o.unit)) * A.num_heads + h;
-  reinterpret_cast<__nv_bfloat162*>(static_cast<__nv_bfloat16*>(A.out) + row * kDim)[threadIdx.x] =
-      __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
-  if (A.lse && threadIdx.x == 0) A.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(A.out) + row * kDim;
+  if constexpr (kMany) {
+    __shared__ float s_o[kJoinWarps][kDim], s_l[kJoinWarps];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) reinterpret_cast<float4*>(s_o[warp])[lane + 32 * k] = v[k];
+    if (lane == 0) s_l[warp] = l;
+    __syncthreads();
+    l = 0.f;
+    float2 sum = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kJoinWarps; ++w) {
+      const float2 y = reinterpret_cast<const float2*>(s_o[w])[threadIdx.x];
+      sum.x += y.x;
+      sum.y += y.y;
+      l += s_l[w];
+    }
+    const float inv = l > 0.f ? 1.f / l : l;
+    reinterpret_cast<__nv_bfloat162*>(out)[threadIdx.x] = __floats2bfloat162_rn(sum.x * inv, sum.y * inv);
+  } else {
+    const float inv = l > 0.f ? 1.f / l : l;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[k].x * inv, v[k].y * inv), b = __floats2bfloat162_rn(v[k].z * inv, v[k].w * inv);
+      reinterpret_cast<uint2*>(out)[lane + 32 * k] = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    }
+  }
+  if (A.lse && (kMany ? threadIdx.x : lane) == 0) A.lse[row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // CTAs of the call: one an SM, fewer when there cannot be as many tiles.
@@ -1145,8 +1157,8 @@ int grid_cap(const csa_latent_attend_args* a) {
 constexpr size_t kOpenBytes = (kMaxGrid * sizeof(Open) + 255) / 256 * 256;
 
 // CTAs that share a unit: where every unit is short (8 tiles a CTA at most) and there are fewer units than
-// SMs, the largest power of two up to 8 that still fits the SMs; else 0, the runs. Measured on 64 rows of
-// 8 tiles: see the note at cluster_join's call.
+// SMs, the largest power of two up to 8 that still fits the SMs; else 0, the runs. 64 rows of 8 tiles: 28.5 us in
+// clusters of two, 49 us cut into 152 runs (whose parts are 28 MB, against 38 MB of records).
 int cluster_of(const csa_latent_attend_args* a, int sms) {
   const int64_t units = static_cast<int64_t>(a->num_q) * ((a->num_heads + kHeads - 1) / kHeads);
   const int64_t per = a->idx ? (a->top + kTile - 1) / kTile : a->pt_stride;
@@ -1258,7 +1270,9 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
                             : (rope ? launch_bf16<64>(K, grid, dev, s) : launch_bf16<0>(K, grid, dev, s));
   if (ls != CSA_OK || grid == 1 || K.cluster) return ls;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, a->num_heads < kHeads ? a->num_heads : kHeads);
+  const bool many = units * kJoinWarps < grid;  // parts a unit, on average
+  const int heads = a->num_heads < kHeads ? a->num_heads : kHeads;
+  cfg.gridDim = dim3(K.by_unit ? static_cast<unsigned>(units) : grid, many ? heads : (heads + kJoinWarps - 1) / kJoinWarps);
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
@@ -1266,5 +1280,5 @@ extern "C" csa_status csa_latent_attend(const csa_latent_attend_args* a, void* w
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel, K, grid) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  return cudaLaunchKernelEx(&cfg, many ? join_kernel<true> : join_kernel<false>, K, grid) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
