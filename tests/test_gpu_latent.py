@@ -374,6 +374,33 @@ def test_attend_same_bits_each_time_on_streams_and_in_graphs():
             assert torch.equal(o, out) and torch.equal(l, lse)
 
 
+def test_attend_on_two_streams_at_once():
+    """Calls that overlap on two streams, each with the workspace kept for its stream."""
+    a, b = Attend([30000, 500], 64, seed=13), Attend([20000, 9000, 3], 128, 64, "mxfp4", seed=14)
+    want = [x.check() for x in (a, b)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = []
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for x, s in zip((a, b), streams):
+            with torch.cuda.stream(s):
+                got.append(latent.csa_latent_attend(x.q, x.cache, x.table, x.lens, scale=x.scale))
+    torch.cuda.synchronize()
+    for k, (o, l) in enumerate(got):
+        assert torch.equal(o, want[k % 2][0]) and torch.equal(l, want[k % 2][1])
+
+
+def test_attend_more_rows_than_a_block_has_threads():
+    """The plan's running sums over rows: several rows a thread, empty rows between others."""
+    lens = [(b * 37) % 130 if b % 3 else 0 for b in range(1500)]
+    a = Attend(lens, 4, 0, "bf16", req=[b % 5 for b in range(1500)], seed=15)
+    out, lse = a.run()
+    assert int(a.st) == 0
+    for b in list(range(0, 1500, 61)) + [1498, 1499]:
+        L.hold(out[b], lse[b], a.want(b))
+    assert torch.equal(torch.isneginf(lse[:, 0]).cpu(), torch.tensor(lens) == 0)
+
+
 # ------------------------------------------------------------------ expanded attention
 
 class Prefill:
@@ -457,6 +484,12 @@ def test_prefill_hidden_keys_do_not_matter():
         t[100:190] = math.nan
         t[110] = math.inf
     p.check(skip=(1,))
+
+
+def test_prefill_without_keys():
+    p = Prefill([5, 200], [0, 0], 2, seed=12)
+    out, lse = p.run()
+    assert int(p.st) == 0 and not out.any() and torch.isneginf(lse).all()
 
 
 def test_prefill_many_requests():
