@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
   extern __shared__ int32_t tab_smem[];
   int32_t* s_row = tab_smem;                   // [num_req + 1] running sum of new records
   int32_t* s_fresh = tab_smem + A.num_req + 1;  // [num_req + 1] running sum of new pages
+  int32_t* s_old = tab_smem + 2 * (A.num_req + 1);  // [num_req] old lengths
   __shared__ Scan3 s_warp[kTabThreads / 32];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (A.num_req + kTabThreads - 1) / kTabThreads;
@@ -92,6 +93,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
     request_lengths(A, r, &o, &n, &ignore);
     s_row[r] = held(at.rows, &bad_len);
     s_fresh[r] = held(at.fresh, &bad_len);
+    s_old[r] = static_cast<int32_t>(o);
     if (first) {
       A.row_start[r] = s_row[r];
       A.kv_start[r] = held(at.kv, &bad_len);
@@ -116,10 +118,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
   if (total_rows > A.n_rows) flags |= CSA_DEV_ROWS;
   for (int64_t j = i0; j < total_fresh; j += step) {
     const int r = last_not_above(s_fresh, A.num_req, static_cast<int32_t>(j));
-    int64_t o, n;
-    bool ignore = false;
-    request_lengths(A, r, &o, &n, &ignore);
-    A.page_table[static_cast<int64_t>(r) * A.pt_stride + pages_of(o) + (j - s_fresh[r])] =
+    A.page_table[static_cast<int64_t>(r) * A.pt_stride + pages_of(s_old[r]) + (j - s_fresh[r])] =
         j < A.n_free ? A.free_pages[j] : -1;
   }
   for (int64_t i = i0; i < A.n_rows; i += step) {
@@ -127,9 +126,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
     int64_t slot = -1;
     if (i < total_rows) {
       req = last_not_above(s_row, A.num_req, static_cast<int32_t>(i));
-      int64_t o, n;
-      bool ignore = false;
-      request_lengths(A, req, &o, &n, &ignore);
+      const int64_t o = s_old[req];
       pos = static_cast<int32_t>(o + (i - s_row[req]));
       const int64_t p = pos / kPageRecs, a = pages_of(o), j = s_fresh[req] + (p - a);
       int32_t page = -1;
@@ -447,13 +444,13 @@ extern "C" csa_status csa_build_tables(const csa_tables_args* a, void* stream) {
       !aligned(a->row_req, 4) || !aligned(a->row_pos, 4) || !aligned(a->row_len, 4) || !aligned(a->row_slot, 8) ||
       !aligned(a->row_start, 4) || !aligned(a->kv_start, 4) || !aligned(a->taken, 4) || !aligned(a->dev_status, 4))
     return CSA_ERR_ALIGNMENT;
-  const size_t smem = 2 * sizeof(int32_t) * (static_cast<size_t>(a->num_req) + 1);
+  const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(a->num_req) + 1);
   if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                static_cast<int>(smem)) != cudaSuccess)
     return CSA_ERR_CUDA;
   static int kept[kMaxDevices];  // of calls of up to about 1000 requests
   unsigned grid = 1;
-  const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 8192 ? 8192 : smem, smem <= 8192 ? kept : nullptr,
+  const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 12288 ? 12288 : smem, smem <= 12288 ? kept : nullptr,
                                   a->n_rows + a->num_req, kTabRowsPerBlock, &grid);
   if (st != CSA_OK) return st;
   build_tables_kernel<<<grid, kTabThreads, smem, static_cast<cudaStream_t>(stream)>>>(*a);
