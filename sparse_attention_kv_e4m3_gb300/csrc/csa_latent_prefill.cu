@@ -12,22 +12,27 @@ using csa::mbar_arrive;
 using csa::mbar_wait;
 using csa::smem_u32;
 
-// The kernel. A CTA takes 256 query rows of one request and head as two tiles of 128, and
-// runs over tiles of 128 keys: S = Q K^T (128 x 128 over 192), p = 2^(S c - m c) with
-// c = scale log2 e, O = O + P V, l = sum p, out = O / l, lse = ln 2 (m c + log2 l). m is the
-// first key tile's maximum of the row and moves only when a tile exceeds it by 2^8 (any reference is
-// right; a stale one only scales O and l alike), so that O is rarely rescaled.
+// The kernel. An item is 256 query rows of one request and head, as two tiles of 128; it runs over tiles of 128 keys:
+// S = Q K^T (128 x 128 over 192), p = 2^(S c - m c) with c = scale log2 e, O = O + P V, l = sum p, out = O / l,
+// lse = ln 2 (m c + log2 l). m is the first key tile's maximum of the row and moves only when a tile exceeds it by 2^8 (any
+// reference is right; a stale one only scales O and l alike), so that O is rarely rescaled.
 //
 // Bound by the tensor cores (20 MMAs of 64 clocks a tile pair) while the exponentials of one query
 // tile run under the MMAs of the other. A row of S is a TMEM lane and belongs to one thread, P goes back over
 // S in TMEM as the A operand of O, V is read from shared memory as it lies (N-major).
+// 4096 rows over 16384 keys, 16 heads: 412 us, 1.46 PFLOP/s. 8 prompts of 130 to 2048, 32 heads: 148 us, 0.94 PFLOP/s:
+// there items are 1 to 16 key tiles, and what is lost is their ends, where the softmax warps write 64 KB (5 k clocks a tile).
+//
+// One block an item, but a block that is at the end of its item takes the place of one that has not started yet, so that the next
+// item's Q and K come in and its first S is computed while the softmax warps write the last one's output (171 us with a block
+// for each item: its start, the first loads and the last O were 42% of the time; the longer case lost 1% then).
 //
 // Shared memory: Q 2 x 48 KB and a ring of eight 16 KB chunks through which K(0), V(0), K(1), V(1), ... go in
-// turn (K(j) takes the place of K(j - 2)'s end and V(j - 2), V(j) that of K(j - 1)'s beginning), so that V has two
+// turn (K(g) takes the place of K(g - 2)'s end and V(g - 2), V(g) that of K(g - 1)'s beginning), so that V has two
 // and a half of the MMAs' rounds to arrive and K one: 224 KB, one CTA an SM. TMEM: S0, S1, O0, O1, all 512 columns.
 // Warps 0-3 and 4-7: softmax and output of the two tiles. Warp 8 issues the MMAs.
 // Warp 9: TMA; it also zeroes the value rows past a request's last key, which belong to
-// others and may hold NaN (P is 0 there, but 0 x NaN is not).
+// others and may hold NaN (P is 0 there, but 0 x NaN is not). Warp 10 finds the items.
 constexpr int kNope = CSA_PREFILL_NOPE, kRope = CSA_PREFILL_ROPE, kV = CSA_PREFILL_V;
 constexpr int kTile = 128;                            // query rows, keys
 constexpr int kColBytes = kTile * 128;                // 64 values of 128 rows
@@ -35,8 +40,9 @@ constexpr int kQCols = (kNope + kRope) / 64;
 constexpr int kQBytes = kQCols * kColBytes;
 constexpr int kRing = 8;                              // chunks of 16 KB: K is 3 (64 values of 128 keys each), V 2 (64 keys each)
 constexpr int kTileChunks = kQCols + 2;
-constexpr int kSoftmaxWarps = 8, kMmaWarp = 8;
-constexpr int kThreads = 32 * 10;
+constexpr int kSoftmaxWarps = 8, kMmaWarp = 8, kLoadWarp = 9;  // and warp 10: role_next
+constexpr int kThreads = 32 * 11;
+constexpr int kAhead = 3;                             // key tiles before an item's last at which the next one is looked for
 constexpr uint32_t kTmemCols = 512, kTmemO = 256;     // S of tile t at 128 t, O at 256 + 128 t
 constexpr float kGrow = 8.0f;                         // log2 of how far p may exceed 1
 
@@ -44,27 +50,37 @@ struct Maps {
   CUtensorMap q, k, rope, v;
 };
 
+// Bounds of a request.
+struct Request {
+  int32_t q0, k0, nq, nk;
+};
+
+struct Item {
+  Request r;
+  int32_t first, head;  // first query row in the request, negative after the last item
+  int32_t n[2];         // key tiles that each query tile sees any key of
+};
+
 struct Smem {
   uint8_t q[2][kQBytes];
   uint8_t ring[kRing][kColBytes];
-  uint64_t bars[24];
+  uint64_t bars[28];
+  alignas(16) uint8_t next[16];          // the answer to a request for another block's place
+  Item items[2];
+  int32_t before[kThreads];              // pairs of query tiles before each thread's requests
   int32_t warp_pairs[kThreads / 32];
-  int32_t total, request, first;  // of the item: its request and its first query row there
+  int32_t total;
   uint32_t tmem;
   int abort;
 };
 // K, V: by the key tile's parity (V also by half: 2 * parity + half); S, P, O, Q: by query tile
 enum { kBarQFull = 0, kBarKFull = 2, kBarKEmpty = 4, kBarVFull = 6, kBarVEmpty = 10, kBarSFull = 12, kBarPFull = 14,
-       kBarOFull = 16, kBarVLand = 18, kBarDrain };
+       kBarOFull = 16, kBarVLand = 18, kBarDrain, kBarQEmpty = 20, kBarItemFull = 22, kBarItemEmpty = 24, kBarNext = 26, kBarAsk };
 
-// Where chunk i of key tile j lies: K 0 .. 2, V 3, 4.
-__device__ __forceinline__ uint32_t ring_slot(int j, int i) { return static_cast<uint32_t>(kTileChunks * j + i) % kRing; }
+// Where chunk i of the CTA's key tile g lies: K 0 .. 2, V 3, 4.
+__device__ __forceinline__ uint32_t ring_slot(uint32_t g, int i) { return (kTileChunks * g + i) % kRing; }
 
-// Bounds of request r, false where they descend or leave the tensors.
-struct Request {
-  int32_t q0, k0, nq, nk;
-};
-
+// False where request r's bounds descend or leave the tensors.
 __device__ __forceinline__ bool request_of(const csa_latent_prefill_args& A, int r, Request* R) {
   const int32_t q0 = A.q_start[r], q1 = A.q_start[r + 1], k0 = A.kv_start[r], k1 = A.kv_start[r + 1];
   if (q0 < 0 || q1 < q0 || q1 > A.total_q || k0 < 0 || k1 < k0 || k1 > A.total_k) return false;
@@ -81,48 +97,6 @@ __device__ __forceinline__ int pairs_of(const csa_latent_prefill_args& A, int r,
   return (R.nq + 2 * kTile - 1) / (2 * kTile);
 }
 
-// Item `at` (from the last pair of query tiles backwards: the longest first, where requests are causal).
-__device__ void find_item(const csa_latent_prefill_args& A, Smem& S, int at, bool* bad) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (A.num_req + kThreads - 1) / kThreads;
-  const int r0 = min(tid * per, A.num_req), r1 = min(r0 + per, A.num_req);
-  int mine = 0;
-  for (int r = r0; r < r1; ++r) mine += pairs_of(A, r, bad);
-  int incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) S.warp_pairs[warp] = incl;
-  __syncthreads();
-  int before = incl - mine, total = 0;
-  for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) before += S.warp_pairs[w];
-    total += S.warp_pairs[w];
-  }
-  if (tid == 0) S.total = total;
-  const int want = total - 1 - at;
-  if (want >= before && want < before + mine) {
-    for (int r = r0; r < r1; ++r) {
-      bool ignore = false;
-      const int n = pairs_of(A, r, &ignore);
-      if (want < before + n) {
-        S.request = r;
-        S.first = (want - before) * 2 * kTile;
-        break;
-      }
-      before += n;
-    }
-  }
-  __syncthreads();
-}
-
-// A whole warp's bounded wait, with one answer for all lanes.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, stop));
-}
-
 // Key tiles that query tile t (rows first + 128 t ..) sees any key of.
 __device__ __forceinline__ int key_tiles(const csa_latent_prefill_args& A, const Request& R, int first, int t) {
   const int row = first + t * kTile;
@@ -132,59 +106,193 @@ __device__ __forceinline__ int key_tiles(const csa_latent_prefill_args& A, const
   return seen <= 0 ? 0 : static_cast<int>((seen + kTile - 1) / kTile);
 }
 
-__device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem& S, const Request& R, int first, int head) {
+__device__ __forceinline__ int running_sum(int x) {  // over the lanes
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, x, o);
+    if ((threadIdx.x & 31) >= o) x += up;
+  }
+  return x;
+}
+
+__device__ __forceinline__ int requests_a_thread(const csa_latent_prefill_args& A) { return (A.num_req + kThreads - 1) / kThreads; }
+
+// Sums of the requests' pairs of query tiles, a run of requests a thread.
+__device__ void sum_pairs(const csa_latent_prefill_args& A, Smem& S, bool* bad) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, per = requests_a_thread(A);
+  const int r0 = min(tid * per, A.num_req), r1 = min(r0 + per, A.num_req);
+  int mine = 0;
+  for (int r = r0; r < r1; ++r) mine += pairs_of(A, r, bad);
+  const int incl = running_sum(mine);
+  if (lane == 31) S.warp_pairs[warp] = incl;
+  __syncthreads();
+  int before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += S.warp_pairs[w];
+    total += S.warp_pairs[w];
+  }
+  S.before[tid] = before;
+  if (tid == 0) S.total = total;
+}
+
+// Item of block `at`, by one warp: pairs from the last backwards (the longest first, where requests are causal),
+// the heads of a pair next to one another. False past the last.
+__device__ bool find_item(const csa_latent_prefill_args& A, Smem& S, uint32_t at, Item* I) {
+  const int lane = threadIdx.x & 31, per = requests_a_thread(A);
+  const int pair = static_cast<int>(at / A.num_heads), want = S.total - 1 - pair;
+  if (want < 0) return false;
+  int run = 0;  // the last run of requests that begins at or before the pair
+  for (int k = lane; k < kThreads; k += 32)
+    if (S.before[k] <= want) run = k;
+  run = __reduce_max_sync(0xFFFFFFFFu, run);
+  int before = S.before[run];
+  bool ignore = false;
+  for (int r0 = run * per; r0 < A.num_req; r0 += 32) {
+    const int n = r0 + lane < A.num_req ? pairs_of(A, r0 + lane, &ignore) : 0, incl = before + running_sum(n);
+    const uint32_t here = __ballot_sync(0xFFFFFFFFu, want < incl);
+    if (here) {
+      const int who = __ffs(here) - 1;
+      const int start = __shfl_sync(0xFFFFFFFFu, incl - n, who);
+      if (!request_of(A, r0 + who, &I->r)) return false;
+      I->first = (want - start) * 2 * kTile;
+      I->head = static_cast<int>(at % A.num_heads);
+      for (int t = 0; t < 2; ++t) I->n[t] = key_tiles(A, I->r, I->first, t);
+      return true;
+    }
+    before = __shfl_sync(0xFFFFFFFFu, incl, 31);
+  }
+  return false;
+}
+
+// A whole warp's bounded wait, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, stop));
+}
+
+// The same, with a limit for each 2^18 of the key tiles that others may be busy with meanwhile (they take a quarter of it).
+__device__ __forceinline__ bool patient_wait(uint32_t bar, uint32_t parity, volatile int* stop, int tiles) {
+  for (int k = tiles >> 18; k > 0 && !*stop; --k) {
+    volatile int over = 0;
+    if (warp_wait(bar, parity, &over)) return true;
+  }
+  return warp_wait(bar, parity, stop);
+}
+
+// Waits for the item at `at`; false after the last one.
+__device__ __forceinline__ bool next_item(Smem& S, uint32_t at, int idle) {
+  return patient_wait(smem_u32(S.bars) + 8 * (kBarItemFull + (at & 1)), (at >> 1) & 1, &S.abort, idle) && S.items[at & 1].first >= 0;
+}
+
+__device__ __forceinline__ void done_with_item(Smem& S, uint32_t at) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(smem_u32(S.bars) + 8 * (kBarItemEmpty + (at & 1)));
+}
+
+// Hands out the items: the block's own, then those of blocks that have not started yet, whose places it asks for,
+// one at a time, when little of the last item is left to load. What the next item begins with is on its way to L2
+// before it is handed out.
+__device__ void role_next(const csa_latent_prefill_args& A, const Maps& M, Smem& S) {
+  const int lane = threadIdx.x & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), next = smem_u32(S.next);
+  Item I;
+  bool ok = true, more = find_item(A, S, blockIdx.x, &I);
+  for (uint32_t at = 0;; ++at) {
+    if (!more) I.first = -1;
+    ok = ok && (at < 2 || warp_wait(bars + 8 * (kBarItemEmpty + (at & 1)), ((at - 2) >> 1) & 1, stop));
+    if (!ok) return;
+    if (lane == 0) {
+      S.items[at & 1] = I;
+      mbar_arrive(bars + 8 * (kBarItemFull + (at & 1)));
+    }
+    __syncwarp();
+    if (!more || !patient_wait(bars + 8 * kBarAsk, at & 1, stop, max(I.n[0], I.n[1]))) return;
+    if (lane == 0) {
+      csa::mbar_arrive_expect_tx(bars + 8 * kBarNext, 16);
+      csa::cancel_next_block(next, bars + 8 * kBarNext);
+    }
+    __syncwarp();
+    if (!warp_wait(bars + 8 * kBarNext, at & 1, stop)) {
+      csa::mbar_wait_drain(bars + 8 * kBarNext, at & 1);
+      return;
+    }
+    uint32_t block = 0;
+    more = csa::cancelled_block(next, &block) && find_item(A, S, block, &I);
+    csa::fence_proxy_async_smem();  // the answer is read before the next one is asked for
+    __syncwarp();
+    if (more && lane == 0) {
+      for (int t = 0; t < 2; ++t)
+        for (int c = 0; I.n[t] > 0 && c < kQCols; ++c) csa::tma_prefetch_3d(&M.q, 64 * c, I.head, I.r.q0 + I.first + t * kTile);
+      if (max(I.n[0], I.n[1]) > 0) {
+        for (int c = 0; c < 2; ++c) csa::tma_prefetch_3d(&M.k, 64 * c, I.head, I.r.k0);
+        csa::tma_prefetch_2d(&M.rope, 0, I.r.k0);
+        for (int c = 0; c < 2; ++c) csa::tma_prefetch_3d(&M.v, 64 * c, I.head, I.r.k0);
+      }
+    }
+  }
+}
+
+__device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem& S) {
   const int lane = threadIdx.x & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
-  const int nt[2] = {key_tiles(A, R, first, 0), key_tiles(A, R, first, 1)}, n = max(nt[0], nt[1]);
-  if (n == 0) return;
-  auto load_q = [&](int t) {
-    if (lane != 0 || nt[t] == 0) return;
-    csa::mbar_arrive_expect_tx(bars + 8 * (kBarQFull + t), kQBytes);
-    for (int c = 0; c < kQCols; ++c)
-      csa::tma_tile_3d(smem_u32(S.q[t]) + c * kColBytes, &M.q, 64 * c, head, R.q0 + first + t * kTile, bars + 8 * (kBarQFull + t));
-  };
+  Item I;
   csa::test_delay();
   bool ok = true, landing = false;  // landing: a copy to kBarVLand is in flight
-  int k_done = 0, v_done[2] = {0, 0}, landed = 0;  // tiles loaded, of V by halves
+  // over all items: tiles of Q loaded, key tiles loaded (of V by halves), copies landed
+  uint32_t q_done[2] = {0, 0}, k_done = 0, v_done[2] = {0, 0}, landed = 0;
   const uint32_t ring = smem_u32(S.ring[0]);
-  auto freed = [&](int bar, int j) {  // what tile j held there has been read (nothing held it where j < 0)
-    ok = ok && (j < 0 || warp_wait(bars + 8 * (bar + (j & 1)), (j >> 1) & 1, stop));
+  uint32_t base = 0;  // key tiles of the items before
+  auto freed = [&](int bar, uint32_t g, uint32_t back) {  // what key tile g - back held there has been read
+    ok = ok && (g < back || warp_wait(bars + 8 * (bar + ((g - back) & 1)), ((g - back) >> 1) & 1, stop));
     return ok;
   };
+  auto load_q = [&](int t) {
+    ok = ok && (q_done[t] == 0 || warp_wait(bars + 8 * (kBarQEmpty + t), (q_done[t] - 1) & 1, stop));
+    if (!ok) return;
+    if (lane == 0) {
+      const uint32_t bar = bars + 8 * (kBarQFull + t);
+      csa::mbar_arrive_expect_tx(bar, kQBytes);
+      for (int c = 0; c < kQCols; ++c)
+        csa::tma_tile_3d(smem_u32(S.q[t]) + c * kColBytes, &M.q, 64 * c, I.head, I.r.q0 + I.first + t * kTile, bar);
+    }
+    ++q_done[t];
+  };
   auto load_k = [&](int j) {
-    if (!freed(kBarKEmpty, j - 2)) return;
-    const uint32_t bar = bars + 8 * (kBarKFull + (j & 1));
-    const int row = R.k0 + j * kTile;
+    const uint32_t g = base + j;
+    if (!freed(kBarKEmpty, g, 2)) return;
+    const uint32_t bar = bars + 8 * (kBarKFull + (g & 1));
+    const int row = I.r.k0 + j * kTile;
     if (lane == 0) {
       csa::mbar_arrive_expect_tx(bar, kColBytes);
-      csa::tma_tile_3d(ring + ring_slot(j, 0) * kColBytes, &M.k, 0, head, row, bar);
+      csa::tma_tile_3d(ring + ring_slot(g, 0) * kColBytes, &M.k, 0, I.head, row, bar);
     }
-    k_done = j + 1;
-    if (!freed(kBarVEmpty, j - 2)) {
+    k_done = g + 1;
+    if (!freed(kBarVEmpty, g, 2)) {
       if (lane == 0) mbar_arrive(bar);  // no more is coming: the first chunk's landing can be waited for
       return;
     }
     if (lane == 0) {
       csa::mbar_arrive_expect_tx(bar, 2 * kColBytes);
-      csa::tma_tile_3d(ring + ring_slot(j, 1) * kColBytes, &M.k, 64, head, row, bar);
-      csa::tma_tile_2d(ring + ring_slot(j, 2) * kColBytes, &M.rope, 0, row, bar);
+      csa::tma_tile_3d(ring + ring_slot(g, 1) * kColBytes, &M.k, 64, I.head, row, bar);
+      csa::tma_tile_2d(ring + ring_slot(g, 2) * kColBytes, &M.rope, 0, row, bar);
     }
   };
   auto load_v = [&](int j) {
-    if (!freed(kBarKEmpty, j - 1)) return;
+    const uint32_t g = base + j;
+    if (!ok || !freed(kBarKEmpty, g, 1)) return;
     for (int half = 0; half < 2; ++half) {
       // rows of the half that are this request's; the others become zeros before the half is handed over
-      const int rows = min(64, R.nk - j * kTile - 64 * half);
+      const int rows = min(64, I.r.nk - j * kTile - 64 * half);
       const bool whole = rows == 64;
-      const uint32_t full = bars + 8 * (kBarVFull + 2 * (j & 1) + half), land = whole ? full : bars + 8 * kBarVLand;
-      const uint32_t dst = ring + ring_slot(j, kQCols + half) * kColBytes;
+      const uint32_t full = bars + 8 * (kBarVFull + 2 * (g & 1) + half), land = whole ? full : bars + 8 * kBarVLand;
+      const uint32_t dst = ring + ring_slot(g, kQCols + half) * kColBytes;
       if (rows > 0 && lane == 0) {
         csa::mbar_arrive_expect_tx(land, kColBytes);
         for (int c = 0; c < kV / 64; ++c)
-          csa::tma_tile_3d(dst + c * (kColBytes / 2), &M.v, 64 * c, head, R.k0 + j * kTile + 64 * half, land);
+          csa::tma_tile_3d(dst + c * (kColBytes / 2), &M.v, 64 * c, I.head, I.r.k0 + j * kTile + 64 * half, land);
       }
-      if (whole) v_done[half] = j + 1;
+      if (whole) v_done[half] = g + 1;
       if (whole) continue;
       if (rows > 0) {
         landing = true;
@@ -198,27 +306,38 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
       csa::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(full);
-      v_done[half] = j + 1;
+      v_done[half] = g + 1;
     }
   };
-  // in the order in which the MMAs give the chunks back
-  load_q(0);
-  load_k(0);
-  load_q(1);
-  load_v(0);
-  if (n > 1) load_k(1);
-  for (int j = 1; ok && j < n; ++j) {
-    load_v(j);
-    if (ok && j + 1 < n) load_k(j + 1);
+  auto ask = [&] {  // for the next item
+    if (lane == 0) mbar_arrive(bars + 8 * kBarAsk);
+  };
+  for (uint32_t at = 0; ok && next_item(S, at, 0); ++at) {
+    I = S.items[at & 1];
+    done_with_item(S, at);
+    const int n = max(I.n[0], I.n[1]);
+    // in the order in which the MMAs give the chunks back
+    if (I.n[0] > 0) load_q(0);
+    if (n > 0) load_k(0);
+    if (I.n[1] > 0) load_q(1);
+    if (n <= kAhead) ask();
+    if (n > 0) load_v(0);
+    if (n > 1) load_k(1);
+    for (int j = 1; ok && j < n; ++j) {
+      if (j + kAhead == n) ask();
+      load_v(j);
+      if (ok && j + 1 < n) load_k(j + 1);
+    }
+    base += n;
   }
   // no copy of this CTA is in flight when it leaves
   if (lane == 0) {
     for (int t = 0; t < 2; ++t)
-      if (nt[t] > 0) csa::mbar_wait_drain(bars + 8 * (kBarQFull + t), 0);
-    for (int j = max(k_done - 2, 0); j < k_done; ++j) csa::mbar_wait_drain(bars + 8 * (kBarKFull + (j & 1)), (j >> 1) & 1);
+      if (q_done[t] > 0) csa::mbar_wait_drain(bars + 8 * (kBarQFull + t), (q_done[t] - 1) & 1);
+    for (uint32_t g = k_done - min(k_done, 2u); g < k_done; ++g) csa::mbar_wait_drain(bars + 8 * (kBarKFull + (g & 1)), (g >> 1) & 1);
     for (int half = 0; half < 2; ++half)
-      for (int j = max(v_done[half] - 2, 0); j < v_done[half]; ++j)
-        csa::mbar_wait_drain(bars + 8 * (kBarVFull + 2 * (j & 1) + half), (j >> 1) & 1);
+      for (uint32_t g = v_done[half] - min(v_done[half], 2u); g < v_done[half]; ++g)
+        csa::mbar_wait_drain(bars + 8 * (kBarVFull + 2 * (g & 1) + half), (g >> 1) & 1);
     if (landing) csa::mbar_wait_drain(bars + 8 * kBarVLand, landed & 1);
   }
   __syncwarp();
@@ -227,11 +346,10 @@ __device__ void role_load(const csa_latent_prefill_args& A, const Maps& M, Smem&
 // One warp issues all MMAs, S0(j), O1(j - 1), S1(j), O0(j) in turn, with as few waits and commits in
 // between as the buffers need: each costs the tensor cores some 80 clocks, and a thread of its own for
 // each query tile costs more (their MMAs interleave, and every softmax waits longer for its S).
-__device__ void role_mma(const csa_latent_prefill_args& A, Smem& S, const Request& R, int first) {
+// O1 of an item's last key tile waits for the next item's S0, if what that needs is there.
+__device__ void role_mma(const csa_latent_prefill_args& A, Smem& S) {
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem), lead = csa::elect_lane();
-  const int n[2] = {static_cast<int>(csa::uniform(key_tiles(A, R, first, 0))), static_cast<int>(csa::uniform(key_tiles(A, R, first, 1)))};
-  const int most = max(n[0], n[1]);
   constexpr uint32_t idesc_s = csa::idesc_bf16_f32(kTile, kTile);
   constexpr uint32_t idesc_o = csa::idesc_bf16_f32(kTile, kV) | csa::kIdescBMnMajor;
   const csa::Desc q[2] = {csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.q[0]))), csa::Desc(csa::sdesc_kmajor_sw128(smem_u32(S.q[1])))};
@@ -242,124 +360,155 @@ __device__ void role_mma(const csa_latent_prefill_args& A, Smem& S, const Reques
     ok = ok && warp_wait(bars + 8 * bar, parity, stop);
     csa::tc_fence_after();
   };
-  // S of tile t over key tile j. `ahead` looks, while these MMAs run, whether what comes after is there.
-  auto issue_s = [&](auto tile, int j, auto ahead) {
+  // Over the items before: key tiles, and of each query tile those that it sees and its loads of Q.
+  uint32_t base = 0, seen_by[2] = {0, 0}, loads[2] = {0, 0};
+  // S of tile t over key tile g. `ahead` looks, while these MMAs run, whether what comes after is there.
+  auto issue_s = [&](auto tile, uint32_t g, bool last, auto ahead) {
     constexpr int t = decltype(tile)::value;
     if (!ok) return;
 #pragma unroll
     for (int c = 0; c < kQCols; ++c) {
-      const csa::Desc b = k_ring.at(ring_slot(j, c) * kColBytes);
+      const csa::Desc b = k_ring.at(ring_slot(g, c) * kColBytes);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         csa::mma_f16_ss(lead, tmem + t * kTile, q[t].at(c * kColBytes + 32 * x), b.at(32 * x), idesc_s, c > 0 || x > 0);
       if (c == 1) ahead();
     }
     csa::mma_commit_if(lead, bars + 8 * (kBarSFull + t));
+    if (last) csa::mma_commit_if(lead, bars + 8 * (kBarQEmpty + t));
   };
-  // O of tile t over key tile j. `last_reader`: V is free afterwards
-  auto issue_o = [&](auto tile, int j, bool last_reader, auto ahead) {
+  // O of a query tile over key tile g, its p-th there. frees: V is free afterwards
+  struct Value {
+    uint32_t g, p;
+    bool begin, last, frees;
+  };
+  auto issue_o = [&](auto tile, const Value& o, auto ahead) {
     constexpr int t = decltype(tile)::value;
     if (!ok) return;
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
-      const csa::Desc b = v_ring.at(ring_slot(j, kQCols + half) * kColBytes);
+      const csa::Desc b = v_ring.at(ring_slot(o.g, kQCols + half) * kColBytes);
 #pragma unroll
       for (int x = 0; x < 4; ++x)
         csa::mma_f16_ts(lead, tmem + kTmemO + t * kTile, tmem + t * kTile + 32 * half + 8 * x, b.at(2048 * x), idesc_o,
-                        j > 0 || half > 0 || x > 0);
+                        !o.begin || half > 0 || x > 0);
       if (half == 0) ahead();
     }
-    if (last_reader) csa::mma_commit_if(lead, bars + 8 * (kBarVEmpty + (j & 1)));
-    if (j + 1 == n[t]) csa::mma_commit_if(lead, bars + 8 * (kBarOFull + t));
+    if (o.frees) csa::mma_commit_if(lead, bars + 8 * (kBarVEmpty + (o.g & 1)));
+    if (o.last) csa::mma_commit_if(lead, bars + 8 * (kBarOFull + t));
   };
   const std::integral_constant<int, 0> t0;
   const std::integral_constant<int, 1> t1;
   const auto nothing = [] {};
-  // What O of tile t over key tile j needs. A first look that finds it costs nothing: MMAs are still queued.
+  // What O of tile t needs. A first look that finds it costs nothing: MMAs are still queued.
   auto there = [&](int bar, uint32_t parity) { return static_cast<bool>(__all_sync(0xFFFFFFFFu, csa::mbar_test(bars + 8 * bar, parity))); };
-  auto look_o = [&](int t, int j) {
-    const int seen = there(kBarPFull + t, j & 1) + 2 * there(kBarVFull + 2 * (j & 1), (j >> 1) & 1) +
-                     4 * there(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
+  auto look_o = [&](int t, const Value& o) {
+    const int seen = there(kBarPFull + t, o.p & 1) + 2 * there(kBarVFull + 2 * (o.g & 1), (o.g >> 1) & 1) +
+                     4 * there(kBarVFull + 2 * (o.g & 1) + 1, (o.g >> 1) & 1);
     csa::tc_fence_after();
     return seen;
   };
-  auto need_o = [&](int t, int j, int seen) {
-    if (!(seen & 2)) need(kBarVFull + 2 * (j & 1), (j >> 1) & 1);
-    if (!(seen & 4)) need(kBarVFull + 2 * (j & 1) + 1, (j >> 1) & 1);
-    if (!(seen & 1)) need(kBarPFull + t, j & 1);
+  auto need_o = [&](int t, const Value& o, int seen) {
+    if (!(seen & 2)) need(kBarVFull + 2 * (o.g & 1), (o.g >> 1) & 1);
+    if (!(seen & 4)) need(kBarVFull + 2 * (o.g & 1) + 1, (o.g >> 1) & 1);
+    if (!(seen & 1)) need(kBarPFull + t, o.p & 1);
   };
-  if (most > 0) need(kBarKFull, 0);
-  if (n[0] > 0) need(kBarQFull, 0);
-  for (int j = 0; ok && j < most; ++j) {
-    const bool s0 = j < n[0], s1 = j < n[1], o1 = j > 0 && j - 1 < n[1];
-    int seen1 = 0, seen0 = 0;
-    bool seen_k = false;
-    if (s0)
-      issue_s(t0, j, [&] {
-        if (o1) seen1 = look_o(1, j - 1);
-      });
-    if (o1) {
-      need_o(1, j - 1, seen1);
-      issue_o(t1, j - 1, true, nothing);
+  Value late{};  // O1 that is still to be issued
+  bool is_late = false;
+  auto issue_late = [&](int seen) {
+    need_o(1, late, seen);
+    issue_o(t1, late, nothing);
+    is_late = false;
+  };
+  for (uint32_t at = 0; ok; ++at) {
+    if (is_late && !there(kBarItemFull + (at & 1), (at >> 1) & 1)) issue_late(0);
+    if (!ok || !next_item(S, at, 0)) break;
+    const Item& I = S.items[at & 1];
+    const int n[2] = {static_cast<int>(csa::uniform(I.n[0])), static_cast<int>(csa::uniform(I.n[1]))};
+    const int most = max(n[0], n[1]);
+    done_with_item(S, at);
+    if (most == 0) continue;
+    if (is_late && !(there(kBarKFull + (base & 1), (base >> 1) & 1) && (n[0] == 0 || there(kBarQFull, loads[0] & 1)))) issue_late(0);
+    need(kBarKFull + (base & 1), (base >> 1) & 1);
+    if (n[0] > 0) need(kBarQFull, loads[0] & 1);
+    for (int j = 0; ok && j < most; ++j) {
+      const uint32_t g = base + j;
+      const bool s0 = j < n[0], s1 = j < n[1];
+      const Value o0{g, seen_by[0] + j, j == 0, j + 1 == n[0], !s1};
+      int seen1 = 0, seen0 = 0;
+      bool seen_k = false;
+      if (s0)
+        issue_s(t0, g, o0.last, [&] {
+          if (is_late) seen1 = look_o(1, late);
+        });
+      if (is_late) issue_late(seen1);
+      if (s1) {
+        if (j == 0) need(kBarQFull + 1, loads[1] & 1);
+        issue_s(t1, g, j + 1 == n[1], [&] {
+          if (s0) seen0 = look_o(0, o0);
+        });
+        late = {g, seen_by[1] + j, j == 0, j + 1 == n[1], true};
+        is_late = true;
+      }
+      csa::mma_commit_if(lead, bars + 8 * (kBarKEmpty + (g & 1)));
+      const int k_bar = kBarKFull + ((g + 1) & 1);
+      const uint32_t k_parity = ((g + 1) >> 1) & 1;
+      if (s0) {
+        need_o(0, o0, seen0);
+        issue_o(t0, o0, [&] {
+          if (j + 1 < most) {
+            seen_k = there(k_bar, k_parity);
+            csa::tc_fence_after();
+          }
+        });
+      }
+      if (j + 1 < most && !seen_k) need(k_bar, k_parity);
     }
-    if (j == 0 && s1) need(kBarQFull + 1, 0);
-    if (s1)
-      issue_s(t1, j, [&] {
-        if (s0) seen0 = look_o(0, j);
-      });
-    csa::mma_commit_if(lead, bars + 8 * (kBarKEmpty + (j & 1)));
-    const int k_bar = kBarKFull + ((j + 1) & 1);
-    const uint32_t k_parity = ((j + 1) >> 1) & 1;
-    if (s0) {
-      need_o(0, j, seen0);
-      issue_o(t0, j, !s1, [&] {
-        if (j + 1 < most) {
-          seen_k = there(k_bar, k_parity);
-          csa::tc_fence_after();
-        }
-      });
+    base += most;
+    for (int t = 0; t < 2; ++t) {
+      seen_by[t] += n[t];
+      loads[t] += n[t] > 0;
     }
-    if (j + 1 < most && !seen_k) need(k_bar, k_parity);
   }
-  if (ok && n[1] == most && most > 0) {
-    need_o(1, most - 1, 0);
-    issue_o(t1, most - 1, true, nothing);
-  }
+  if (is_late) issue_late(0);
   csa::mma_commit_if(lead, bars + 8 * kBarDrain);  // nothing of this thread's is in flight when it leaves
   csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
 }
 
-__device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Request& R, int first, int head) {
+// Softmax and output of query tile t of an item; `n`: its key tiles there, `seen_by` and `items`: its key tiles and its items
+// with any so far. What is needed only at the ends is read from shared memory there: registers are short in between.
+__device__ __forceinline__ bool softmax_item(const csa_latent_prefill_args& A, Smem& S, uint32_t which, int n, uint32_t seen_by,
+                                             uint32_t items) {
+  const Item& I = S.items[which & 1];
   const int t = threadIdx.x >> 7, warp = (threadIdx.x >> 5) & 3, lane = threadIdx.x & 31;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars);
   const uint32_t s_at = S.tmem + t * kTile + (static_cast<uint32_t>(32 * warp) << 16);
-  const uint32_t o_at = s_at + kTmemO;
-  const int n = key_tiles(A, R, first, t);
-  const int row = first + t * kTile + 32 * warp + lane;
-  // keys that this row sees, and that every row of the warp sees
-  const int64_t past = static_cast<int64_t>(R.nk) - R.nq;
-  const int64_t seen = A.causal ? min(max(row + past + 1, int64_t(0)), static_cast<int64_t>(R.nk)) : R.nk;
-  const int64_t all_see = A.causal ? min(max(row - lane + past + 1, int64_t(0)), static_cast<int64_t>(R.nk)) : R.nk;
-  const float c = A.scale * 1.4426950408889634f, grow = kGrow / c;
+  int seen;  // keys from tile j on that this row sees
+  {
+    const int row = I.first + t * kTile + 32 * warp + lane;
+    const int64_t past = static_cast<int64_t>(I.r.nk) - I.r.nq;
+    seen = A.causal ? static_cast<int>(min(max(row + past + 1, int64_t(0)), static_cast<int64_t>(I.r.nk))) : I.r.nk;
+  }
+  const float c = A.scale * 1.4426950408889634f;
   float m = -INFINITY, l = 0.f;
   bool ok = true;
   for (int j = 0; j < n; ++j) {
-    ok = ok && warp_wait(bars + 8 * (kBarSFull + t), j & 1, stop);
+    ok = ok && warp_wait(bars + 8 * (kBarSFull + t), (seen_by + j) & 1, stop);
     if (!ok) break;
     csa::tc_fence_after();
     float s[4][32];
 #pragma unroll
     for (int k = 0; k < 4; ++k) csa::tmem_ld32(s_at + 32 * k, reinterpret_cast<uint32_t(&)[32]>(s[k]));
     csa::tmem_wait_ld();
-    if (static_cast<int64_t>(j + 1) * kTile > all_see) {
-      const int lim = static_cast<int>(min(seen - static_cast<int64_t>(j) * kTile, static_cast<int64_t>(kTile)));
+    if (__any_sync(0xFFFFFFFFu, seen < kTile)) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
 #pragma unroll
         for (int x = 0; x < 32; ++x)
-          if (32 * k + x >= lim) s[k][x] = -INFINITY;
+          if (32 * k + x >= seen) s[k][x] = -INFINITY;
     }
+    seen -= kTile;
     float top4[4];
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
@@ -368,7 +517,7 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
       for (int x = 1; x < 32; ++x) top4[k] = fmaxf(top4[k], s[k][x]);
     }
     const float top = fmaxf(fmaxf(top4[0], top4[1]), fmaxf(top4[2], top4[3]));
-    const bool up = top > m + grow;
+    const bool up = (top - m) * c > kGrow;  // also when there was nothing; not where there is still nothing
     if (__any_sync(0xFFFFFFFFu, up)) {
       const float keep = up ? csa::ex2((m - top) * c) : 1.f;  // 0 when there was nothing
       if (up) m = top;
@@ -377,17 +526,17 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
 #pragma unroll 1
         for (int k = 0; k < kV; k += 32) {
           uint32_t v[32];
-          csa::tmem_ld32(o_at + k, v);
+          csa::tmem_ld32(s_at + kTmemO + k, v);
           csa::tmem_wait_ld();
 #pragma unroll
           for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
-          csa::tmem_st32(o_at + k, v);
+          csa::tmem_st32(s_at + kTmemO + k, v);
         }
       }
     }
     const float mc = m == -INFINITY ? 0.f : m * c;
     const csa::F2 c2(c, c), mc2(-mc, -mc);
-    csa::F2 sum[4];
+    csa::F2 sum[2];
     // the exponentials of 32 keys ahead of the rounding of the 32 before them
     auto exps = [&](int k) {
 #pragma unroll
@@ -404,7 +553,7 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
       uint32_t w[16];
 #pragma unroll
       for (int x = 0; x < 32; x += 2) {
-        sum[x / 2 % 4] = csa::add2(sum[x / 2 % 4], csa::F2(s[k][x], s[k][x + 1]));
+        sum[x / 2 % 2] = csa::add2(sum[x / 2 % 2], csa::F2(s[k][x], s[k][x + 1]));
         // rounded to bf16 here, the tensor cores' operand type; l sums p unrounded
         const __nv_bfloat162 two = __floats2bfloat162_rn(s[k][x], s[k][x + 1]);
         w[x / 2] = *reinterpret_cast<const uint32_t*>(&two);
@@ -412,52 +561,58 @@ __device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S, const Re
       csa::tmem_st16(s_at + 16 * k, w);
     }
     float l0, l1;
-    csa::add2(csa::add2(sum[0], sum[1]), csa::add2(sum[2], sum[3])).get(l0, l1);
+    csa::add2(sum[0], sum[1]).get(l0, l1);
     l += l0 + l1;
     csa::tmem_wait_st();
     csa::tc_fence_before();
     __syncwarp();
     if (lane == 0) mbar_arrive(bars + 8 * (kBarPFull + t));
   }
-  if (n > 0) ok = ok && warp_wait(bars + 8 * (kBarOFull + t), 0, stop);
+  if (n > 0) ok = ok && warp_wait(bars + 8 * (kBarOFull + t), items & 1, stop);
+  if (!ok) return false;
   csa::tc_fence_after();
   const float inv = l > 0.f ? 1.f / l : l;  // a NaN stays one
-  const bool there = row < R.nq;
-  const int64_t at = static_cast<int64_t>(R.q0 + row) * A.num_heads + head;
-  if (there && A.lse) A.lse[at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
-  // through this tile's Q (its last S is done), so that a row is written as 256 contiguous bytes: row r of the warp at 256 r, its
-  // 16-byte chunks exchanged by r so that neither side has lanes on one bank
-  const uint32_t stage = smem_u32(S.q[t]) + warp * 32 * 256;
-#pragma unroll 1
-  for (int k = 0; k < kV; k += 32) {
-    uint32_t v[32] = {};
-    if (n > 0) {
-      csa::tmem_ld32(o_at + k, v);
-      csa::tmem_wait_ld();
-    }
+  const int row0 = I.first + t * kTile + 32 * warp, rows = I.r.nq - row0;  // of this warp, and how many are left from there
+  const int64_t at0 = static_cast<int64_t>(I.r.q0 + row0) * A.num_heads + I.head;
+  done_with_item(S, which);  // before the stores, whose completion an arrival waits for
+  float o[4][32] = {};
+  if (n > 0) {  // all of a row before the first wait: a load takes 700 clocks beside the MMAs
 #pragma unroll
-    for (int x = 0; x < 32; x += 8) {
-      uint32_t w[4];
-#pragma unroll
-      for (int y = 0; y < 4; ++y) {
-        const __nv_bfloat162 two = __floats2bfloat162_rn(__uint_as_float(v[x + 2 * y]) * inv, __uint_as_float(v[x + 2 * y + 1]) * inv);
-        w[y] = *reinterpret_cast<const uint32_t*>(&two);
-      }
-      csa::st_shared_v4(stage + lane * 256 + ((((k + x) / 8) ^ (lane & 15)) << 4), w[0], w[1], w[2], w[3]);
-    }
+    for (int k = 0; k < 4; ++k) csa::tmem_ld32(s_at + kTmemO + 32 * k, reinterpret_cast<uint32_t(&)[32]>(o[k]));
+    csa::tmem_wait_ld();
   }
-  __syncwarp();
-  const int rows = min(32, R.nq - (first + t * kTile + 32 * warp));  // of this warp's
-  uint8_t* out = static_cast<uint8_t*>(A.out) +
-                 2 * ((static_cast<int64_t>(R.q0 + first + t * kTile + 32 * warp) * A.num_heads + head) * kV) + 16 * (lane & 15);
-#pragma unroll 4
-  for (int r = lane >> 4; r < rows; r += 2) {
-    uint4 x;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
-                 : "r"(stage + r * 256 + (((lane & 15) ^ (r & 15)) << 4))
-                 : "memory");
-    *reinterpret_cast<uint4*>(out + static_cast<int64_t>(r) * A.num_heads * (2 * kV)) = x;
+  if (lane >= rows) return true;
+  const int64_t at = at0 + static_cast<int64_t>(lane) * A.num_heads;
+  if (A.lse) A.lse[at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
+  // Each lane writes its row, 32 bytes (a sector) at a time: staged through Q's place the rows would be whole lines, but
+  // that is being loaded with the next item's rows meanwhile, and lines made by exchanges between lanes are no faster.
+  uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * kV * at;
+  const bool wide = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    uint32_t w[16];
+#pragma unroll
+    for (int x = 0; x < 32; x += 2) {
+      const __nv_bfloat162 two = __floats2bfloat162_rn(o[k][x] * inv, o[k][x + 1] * inv);
+      w[x / 2] = *reinterpret_cast<const uint32_t*>(&two);
+    }
+#pragma unroll
+    for (int x = 0; x < 16; x += 8) csa::st_global_v8(out + 64 * k + 4 * x, &w[x], wide);
+  }
+  return true;
+}
+
+__device__ void role_softmax(const csa_latent_prefill_args& A, Smem& S) {
+  const int t = threadIdx.x >> 7;
+  uint32_t seen_by = 0, items = 0;
+  int idle = 0;  // key tiles that the other query tile has more than this one
+  for (uint32_t at = 0;; ++at) {
+    if (!next_item(S, at, idle)) return;
+    const int n = S.items[at & 1].n[t];
+    idle = max(S.items[at & 1].n[t ^ 1] - n, 0);
+    if (!softmax_item(A, S, at, n, seen_by, items)) return;
+    seen_by += n;
+    items += n > 0;
   }
 }
 
@@ -467,17 +622,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   Smem& S = *reinterpret_cast<Smem*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const uint32_t bars = smem_u32(S.bars);
-  const int head = blockIdx.x % A.num_heads;
   bool bad = false;
-  find_item(A, S, blockIdx.x / A.num_heads, &bad);
-  if (bad && A.dev_status && blockIdx.x == 0) atomicOr(A.dev_status, CSA_DEV_LEN_OOB);
-  if (static_cast<int>(blockIdx.x / A.num_heads) >= S.total) return;
-  Request R;
-  request_of(A, S.request, &R);
-  const int first = S.first;
+  sum_pairs(A, S, &bad);
+  if (bad && A.dev_status) atomicOr(A.dev_status, CSA_DEV_LEN_OOB);
   if (threadIdx.x == 0) {
     csa::mbar_init(bars + 8 * kBarVLand, 1);
     csa::mbar_init(bars + 8 * kBarDrain, 1);
+    csa::mbar_init(bars + 8 * kBarNext, 1);
+    csa::mbar_init(bars + 8 * kBarAsk, 1);
     for (int k = 0; k < 2; ++k) {
       csa::mbar_init(bars + 8 * (kBarQFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarKFull + k), 2);  // K comes in two parts
@@ -488,10 +640,15 @@ __global__ void __launch_bounds__(kThreads, 1)
       csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
       csa::mbar_init(bars + 8 * (kBarPFull + k), 4);
       csa::mbar_init(bars + 8 * (kBarOFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarQEmpty + k), 1);
+      csa::mbar_init(bars + 8 * (kBarItemFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarItemEmpty + k), kSoftmaxWarps + 2);
     }
     csa::mbar_init_fence();
     S.abort = 0;
   }
+  __syncthreads();
+  if (static_cast<int>(blockIdx.x / A.num_heads) >= S.total) return;
   if (warp == kMmaWarp) {
     csa::tmem_alloc(smem_u32(&S.tmem), kTmemCols);
     csa::tmem_relinquish();
@@ -500,12 +657,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   csa::tc_fence_after();
   if (warp < kSoftmaxWarps) {
-    role_softmax(A, S, R, first, head);
+    role_softmax(A, S);
   } else if (warp == kMmaWarp) {
-    role_mma(A, S, R, first);
+    role_mma(A, S);
     __syncwarp();
+  } else if (warp == kLoadWarp) {
+    role_load(A, M, S);
   } else {
-    role_load(A, M, S, R, first, head);
+    role_next(A, M, S);
   }
   csa::tc_fence_before();
   __syncthreads();
