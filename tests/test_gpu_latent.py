@@ -497,6 +497,26 @@ def test_prefill_many_requests():
     Prefill(lq, [n + (7 * i) % 30 for i, n in enumerate(lq)], 2, seed=8).check()
 
 
+@pytest.mark.parametrize("causal", [True, False])
+def test_prefill_more_items_than_sms(causal):
+    """Blocks take over others' items: of all lengths, with one query tile or two, and with tiles that see no key."""
+    Prefill([300, 1, 0, 520, 129, 64, 700, 257, 40, 256, 300], [300, 900, 7, 520, 100, 0, 900, 257, 3, 200, 150], 24, seed=13, causal=causal).check()
+
+
+def test_prefill_more_requests_than_threads():
+    lq = [(13 * i) % 40 for i in range(1000)]
+    Prefill(lq, [n + (7 * i) % 30 for i, n in enumerate(lq)], 1, seed=14).check()
+
+
+def test_prefill_output_on_16_bytes():
+    p = Prefill([200, 31], [250, 31], 3, seed=15)
+    want, want_lse = p.check()
+    room = torch.full((231 * 3 * 128 + 16,), 7.0, dtype=torch.bfloat16, device=DEV)
+    out, lse = p.run(out=room[8:-8].view(231, 3, 128))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert (room[:8] == 7.0).all() and (room[-8:] == 7.0).all()
+
+
 def test_prefill_bad_bounds():
     p = Prefill([20, 20, 20], [20, 20, 20], 2, seed=9)
     out = torch.full((60, 2, 128), 7.0, dtype=torch.bfloat16, device=DEV)
