@@ -257,20 +257,13 @@ def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torc
     return out
 
 
-_workspaces = {}  # (device index, stream): the workspace of calls on that stream, which run one after the other
-
-
-def _workspace(device, stream_address: int, stream, size: int) -> torch.Tensor:
-    """A stream's workspace of at least `size` bytes. A captured call gets one of its own: its graph may be
-    replayed on any stream, beside eager calls on this one."""
-    if torch.cuda.is_current_stream_capturing():
+def _workspace(device, stream, size: int) -> torch.Tensor:
+    """A call's own workspace of at least `size` bytes. None is kept for the next call: a call is two launches, and
+    another host thread's call on the same stream may be enqueued between them."""
+    if stream is None or torch.cuda.is_current_stream_capturing():
         return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
-    ws = _workspaces.get((device.index, stream_address))
-    if ws is None or ws.shape[0] < size:
-        on = stream if stream is not None else torch.cuda.current_stream(device)
-        with torch.cuda.stream(on):  # the allocator reuses its memory in that stream's order
-            ws = _workspaces[device.index, stream_address] = torch.empty(max(size, 16), dtype=torch.uint8, device=device)
-    return ws
+    with torch.cuda.stream(stream):  # the allocator reuses its memory in that stream's order
+        return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
 
 
 def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Tensor, row_len: torch.Tensor, *,
@@ -279,8 +272,8 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
                       ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """Latent attention, absorbed form: q [num_q, heads, 512 + rope] bf16 over the records below row_len[b]
     of request row_req[b] (identity when None), or over the positions idx [num_q, top] (-1: none) among
-    them. `ws` is a uint8 workspace of attend_workspace_bytes(...) or more; None takes one that is kept for
-    the stream (42 MB at most), or a new one while a graph is captured.
+    them. `ws` is a uint8 workspace of attend_workspace_bytes(...) or more, not in use by another call
+    meanwhile; None takes one for the call (42 MB at most) from torch's allocator.
     Returns (out [num_q, heads, 512] bf16, lse [num_q, heads] fp32)."""
     _want(q, torch.bfloat16, 3, "q")
     _want(page_table, torch.int32, 2, "page_table", whole=True)
@@ -308,7 +301,7 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
                    out.data_ptr(), lse.data_ptr(), _status(dev_status, dev))
     lib, ref, st = load(), ctypes.byref(a), _stream(stream, dev)
     if ws is None:
-        ws = _workspace(dev, st, stream, lib.csa_latent_attend_workspace_bytes(ref))
+        ws = _workspace(dev, stream, lib.csa_latent_attend_workspace_bytes(ref))
     elif _want(ws, torch.uint8, 1, "ws").device != dev:
         raise ValueError(f"ws is on {ws.device}, not on {dev}")
     _done(lib.csa_latent_attend(ref, ws.data_ptr(), ws.shape[0], st), "csa_latent_attend")

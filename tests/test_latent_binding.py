@@ -1,0 +1,93 @@
+"""The binding of the latent-cache operators without a GPU: what it hands to the library, where it takes
+memory from, and what it refuses. Tensors are on the host here and the library only records its calls;
+struct layouts and the library's own refusals are tested in test_latent_abi.py."""
+import contextlib
+import threading
+
+import pytest
+import torch
+
+from sparse_attention_kv_e4m3_gb300 import build, latent
+
+OK = 0
+
+
+class Recorder:
+    """Entry points that note their arguments and launch nothing; sizes come from the library itself."""
+
+    def __init__(self, lib, on_call):
+        self.lib, self.on_call, self.calls = lib, on_call, []
+
+    def __getattr__(self, name):
+        if name.endswith("_bytes"):
+            return getattr(self.lib, name)
+
+        def entry(ref, *rest):
+            self.calls.append((name, ref._obj, rest))
+            self.on_call(name, ref._obj, rest)
+            return OK
+
+        return entry
+
+
+class Stream:
+    def __init__(self, address):
+        self.cuda_stream = address
+
+
+@pytest.fixture
+def host(monkeypatch):
+    """The binding on host tensors. `host.current()` is the stream that the calling thread has entered, None for its own."""
+    build.build()
+    state = threading.local()
+    host = Recorder(latent.load(), lambda *a: None)
+    host.current = lambda: getattr(state, "stream", None)
+    host.home = Stream(0x77)
+
+    @contextlib.contextmanager
+    def enter(stream):
+        before, state.stream = host.current(), stream
+        yield
+        state.stream = before
+
+    monkeypatch.setattr(latent, "_want", lambda t, *a, **k: t)
+    monkeypatch.setattr(latent, "_stream", lambda stream, device: 0 if stream is None else stream.cuda_stream)
+    monkeypatch.setattr(latent, "load", lambda: host)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: host.current() or host.home)
+    monkeypatch.setattr(torch.cuda, "stream", enter)
+    return host
+
+
+def ints(*v):
+    return torch.tensor(v, dtype=torch.int32)
+
+
+def attend(rows=3, heads=2, **kw):
+    cache = latent.LatentCache.empty(8, 64, "bf16", device="cpu")
+    q = torch.zeros(rows, heads, 576, dtype=torch.bfloat16)
+    return latent.csa_latent_attend(q, cache, torch.zeros(rows, 4, dtype=torch.int32), torch.ones(rows, dtype=torch.int32), scale=0.1, **kw)
+
+
+# ------------------------------------------------------------------ workspaces
+
+def test_calls_in_flight_in_two_threads_do_not_share_a_workspace(host):
+    """A call is two launches, and the library runs without the interpreter's lock: another thread's call on the
+    same stream may be enqueued between them."""
+    both = threading.Barrier(2, timeout=20)
+    spans = []
+
+    def on_call(name, args, rest):
+        ws, size, _ = rest
+        spans.append((ws, ws + size))
+        both.wait()  # the two calls are inside the library at once
+
+    attend(5)  # whatever a first call may leave behind is there
+    host.on_call = on_call
+    threads = [threading.Thread(target=attend, args=(rows,)) for rows in (3, 5)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    (a0, a1), (b0, b1) = spans
+    assert a1 <= b0 or b1 <= a0
