@@ -7,6 +7,7 @@ on the GPU; work goes to `stream`, or the current stream.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
@@ -257,12 +258,16 @@ def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torc
     return out
 
 
+def _on(stream):
+    """Where a call's own memory comes from: the stream that the call runs on. The allocator gives memory out and
+    takes it back in that stream's order, and from a graph's own pool where that stream is being captured."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
 def _workspace(device, stream, size: int) -> torch.Tensor:
     """A call's own workspace of at least `size` bytes. None is kept for the next call: a call is two launches, and
     another host thread's call on the same stream may be enqueued between them."""
-    if stream is None or torch.cuda.is_current_stream_capturing():
-        return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
-    with torch.cuda.stream(stream):  # the allocator reuses its memory in that stream's order
+    with _on(stream):
         return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
 
 

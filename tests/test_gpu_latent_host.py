@@ -48,3 +48,27 @@ def test_attend_in_two_threads_on_one_stream():
         assert len(got[k]) == 50
         for out, lse in got[k]:
             assert torch.equal(out, want[k][0]) and torch.equal(lse, want[k][1])
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+def test_attend_on_a_branch_of_a_capture(fmt):
+    """The call goes to a stream forked from the capturing one, which allocates and fills memory meanwhile."""
+    a = Attend([30000, 500, 9000], 64, 64, fmt, seed=23)
+    want, want_lse = a.check()
+    out, lse = torch.zeros_like(want), torch.zeros_like(want_lse)
+    size = latent.attend_workspace_bytes(3, 64, a.table.shape[1])
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        latent.csa_latent_attend(a.q, a.cache, a.table, a.lens, scale=a.scale, out=out, lse=lse, stream=side)
+        rest = [torch.empty(size, dtype=torch.uint8, device=DEV).fill_(255) for _ in range(8)]
+        main.wait_stream(side)
+    for _ in range(20):
+        out.zero_()
+        lse.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    assert all(bool((r == 255).all()) for r in rest)

@@ -91,3 +91,32 @@ def test_calls_in_flight_in_two_threads_do_not_share_a_workspace(host):
         t.join()
     (a0, a1), (b0, b1) = spans
     assert a1 <= b0 or b1 <= a0
+
+
+# ------------------------------------------------------------------ streams
+
+@pytest.fixture
+def made(host, monkeypatch):
+    """(tensor, stream that had been entered) of each tensor that the binding makes with torch.empty."""
+    made, empty = [], torch.empty
+
+    def note(*a, **k):
+        t = empty(*a, **k)
+        made.append((t, host.current()))
+        return t
+
+    monkeypatch.setattr(torch, "empty", note)
+    return made
+
+
+def test_workspace_comes_from_the_stream_of_the_call(host, made, monkeypatch):
+    """Also while the current stream is captured: the call's stream may be a branch of that capture, and memory given
+    back to the capturing stream's order would be handed out again while the branch still uses it."""
+    for capturing in (False, True):
+        monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: capturing)
+        side = Stream(0x99)
+        made.clear()
+        attend(stream=side)
+        ws, _, on = host.calls[-1][2]
+        assert on == side.cuda_stream
+        assert [s for t, s in made if t.data_ptr() == ws] == [side], capturing
