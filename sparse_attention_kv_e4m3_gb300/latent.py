@@ -3,11 +3,12 @@
 and latent attention, absorbed (over the cache) and expanded (prompts).
 
 Argument marshalling only, as in `native`; there is no fallback. Every tensor is
-on the GPU; work goes to `stream`, or the current stream.
+on the GPU; work goes to `stream`, or the current stream. Outputs and workspaces that
+a call makes itself come from that stream's memory; what the caller passes has to be
+ready on it, and the caller waits for it before reading results on another one.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from typing import NamedTuple, Optional
 
@@ -114,10 +115,27 @@ def _want(t: torch.Tensor, dtype, dims: int, name: str, whole: bool = False) -> 
     return t
 
 
-def _pick(out, shape, dtype, device, name):
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """A call's own memory, from the stream that the call runs on: the allocator gives memory out and takes it back in
+    that stream's order, and from a graph's own pool where that stream is being captured."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory of a result, noted as used on the current stream too, where the caller waits for it and reads it."""
+    t = _empty(shape, dtype, device, stream)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _pick(out, shape, dtype, device, name, stream):
     """The caller's output tensor, checked, or a new one."""
     if out is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return _new(shape, dtype, device, stream)
     _want(out, dtype, len(shape), name, whole=True)
     if out.shape != shape or out.device != device:
         raise ValueError(f"{name}: {tuple(shape)} on {device}, not {tuple(out.shape)} on {out.device}")
@@ -183,9 +201,9 @@ class StepTables(NamedTuple):
     taken: torch.Tensor      # [1] int32
 
 
-def empty_tables(num_req: int, n_rows: int, device="cuda") -> StepTables:
-    """Tables for csa_build_tables to fill, in one allocation."""
-    buf = torch.empty(5 * n_rows + 2 * num_req + 3, dtype=torch.int32, device=device)
+def empty_tables(num_req: int, n_rows: int, device="cuda", stream=None) -> StepTables:
+    """Tables for csa_build_tables to fill (on `stream`, or the current stream), in one allocation."""
+    buf = _new((5 * n_rows + 2 * num_req + 3,), torch.int32, device, stream)
     slot, req, pos, length, row_start, kv_start, taken = torch.unsafe_split_with_sizes(
         buf, (2 * n_rows, n_rows, n_rows, n_rows, num_req + 1, num_req + 1, 1))
     return StepTables(req, pos, length, slot.view(torch.int64), row_start, kv_start, taken)
@@ -206,7 +224,7 @@ def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: t
     if new_len.shape[0] != n or page_table.shape[0] != n or n_rows < 0:
         raise ValueError("old_len, new_len and page_table: one row a request; n_rows at least 0")
     if out is None:
-        out = empty_tables(n, n_rows, dev)
+        out = empty_tables(n, n_rows, dev, stream)
         at = out.row_slot.data_ptr()  # one allocation: slots, three maps, two running sums, the count
         req, pos, length = at + 8 * n_rows, at + 12 * n_rows, at + 16 * n_rows
         start = at + 20 * n_rows
@@ -214,7 +232,7 @@ def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: t
     else:
         for t, (size, dtype), name in zip(out, [(n_rows, torch.int32)] * 3 + [(n_rows, torch.int64)] +
                                           [(n + 1, torch.int32)] * 2 + [(1, torch.int32)], StepTables._fields):
-            _pick(t, (size,), dtype, dev, name)
+            _pick(t, (size,), dtype, dev, name, stream)
         ptrs = tuple(t.data_ptr() for t in out)
     a = TablesArgs(old_len.data_ptr(), new_len.data_ptr(), n, page_table.shape[1], page_table.data_ptr(),
                    free_pages.data_ptr(), free_pages.shape[0], n_rows, *ptrs, _status(dev_status, dev))
@@ -251,24 +269,17 @@ def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torc
     num_req, width = page_table.shape
     if kv_start.shape[0] != num_req + 1 or n_rows < 0:
         raise ValueError("page_table [num_req, pt_stride], kv_start [num_req + 1], n_rows at least 0")
-    out = _pick(out, (n_rows, cache.width), torch.bfloat16, dev, "out")
+    out = _pick(out, (n_rows, cache.width), torch.bfloat16, dev, "out", stream)
     a = LatentReadArgs(cache.args, page_table.data_ptr(), num_req, width, kv_start.data_ptr(), n_rows, out.data_ptr(),
                        _status(dev_status, dev))
     _done(load().csa_latent_read(ctypes.byref(a), _stream(stream, dev)), "csa_latent_read")
     return out
 
 
-def _on(stream):
-    """Where a call's own memory comes from: the stream that the call runs on. The allocator gives memory out and
-    takes it back in that stream's order, and from a graph's own pool where that stream is being captured."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
-
-
 def _workspace(device, stream, size: int) -> torch.Tensor:
     """A call's own workspace of at least `size` bytes. None is kept for the next call: a call is two launches, and
     another host thread's call on the same stream may be enqueued between them."""
-    with _on(stream):
-        return torch.empty(max(size, 16), dtype=torch.uint8, device=device)
+    return _empty(max(size, 16), torch.uint8, device, stream)
 
 
 def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Tensor, row_len: torch.Tensor, *,
@@ -299,8 +310,8 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
         if _want(row_req, torch.int32, 1, "row_req").shape[0] != n:
             raise ValueError("row_req [num_q]")
         req_ptr = row_req.data_ptr()
-    out = _pick(out, (n, heads, LATENT_DIM), torch.bfloat16, dev, "out")
-    lse = _pick(lse, (n, heads), torch.float32, dev, "lse")
+    out = _pick(out, (n, heads, LATENT_DIM), torch.bfloat16, dev, "out", stream)
+    lse = _pick(lse, (n, heads), torch.float32, dev, "lse", stream)
     a = AttendArgs(cache.args, q.data_ptr(), _step(q, 0, width), _step(q, 1, width), n, heads, page_table.data_ptr(),
                    num_req, pt_stride, req_ptr, row_len.data_ptr(), idx_ptr, idx_step, top, float(scale),
                    out.data_ptr(), lse.data_ptr(), _status(dev_status, dev))
@@ -340,8 +351,8 @@ def csa_latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tens
             v.shape != (tk, heads, PREFILL_V) or k_rope.shape != (tk, PREFILL_ROPE) or
             q_start.shape != kv_start.shape or q_start.shape[0] < 1):
         raise ValueError("q [tq, h, 192], k_nope and v [tk, h, 128], k_rope [tk, 64], q_start and kv_start [num_req + 1]")
-    out = _pick(out, (tq, heads, PREFILL_V), torch.bfloat16, dev, "out")
-    lse = _pick(lse, (tq, heads), torch.float32, dev, "lse")
+    out = _pick(out, (tq, heads, PREFILL_V), torch.bfloat16, dev, "out", stream)
+    lse = _pick(lse, (tq, heads), torch.float32, dev, "lse", stream)
     a = PrefillArgs(q.data_ptr(), k_nope.data_ptr(), k_rope.data_ptr(), v.data_ptr(), _step(q, 0, width),
                     _step(q, 1, width), _step(k_nope, 0, 128), _step(k_nope, 1, 128), _step(k_rope, 0, 64),
                     _step(v, 0, 128), _step(v, 1, 128), tq, tk, q_start.data_ptr(), kv_start.data_ptr(),

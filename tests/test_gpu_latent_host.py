@@ -72,3 +72,28 @@ def test_attend_on_a_branch_of_a_capture(fmt):
         torch.cuda.synchronize()
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
     assert all(bool((r == 255).all()) for r in rest)
+
+
+def test_results_made_on_another_stream():
+    """The current stream's queued work still reads memory that it has given back when a call on a side stream makes
+    its outputs."""
+    a = Attend([700, 90], 64, 64, "bf16", seed=24)
+    want, want_lse = a.check()
+    side = torch.cuda.Stream()
+    big = torch.randn(64 << 20, device=DEV)
+    for _ in range(10):
+        torch.cuda.synchronize()
+        side.wait_stream(torch.cuda.current_stream())
+        old = [torch.full_like(want, 3.0) for _ in range(4)]
+        for _ in range(4):
+            big.mul_(1.0)  # keeps the current stream busy before it reads `old`
+        read = [t.clone() for t in old]
+        del old
+        out, lse = latent.csa_latent_attend(a.q, a.cache, a.table, a.lens, scale=a.scale, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        copy = out.clone()
+        del out
+        again = latent.csa_latent_attend(a.q, a.cache, a.table, a.lens, scale=2 * a.scale, stream=side)[0]
+        torch.cuda.synchronize()
+        assert all(bool((t == 3.0).all()) for t in read)
+        assert torch.equal(copy, want) and torch.equal(lse, want_lse) and not torch.equal(again, want)

@@ -56,6 +56,8 @@ def host(monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: host.current() or host.home)
     monkeypatch.setattr(torch.cuda, "stream", enter)
+    host.used = []  # (address, stream) that a tensor was noted as used on
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: host.used.append((t.data_ptr(), s)), raising=False)
     return host
 
 
@@ -120,3 +122,38 @@ def test_workspace_comes_from_the_stream_of_the_call(host, made, monkeypatch):
         ws, _, on = host.calls[-1][2]
         assert on == side.cuda_stream
         assert [s for t, s in made if t.data_ptr() == ws] == [side], capturing
+
+
+def prefill(tq=4, tk=6, heads=2, **kw):
+    def rows(*shape):
+        return torch.zeros(*shape, dtype=torch.bfloat16)
+
+    return latent.csa_latent_prefill(rows(tq, heads, 192), rows(tk, heads, 128), rows(tk, 64), rows(tk, heads, 128), ints(0, tq), ints(0, tk),
+                                     scale=0.1, **kw)
+
+
+def tables(n_rows=5, **kw):
+    return latent.csa_build_tables(ints(3, 64), ints(4, 1), torch.zeros(2, 3, dtype=torch.int32), ints(7, 8, 9), n_rows, **kw)
+
+
+def read(n_rows=5, **kw):
+    cache = latent.LatentCache.empty(8, 64, "bf16", device="cpu")
+    return latent.csa_latent_read(cache, torch.zeros(1, 2, dtype=torch.int32), ints(0, 5), n_rows, **kw)
+
+
+@pytest.mark.parametrize("call", [attend, prefill, tables, read])
+def test_outputs_come_from_the_stream_of_the_call(host, made, call):
+    """Memory of the current stream's order may still be read by work queued there. The results are noted as used on
+    the current stream too, where the caller waits for them."""
+    side = Stream(0x99)
+    made.clear()
+    host.used.clear()
+    got = call(stream=side)
+    got = got if isinstance(got, tuple) else (got,)
+    for t in got:
+        base = t.untyped_storage().data_ptr()
+        assert [s for m, s in made if m.untyped_storage().data_ptr() == base] == [side]
+        assert any(s is host.home for p, s in host.used if base <= p < base + t.untyped_storage().nbytes())
+    host.used.clear()
+    call()  # on the current stream: nothing to note
+    assert not host.used
