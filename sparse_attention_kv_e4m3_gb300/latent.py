@@ -225,9 +225,10 @@ def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: t
         raise ValueError("old_len, new_len and page_table: one row a request; n_rows at least 0")
     if out is None:
         out = empty_tables(n, n_rows, dev, stream)
-        at = out.row_slot.data_ptr()  # one allocation: slots, three maps, two running sums, the count
+        # one allocation: slots, three maps, two running sums (never empty, as the maps may be), the count
+        start = out.row_start.data_ptr()
+        at = start - 20 * n_rows
         req, pos, length = at + 8 * n_rows, at + 12 * n_rows, at + 16 * n_rows
-        start = at + 20 * n_rows
         ptrs = (req, pos, length, at, start, start + 4 * (n + 1), start + 8 * (n + 1))
     else:
         for t, (size, dtype), name in zip(out, [(n_rows, torch.int32)] * 3 + [(n_rows, torch.int64)] +

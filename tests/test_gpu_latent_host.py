@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from sparse_attention_kv_e4m3_gb300 import latent
-from test_gpu_latent import DEV, Attend, _lib  # noqa: F401
+from test_gpu_latent import DEV, Attend, _lib, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +97,13 @@ def test_results_made_on_another_stream():
         torch.cuda.synchronize()
         assert all(bool((t == 3.0).all()) for t in read)
         assert torch.equal(copy, want) and torch.equal(lse, want_lse) and not torch.equal(again, want)
+
+
+def test_tables_without_rows():
+    for own in (False, True):
+        st, t = torch.zeros(1, dtype=torch.int32, device=DEV), torch.full((2, 3), -1, dtype=torch.int32, device=DEV)
+        out = latent.empty_tables(2, 0) if own else None
+        got = latent.csa_build_tables(ints([0, 0]), ints([65, 0]), t, ints([5, 6, 7]), 0, out=out, dev_status=st)
+        assert got.row_start.tolist() == got.kv_start.tolist() == [0, 65, 65] and got.taken.tolist() == [2]
+        assert t.tolist() == [[5, 6, -1], [-1, -1, -1]] and got.row_slot.shape == (0,)
+        assert int(st) == 128  # records without a row of their own

@@ -157,3 +157,15 @@ def test_outputs_come_from_the_stream_of_the_call(host, made, call):
     host.used.clear()
     call()  # on the current stream: nothing to note
     assert not host.used
+
+
+# ------------------------------------------------------------------ sizes of zero
+
+@pytest.mark.parametrize("n_rows", [0, 1])
+def test_tables_without_rows(host, n_rows):
+    """A step that only takes pages, or a captured one of no rows: every table that is not empty has its address."""
+    got = tables(n_rows)
+    name, args, _ = host.calls[-1]
+    assert name == "csa_build_tables" and args.n_rows == n_rows
+    for field in ("row_start", "kv_start", "taken") + (("row_req", "row_pos", "row_len", "row_slot") if n_rows else ()):
+        assert getattr(args, field) == getattr(got, field).data_ptr() != 0, field
