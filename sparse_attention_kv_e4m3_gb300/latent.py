@@ -305,6 +305,9 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
     if idx is not None:
         if _want(idx, torch.int32, 2, "idx").shape[0] != n:
             raise ValueError("idx [num_q, top]")
+        if idx.shape[1] == 0:  # its address is null, which the library reads as whole histories: nothing is listed instead
+            with torch.cuda.stream(stream):
+                idx = torch.full((n, 1), -1, dtype=torch.int32, device=dev)
         top = idx.shape[1]
         idx_ptr, idx_step = idx.data_ptr(), _step(idx, 0, top)
     if row_req is not None:

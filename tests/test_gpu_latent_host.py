@@ -107,3 +107,15 @@ def test_tables_without_rows():
         assert got.row_start.tolist() == got.kv_start.tolist() == [0, 65, 65] and got.taken.tolist() == [2]
         assert t.tolist() == [[5, 6, -1], [-1, -1, -1]] and got.row_slot.shape == (0,)
         assert int(st) == 128  # records without a row of their own
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+def test_attend_with_no_positions(fmt):
+    a = Attend([300, 0, 70], 16, 64, fmt, seed=25)
+    a.idx = torch.zeros(3, 0, dtype=torch.int32, device=DEV)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    for stream in (None, side):
+        out, lse = a.run(stream=stream)
+        torch.cuda.synchronize()
+        assert int(a.st) == 0 and not out.any() and bool(torch.isneginf(lse).all())

@@ -169,3 +169,11 @@ def test_tables_without_rows(host, n_rows):
     assert name == "csa_build_tables" and args.n_rows == n_rows
     for field in ("row_start", "kv_start", "taken") + (("row_req", "row_pos", "row_len", "row_slot") if n_rows else ()):
         assert getattr(args, field) == getattr(got, field).data_ptr() != 0, field
+
+
+def test_positions_that_list_nothing_are_not_the_whole_history(host):
+    """An empty tensor's address is null, which the library reads as "no list"."""
+    for stream in (None, Stream(0x99)):
+        attend(3, idx=torch.zeros(3, 0, dtype=torch.int32), stream=stream)
+        args = host.calls[-1][1]
+        assert args.idx and args.top >= 1 and args.idx_stride >= args.top
