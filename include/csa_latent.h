@@ -4,7 +4,8 @@
  * in its absorbed form (over the cache, at the indexer's positions or over the whole
  * history) and its expanded form (prompts). Same library, same conventions: every pointer
  * is device memory owned by the caller, nothing is allocated, freed or synchronised, all
- * work is enqueued on `stream`, calls are re-entrant and capturable as long as their
+ * work is enqueued on `stream`, which like the pointers belongs to the calling thread's current
+ * device, calls are re-entrant and capturable as long as their
  * workspaces do not overlap while in flight, host-detectable errors launch nothing, and
  * data-dependent errors OR a CSA_DEV_* bit into *dev_status (when given) and leave the
  * offending record, row or request out.
