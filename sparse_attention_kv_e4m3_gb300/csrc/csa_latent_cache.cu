@@ -10,7 +10,7 @@ namespace {
 // ------------------------------------------------------------- block tables
 //
 // One launch: every block takes the running sums over all requests for itself
-// (num_req is at most CSA_TABLES_MAX_REQ, two words a request in shared memory),
+// (num_req is at most CSA_TABLES_MAX_REQ, three words a request in shared memory),
 // so no block waits for another, then does its share of the new pages and of the
 // rows, each found by bisection in the running sums. A row's page is looked up in
 // the old entries of the table or in the free list, never in an entry that this
@@ -447,9 +447,16 @@ extern "C" csa_status csa_build_tables(const csa_tables_args* a, void* stream) {
       !aligned(a->row_start, 4) || !aligned(a->kv_start, 4) || !aligned(a->taken, 4) || !aligned(a->dev_status, 4))
     return CSA_ERR_ALIGNMENT;
   const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(a->num_req) + 1);
-  if (smem > 48 * 1024 && cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(smem)) != cudaSuccess)
-    return CSA_ERR_CUDA;
+  static bool ready[kMaxDevices];
+  if (smem > 48 * 1024) {  // the limit is the kernel's, not the call's: set to what the most requests need, never lowered
+    int sms = 0, dev = 0;
+    if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
+    constexpr int most = 3 * sizeof(int32_t) * (CSA_TABLES_MAX_REQ + 1);
+    if (!ready[dev]) {
+      if (cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return CSA_ERR_CUDA;
+      ready[dev] = true;
+    }
+  }
   static int kept[kMaxDevices];  // of calls of up to about 1000 requests
   unsigned grid = 1;
   const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 12288 ? 12288 : smem, smem <= 12288 ? kept : nullptr,

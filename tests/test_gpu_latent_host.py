@@ -119,3 +119,16 @@ def test_attend_with_no_positions(fmt):
         out, lse = a.run(stream=stream)
         torch.cuda.synchronize()
         assert int(a.st) == 0 and not out.any() and bool(torch.isneginf(lse).all())
+
+
+def test_tables_of_many_sizes_in_threads():
+    """Tables of more requests than the default limit of shared memory holds, of other sizes in each thread."""
+    def calls(n):
+        zero, one = torch.zeros(n, dtype=torch.int32, device=DEV), torch.ones(n, dtype=torch.int32, device=DEV)
+        table, free = torch.full((n, 1), -1, dtype=torch.int32, device=DEV), torch.arange(n, dtype=torch.int32, device=DEV)
+        for _ in range(1500):
+            got = latent.csa_build_tables(zero, one, table, free, n)
+        assert torch.equal(got.row_slot, 64 * torch.arange(n, device=DEV)) and int(got.taken) == n
+
+    _in_threads(*(lambda n=n: calls(n) for n in (16384, 4200, 9000, 16384)))
+    torch.cuda.synchronize()

@@ -2,6 +2,7 @@
 memory from, and what it refuses. Tensors are on the host here and the library only records its calls;
 struct layouts and the library's own refusals are tested in test_latent_abi.py."""
 import contextlib
+import subprocess
 import threading
 
 import pytest
@@ -193,3 +194,42 @@ def test_a_call_goes_to_the_current_device_only(monkeypatch):
     for stream, device in ((None, there), (side, there), (far, there), (far, here)):
         with pytest.raises(ValueError):
             latent._stream(stream, device)
+
+
+# ------------------------------------------------------------------ the library's host code
+
+HARNESS = r"""
+#include <cstdio>
+#include <cuda_runtime.h>
+static int limit = 49152;  // shared memory that the kernel may be launched with, as the driver keeps it for all threads
+static cudaError_t set_limit(int bytes) { limit = bytes; return cudaSuccess; }
+static cudaError_t number(int* out, int v) { *out = v; return cudaSuccess; }
+#define cudaGetDevice(p) number(p, 0)
+#define cudaDeviceGetAttribute(p, what, dev) number(p, 152)
+#define cudaFuncSetAttribute(kernel, what, bytes) set_limit(static_cast<int>(bytes))
+#define cudaOccupancyMaxActiveBlocksPerMultiprocessor(...) cudaErrorUnknown  // ends the call before its launch
+#include "csa_latent_cache.cu"
+int main() {
+  const int requests[] = {16384, 5000, 16384, 100, 4200};
+  int32_t* at = reinterpret_cast<int32_t*>(0x1000);
+  for (int n : requests) {
+    csa_tables_args a = {at, at, n, 8, at, at, 5, 7, at, at, at, reinterpret_cast<int64_t*>(at), at, at, at, nullptr};
+    const int status = csa_build_tables(&a, nullptr);
+    std::printf("%d %d %d\n", n, status, limit);
+  }
+  return 0;
+}
+"""
+
+
+def test_tables_never_lower_the_kernels_shared_memory_limit(tmp_path):
+    """The limit belongs to the kernel, not to the call: another thread's call may be between setting it and its launch."""
+    src, exe = tmp_path / "limit.cu", tmp_path / "limit"
+    src.write_text(HARNESS)
+    subprocess.run([build.nvcc_path(), build.ARCH, "-std=c++17", f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-o", str(exe), str(src)], check=True)
+    lines = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split("\n")
+    most = 0
+    for line in lines[:-1]:
+        n, status, limit = map(int, line.split())
+        most = max(most, 3 * 4 * (n + 1))
+        assert status == 5 and limit >= most, line  # CSA_ERR_CUDA, by the harness
