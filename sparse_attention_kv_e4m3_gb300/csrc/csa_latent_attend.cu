@@ -1174,14 +1174,14 @@ int cluster_of(const csa_latent_attend_args* a, int sms) {
 
 template <int kLoad, int kRope>
 csa_status launch(const Kernel& K, const MapsOf<kLoad>& M, int grid, int dev, cudaStream_t stream) {
-  static bool ready[kMaxDevices];  // the kernel's shared memory size is set on each device once
+  static Kept ready;  // the kernel's shared memory size is set on each device once
   constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
   static_assert(smem + 256 <= 232448, "shared memory of one CTA");
-  if (!ready[dev]) {
+  if (!ready.get(dev)) {
     if (cudaFuncSetAttribute(attend_kernel<kLoad, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem)) != cudaSuccess)
       return CSA_ERR_CUDA;
-    ready[dev] = true;
+    ready.set(dev, 1);
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(grid);

@@ -385,14 +385,14 @@ __global__ void __launch_bounds__(kCopyThreads) latent_read_kernel(const csa_lat
 // At most one full wave of blocks, each taking `per_block` rows at a time. `kept` (or null): the kernel's resident
 // blocks an SM on each device, asked for once.
 template <typename K>
-csa_status wave_grid(K kernel, int threads, size_t smem, int* kept, int64_t rows, int64_t per_block, unsigned* grid) {
+csa_status wave_grid(K kernel, int threads, size_t smem, Kept* kept, int64_t rows, int64_t per_block, unsigned* grid) {
   int sms = 0, dev = 0;
   if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
-  int per_sm = kept ? kept[dev] : 0;
+  int per_sm = kept ? kept->get(dev) : 0;
   if (per_sm == 0) {
     if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, threads, smem) != cudaSuccess || per_sm < 1)
       return CSA_ERR_CUDA;
-    if (kept) kept[dev] = per_sm;
+    if (kept) kept->set(dev, per_sm);
   }
   const int64_t want = (rows + per_block - 1) / per_block, cap = static_cast<int64_t>(sms) * per_sm;
   *grid = static_cast<unsigned>(want < 1 ? 1 : (want < cap ? want : cap));
@@ -401,9 +401,9 @@ csa_status wave_grid(K kernel, int threads, size_t smem, int* kept, int64_t rows
 
 template <bool kBf16In, bool kFp4>
 csa_status launch_write(const csa_latent_write_args& a, cudaStream_t stream) {
-  static int kept[kMaxDevices];
+  static Kept kept;
   unsigned grid = 1;
-  const csa_status st = wave_grid(latent_write_kernel<kBf16In, kFp4>, kCopyThreads, 0, kept, a.n, kCopyThreads / 32, &grid);
+  const csa_status st = wave_grid(latent_write_kernel<kBf16In, kFp4>, kCopyThreads, 0, &kept, a.n, kCopyThreads / 32, &grid);
   if (st != CSA_OK) return st;
   latent_write_kernel<kBf16In, kFp4><<<grid, kCopyThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
@@ -411,10 +411,10 @@ csa_status launch_write(const csa_latent_write_args& a, cudaStream_t stream) {
 
 template <bool kFp4, int kRope>
 csa_status launch_read(const csa_latent_read_args& a, cudaStream_t stream) {
-  static int kept[kMaxDevices];
+  static Kept kept;
   unsigned grid = 1;
   const csa_status st =
-      wave_grid(latent_read_kernel<kFp4, kRope>, kCopyThreads, 0, kept, a.n_rows, kCopyThreads / 32 * kReadRows, &grid);
+      wave_grid(latent_read_kernel<kFp4, kRope>, kCopyThreads, 0, &kept, a.n_rows, kCopyThreads / 32 * kReadRows, &grid);
   if (st != CSA_OK) return st;
   latent_read_kernel<kFp4, kRope><<<grid, kCopyThreads, 0, stream>>>(a);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
@@ -447,19 +447,19 @@ extern "C" csa_status csa_build_tables(const csa_tables_args* a, void* stream) {
       !aligned(a->row_start, 4) || !aligned(a->kv_start, 4) || !aligned(a->taken, 4) || !aligned(a->dev_status, 4))
     return CSA_ERR_ALIGNMENT;
   const size_t smem = 3 * sizeof(int32_t) * (static_cast<size_t>(a->num_req) + 1);
-  static bool ready[kMaxDevices];
+  static Kept ready;
   if (smem > 48 * 1024) {  // the limit is the kernel's, not the call's: set to what the most requests need, never lowered
     int sms = 0, dev = 0;
     if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
     constexpr int most = 3 * sizeof(int32_t) * (CSA_TABLES_MAX_REQ + 1);
-    if (!ready[dev]) {
+    if (!ready.get(dev)) {
       if (cudaFuncSetAttribute(build_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, most) != cudaSuccess) return CSA_ERR_CUDA;
-      ready[dev] = true;
+      ready.set(dev, 1);
     }
   }
-  static int kept[kMaxDevices];  // of calls of up to about 1000 requests
+  static Kept kept;  // of calls of up to about 1000 requests
   unsigned grid = 1;
-  const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 12288 ? 12288 : smem, smem <= 12288 ? kept : nullptr,
+  const csa_status st = wave_grid(build_tables_kernel, kTabThreads, smem < 12288 ? 12288 : smem, smem <= 12288 ? &kept : nullptr,
                                   a->n_rows + a->num_req, kTabRowsPerBlock, &grid);
   if (st != CSA_OK) return st;
   build_tables_kernel<<<grid, kTabThreads, smem, static_cast<cudaStream_t>(stream)>>>(*a);

@@ -5,6 +5,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -42,14 +43,22 @@ inline csa_status check_cache(const csa_latent_cache& c) {
 // each query costs about a microsecond of a small call).
 constexpr int kMaxDevices = 64;
 
+// What the host code keeps for each device, 0 until it is known. Two threads may both find it out, with the same
+// answer; it stands alone, so no order with other memory is needed.
+struct Kept {
+  std::atomic<int> of[kMaxDevices];
+  int get(int dev) const { return of[dev].load(std::memory_order_relaxed); }
+  void set(int dev, int v) { of[dev].store(v, std::memory_order_relaxed); }
+};
+
 inline csa_status sm_count(int* sms, int* device = nullptr) {
-  static int kept[kMaxDevices];  // 0: not asked yet; two threads may both ask, with the same answer
+  static Kept kept;
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) return CSA_ERR_CUDA;
-  int n = kept[dev];
+  int n = kept.get(dev);
   if (n == 0) {
     if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || n < 1) return CSA_ERR_CUDA;
-    kept[dev] = n;
+    kept.set(dev, n);
   }
   *sms = n;
   if (device) *device = dev;

@@ -716,13 +716,13 @@ extern "C" csa_status csa_latent_prefill(const csa_latent_prefill_args* a, void*
   if (pairs * a->num_heads > INT32_MAX) return CSA_ERR_INVALID_ARG;
   int sms = 0, dev = 0;
   if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
-  static bool ready[kMaxDevices];  // the kernel's shared memory size is set on each device once
+  static Kept ready;  // the kernel's shared memory size is set on each device once
   constexpr size_t smem = sizeof(Smem) + 1024;
   static_assert(smem <= 232448, "shared memory of one CTA");
-  if (!ready[dev]) {
+  if (!ready.get(dev)) {
     if (cudaFuncSetAttribute(prefill_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
       return CSA_ERR_CUDA;
-    ready[dev] = true;
+    ready.set(dev, 1);
   }
   if (!encode_tiled()) return CSA_ERR_CUDA;
   Maps M;

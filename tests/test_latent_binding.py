@@ -2,6 +2,7 @@
 memory from, and what it refuses. Tensors are on the host here and the library only records its calls;
 struct layouts and the library's own refusals are tested in test_latent_abi.py."""
 import contextlib
+import os
 import subprocess
 import threading
 
@@ -233,3 +234,62 @@ def test_tables_never_lower_the_kernels_shared_memory_limit(tmp_path):
         n, status, limit = map(int, line.split())
         most = max(most, 3 * 4 * (n + 1))
         assert status == 5 and limit >= most, line  # CSA_ERR_CUDA, by the harness
+
+
+FAKES = r"""
+#include <cuda_runtime.h>
+static inline cudaError_t number(int* out, int v) { *out = v; return cudaSuccess; }
+#define cudaGetDevice(p) number(p, 0)
+#define cudaDeviceGetAttribute(p, what, dev) number(p, 152)
+#define cudaFuncSetAttribute(...) cudaSuccess
+#define cudaOccupancyMaxActiveBlocksPerMultiprocessor(p, ...) number(p, 2)
+#define cudaGetLastError() cudaSuccess
+"""
+
+RACES = r"""
+#include <cstdio>
+#include <thread>
+#include "csa_latent.h"
+static void calls() {
+  auto* p = reinterpret_cast<uint8_t*>(0x10000);
+  auto* i = reinterpret_cast<int32_t*>(0x10000);
+  auto* l = reinterpret_cast<int64_t*>(0x10000);
+  auto* f = reinterpret_cast<float*>(0x10000);
+  const csa_latent_cache cache = {p, 8, 64 * 1152, 64, CSA_LATENT_BF16};
+  const csa_latent_write_args w = {cache, p, 576, CSA_KEYS_BF16, 0, 3, l, nullptr};
+  const csa_latent_read_args r = {cache, i, 2, 4, i, 9, p, nullptr};
+  const csa_latent_attend_args a = {cache, p, 16 * 576, 576, 4, 16, i, 4, 4, nullptr, i, nullptr, 0, 0, 0.1f, p, f, nullptr};
+  const csa_latent_prefill_args e = {p, p, p, p, 768, 192, 1024, 256, 576, 1024, 256, 10, 20, i, i, 2, 4, 1, 0.1f, p, f, nullptr};
+  for (int n : {4, 9000}) {
+    const csa_tables_args t = {i, i, n, 8, i, i, 5, 7, i, i, i, l, i, i, i, nullptr};
+    csa_build_tables(&t, nullptr);
+  }
+  csa_latent_write(&w, nullptr);
+  csa_latent_read(&r, nullptr);
+  csa_latent_attend(&a, p, size_t(1) << 40, nullptr);
+  csa_latent_prefill(&e, nullptr);
+}
+int main() {
+  std::thread a(calls), b(calls);
+  a.join();
+  b.join();
+  std::printf("done\n");
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="its calls must not reach a GPU: the addresses are made up")
+def test_what_the_host_code_keeps_may_be_shared_by_threads(tmp_path):
+    """Calls of two threads under the compiler's race detector, without a driver: their launches fail."""
+    (tmp_path / "fakes.h").write_text(FAKES)
+    (tmp_path / "races.cu").write_text(RACES)
+    sources = [str(tmp_path / "races.cu")] + [os.path.join(build.CSRC, f"csa_latent_{f}.cu") for f in ("cache", "attend", "prefill")]
+    exe = str(tmp_path / "races")
+    subprocess.run([build.nvcc_path(), "-gencode=arch=compute_103a,code=compute_103a", "-std=c++17", "-t4", "-Xcompiler", "-fsanitize=thread",
+                    "-include", str(tmp_path / "fakes.h"), f"-I{build.INCLUDE}", f"-I{build.CSRC}", "-o", exe] + sources, check=True)
+    (tmp_path / "known").write_text("race:__device_stub__\n")  # the compiler's launch stubs keep the kernel's address
+    ran = subprocess.run([exe], capture_output=True, text=True, env={**os.environ, "TSAN_OPTIONS": f"suppressions={tmp_path}/known"})
+    if "FATAL: ThreadSanitizer" in ran.stderr:
+        pytest.skip("the race detector does not run here")
+    assert "done" in ran.stdout and "csa_latent" not in ran.stderr, ran.stderr
