@@ -1,4 +1,6 @@
 // csa_latent_attend.cu — latent attention, absorbed form (include/csa_latent.h).
+#include <cfloat>
+
 #include "csa_latent_common.cuh"
 #include "csa_latent_maps.h"
 #include "csa_latent_ptx.cuh"
@@ -756,7 +758,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
   const int p_head = 16 * warp + (lane & 15);
   const uint32_t p_row = smem_u32(S.p) + p_head * 128;
   const float c = A.scale * 1.4426950408889634f;
-  const float grow = kGrow / c;
+  const float grow = fminf(kGrow / c, FLT_MAX);  // finite also where the scale is almost nothing
   // O of the tile before tile g is complete: its second half is free (there is nothing before tile 0)
   auto o_done = [&](uint32_t tile) {
     return tile == 0 || warp_wait(bars + 8 * (kBarCEmpty + 2 * ((tile - 1) & 1) + 1), ((tile - 1) >> 1) & 1, stop);
@@ -795,7 +797,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
         keep[r] = 1.f;
-        if (top > m[r] + grow) {
+        if (top > m[r] + grow) {  // also when there was nothing (-infinity), not where there is still nothing
           up = true;
           keep[r] = csa::ex2((m[r] - top) * c);  // 0 when there was nothing
           m[r] = top;
