@@ -204,7 +204,9 @@ csa_status csa_latent_attend(const csa_latent_attend_args* args, void* ws, size_
  *   s_ij = scale * (q_ih[0:128] . k_nope_jh + q_ih[128:192] . k_rope_j)
  *   visible: j <= i + past (causal), or every j of the request
  *   out_ih = sum_j softmax_j(s_ij) v_jh,  lse_ih = log sum_j exp(s_ij)
- * A row that sees no key gets out 0 and lse -infinity.
+ * A row that sees no key gets out 0 and lse -infinity. What keys and values of other requests
+ * hold does not matter. Within a request a value v_jh that is not finite may reach rows that do
+ * not see key j too (as 0 times it); rows that see no key stay 0.
  *
  * q        [total_q, num_heads, 192] bf16; k_nope, v [total_k, num_heads, 128] bf16; k_rope
  *          [total_k, 64] bf16: 16-byte aligned, strides in elements and multiples of 8 (k_nope and

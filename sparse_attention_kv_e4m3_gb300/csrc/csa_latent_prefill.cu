@@ -581,6 +581,12 @@ __device__ __forceinline__ bool softmax_item(const csa_latent_prefill_args& A, S
     for (int k = 0; k < 4; ++k) csa::tmem_ld32(s_at + kTmemO + 32 * k, reinterpret_cast<uint32_t(&)[32]>(o[k]));
     csa::tmem_wait_ld();
   }
+  if (l == 0.f) {  // the row sees no key; its O is 0 times the values of keys that other rows see, NaN where those are not finite
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int x = 0; x < 32; ++x) o[k][x] = 0.f;
+  }
   if (lane >= rows) return true;
   const int64_t at = at0 + static_cast<int64_t>(lane) * A.num_heads;
   if (A.lse) A.lse[at] = l == 0.f ? -INFINITY : (m * c + log2f(l)) * 0.6931471805599453f;
