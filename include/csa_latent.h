@@ -162,7 +162,7 @@ csa_status csa_latent_read(const csa_latent_read_args* args, void* stream);
  * row_req    [num_q] int32, or NULL for row b -> request b
  * row_len    [num_q] int32
  * idx        [num_q, top] int32 rows idx_stride apart, or NULL (then top is 0)
- * scale      finite, above 0
+ * scale      above 0, below 2^127
  * out        [num_q, num_heads, 512] bf16, contiguous, 16-byte aligned
  * lse        [num_q, num_heads] fp32, or NULL
  * ws         csa_latent_attend_workspace_bytes(args) bytes, 16-byte aligned
@@ -233,7 +233,7 @@ typedef struct csa_latent_prefill_args {
   int32_t num_req;
   int32_t num_heads;
   int32_t causal;            /* 0 or 1 */
-  float scale;               /* finite, above 0 */
+  float scale;               /* above 0, below 2^127 */
   void* out;
   float* lse;
   int32_t* dev_status;

@@ -1221,7 +1221,7 @@ csa_status launch_bf16(const Kernel& K, int grid, int dev, cudaStream_t stream) 
 csa_status check_args(const csa_latent_attend_args* a) {
   if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->top < 0) return CSA_ERR_INVALID_ARG;
   if (a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return CSA_ERR_UNSUPPORTED;
-  if (!std::isfinite(a->scale) || !(a->scale > 0.f)) return CSA_ERR_INVALID_ARG;
+  if (!good_scale(a->scale)) return CSA_ERR_INVALID_ARG;
   if (a->num_q == 0) return CSA_OK;
   const csa_status st = check_cache(a->cache);
   if (st != CSA_OK) return st;

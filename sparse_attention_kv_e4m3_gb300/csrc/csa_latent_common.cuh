@@ -30,6 +30,9 @@ __device__ __forceinline__ float ue8m0(uint32_t b) {
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// A softmax scale: the kernels multiply it by log2 e, which has to stay finite.
+inline bool good_scale(float scale) { return scale > 0.f && scale < 0x1p127f; }
+
 inline csa_status check_cache(const csa_latent_cache& c) {
   if (!c.pages || c.num_pages < 1 || c.num_pages > INT32_MAX) return CSA_ERR_INVALID_ARG;
   const int64_t rec = csa_latent_record_bytes(c.record_format, c.rope_dim);

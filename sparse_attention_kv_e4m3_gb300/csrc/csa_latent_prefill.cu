@@ -685,7 +685,7 @@ csa_status check_args(const csa_latent_prefill_args* a) {
   if (!a || a->num_req < 0 || a->total_q < 0 || a->total_k < 0 || (a->causal != 0 && a->causal != 1))
     return CSA_ERR_INVALID_ARG;
   if (a->num_heads < 1 || a->num_heads > 65535) return CSA_ERR_UNSUPPORTED;
-  if (!std::isfinite(a->scale) || !(a->scale > 0.f)) return CSA_ERR_INVALID_ARG;
+  if (!good_scale(a->scale)) return CSA_ERR_INVALID_ARG;
   if (a->total_q > INT32_MAX || a->total_k > INT32_MAX || a->total_q * a->num_heads > INT32_MAX)
     return CSA_ERR_INVALID_ARG;
   if (a->num_req == 0 || a->total_q == 0) return CSA_OK;

@@ -2,6 +2,7 @@
 memory from, and what it refuses. Tensors are on the host here and the library only records its calls;
 struct layouts and the library's own refusals are tested in test_latent_abi.py."""
 import contextlib
+import ctypes
 import os
 import subprocess
 import threading
@@ -293,3 +294,20 @@ def test_what_the_host_code_keeps_may_be_shared_by_threads(tmp_path):
     if "FATAL: ThreadSanitizer" in ran.stderr:
         pytest.skip("the race detector does not run here")
     assert "done" in ran.stdout and "csa_latent" not in ran.stderr, ran.stderr
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build.build()
+    return latent.load()
+
+
+@pytest.mark.parametrize("scale", [2.0 ** 127, 3e38])
+def test_scales_whose_base_two_form_overflows_are_refused(lib, scale):
+    """The kernels compute in powers of two: scale times log2 e has to be finite."""
+    at = 0x10000
+    cache = latent.CacheArgs(at, 8, 64 * 1152, 64, 0)
+    a = latent.AttendArgs(cache, at, 16 * 576, 576, 4, 16, at, 4, 4, None, at, None, 0, 0, scale, at, at, None)
+    assert lib.csa_latent_attend(ctypes.byref(a), at, 1 << 40, None) == 1
+    p = latent.PrefillArgs(at, at, at, at, 768, 192, 1024, 256, 576, 1024, 256, 10, 20, at, at, 2, 4, 1, scale, at, at, None)
+    assert lib.csa_latent_prefill(ctypes.byref(p), None) == 1
