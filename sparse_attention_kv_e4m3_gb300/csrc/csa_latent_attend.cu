@@ -1246,7 +1246,8 @@ csa_status check_args(const csa_latent_attend_args* a) {
 using namespace csa_latent;
 
 extern "C" size_t csa_latent_attend_workspace_bytes(const csa_latent_attend_args* a) {
-  if (!a || a->num_q < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
+  if (!a || a->num_q < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS || a->pt_stride < 0 || a->top < 0) return 0;
+  if (a->num_q > 0 && (a->pt_stride < 1 || (a->idx != nullptr) != (a->top > 0))) return 0;
   return kOpenBytes + 2 * static_cast<size_t>(grid_cap(a)) * kPartFloats * sizeof(float);
 }
 

@@ -311,3 +311,10 @@ def test_scales_whose_base_two_form_overflows_are_refused(lib, scale):
     assert lib.csa_latent_attend(ctypes.byref(a), at, 1 << 40, None) == 1
     p = latent.PrefillArgs(at, at, at, at, 768, 192, 1024, 256, 576, 1024, 256, 10, 20, at, at, 2, 4, 1, scale, at, at, None)
     assert lib.csa_latent_prefill(ctypes.byref(p), None) == 1
+
+
+@pytest.mark.parametrize("change", [dict(pt_stride=0), dict(pt_stride=-1), dict(top=-1), dict(top=5), dict(idx=16), dict(idx=16, top=-2)])
+def test_workspace_of_sizes_that_the_call_refuses_is_0(lib, change):
+    sizes = dict(num_q=4, num_heads=16, pt_stride=4)
+    assert lib.csa_latent_attend_workspace_bytes(ctypes.byref(latent.AttendArgs(**sizes))) > 0
+    assert lib.csa_latent_attend_workspace_bytes(ctypes.byref(latent.AttendArgs(**{**sizes, **change}))) == 0
