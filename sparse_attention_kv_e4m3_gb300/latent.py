@@ -15,7 +15,7 @@ from typing import NamedTuple, Optional
 import torch
 
 from . import native
-from .native import CSA_OK, _check
+from .native import CSA_OK, _check, _empty, _new
 
 LATENT_DIM, MAX_HEADS, TABLES_MAX_REQ = 512, 128, 16384
 PREFILL_NOPE, PREFILL_ROPE, PREFILL_V = 128, 64, 128
@@ -112,23 +112,6 @@ def _want(t: torch.Tensor, dtype, dims: int, name: str, whole: bool = False) -> 
         raise ValueError(f"{name}: a {dims}-d {dtype} CUDA tensor, not {tuple(t.shape)} {t.dtype} on {t.device}")
     if not t.is_contiguous() and (whole or (t.stride(-1) != 1 and t.shape[-1] != 1)):
         raise ValueError(f"{name}: contiguous{'' if whole else ' in its last axis'}")
-    return t
-
-
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """A call's own memory, from the stream that the call runs on: the allocator gives memory out and takes it back in
-    that stream's order, and from a graph's own pool where that stream is being captured."""
-    if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """Memory of a result, noted as used on the current stream too, where the caller waits for it and reads it."""
-    t = _empty(shape, dtype, device, stream)
-    if stream is not None:
-        t.record_stream(torch.cuda.current_stream(device))
     return t
 
 
@@ -310,8 +293,7 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
         if _want(idx, torch.int32, 2, "idx").shape[0] != n:
             raise ValueError("idx [num_q, top]")
         if idx.shape[1] == 0:  # its address is null, which the library reads as whole histories: nothing is listed instead
-            with torch.cuda.stream(stream):
-                idx = torch.full((n, 1), -1, dtype=torch.int32, device=dev)
+            idx = _empty((n, 1), torch.int32, dev, stream, -1)
         top = idx.shape[1]
         idx_ptr, idx_step = idx.data_ptr(), _step(idx, 0, top)
     if row_req is not None:

@@ -249,12 +249,36 @@ def alloc_workspace(problem: Problem, k: int, device="cuda") -> torch.Tensor:
     return torch.empty(max(n, 16), dtype=torch.uint8, device=device)
 
 
+def _empty(shape, dtype, device, stream, fill=None) -> torch.Tensor:
+    """A call's own memory, filled where `fill` is given, from the stream that the call runs on: the allocator gives
+    memory out and takes it back in that stream's order, and from a graph's own pool where that stream is being captured."""
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _empty(shape, dtype, device, None, fill)
+    return torch.empty(shape, dtype=dtype, device=device) if fill is None else torch.full(shape, fill, dtype=dtype, device=device)
+
+
+def _new(shape, dtype, device, stream, fill=None) -> torch.Tensor:
+    """Memory of a result, noted as used on the current stream too, where the caller waits for it and reads it."""
+    t = _empty(shape, dtype, device, stream, fill)
+    if stream is not None:
+        t.record_stream(torch.cuda.current_stream(device))
+    return t
+
+
+def _contiguous(t: torch.Tensor, stream) -> torch.Tensor:
+    """The tensor, or a contiguous copy made on the stream that the call runs on."""
+    if t.is_contiguous():
+        return t
+    with torch.cuda.stream(stream):
+        return t.contiguous()
+
+
 def csa_index_score(problem: Problem, scores: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Scores of every visible record; invisible columns keep their initial value (NaN)."""
     a = problem.args()
     if scores is None:
-        scores = torch.full((problem.num_q, problem.score_stride()), float("nan"), dtype=torch.float32,
-                            device=problem.q_len.device)
+        scores = _new((problem.num_q, problem.score_stride()), torch.float32, problem.q_len.device, stream, float("nan"))
     st = load().csa_index_score(ctypes.byref(a), scores.data_ptr(), int(scores.stride(0)), _stream(stream))
     _check(st, "csa_index_score")
     return scores
@@ -269,11 +293,11 @@ def csa_index_score_topk_fused(problem: Problem, k: int = 512, ws: Optional[torc
     a = problem.args()
     dev = problem.q_len.device
     if ws is None:
-        ws = alloc_workspace(problem, k, dev)
+        ws = _empty((max(workspace_bytes(a, k), 16),), torch.uint8, dev, stream)
     if idx is None:
-        idx = torch.empty((problem.num_q, k), dtype=torch.int32, device=dev)
+        idx = _new((problem.num_q, k), torch.int32, dev, stream)
     if vals is None:
-        vals = torch.empty((problem.num_q, k), dtype=torch.float32, device=dev)
+        vals = _new((problem.num_q, k), torch.float32, dev, stream)
     if mark is None:
         st = load().csa_index_score_topk_fused(ctypes.byref(a), int(k), idx.data_ptr(), vals.data_ptr(),
                                                ws.data_ptr(), ws.numel(), _stream(stream))
@@ -330,11 +354,11 @@ def csa_index_topk(scores: torch.Tensor, problem: Problem, k: int = 512, ws: Opt
     a = problem.args()
     dev = problem.q_len.device
     if ws is None:
-        ws = alloc_workspace(problem, k, dev)
+        ws = _empty((max(workspace_bytes(a, k), 16),), torch.uint8, dev, stream)
     if idx is None:
-        idx = torch.empty((problem.num_q, k), dtype=torch.int32, device=dev)
+        idx = _new((problem.num_q, k), torch.int32, dev, stream)
     if vals is None:
-        vals = torch.empty((problem.num_q, k), dtype=torch.float32, device=dev)
+        vals = _new((problem.num_q, k), torch.float32, dev, stream)
     st = load().csa_index_topk(scores.data_ptr(), int(scores.stride(0)), ctypes.byref(a), int(k), idx.data_ptr(),
                                vals.data_ptr(), ws.data_ptr(), ws.numel(), _stream(stream))
     _check(st, "csa_index_topk")
@@ -357,7 +381,7 @@ def csa_index_write_keys(keys: torch.Tensor, row_pos: torch.Tensor, kv: torch.Te
     assert keys.dim() == 2 and keys.shape[1] == HEAD_DIM and keys.is_contiguous()
     assert kv.dtype == torch.uint8 and kv.dim() == 2 and kv.is_contiguous()
     assert row_pos.dtype == torch.int32 and page_table.dtype == torch.int32
-    pt = page_table.contiguous()
+    pt = _contiguous(page_table, stream)
     a = WriteArgs(keys.data_ptr(), dt, 0, int(keys.shape[0]), _ptr(row_req), row_pos.data_ptr(), kv.data_ptr(),
                   int(kv.shape[0]), int(kv.shape[1]), pt.data_ptr(), int(pt.shape[0]), int(pt.shape[1]),
                   _ptr(dev_status))
@@ -370,12 +394,12 @@ def csa_index_merge_topk(idx: torch.Tensor, vals: torch.Tensor, k: int, out_idx:
     both [G, num_q, k_in] on the device. Returns (out_idx [num_q, k], out_vals)."""
     if idx.dim() != 3 or vals.shape != idx.shape or idx.dtype != torch.int32 or vals.dtype != torch.float32:
         raise ValueError("idx int32 and vals fp32 of one shape [G, num_q, k_in]")
-    idx, vals = idx.contiguous(), vals.contiguous()
+    idx, vals = _contiguous(idx, stream), _contiguous(vals, stream)
     g, nq, k_in = idx.shape
     if out_idx is None:
-        out_idx = torch.empty((nq, k), dtype=torch.int32, device=idx.device)
+        out_idx = _new((nq, k), torch.int32, idx.device, stream)
     if out_vals is None:
-        out_vals = torch.empty((nq, k), dtype=torch.float32, device=idx.device)
+        out_vals = _new((nq, k), torch.float32, idx.device, stream)
     _check(load().csa_index_merge_topk(idx.data_ptr(), vals.data_ptr(), int(g), int(nq), int(k_in), int(k),
                                        out_idx.data_ptr(), out_vals.data_ptr(), _stream(stream)),
            "csa_index_merge_topk")
@@ -387,7 +411,7 @@ def csa_index_logits(problem: "Problem", logits: Optional[torch.Tensor] = None, 
     a = problem.args()
     stride = stride or problem.score_stride()
     if logits is None:
-        logits = torch.full((problem.num_q, stride), float("nan"), dtype=torch.float32, device=problem.q_len.device)
+        logits = _new((problem.num_q, stride), torch.float32, problem.q_len.device, stream, float("nan"))
     _check(load().csa_index_logits(ctypes.byref(a), logits.data_ptr(), int(stride), _stream(stream)),
            "csa_index_logits")
     return logits
@@ -406,10 +430,10 @@ def csa_recall_level1(layers, mean: bool = False, threshold: float = 0.5, sink: 
     stride = PAGE_RECORDS * pts
     dev = p0.q_len.device
     if out is None:
-        keep = torch.zeros((num_q, stride), dtype=torch.uint8, device=dev)
-        pages = torch.full((num_q, pts), -1, dtype=torch.int32, device=dev)
-        npg = torch.zeros(num_q, dtype=torch.int32, device=dev)
-        sc = torch.full((num_q, stride), float("nan"), dtype=torch.float32, device=dev) if scores else None
+        keep = _new((num_q, stride), torch.uint8, dev, stream, 0)
+        pages = _new((num_q, pts), torch.int32, dev, stream, -1)
+        npg = _new((num_q,), torch.int32, dev, stream, 0)
+        sc = _new((num_q, stride), torch.float32, dev, stream, float("nan")) if scores else None
     else:
         keep, pages, npg, sc = out
         stride = int(keep.stride(0))
@@ -419,7 +443,7 @@ def csa_recall_level1(layers, mean: bool = False, threshold: float = 0.5, sink: 
                     npg.data_ptr(), _ptr(sc))
     need = load().csa_recall_workspace_bytes(ctypes.byref(ra))
     if ws is None:
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        ws = _empty((max(need, 256),), torch.uint8, dev, stream)
     _check(load().csa_recall_level1(ctypes.byref(ra), ws.data_ptr(), ws.numel(), _stream(stream)),
            "csa_recall_level1")
     return keep, pages, npg, sc
