@@ -136,9 +136,9 @@ def _status(t, device):
 def _stream(stream, device) -> int:
     """The given stream, or the current one, as an address. The library launches on the current device, so the tensors
     and the stream have to be there."""
-    if device.index != torch.cuda.current_device() or (stream is not None and stream.device != device):
+    if device.index != torch._C._cuda_getDevice() or (stream is not None and stream.device != device):
         where = "" if stream is None else f", the stream on {stream.device}"
-        raise ValueError(f"tensors on {device}, the current device is cuda:{torch.cuda.current_device()}{where}")
+        raise ValueError(f"tensors on {device}, the current device is cuda:{torch._C._cuda_getDevice()}{where}")
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 

@@ -187,7 +187,6 @@ def test_positions_that_list_nothing_are_not_the_whole_history(host):
 def test_a_call_goes_to_the_current_device_only(monkeypatch):
     """The library launches on the current device: tensors and streams of another one are refused."""
     here, there = torch.device("cuda", 0), torch.device("cuda", 1)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
     monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: 0x55 + index, raising=False)
     side, far = Stream(0x99), Stream(0x99)
