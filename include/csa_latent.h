@@ -70,6 +70,9 @@ typedef struct csa_latent_cache {
  *     row_slot page_table[r][row_pos / 64] * 64 + row_pos % 64
  * Rows past the last new record get row_req 0, row_pos -1, row_len 0, row_slot -1: an empty
  * query row and a row that csa_latent_write skips, so that a captured graph can keep n_rows.
+ * A row stands for a new record. As the indexer's q_req and q_len, row_req and row_len are right
+ * where each query token brings one record; where a record stands for several tokens, a query row
+ * has to be made for each token by the caller (the slots and sums stay as they are).
  *
  * old_len, new_len  [num_req] int32; num_req 0 .. CSA_TABLES_MAX_REQ
  * page_table        [num_req, pt_stride] int32, in place

@@ -39,9 +39,11 @@ using csa::smem_u32;
 // fp32) in the workspace, which a second kernel joins in the order of the runs, so results do not
 // depend on timing.
 //
-// 4 rows of 65536 to 131072 bf16 records, 64 heads: 96 us, 5.0 TB/s, bound by HBM. 32 rows of 32768 4-bit records, 64 heads: 234 us,
-// 0.59 PFLOP/s, and 1024 rows of 512 positions, 128 heads: 280 us, 0.52 PFLOP/s, bound by the MMAs of S (64 rows
-// high: half the rate) and the hand-over of the two tiles between the roles, 3.5 k clocks a tile of which 2.4 k are MMAs.
+// 4 rows of 65536 to 131072 bf16 records, 64 heads: 96 us, 5.0 TB/s, bound by HBM. 32 rows of 32768 4-bit records, 64 heads: 233 us,
+// 0.60 PFLOP/s, and 1024 rows of 512 positions, 128 heads: 281 us, 0.52 PFLOP/s: 4.0 k and 4.7 k clocks a tile, of which the tensor
+// cores are active 1.66 k (S, 64 rows high and so at half rate, 1152, and O 512). What is full is shared memory: the
+// MMAs read 240 KB of operands a tile (Q and the records for S, the records again and four times P for O), 1.9 k clocks at 128
+// bytes a clock, and the roles' own loads and stores are 1.2 k wavefronts more; the second case adds the hand-over between units.
 constexpr int kTile = 64, kHeads = 64;            // records a tile, heads a unit
 constexpr int kColBytes = kTile * 128;            // 64 values of a tile's 64 records (or of Q's 64 heads)
 constexpr int kSoftmaxWarps = 4;
@@ -483,8 +485,9 @@ __device__ void role_load_regs(const Kernel& K, Smem<kRope>& S, int32_t* flags) 
 #pragma unroll
       for (int k = 0; k < Regs::kRecords; ++k) live[k] = rec[k] != nullptr;
       // While the tile's turn has not come: the records of the one after it, on their way to L2. Not where many
-      // rows list positions: such rows are a prompt chunk's, whose request's records are in L2 already (1024 rows
-      // of 512 positions: 333 us with it, 322 without).
+      // rows list positions: 1024 rows of one request, 512 positions, 128 heads take 289 us with it and 286
+      // without, their records being in L2 already. Rows of 128 different requests, which take this branch too, would be
+      // better off with it: 73 us, 79 without (bf16; 65 and 67 of 4-bit records).
       locate();
       find();
       if (!A.idx || K.cluster) x.prefetch(rec, t);
@@ -1163,8 +1166,10 @@ int grid_cap(const csa_latent_attend_args* a) {
 constexpr size_t kOpenBytes = (kMaxGrid * sizeof(Open) + 255) / 256 * 256;
 
 // CTAs that share a unit: where every unit is short (8 tiles a CTA at most) and there are fewer units than
-// SMs, the largest power of two up to 8 that still fits the SMs; else 0, the runs. 64 rows of 8 tiles: 28.5 us in
-// clusters of two, 49 us cut into 152 runs (whose parts are 28 MB, against 38 MB of records).
+// SMs, the largest power of two up to 8 that still fits the SMs; else 0, the runs. How long a unit can be is all that the
+// host knows: the table's width, or the number of positions. In a graph, L2 cold: 64 rows of 8 tiles take 31.8 us in
+// clusters of two, 38.0 us cut into 152 runs (whose parts are 28 MB, against 38 MB of records), in two launches; one row
+// of 16 tiles is the other way round, 23.7 us in a cluster of eight and 19.6 us in 16 runs.
 int cluster_of(const csa_latent_attend_args* a, int sms) {
   const int64_t units = static_cast<int64_t>(a->num_q) * ((a->num_heads + kHeads - 1) / kHeads);
   const int64_t per = a->idx ? (a->top + kTile - 1) / kTile : a->pt_stride;
@@ -1199,9 +1204,9 @@ csa_status launch(const Kernel& K, const MapsOf<kLoad>& M, int grid, int dev, cu
 }
 
 // Whole histories of bf16 records go through TMA where the cache's pages are a tensor of 128-byte columns (pages that
-// are not padded, or by such columns): long rows 102 us, 108 through registers. Listed positions do not (gathered four
-// rows a copy, 64 rows of 512 positions took 47 us, through registers 28), nor do short units in a cluster, whose few
-// tiles do not pay for the maps (one row of 1000 records: 20.8 us, 17.4).
+// are not padded, or by such columns): long rows 112 us with L2 cold, 118 through registers. Listed positions do not (gathered
+// four rows a copy, 64 rows of 512 positions took 47 us where registers took 28), nor do short units in a cluster, whose few
+// tiles do not pay for the maps (one row of 1000 records: 20.8 us where registers took 17.4).
 template <int kRope>
 csa_status launch_bf16(const Kernel& K, int grid, int dev, cudaStream_t stream) {
   const csa_latent_attend_args& a = K.A;

@@ -14,7 +14,7 @@ namespace {
 // so no block waits for another, then does its share of the new pages and of the
 // rows, each found by bisection in the running sums. A row's page is looked up in
 // the old entries of the table or in the free list, never in an entry that this
-// launch writes. 509 requests and a million rows: 12.7 us, of which 3.2 us are the bytes; the call costs the host more.
+// launch writes. 509 requests and a million rows: 11.2 us in a graph, of which 3.2 us are the bytes; the call costs the host more.
 
 constexpr int kTabThreads = 512;
 constexpr int kTabRowsPerBlock = 2048;  // rows a block is launched for
@@ -153,7 +153,7 @@ __global__ void __launch_bounds__(kTabThreads) build_tables_kernel(const csa_tab
 // A warp stores kRowsInFlight rows at a time, their loads all issued first: lane l holds the 16 latent
 // values 16 l .. 16 l + 15 (half a 32-value block, so a block's amax takes one exchange with the
 // neighbour lane) and the rope values 2 l, 2 l + 1. Rows are read once, coalesced. Bound by HBM:
-// 65537 fp32 rows stored in 4 bits and read back (two launches, 279 MB) take 52 us, 5.3 TB/s.
+// 65537 fp32 rows stored in 4 bits and read back (two launches, 279 MB) take 53 us, 5.3 TB/s.
 
 constexpr int kCopyThreads = 256;
 

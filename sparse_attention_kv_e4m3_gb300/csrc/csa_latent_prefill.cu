@@ -20,7 +20,7 @@ using csa::smem_u32;
 // Bound by the tensor cores (20 MMAs of 64 clocks a tile pair) while the exponentials of one query
 // tile run under the MMAs of the other. A row of S is a TMEM lane and belongs to one thread, P goes back over
 // S in TMEM as the A operand of O, V is read from shared memory as it lies (N-major).
-// 4096 rows over 16384 keys, 16 heads: 412 us, 1.46 PFLOP/s. 8 prompts of 130 to 2048, 32 heads: 148 us, 0.94 PFLOP/s:
+// 4096 rows over 16384 keys, 16 heads: 430 us, 1.40 PFLOP/s. 8 prompts of 130 to 2048, 32 heads: 150 us, 0.93 PFLOP/s:
 // there items are 1 to 16 key tiles, and what is lost is their ends, where the softmax warps write 64 KB (5 k clocks a tile).
 //
 // One block an item, but a block that is at the end of its item takes the place of one that has not started yet, so that the next

@@ -201,7 +201,7 @@ def csa_build_tables(old_len: torch.Tensor, new_len: torch.Tensor, page_table: t
                      stream=None) -> StepTables:
     """Block tables and slot maps of one step: request r holds old_len[r] records and gets new_len[r]
     more. page_table [num_req, pt_stride] gets the new pages in place, out of free_pages; the maps of
-    the new records (n_rows of them, the rest padding) are returned."""
+    the new records, one row each (n_rows of them, the rest padding), are returned."""
     _want(old_len, torch.int32, 1, "old_len")
     _want(new_len, torch.int32, 1, "new_len")
     _want(page_table, torch.int32, 2, "page_table", whole=True)
@@ -249,7 +249,8 @@ def csa_latent_write(x: torch.Tensor, slots: torch.Tensor, cache: LatentCache,
 def csa_latent_read(cache: LatentCache, page_table: torch.Tensor, kv_start: torch.Tensor, n_rows: int,
                     out: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None,
                     stream=None) -> torch.Tensor:
-    """Histories as rows [n_rows, 512 + rope] in bf16: record j of request r at kv_start[r] + j."""
+    """Histories as rows [n_rows, 512 + rope] in bf16: record j of request r at kv_start[r] + j.
+    Rows that no request covers are left as they are (whatever was there, where `out` is not given)."""
     _want(page_table, torch.int32, 2, "page_table", whole=True)
     _want(kv_start, torch.int32, 1, "kv_start")
     dev, n_rows = cache.device, int(n_rows)
@@ -275,8 +276,8 @@ def csa_latent_attend(q: torch.Tensor, cache: LatentCache, page_table: torch.Ten
                       out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
                       ws: Optional[torch.Tensor] = None, dev_status: Optional[torch.Tensor] = None, stream=None):
     """Latent attention, absorbed form: q [num_q, heads, 512 + rope] bf16 over the records below row_len[b]
-    of request row_req[b] (identity when None), or over the positions idx [num_q, top] (-1: none) among
-    them. `ws` is a uint8 workspace of attend_workspace_bytes(...) or more, not in use by another call
+    of request row_req[b] (identity when None), or over the positions idx [num_q, top] (-1: none; top
+    may be 0) among them. `ws` is a uint8 workspace of attend_workspace_bytes(...) or more, not in use by another call
     meanwhile; None takes one for the call (42 MB at most) from torch's allocator.
     Returns (out [num_q, heads, 512] bf16, lse [num_q, heads] fp32)."""
     _want(q, torch.bfloat16, 3, "q")
@@ -326,7 +327,7 @@ def csa_latent_prefill(q: torch.Tensor, k_nope: torch.Tensor, k_rope: torch.Tens
                        dev_status: Optional[torch.Tensor] = None, stream=None):
     """Latent attention, expanded form: q [total_q, heads, 192], k_nope and v [total_k, heads, 128], k_rope
     [total_k, 64], all bf16; request r has rows q_start[r] .. q_start[r + 1] of q and kv_start[r] ..
-    kv_start[r + 1] of the keys. Returns (out [total_q, heads, 128] bf16, lse [total_q, heads] fp32)."""
+    kv_start[r + 1] of the keys. Rows of no request are left as they are. Returns (out [total_q, heads, 128] bf16, lse [total_q, heads] fp32)."""
     _want(q, torch.bfloat16, 3, "q")
     _want(k_nope, torch.bfloat16, 3, "k_nope")
     _want(v, torch.bfloat16, 3, "v")
