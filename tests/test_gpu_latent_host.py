@@ -6,7 +6,7 @@ import pytest
 import torch
 
 from sparse_attention_kv_e4m3_gb300 import latent
-from test_gpu_latent import DEV, Attend, _lib, ints  # noqa: F401
+from test_gpu_latent import DEV, Attend, Prefill, _lib, ints  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +132,36 @@ def test_tables_of_many_sizes_in_threads():
 
     _in_threads(*(lambda n=n: calls(n) for n in (16384, 4200, 9000, 16384)))
     torch.cuda.synchronize()
+
+
+def test_results_made_on_a_branch_of_a_capture():
+    """Every operator on a stream forked from the capturing one, with the outputs that the calls make themselves."""
+    a, p = Attend([900, 70], 16, 64, "bf16", seed=26), Prefill([40, 9], [60, 9], 2, seed=27)
+    qs, ks, start = ints(p.qs), ints(p.ks), ints([0, 900, 970])
+    old, new, free = ints([900, 70]), ints([3, 0]), ints([50, 51])
+
+    def calls(**kw):
+        table = a.table.clone() if not kw else own_table
+        t = latent.csa_build_tables(old, new, table, free, 4, **kw)
+        rows = latent.csa_latent_read(a.cache, a.table, start, 970, **kw)
+        o = latent.csa_latent_attend(a.q, a.cache, a.table, a.lens, scale=a.scale, **kw)
+        none = latent.csa_latent_attend(a.q, a.cache, a.table, a.lens, scale=a.scale, idx=old.reshape(2, 1)[:, :0], **kw)
+        e = latent.csa_latent_prefill(p.q, p.kn, p.kr, p.v, qs, ks, scale=p.scale, **kw)
+        return (table, *t, rows, *o, *none, *e)
+
+    own_table = a.table.clone()
+    want = calls()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        got = calls(stream=side)
+        main.wait_stream(side)
+    for _ in range(3):
+        for g in got[1:]:
+            g.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        for g, w in zip(got, want):
+            assert torch.equal(g, w)
