@@ -11,11 +11,12 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB_PATH = os.path.join(PKG, "libcsa_index.so")
 SOURCES = [os.path.join(CSRC, f) for f in ("csa_index.cu", "csa_writer.cu", "csa_recall.cu", "csa_latent_cache.cu",
-                                               "csa_latent_attend.cu", "csa_latent_prefill.cu")]
+                                               "csa_latent_attend.cu", "csa_latent_prefill.cu", "csa_draft_rows.cu",
+                                               "csa_draft_attend.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in ("csa_ptx.cuh", "csa_select.cuh", "csa_score64.cuh",
                                                   "csa_internal.h", "csa_latent_common.cuh", "csa_latent_maps.h",
-                                                  "csa_latent_ptx.cuh")] + [
-    os.path.join(INCLUDE, f) for f in ("csa_index.h", "csa_latent.h")]
+                                                  "csa_latent_ptx.cuh", "csa_latent_rows.cuh", "csa_rotation.cuh")] + [
+    os.path.join(INCLUDE, f) for f in ("csa_index.h", "csa_latent.h", "csa_draft.h")]
 ARCH = "-gencode=arch=compute_103a,code=sm_103a"
 
 
