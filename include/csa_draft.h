@@ -122,9 +122,7 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  *   with mask     those i whose bit i % 64 of word i / 64 of its mask is set (drafts past the words are not seen), or
  *   without       those i <= j (a chain).
  * A mask may leave out the draft itself, and all drafts. A row that sees nothing gets out 0 and lse -infinity. What
- * records hold that no draft of the request sees (NaN, infinities) does not matter; a latent value that is not
- * finite in a draft's record that some draft sees may reach those that do not, as 0 times it (csa_latent_append and
- * csa_latent_write store none).
+ * records hold that a row does not see (NaN, infinities) does not matter to it.
  *
  * q          [num_q, num_heads, 512 + rope_dim] bf16, 16-byte aligned, the strides in elements
  *            and multiples of 8; num_heads 1 .. CSA_LATENT_MAX_HEADS
@@ -135,7 +133,7 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  * scale      above 0, below 2^127
  * out        [num_q, num_heads, 512] bf16, contiguous, 16-byte aligned
  * lse        [num_q, num_heads] fp32, or NULL
- * ws         csa_draft_attend_workspace_bytes(args) bytes, 16-byte aligned
+ * ws         csa_draft_attend_workspace_bytes(args) bytes, 32-byte aligned
  * Device errors: CSA_DEV_LEN_OOB (base_len below 0 or beyond the table: cut to it; drafts beyond the table are not
  * seen; bounds of rows that descend or leave [0, num_q]: that request's rows are left as they are), CSA_DEV_PAGE_OOB (the page's
  * records are left out), CSA_DEV_TIMEOUT (an on-chip wait ran past its limit; output invalid).

@@ -1,9 +1,27 @@
 // csa_draft_attend.cu — latent attention of drafted tokens (include/csa_draft.h).
+#include <cfloat>
+
 #include "csa_draft.h"
+#include "csa_latent_maps.h"
+#include "csa_latent_ptx.cuh"
 #include "csa_latent_rows.cuh"
 
 namespace csa_latent {
 namespace {
+
+using csa::smem_u32;
+
+constexpr int kTile = 128;                     // records a tile: two pages, one for each CTA's keys
+constexpr int kRows = 64;                      // query rows (draft and head) of a CTA; a unit is the pair's 128
+constexpr int kSlots = 8;                      // of the ring: 64 records x 128 values each, two 8 KB columns of 64 values
+constexpr int kColBytes = kRows * 128, kSlotBytes = 2 * kColBytes;
+constexpr int kSoftmaxWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kQueryWarps = 2;
+constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
+constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O in columns 0 .. 255, S of even and odd tiles in 256 and 320
+constexpr float kGrow = 8.0f;                  // log2 of how far p may exceed 1
+constexpr int kMaxPairs = 80;                  // CTA pairs at most: sizes the workspace
+constexpr int kParts = 4;                      // cut pieces of a run at most, see Walk
+constexpr int kBarRows = 1;                    // named barriers 1, 2: the two warps of rows 0 .. 31, and of 32 .. 63
 
 struct Request {
   int32_t row0, drafts, base, total;  // total: records that there are, history and drafts
@@ -102,6 +120,805 @@ __global__ void __launch_bounds__(128) attend_simple(const csa_draft_attend_args
   if (flags && A.dev_status) atomicOr(A.dev_status, flags);
 }
 
+// ------------------------------------------------------------- work
+//
+// A unit is 128 query rows (drafts times heads, in that order) of a request; its tiles are the request's. The tiles of
+// all units are put in an order and cut into equal runs, one a pair. A request of many tiles is cut into segments of about
+// a run's length first, and the order is request, segment, unit, tile: the units of a request read the same segment at
+// about the same time, so its records come from HBM once and from L2 for the others. What a run has of one unit's segment is
+// a piece; a unit that is not one whole piece leaves parts, which a second kernel joins in their order.
+
+struct Work {
+  Request R;
+  int32_t units, tiles, segments;
+};
+
+// Request r's share; units 0 where it has no rows.
+__device__ __forceinline__ Work work_of(const csa_draft_attend_args& A, int r, int64_t run, int32_t* flags) {
+  Work w = {{0, 0, 0, 0}, 0, 1, 1};
+  if (!request_of(A, r, &w.R, flags) || w.R.drafts == 0) return w;
+  w.units = static_cast<int32_t>((static_cast<int64_t>(w.R.drafts) * A.num_heads + 2 * kRows - 1) / (2 * kRows));
+  w.tiles = (w.R.total + kTile - 1) / kTile;
+  w.segments = max(1, static_cast<int32_t>((2 * static_cast<int64_t>(w.tiles) + run) / (2 * run)));  // tiles / run, rounded
+  return w;
+}
+
+__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int p, int pairs) { return total * p / pairs; }
+
+__device__ __forceinline__ int32_t segment_start(const Work& w, int s) { return static_cast<int32_t>(static_cast<int64_t>(w.tiles) * s / w.segments); }
+
+struct Kernel {
+  csa_draft_attend_args A;
+  struct Part* parts_of;  // [pairs][kParts]
+  float* parts;
+  int32_t pairs;
+};
+
+// A cut piece: where its rows begin among all rows (draft and head), and how many there are; 0 where there is no piece.
+struct Part {
+  int64_t first;
+  int32_t rows, reserved;
+};
+constexpr size_t kPartFloats = 2 * kRows * (static_cast<size_t>(kDim) + 2);  // O, then m c and l of its rows
+
+struct Plan {
+  int64_t total, run, at, end;  // tiles in all, a run's length (at least 1), this run
+  int32_t request;              // that `at` lies in
+  int64_t before;               // tiles of the requests before it
+};
+
+// Walks a run piece by piece. A segment has at least 3/4 of a run's tiles (segments = tiles / run rounded, 2 at least), so a run
+// meets at most two whole ones, or one and the ends of two others: kParts are enough for its cut pieces. (A unit of a
+// request with one segment is cut at a run's ends only.)
+struct Walk {
+  Work w;
+  int64_t left, run;
+  int32_t request, segment, unit, first, n;  // the piece: its first tile in the request, its tiles
+  bool cut;
+  __device__ __forceinline__ Walk(const csa_draft_attend_args& A, const Plan& P) : left(P.end - P.at), run(P.run), request(P.request) {
+    n = 0;
+    if (left <= 0) return;
+    int32_t ignore = 0;
+    w = work_of(A, request, run, &ignore);
+    const int64_t x = P.at - P.before;
+    const int32_t t = static_cast<int32_t>(x / w.units);
+    segment = static_cast<int32_t>(((static_cast<int64_t>(t) + 1) * w.segments - 1) / w.tiles);
+    const int32_t s0 = segment_start(w, segment), len = segment_start(w, segment + 1) - s0;
+    const int64_t y = x - static_cast<int64_t>(s0) * w.units;
+    unit = static_cast<int32_t>(y / len);
+    size(s0, len, static_cast<int32_t>(y % len));
+  }
+  __device__ __forceinline__ void size(int32_t s0, int32_t len, int32_t off) {
+    first = s0 + off;
+    n = static_cast<int32_t>(min(left, static_cast<int64_t>(len - off)));
+    cut = n < w.tiles;
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ void next(const csa_draft_attend_args& A) {
+    left -= n;
+    if (left <= 0) return;
+    int32_t s0 = segment_start(w, segment), len = segment_start(w, segment + 1) - s0;
+    if (first + n == s0 + len && ++unit == w.units) {
+      unit = 0;
+      if (++segment == w.segments) {
+        segment = 0;
+        int32_t ignore = 0;
+        do w = work_of(A, ++request, run, &ignore);
+        while (w.units == 0);
+      }
+      s0 = segment_start(w, segment);
+      len = segment_start(w, segment + 1) - s0;
+    }
+    size(s0, len, 0);
+  }
+  __device__ __forceinline__ int64_t first_row(const csa_draft_attend_args& A) const {  // of the unit, among all rows
+    return static_cast<int64_t>(w.R.row0) * A.num_heads + static_cast<int64_t>(unit) * 2 * kRows;
+  }
+  __device__ __forceinline__ int32_t rows(const csa_draft_attend_args& A) const {
+    return static_cast<int32_t>(min(static_cast<int64_t>(2 * kRows), static_cast<int64_t>(w.R.drafts) * A.num_heads - static_cast<int64_t>(unit) * 2 * kRows));
+  }
+};
+
+template <int kRope>
+struct Smem {
+  static constexpr int kCols = (kDim + kRope) / 64;
+  uint8_t q[kCols * kColBytes];
+  uint8_t ring[kSlots][kSlotBytes];
+  uint8_t rope[kRope ? kColBytes : 16];
+  alignas(1024) uint8_t p[2 * kColBytes];  // 64 rows x 128 keys, two columns of 64 keys
+  uint64_t bars[32];
+  float top[2][kRows], sum[2][kRows];  // of the two halves of a row's keys
+  uint32_t fills[2];                   // slots and rope columns that this CTA filled
+  int64_t scan[kThreads / 32];
+  Plan plan;
+  uint32_t tmem;
+  int abort;
+};
+enum { kBarFull = 0, kBarEmpty = kSlots, kBarRopeFull = 2 * kSlots, kBarRopeEmpty, kBarSFull, kBarSEmpty = kBarSFull + 2,
+       kBarPFull = kBarSEmpty + 2, kBarODone, kBarQFull, kBarQEmpty, kBarOEmpty, kBarLand, kBarDrain, kBars };
+static_assert(kBars <= 32, "barriers");
+
+// The run of this pair: the requests' tiles are summed by the block.
+template <int kRope>
+__device__ void make_plan(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
+  const csa_draft_attend_args& A = K.A;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = blockIdx.x >> 1;
+  const int per = (A.num_req + kThreads - 1) / kThreads, r0 = min(tid * per, A.num_req), r1 = min(r0 + per, A.num_req);
+  int64_t mine = 0;
+  for (int r = r0; r < r1; ++r) {
+    const Work w = work_of(A, r, 1, flags);
+    mine += static_cast<int64_t>(w.units) * w.tiles;
+  }
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) S.scan[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += S.scan[w];
+    total += S.scan[w];
+  }
+  const int64_t at = run_start(total, pair, K.pairs), end = run_start(total, pair + 1, K.pairs);
+  if (tid == 0 && at == end) S.plan = {total, 1, at, end, 0, 0};
+  if (at < end && at >= before && at < before + mine) {
+    int32_t ignore = 0;
+    for (int r = r0; r < r1; ++r) {
+      const Work w = work_of(A, r, 1, &ignore);
+      const int64_t all = static_cast<int64_t>(w.units) * w.tiles;
+      if (at < before + all) {
+        S.plan = {total, max(total / K.pairs, int64_t(1)), at, end, r, before};
+        break;
+      }
+      before += all;
+    }
+  }
+  __syncthreads();
+}
+
+// ------------------------------------------------------------- the pair's barriers
+//
+// Operands that the MMAs of a pair read lie in both CTAs; what makes them full is counted at the first one's barriers,
+// whose MMA warp issues for both. What gives them back is told to both by the MMAs' commits.
+
+__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity), "r"(csa::kSuspendHintNs)
+      : "memory");
+  return ok != 0;
+}
+
+// A whole warp's bounded wait on a barrier that either CTA arrives at, with one answer for all lanes.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
+  bool ok = try_wait_cluster(bar, parity);
+  if (!ok && csa::mbar_wait_slow(bar, parity, stop)) ok = try_wait_cluster(bar, parity);
+  return __all_sync(0xFFFFFFFFu, ok);
+}
+
+__device__ __forceinline__ void arrive_at(uint32_t remote) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+}
+
+__device__ __forceinline__ void arrive_expect_at(uint32_t remote, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(remote), "r"(bytes) : "memory");
+}
+
+// A tile to this CTA's shared memory that completes at either CTA's barrier.
+__device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* map, int32_t x, int32_t y, int32_t z, int32_t w, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar)
+      : "memory");
+}
+
+// D[tmem] (+)= A[smem] B[smem]^T over the pair: 128 rows of A, 64 in each CTA, and N columns, half of B in each. A CTA's D
+// are its 64 rows: the first CTA's columns in lanes 0 .. 63, the second one's in lanes 64 .. 127.
+__device__ __forceinline__ void mma_pair(uint32_t lead, uint32_t d, csa::Desc a, csa::Desc b, uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.u32 q, %7, 0;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 a, {%1, %2};\n\tmov.b64 b, {%3, %4};\n\t"
+      "@q tcgen05.mma.cta_group::2.kind::f16 [%0], a, b, %5, p;\n\t}" ::"r"(d),
+      "r"(a.lo), "r"(a.hi), "r"(b.lo), "r"(b.hi), "r"(idesc), "r"(static_cast<uint32_t>(accumulate)), "r"(lead)
+      : "memory");
+}
+
+// Arrives at the barrier in both CTAs when the MMAs issued so far are done.
+__device__ __forceinline__ void commit_pair(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %2;\n\t}" ::"r"(bar),
+      "r"(lead), "h"(static_cast<uint16_t>(3))
+      : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+struct Maps {  // [page][column of 64 values][record][value]: boxes of a page's two columns, and of one
+  CUtensorMap two, one;
+};
+
+// ------------------------------------------------------------- roles
+
+// The records, through the ring in the order in which the MMAs take them: the keys of tile 0, then keys of tile i + 1
+// and values of tile i. A CTA loads its page's 64 records whole as keys, and its 256 values' columns of both pages.
+// The values of a page with drafts or with an end in it are looked at before they are handed over: rows past the end
+// become 0, and so do values of drafts that are not finite (0 x NaN is not 0; a row that sees the draft has the NaN of its score).
+template <int kRope>
+__device__ void role_load(const Kernel& K, const Maps& M, Smem<kRope>& S, uint32_t rank, int32_t* flags) {
+  const csa_draft_attend_args& A = K.A;
+  const int lane = threadIdx.x & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0), ring = smem_u32(S.ring[0]);
+  csa::test_delay();
+  uint32_t q = 0, ropes = 0, landed = 0;  // slots filled, rope columns filled, landings
+  bool ok = true;
+  auto free_slot = [&](uint32_t k) { return ok = ok && warp_wait(bars + 8 * (kBarEmpty + k % kSlots), (k / kSlots & 1) ^ 1, stop); };
+  for (Walk W(A, S.plan); ok && W.more(); W.next(A)) {
+    const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
+    auto page_of = [&](int32_t p) {  // of the request's page p, or -1
+      if (p * kPageRecs >= W.w.R.total) return -1;
+      const int32_t page = __ldg(table + p);
+      if (page >= 0 && page < A.cache.num_pages) return page;
+      *flags |= CSA_DEV_PAGE_OOB;
+      return -1;
+    };
+    auto keys = [&](int32_t tile) {
+      const int32_t page = page_of(2 * tile + static_cast<int32_t>(rank));
+      if (kRope != 0) {
+        ok = ok && warp_wait(bars + 8 * kBarRopeEmpty, (ropes & 1) ^ 1, stop);
+        if (!ok) return;
+        ++ropes;
+        if (lane == 0) {
+          const uint32_t full = lead_bars + 8 * kBarRopeFull;
+          if (page >= 0) {
+            arrive_expect_at(full, kColBytes);
+            tma_pair_4d(smem_u32(S.rope), &M.one, 0, 0, kDim / 64, page, full);
+          } else {
+            arrive_at(full);
+          }
+        }
+      }
+      for (int d = 0; d < kDim / 128; ++d) {
+        if (!free_slot(q)) return;
+        if (lane == 0) {
+          const uint32_t full = lead_bars + 8 * (kBarFull + q % kSlots);
+          if (page >= 0) {
+            arrive_expect_at(full, kSlotBytes);
+            tma_pair_4d(ring + q % kSlots * kSlotBytes, &M.two, 0, 0, 2 * d, page, full);
+          } else {
+            arrive_at(full);
+          }
+        }
+        ++q;
+      }
+    };
+    auto values = [&](int32_t tile) {
+      for (int half = 0; half < 2; ++half) {
+        const int32_t p = 2 * tile + half, page = page_of(p), p0 = p * kPageRecs;
+        const int rows = page < 0 ? 0 : min(kPageRecs, W.w.R.total - p0);
+        const bool plain = rows == kPageRecs && p0 + kPageRecs <= W.w.R.base;
+        const uint32_t q0 = q;
+        if (plain) {
+          for (int b = 0; b < 2; ++b, ++q) {
+            if (!free_slot(q)) return;
+            if (lane == 0) {
+              const uint32_t full = lead_bars + 8 * (kBarFull + q % kSlots);
+              arrive_expect_at(full, kSlotBytes);
+              tma_pair_4d(ring + q % kSlots * kSlotBytes, &M.two, 0, 0, 4 * static_cast<int>(rank) + 2 * b, page, full);
+            }
+          }
+          continue;
+        }
+        if (!free_slot(q) || !free_slot(q + 1)) return;
+        if (lane == 0 && rows > 0) {
+          const uint32_t land = bars + 8 * kBarLand;
+          csa::mbar_arrive_expect_tx(land, 2 * kSlotBytes);
+          for (int b = 0; b < 2; ++b) csa::tma_tile_4d(ring + (q0 + b) % kSlots * kSlotBytes, &M.two, 0, 0, 4 * static_cast<int>(rank) + 2 * b, page, land);
+        }
+        q += 2;
+        if (rows > 0) {
+          if (!warp_wait(bars + 8 * kBarLand, landed & 1, stop)) {
+            ok = false;
+            csa::mbar_wait_drain(bars + 8 * kBarLand, landed & 1);  // no copy of this CTA is in flight when it leaves
+            return;
+          }
+          ++landed;
+        }
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t slot = ring + (q0 + b) % kSlots * kSlotBytes;
+          const int drafts = min(rows, max(0, W.w.R.base - p0));  // the first draft's row
+          for (int at = 8 * drafts + lane; at < 2 * 8 * kPageRecs; at += 32) {  // 16 bytes each, of 2 columns of 64 rows
+            const int row = at / 8 % kPageRecs;
+            if (row < drafts) continue;
+            const uint32_t addr = slot + 16 * at;
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (row < rows) {
+              v = csa::ld_shared_v4(addr);
+              if (!(nonfinite_bf16x2(v.x) | nonfinite_bf16x2(v.y) | nonfinite_bf16x2(v.z) | nonfinite_bf16x2(v.w))) continue;
+              auto clean = [](uint32_t w) { return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u); };
+              v = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+            }
+            csa::st_shared_v4(addr, v.x, v.y, v.z, v.w);
+          }
+        }
+        csa::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0)
+          for (int b = 0; b < 2; ++b) arrive_at(lead_bars + 8 * (kBarFull + (q0 + b) % kSlots));
+      }
+    };
+    keys(W.first);
+    for (int i = 0; ok && i < W.n; ++i) {
+      if (i + 1 < W.n) keys(W.first + i + 1);
+      if (ok) values(W.first + i);
+    }
+  }
+  __syncwarp();
+  // for the drain, should a wait have run out: how often each slot was filled
+  if (lane == 0) {
+    S.fills[0] = q;
+    S.fills[1] = ropes;
+  }
+}
+
+// Q of a piece: row i of this CTA's 64 is row first + 64 rank + i of all (draft and head); zeros past the unit's last.
+template <int kRope>
+__device__ void role_query(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
+  constexpr int kCols = Smem<kRope>::kCols;
+  const csa_draft_attend_args& A = K.A;
+  const int t = threadIdx.x - 32 * kQueryWarp, lane = t & 31;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0);
+  uint32_t piece = 0;
+  for (Walk W(A, S.plan); W.more(); W.next(A), ++piece) {
+    const int64_t first = W.first_row(A) + kRows * rank;
+    const int rows = W.rows(A) - kRows * static_cast<int>(rank);
+    if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
+#pragma unroll 2
+    for (int i = t >> 3; i < kRows; i += 4 * kQueryWarps) {
+      const int64_t row = i < rows ? first + i : first;
+      const uint8_t* q = static_cast<const uint8_t*>(A.q) + 2 * (row / A.num_heads * A.q_row_stride + row % A.num_heads * A.q_head_stride) + 16 * (t & 7);
+#pragma unroll
+      for (int c = 0; c < kCols; ++c) csa::cp_async16(smem_u32(S.q) + c * kColBytes + i * 128 + (((t & 7) ^ (i & 7)) << 4), i < rows ? q + 128 * c : A.q, i < rows);
+    }
+    csa::cp_async_wait_all();
+    csa::fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) arrive_at(lead_bars + 8 * kBarQFull);
+  }
+}
+
+// One warp of the first CTA issues the pair's MMAs: S(0), then S(i + 1) and O(i) in turn.
+template <int kRope>
+__device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
+  const csa_draft_attend_args& A = K.A;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem), lead = csa::elect_lane();
+  constexpr uint32_t idesc_s = csa::idesc_bf16_f32(2 * kRows, kTile), idesc_o = csa::idesc_bf16_f32(2 * kRows, 256) | csa::kIdescBMnMajor;
+  const csa::Desc q_desc(csa::sdesc_kmajor_sw128(smem_u32(S.q))), p_desc(csa::sdesc_kmajor_sw128(smem_u32(S.p))),
+      k_ring(csa::sdesc_kmajor_sw128(smem_u32(S.ring[0]))), k_rope(csa::sdesc_kmajor_sw128(smem_u32(S.rope))),
+      v_ring(csa::sdesc_mn_sw128_b16(smem_u32(S.ring[0]), kColBytes));
+  uint32_t q = 0, ropes = 0, g = 0, done = 0, piece = 0;  // slots and rope columns taken; tiles of which S, O was issued
+  bool ok = true;
+  auto need = [&](int bar, uint32_t parity) {
+    ok = ok && warp_wait(bars + 8 * bar, parity, stop);
+    csa::tc_fence_after();
+    return ok;
+  };
+  auto scores = [&](bool last) {
+    if (!need(kBarSEmpty + (g & 1), (g >> 1 & 1) ^ 1)) return;
+    const uint32_t d = tmem + kTmemS + (g & 1) * (kTile / 2);
+    if (kRope != 0) {
+      if (!need(kBarRopeFull, ropes & 1)) return;
+      ++ropes;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mma_pair(lead, d, q_desc.at(kDim / 64 * kColBytes + 32 * x), k_rope.at(32 * x), idesc_s, x > 0);
+      commit_pair(lead, bars + 8 * kBarRopeEmpty);
+    }
+#pragma unroll
+    for (int c = 0; c < kDim / 128; ++c) {
+      const uint32_t slot = q % kSlots;
+      if (!need(kBarFull + slot, q / kSlots & 1)) return;
+      const csa::Desc k = k_ring.at(slot * kSlotBytes);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint32_t at = x / 4 * kColBytes + x % 4 * 32;
+        mma_pair(lead, d, q_desc.at(c * kSlotBytes + at), k.at(at), idesc_s, kRope != 0 || c > 0 || x > 0);
+      }
+      commit_pair(lead, bars + 8 * (kBarEmpty + slot));
+      ++q;
+    }
+    commit_pair(lead, bars + 8 * (kBarSFull + (g & 1)));
+    if (last) commit_pair(lead, bars + 8 * kBarQEmpty);
+    ++g;
+  };
+  auto outputs = [&](bool begin) {
+    if (!need(kBarPFull, done & 1)) return;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const uint32_t slot = q % kSlots;
+        if (!need(kBarFull + slot, q / kSlots & 1)) return;
+        const csa::Desc v = v_ring.at(slot * kSlotBytes);
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          mma_pair(lead, tmem + 128 * b, p_desc.at(half * kColBytes + 32 * x), v.at(2048 * x), idesc_o, !begin || half > 0 || x > 0);
+        commit_pair(lead, bars + 8 * (kBarEmpty + slot));
+        ++q;
+      }
+    }
+    commit_pair(lead, bars + 8 * kBarODone);
+    ++done;
+  };
+  for (Walk W(A, S.plan); ok && W.more(); W.next(A), ++piece) {
+    const int n = static_cast<int>(csa::uniform(W.n));
+    if (!need(kBarQFull, piece & 1)) break;
+    scores(n == 1);
+    for (int i = 0; ok && i < n; ++i) {
+      if (i + 1 < n) scores(i + 2 == n);
+      if (ok && i == 0) need(kBarOEmpty, (piece & 1) ^ 1);
+      if (ok) outputs(i == 0);
+    }
+  }
+  commit_pair(lead, bars + 8 * kBarDrain);  // nothing of the pair's MMAs is in flight when it leaves
+  csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
+  __syncwarp();
+}
+
+// Which of 64 records from position p0 on the row of draft j sees.
+__device__ __forceinline__ uint64_t seen_bits(const csa_draft_attend_args& A, const Request& R, int32_t j, int32_t p0) {
+  auto below = [](int64_t n) { return n <= 0 ? 0ull : (n >= 64 ? ~0ull : (1ull << n) - 1); };
+  const uint64_t there = below(static_cast<int64_t>(R.total) - p0), history = below(static_cast<int64_t>(R.base) - p0);
+  uint64_t drafts = 0;
+  const int32_t i0 = p0 - R.base;  // the draft at p0, below 0 where that is history
+  if (!A.mask) {
+    drafts = below(static_cast<int64_t>(j) + 1 - i0);
+  } else if (i0 > -64) {
+    const uint64_t* words = A.mask + (R.row0 + static_cast<int64_t>(j)) * A.mask_stride;
+    auto word = [&](int32_t w) { return w >= 0 && w < A.mask_words ? __ldg(reinterpret_cast<const unsigned long long*>(words) + w) : 0ull; };
+    if (i0 < 0) drafts = word(0) << -i0;
+    else drafts = i0 % 64 ? word(i0 / 64) >> (i0 % 64) | word(i0 / 64 + 1) << (64 - i0 % 64) : word(i0 / 64);
+  }
+  return there & (history | drafts);
+}
+
+// A thread has a row and half of its tile's keys: warps 0, 1 the first page's (rows 0 .. 31, 32 .. 63), 2, 3 the second's.
+// For the output it has the row's values 0 .. 255 or 256 .. 511, its lane of TMEM. m is the row's reference, any: it
+// moves only when a tile exceeds it by 2^8, so that O is rarely scaled.
+template <int kRope>
+__device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
+  const csa_draft_attend_args& A = K.A;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & (kRows - 1), half = tid >> 6, pair_bar = kBarRows + (warp & 1);
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0);
+  const uint32_t tmem = S.tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  const float c = A.scale * 1.4426950408889634f;
+  const float grow = fminf(kGrow / c, FLT_MAX);
+  const uint32_t p_row = smem_u32(S.p) + half * kColBytes + row * 128;
+  uint32_t g = 0;
+  bool ok = true;  // once a wait has run out, the rest runs through without waiting: the warps meet at every barrier
+  auto o_done = [&](uint32_t tiles) { return tiles == 0 || warp_wait(bars + 8 * kBarODone, (tiles - 1) & 1, stop); };
+  uint32_t ordinal = 0;  // of the run's cut pieces
+  for (Walk W(A, S.plan); W.more(); W.next(A)) {
+    const Request R = W.w.R;
+    const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
+    const int64_t flat = W.first_row(A) + kRows * rank + row;
+    const bool there = kRows * static_cast<int>(rank) + row < W.rows(A);
+    const int32_t j = there ? static_cast<int32_t>(flat / A.num_heads) - R.row0 : 0;
+    auto page_at = [&](int32_t tile) { return (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : 0; };
+    int32_t page = page_at(W.first);
+    float m = -INFINITY, l = 0.f;  // l: of this thread's half of the keys
+    for (int i = 0; i < W.n; ++i, ++g) {
+      const int32_t p0 = (2 * (W.first + i) + half) * kPageRecs;
+      const bool good = page >= 0 && page < A.cache.num_pages;
+      if (i + 1 < W.n) page = page_at(W.first + i + 1);
+      ok = ok && warp_wait(bars + 8 * (kBarSFull + (g & 1)), g >> 1 & 1, stop);
+      csa::tc_fence_after();
+      float s[64];
+      {
+        uint32_t raw[32];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          csa::tmem_ld32(tmem + kTmemS + (g & 1) * (kTile / 2) + 32 * k, raw);
+          csa::tmem_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) s[32 * k + x] = __uint_as_float(raw[x]);
+        }
+      }
+      csa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(lead_bars + 8 * (kBarSEmpty + (g & 1)));
+      if (!(good && p0 + kPageRecs <= R.base && there)) {
+        const uint64_t seen = good && there ? seen_bits(A, R, j, p0) : 0;
+#pragma unroll
+        for (int x = 0; x < 64; ++x)
+          if (!(seen >> x & 1)) s[x] = -INFINITY;
+      }
+      float top = s[0];
+#pragma unroll
+      for (int x = 1; x < 64; ++x) top = fmaxf(top, s[x]);
+      if (csa::named_bar_any(pair_bar, 2 * 32, top > m + grow)) {  // also when there was nothing (-infinity), not where there is still nothing
+        S.top[half][row] = top;
+        csa::named_bar_sync(pair_bar, 2 * 32);
+        top = fmaxf(top, S.top[half ^ 1][row]);
+        csa::named_bar_sync(pair_bar, 2 * 32);
+        float keep = 1.f;
+        if (top > m + grow) {
+          keep = csa::ex2((m - top) * c);  // 0 when there was nothing
+          m = top;
+          l *= keep;
+        }
+        if (i > 0) {
+          ok = ok && o_done(g);
+          csa::tc_fence_after();
+#pragma unroll 1
+          for (int at = 0; at < 256; at += 32) {
+            uint32_t v[32];
+            csa::tmem_ld32(tmem + at, v);
+            csa::tmem_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
+            csa::tmem_st32(tmem + at, v);
+          }
+          csa::tmem_wait_st();
+          csa::tc_fence_before();
+        }
+      }
+      // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
+      const float mc = m == -INFINITY ? 0.f : m * c;
+      uint32_t w[32];
+      float sum[2] = {0.f, 0.f};
+#pragma unroll
+      for (int x = 0; x < 32; ++x) {
+        const float a = csa::ex2(fmaf(s[2 * x], c, -mc)), b = csa::ex2(fmaf(s[2 * x + 1], c, -mc));
+        sum[x & 1] += a + b;
+        w[x] = pack_bf16(a, b);
+      }
+      l += sum[0] + sum[1];
+      ok = ok && o_done(g);  // the tile before has been read
+#pragma unroll
+      for (int x = 0; x < 8; ++x) csa::st_shared_v4(p_row + ((x ^ (row & 7)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      csa::fence_proxy_async_smem();
+      csa::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) arrive_at(lead_bars + 8 * kBarPFull);
+    }
+    // the piece's output
+    S.sum[half][row] = l;
+    csa::named_bar_sync(pair_bar, 2 * 32);
+    l = half == 0 ? l + S.sum[1][row] : S.sum[0][row] + l;  // the same for both halves
+    csa::named_bar_sync(pair_bar, 2 * 32);
+    ok = ok && o_done(g);
+    csa::tc_fence_after();
+    const float mc = m == -INFINITY ? -INFINITY : m * c;
+    if (!W.cut) {
+      const float inv = l > 0.f ? 1.f / l : l;  // 0 for an empty row; a NaN stays one
+      if (there && half == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
+      uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * (flat * kDim + 256 * half);
+      const bool wide = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;
+#pragma unroll 1
+      for (int at = 0; at < 256; at += 32) {
+        uint32_t v[32], y[16];
+        csa::tmem_ld32(tmem + at, v);
+        csa::tmem_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 16; ++x) y[x] = pack_bf16(__uint_as_float(v[2 * x]) * inv, __uint_as_float(v[2 * x + 1]) * inv);
+        if (there) {
+          csa::st_global_v8(out + 2 * at, y, wide);
+          csa::st_global_v8(out + 2 * at + 32, y + 8, wide);
+        }
+      }
+    } else {
+      float* part = K.parts + (static_cast<size_t>(blockIdx.x >> 1) * kParts + ordinal) * kPartFloats;
+      const int at_row = kRows * rank + row;
+      if (half == 0) {
+        part[2 * kRows * kDim + at_row] = mc;
+        part[2 * kRows * (kDim + 1) + at_row] = l;
+      }
+#pragma unroll 1
+      for (int at = 0; at < 256; at += 32) {
+        uint32_t v[32];
+        csa::tmem_ld32(tmem + at, v);
+        csa::tmem_wait_ld();
+        if (there)
+#pragma unroll
+          for (int x = 0; x < 32; x += 8) csa::st_global_v8(part + static_cast<size_t>(at_row) * kDim + 256 * half + at + x, v + x, true);
+      }
+      ++ordinal;
+    }
+    csa::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) arrive_at(lead_bars + 8 * kBarOEmpty);
+  }
+}
+
+template <int kRope>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Kernel K, const __grid_constant__ Maps M) {
+  extern __shared__ uint8_t smem_raw[];
+  Smem<kRope>& S = *reinterpret_cast<Smem<kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = blockIdx.x & 1, bars = smem_u32(S.bars);
+  if (threadIdx.x == 0) {
+    for (int k = 0; k < kSlots; ++k) {
+      csa::mbar_init(bars + 8 * (kBarFull + k), 2);  // a loader of each CTA
+      csa::mbar_init(bars + 8 * (kBarEmpty + k), 1);
+    }
+    csa::mbar_init(bars + 8 * kBarRopeFull, 2);
+    csa::mbar_init(bars + 8 * kBarRopeEmpty, 1);
+    for (int k = 0; k < 2; ++k) {
+      csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
+      csa::mbar_init(bars + 8 * (kBarSEmpty + k), 2 * kSoftmaxWarps);
+    }
+    csa::mbar_init(bars + 8 * kBarPFull, 2 * kSoftmaxWarps);
+    csa::mbar_init(bars + 8 * kBarODone, 1);
+    csa::mbar_init(bars + 8 * kBarQFull, 2 * kQueryWarps);
+    csa::mbar_init(bars + 8 * kBarQEmpty, 1);
+    csa::mbar_init(bars + 8 * kBarOEmpty, 2 * kSoftmaxWarps);
+    csa::mbar_init(bars + 8 * kBarLand, 1);
+    csa::mbar_init(bars + 8 * kBarDrain, 1);
+    csa::mbar_init_fence();
+    S.abort = 0;
+    S.fills[0] = S.fills[1] = 0;
+  }
+  if (warp == kMmaWarp) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
+  int32_t flags = 0;
+  csa::tc_fence_before();
+  make_plan(K, S, &flags);  // ends with a block barrier
+  csa::cluster_arrive();
+  csa::cluster_wait();  // the other CTA's barriers are there
+  csa::tc_fence_after();
+  if (warp < kSoftmaxWarps) {
+    role_softmax(K, S, rank);
+  } else if (warp == kLoadWarp) {
+    role_load(K, M, S, rank, &flags);
+  } else if (warp == kMmaWarp) {
+    if (rank == 0) role_mma(K, S);
+  } else {
+    if (rank == 0 && warp == kQueryWarp && lane == 0) {  // what this run leaves for the join
+      Part* parts = K.parts_of + (blockIdx.x >> 1) * kParts;
+      int k = 0;
+      for (Walk W(K.A, S.plan); W.more(); W.next(K.A))
+        if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), 0};
+      while (k < kParts) parts[k++] = {0, 0, 0};
+    }
+    __syncwarp();
+    role_query(K, S, rank);
+  }
+  csa::tc_fence_before();
+  __syncthreads();
+  csa::cluster_arrive();
+  csa::cluster_wait();
+  // A wait that ran out may have left copies in flight, to be waited for before either CTA leaves. A slot's full barrier wants both
+  // CTAs' arrival: the first CTA arrives for the one that did not fill the slot.
+  if (rank == 0 && threadIdx.x == 0) {
+    const uint32_t other = csa::peer_smem(smem_u32(S.fills), 1);
+    const uint32_t theirs[2] = {ld_peer_u32(other), ld_peer_u32(other + 4)};
+    if (S.abort || ld_peer_u32(csa::peer_smem(smem_u32(&S.abort), 1))) {
+      auto drain = [&](int bar, uint32_t a, uint32_t b) {  // filled a and b times
+        for (uint32_t k = min(a, b); k < max(a, b); ++k) csa::mbar_arrive(bars + 8 * bar);
+        if (max(a, b) > 0) csa::mbar_wait_drain(bars + 8 * bar, (max(a, b) - 1) & 1);
+      };
+      for (uint32_t k = 0; k < kSlots; ++k) drain(kBarFull + k, (S.fills[0] + kSlots - 1 - k) / kSlots, (theirs[0] + kSlots - 1 - k) / kSlots);
+      drain(kBarRopeFull, S.fills[1], theirs[1]);
+    }
+  }
+  csa::cluster_arrive();
+  csa::cluster_wait();
+  if (warp == kMmaWarp) {
+    csa::tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(kTmemCols));
+  }
+  if (threadIdx.x == 0 && S.abort) flags |= CSA_DEV_TIMEOUT;
+  flags = static_cast<int32_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(flags)));
+  if (flags && K.A.dev_status && lane == 0) atomicOr(K.A.dev_status, flags);
+}
+
+// A part's weight 2^x, x <= 0: as a square, so that it becomes subnormal before it becomes 0.
+__device__ __forceinline__ float weight(float x) {
+  const float h = csa::ex2(0.5f * x);
+  return h * h;
+}
+
+// Joins the units that are in parts. Block (k, y) takes 8 rows of the unit that entry k of the runs' parts is the first
+// part of; the unit's other parts come after it, in the order of its tiles, and are added in that order, so the result does not
+// depend on timing. A warp a row, 16 values a lane.
+constexpr int kJoinWarps = 8;
+__global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
+  const csa_draft_attend_args& A = K.A;
+  __shared__ int32_t next[kMaxPairs * kParts], count;
+  const int tid = threadIdx.x, lane = tid & 31, row = blockIdx.y * kJoinWarps + (tid >> 5), all = K.pairs * kParts;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Part mine = K.parts_of[blockIdx.x];
+  if (static_cast<int>(blockIdx.y) * kJoinWarps >= mine.rows) return;
+  bool before = false;
+  for (int k = tid; k < static_cast<int>(blockIdx.x); k += 32 * kJoinWarps) before |= K.parts_of[k].rows > 0 && K.parts_of[k].first == mine.first;
+  if (__syncthreads_or(before)) return;
+  if (tid < 32) {  // the unit's parts, in order
+    int n = 0;
+    for (int k0 = blockIdx.x; k0 < all; k0 += 32) {
+      const int k = k0 + lane;
+      const bool is = k < all && K.parts_of[k].rows > 0 && K.parts_of[k].first == mine.first;
+      const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
+      if (is) next[n + __popc(who & ((1u << lane) - 1))] = k;
+      n += __popc(who);
+    }
+    if (lane == 0) count = n;
+  }
+  __syncthreads();
+  if (row >= mine.rows) return;
+  const int n = count;
+  float top = -INFINITY;
+  for (int i = lane; i < n; i += 32) top = fmaxf(top, K.parts[next[i] * kPartFloats + 2 * kRows * kDim + row]);
+#pragma unroll
+  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float l = 0.f;
+  float4 v[4] = {};
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const float* part = K.parts + next[i] * kPartFloats;
+    const float w = weight(part[2 * kRows * kDim + row] - ref);
+    const float4* x = reinterpret_cast<const float4*>(part + static_cast<size_t>(row) * kDim);
+    l = fmaf(part[2 * kRows * (kDim + 1) + row], w, l);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float4 y = x[lane + 32 * k];
+      v[k] = make_float4(fmaf(y.x, w, v[k].x), fmaf(y.y, w, v[k].y), fmaf(y.z, w, v[k].z), fmaf(y.w, w, v[k].w));
+    }
+  }
+  const float inv = l > 0.f ? 1.f / l : l;
+  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + (mine.first + row) * kDim);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) out[lane + 32 * k] = make_uint2(pack_bf16(v[k].x * inv, v[k].y * inv), pack_bf16(v[k].z * inv, v[k].w * inv));
+  if (A.lse && lane == 0) A.lse[mine.first + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
+// Pairs of the call: one for every two SMs, fewer when there cannot be as many tiles.
+int pairs_cap(const csa_draft_attend_args* a) {
+  const int64_t rows = static_cast<int64_t>(a->num_q) * a->num_heads, units = rows / (2 * kRows) + a->num_req;
+  const int64_t tiles = (static_cast<int64_t>(a->pt_stride) + 1) / 2;
+  return static_cast<int>(units >= kMaxPairs || tiles >= kMaxPairs || units * tiles >= kMaxPairs ? kMaxPairs : units * tiles);
+}
+
+constexpr size_t kPartsOfBytes = (kMaxPairs * kParts * sizeof(Part) + 255) / 256 * 256;
+
+template <int kRope>
+csa_status launch_bf16(const Kernel& K, int dev, cudaStream_t stream) {
+  static Kept ready;  // the kernel's shared memory size is set on each device once
+  constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
+  static_assert(smem <= 232448, "shared memory of one CTA");
+  const csa_latent_cache& cache = K.A.cache;
+  constexpr int64_t kRec = record_bytes(false, kRope);
+  Maps M;
+  const cuuint64_t dims[4] = {64, kPageRecs, static_cast<cuuint64_t>(kRec / 128), static_cast<cuuint64_t>(cache.num_pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kRec), 128, static_cast<cuuint64_t>(cache.page_stride_bytes)};
+  const cuuint32_t two[4] = {64, kPageRecs, 2, 1}, one[4] = {64, kPageRecs, 1, 1};
+  if (!encode_map(&M.two, cache.pages, 4, dims, strides, two) || !encode_map(&M.one, cache.pages, 4, dims, strides, one)) return CSA_ERR_INVALID_ARG;
+  if (!ready.get(dev)) {
+    if (cudaFuncSetAttribute(attend_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return CSA_ERR_CUDA;
+    ready.set(dev, 1);
+  }
+  attend_kernel<kRope><<<2 * K.pairs, kThreads, smem, stream>>>(K, M);
+  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+}
+
 csa_status check_args(const csa_draft_attend_args* a) {
   if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->mask_words < 0) return CSA_ERR_INVALID_ARG;
   if (a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS || a->mask_words > CSA_DRAFT_MAX_WORDS) return CSA_ERR_UNSUPPORTED;
@@ -126,8 +943,8 @@ csa_status check_args(const csa_draft_attend_args* a) {
 using namespace csa_latent;
 
 extern "C" size_t csa_draft_attend_workspace_bytes(const csa_draft_attend_args* a) {
-  if (!a || a->num_q < 0 || a->num_req < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
-  return 16;
+  if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
+  return kPartsOfBytes + kParts * static_cast<size_t>(pairs_cap(a)) * kPartFloats * sizeof(float);
 }
 
 extern "C" csa_status csa_draft_attend(const csa_draft_attend_args* a, void* ws, size_t ws_bytes, void* stream) {
@@ -135,8 +952,31 @@ extern "C" csa_status csa_draft_attend(const csa_draft_attend_args* a, void* ws,
   if (st != CSA_OK) return st;
   if (a->num_q == 0 || a->num_req == 0) return CSA_OK;
   if (!ws || ws_bytes < csa_draft_attend_workspace_bytes(a)) return CSA_ERR_WORKSPACE;
-  if (!aligned(ws, 16)) return CSA_ERR_ALIGNMENT;
-  if (static_cast<int64_t>(a->num_q) * a->num_heads > INT32_MAX) return CSA_ERR_INVALID_ARG;
-  attend_simple<<<static_cast<unsigned>(a->num_q * a->num_heads), 128, 0, static_cast<cudaStream_t>(stream)>>>(*a);
-  return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  if (!aligned(ws, 32)) return CSA_ERR_ALIGNMENT;
+  const auto s = static_cast<cudaStream_t>(stream);
+  if (a->cache.record_format == CSA_LATENT_MXFP4) {
+    if (static_cast<int64_t>(a->num_q) * a->num_heads > INT32_MAX) return CSA_ERR_INVALID_ARG;
+    attend_simple<<<static_cast<unsigned>(a->num_q * a->num_heads), 128, 0, s>>>(*a);
+    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
+  }
+  int sms = 0, dev = 0;
+  if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
+  Kernel K;
+  K.A = *a;
+  K.pairs = pairs_cap(a) < sms / 2 ? pairs_cap(a) : sms / 2;
+  K.parts_of = static_cast<Part*>(ws);
+  K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPartsOfBytes);
+  const csa_status ls = a->cache.rope_dim ? launch_bf16<64>(K, dev, s) : launch_bf16<0>(K, dev, s);
+  if (ls != CSA_OK || K.pairs == 1) return ls;
+  cudaLaunchConfig_t cfg = {};
+  const int64_t rows = static_cast<int64_t>(a->num_q) * a->num_heads;
+  cfg.gridDim = dim3(K.pairs * kParts, static_cast<unsigned>(((rows < 2 * kRows ? rows : 2 * kRows) + kJoinWarps - 1) / kJoinWarps));
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel, K) == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
