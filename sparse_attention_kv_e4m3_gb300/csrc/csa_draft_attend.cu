@@ -284,31 +284,21 @@ __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
 // Operands that the MMAs of a pair read lie in both CTAs; what makes them full is counted at the first one's barriers,
 // whose MMA warp issues for both. What gives them back is told to both by the MMAs' commits.
 
-__device__ __forceinline__ bool try_wait_cluster(uint32_t bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(bar), "r"(parity), "r"(csa::kSuspendHintNs)
-      : "memory");
-  return ok != 0;
-}
+// What they order are a CTA's own writes before its own tensor core's reads (a fence to the async proxy, then the arrival, then the
+// MMA that the other CTA issues for both), so the arrivals and waits need no memory order between the CTAs: with cluster
+// scope each cost several hundred clocks, and 16 drafts of two long histories took 1165 us instead of 359.
 
-// A whole warp's bounded wait on a barrier that either CTA arrives at, with one answer for all lanes.
+// A whole warp's bounded wait, with one answer for all lanes.
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* stop) {
-  bool ok = try_wait_cluster(bar, parity);
-  if (!ok && csa::mbar_wait_slow(bar, parity, stop)) ok = try_wait_cluster(bar, parity);
-  return __all_sync(0xFFFFFFFFu, ok);
+  return __all_sync(0xFFFFFFFFu, csa::mbar_wait(bar, parity, stop));
 }
 
 __device__ __forceinline__ void arrive_at(uint32_t remote) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
 
 __device__ __forceinline__ void arrive_expect_at(uint32_t remote, uint32_t bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(remote), "r"(bytes) : "memory");
+  asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(remote), "r"(bytes) : "memory");
 }
 
 // A tile to this CTA's shared memory that completes at either CTA's barrier.
