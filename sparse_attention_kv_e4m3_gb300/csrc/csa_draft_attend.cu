@@ -1,5 +1,6 @@
 // csa_draft_attend.cu — latent attention of drafted tokens (include/csa_draft.h).
 #include <cfloat>
+#include <type_traits>
 
 #include "csa_draft.h"
 #include "csa_latent_maps.h"
@@ -128,6 +129,12 @@ __global__ void __launch_bounds__(128) attend_simple(const csa_draft_attend_args
 // about the same time, so its records come from HBM once and from L2 for the others. What a run has of one unit's segment is
 // a piece; a unit that is not one whole piece leaves parts, which a second kernel joins in their order.
 
+// a / b of numbers that are not negative: most fit in 32 bits, whose division takes a fifth of the time.
+__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+  return a / b;
+}
+
 struct Work {
   Request R;
   int32_t units, tiles, segments;
@@ -139,13 +146,13 @@ __device__ __forceinline__ Work work_of(const csa_draft_attend_args& A, int r, i
   if (!request_of(A, r, &w.R, flags) || w.R.drafts == 0) return w;
   w.units = static_cast<int32_t>((static_cast<int64_t>(w.R.drafts) * A.num_heads + 2 * kRows - 1) / (2 * kRows));
   w.tiles = (w.R.total + kTile - 1) / kTile;
-  w.segments = max(1, static_cast<int32_t>((2 * static_cast<int64_t>(w.tiles) + run) / (2 * run)));  // tiles / run, rounded
+  w.segments = max(1, static_cast<int32_t>(quotient(2 * static_cast<int64_t>(w.tiles) + run, 2 * run)));  // tiles / run, rounded
   return w;
 }
 
-__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int p, int pairs) { return total * p / pairs; }
+__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int p, int pairs) { return quotient(total * p, pairs); }
 
-__device__ __forceinline__ int32_t segment_start(const Work& w, int s) { return static_cast<int32_t>(static_cast<int64_t>(w.tiles) * s / w.segments); }
+__device__ __forceinline__ int32_t segment_start(const Work& w, int s) { return static_cast<int32_t>(quotient(static_cast<int64_t>(w.tiles) * s, w.segments)); }
 
 struct Kernel {
   csa_draft_attend_args A;
@@ -161,12 +168,6 @@ struct Part {
 };
 constexpr size_t kPartFloats = 2 * kRows * (static_cast<size_t>(kDim) + 2);  // O, then m c and l of its rows
 
-struct Plan {
-  int64_t total, run, at, end;  // tiles in all, a run's length (at least 1), this run
-  int32_t request;              // that `at` lies in
-  int64_t before;               // tiles of the requests before it
-};
-
 // Walks a run piece by piece. A segment has at least 3/4 of a run's tiles (segments = tiles / run rounded, 2 at least), so a run
 // meets at most two whole ones, or one and the ends of two others: kParts are enough for its cut pieces. (A unit of a
 // request with one segment is cut at a run's ends only.)
@@ -175,18 +176,19 @@ struct Walk {
   int64_t left, run;
   int32_t request, segment, unit, first, n;  // the piece: its first tile in the request, its tiles
   bool cut;
-  __device__ __forceinline__ Walk(const csa_draft_attend_args& A, const Plan& P) : left(P.end - P.at), run(P.run), request(P.request) {
-    n = 0;
-    if (left <= 0) return;
+  // The run of `tiles` tiles from tile x of request r's.
+  __device__ __forceinline__ void start(const csa_draft_attend_args& A, int32_t r, int64_t x, int64_t tiles, int64_t run_tiles) {
+    left = tiles;
+    run = run_tiles;
+    request = r;
     int32_t ignore = 0;
     w = work_of(A, request, run, &ignore);
-    const int64_t x = P.at - P.before;
-    const int32_t t = static_cast<int32_t>(x / w.units);
-    segment = static_cast<int32_t>(((static_cast<int64_t>(t) + 1) * w.segments - 1) / w.tiles);
+    const int32_t t = static_cast<int32_t>(quotient(x, w.units));
+    segment = static_cast<int32_t>(quotient((static_cast<int64_t>(t) + 1) * w.segments - 1, w.tiles));
     const int32_t s0 = segment_start(w, segment), len = segment_start(w, segment + 1) - s0;
     const int64_t y = x - static_cast<int64_t>(s0) * w.units;
-    unit = static_cast<int32_t>(y / len);
-    size(s0, len, static_cast<int32_t>(y % len));
+    unit = static_cast<int32_t>(quotient(y, len));
+    size(s0, len, static_cast<int32_t>(y - static_cast<int64_t>(unit) * len));
   }
   __device__ __forceinline__ void size(int32_t s0, int32_t len, int32_t off) {
     first = s0 + off;
@@ -230,7 +232,8 @@ struct Smem {
   float top[2][kRows], sum[2][kRows];  // of the two halves of a row's keys
   uint32_t fills[2];                   // slots and rope columns that this CTA filled
   int64_t scan[kThreads / 32];
-  Plan plan;
+  Walk walk;  // at the run's first piece
+  uint32_t theirs[3];                  // the other CTA's fills, and whether a wait of its ran out
   uint32_t tmem;
   int abort;
 };
@@ -263,14 +266,14 @@ __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
     total += S.scan[w];
   }
   const int64_t at = run_start(total, pair, K.pairs), end = run_start(total, pair + 1, K.pairs);
-  if (tid == 0 && at == end) S.plan = {total, 1, at, end, 0, 0};
+  if (tid == 0 && at == end) S.walk.left = 0;
   if (at < end && at >= before && at < before + mine) {
     int32_t ignore = 0;
     for (int r = r0; r < r1; ++r) {
       const Work w = work_of(A, r, 1, &ignore);
       const int64_t all = static_cast<int64_t>(w.units) * w.tiles;
       if (at < before + all) {
-        S.plan = {total, max(total / K.pairs, int64_t(1)), at, end, r, before};
+        S.walk.start(A, r, at - before, end - at, max(quotient(total, K.pairs), int64_t(1)));
         break;
       }
       before += all;
@@ -331,10 +334,8 @@ __device__ __forceinline__ void commit_pair(uint32_t lead, uint32_t bar) {
       : "memory");
 }
 
-__device__ __forceinline__ uint32_t ld_peer_u32(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-  return v;
+__device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
 
 struct Maps {  // [page][column of 64 values][record][value]: boxes of a page's two columns, and of one
@@ -357,7 +358,7 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<kRope>& S, uint32
   uint32_t q = 0, ropes = 0, landed = 0;  // slots filled, rope columns filled, landings
   bool ok = true;
   auto free_slot = [&](uint32_t k) { return ok = ok && warp_wait(bars + 8 * (kBarEmpty + k % kSlots), (k / kSlots & 1) ^ 1, stop); };
-  for (Walk W(A, S.plan); ok && W.more(); W.next(A)) {
+  for (Walk W = S.walk; ok && W.more(); W.next(A)) {
     const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
     auto page_of = [&](int32_t p) {  // of the request's page p, or -1
       if (p * kPageRecs >= W.w.R.total) return -1;
@@ -474,14 +475,15 @@ __device__ void role_query(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0);
   uint32_t piece = 0;
-  for (Walk W(A, S.plan); W.more(); W.next(A), ++piece) {
-    const int64_t first = W.first_row(A) + kRows * rank;
-    const int rows = W.rows(A) - kRows * static_cast<int>(rank);
+  for (Walk W = S.walk; W.more(); W.next(A), ++piece) {
+    const int64_t first = static_cast<int64_t>(W.unit) * 2 * kRows + kRows * rank, draft = quotient(first, A.num_heads);  // of the request's rows
+    const int head = static_cast<int>(first - draft * A.num_heads), rows = W.rows(A) - kRows * static_cast<int>(rank);
     if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
 #pragma unroll 2
     for (int i = t >> 3; i < kRows; i += 4 * kQueryWarps) {
-      const int64_t row = i < rows ? first + i : first;
-      const uint8_t* q = static_cast<const uint8_t*>(A.q) + 2 * (row / A.num_heads * A.q_row_stride + row % A.num_heads * A.q_head_stride) + 16 * (t & 7);
+      const uint32_t x = head + i, j = x / static_cast<uint32_t>(A.num_heads), h = x - j * A.num_heads;
+      const uint8_t* q = static_cast<const uint8_t*>(A.q) + 16 * (t & 7);
+      if (i < rows) q += 2 * ((W.w.R.row0 + draft + j) * A.q_row_stride + h * A.q_head_stride);
 #pragma unroll
       for (int c = 0; c < kCols; ++c) csa::cp_async16(smem_u32(S.q) + c * kColBytes + i * 128 + (((t & 7) ^ (i & 7)) << 4), i < rows ? q + 128 * c : A.q, i < rows);
     }
@@ -555,7 +557,7 @@ __device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
     commit_pair(lead, bars + 8 * kBarODone);
     ++done;
   };
-  for (Walk W(A, S.plan); ok && W.more(); W.next(A), ++piece) {
+  for (Walk W = S.walk; ok && W.more(); W.next(A), ++piece) {
     const int n = static_cast<int>(csa::uniform(W.n));
     if (!need(kBarQFull, piece & 1)) break;
     scores(n == 1);
@@ -604,12 +606,12 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
   bool ok = true;  // once a wait has run out, the rest runs through without waiting: the warps meet at every barrier
   auto o_done = [&](uint32_t tiles) { return tiles == 0 || warp_wait(bars + 8 * kBarODone, (tiles - 1) & 1, stop); };
   uint32_t ordinal = 0;  // of the run's cut pieces
-  for (Walk W(A, S.plan); W.more(); W.next(A)) {
+  for (Walk W = S.walk; W.more(); W.next(A)) {
     const Request R = W.w.R;
     const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
     const int64_t flat = W.first_row(A) + kRows * rank + row;
     const bool there = kRows * static_cast<int>(rank) + row < W.rows(A);
-    const int32_t j = there ? static_cast<int32_t>(flat / A.num_heads) - R.row0 : 0;
+    const int32_t j = there ? static_cast<int32_t>(quotient(flat, A.num_heads)) - R.row0 : 0;
     auto page_at = [&](int32_t tile) { return (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : 0; };
     int32_t page = page_at(W.first);
     float m = -INFINITY, l = 0.f;  // l: of this thread's half of the keys
@@ -696,22 +698,43 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
     ok = ok && o_done(g);
     csa::tc_fence_after();
     const float mc = m == -INFINITY ? -INFINITY : m * c;
+    // 128 bytes of each of the warp's 32 rows at a time go through its 4 KB of P (which is not in use between a piece's last
+    // O and the next one's first P) and out as whole lines: stores of 32 bytes a row took 7.8 k clocks a piece.
+    const int rows_here = W.rows(A) - kRows * static_cast<int>(rank) - 32 * (warp & 1);  // of the warp's, that there are
+    const uint32_t stage = smem_u32(S.p) + 4096 * warp, r0 = lane >> 3, chunk = lane & 7;
+    auto lines_in = [&](const uint32_t (&v)[32]) {
+      __syncwarp();
+#pragma unroll
+      for (int x = 0; x < 8; ++x) csa::st_shared_v4(p_row + ((x ^ (row & 7)) << 4), v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+      __syncwarp();
+    };
+    auto lines_out = [&](uint8_t* to, int64_t row_bytes) {  // `to`: the warp's first row
+      uint4 y[8];
+#pragma unroll
+      for (int x = 0; x < 8; ++x) y[x] = csa::ld_shared_v4(stage + (r0 + 4 * x) * 128 + ((chunk ^ ((r0 + 4 * x) & 7)) << 4));
+#pragma unroll
+      for (int x = 0; x < 8; ++x)
+        if (static_cast<int>(r0) + 4 * x < rows_here) *reinterpret_cast<uint4*>(to + (r0 + 4 * x) * row_bytes + 16 * chunk) = y[x];
+    };
     if (!W.cut) {
       const float inv = l > 0.f ? 1.f / l : l;  // 0 for an empty row; a NaN stays one
       if (there && half == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
-      uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * (flat * kDim + 256 * half);
-      const bool wide = (reinterpret_cast<uintptr_t>(A.out) & 31) == 0;
+      uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * ((W.first_row(A) + kRows * rank + 32 * (warp & 1)) * kDim + 256 * half);
+      uint32_t v[2][32];
+      csa::tmem_ld32(tmem, v[0]);
+      csa::tmem_ld32(tmem + 32, v[1]);
 #pragma unroll 1
-      for (int at = 0; at < 256; at += 32) {
-        uint32_t v[32], y[16];
-        csa::tmem_ld32(tmem + at, v);
+      for (int at = 0; at < 256; at += 64) {
+        uint32_t y[32];
         csa::tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 16; ++x) y[x] = pack_bf16(__uint_as_float(v[2 * x]) * inv, __uint_as_float(v[2 * x + 1]) * inv);
-        if (there) {
-          csa::st_global_v8(out + 2 * at, y, wide);
-          csa::st_global_v8(out + 2 * at + 32, y + 8, wide);
+        for (int x = 0; x < 32; ++x) y[x] = pack_bf16(__uint_as_float(v[x >> 4][2 * (x & 15)]) * inv, __uint_as_float(v[x >> 4][2 * (x & 15) + 1]) * inv);
+        lines_in(y);
+        if (at + 64 < 256) {  // the next ones, while these go out
+          csa::tmem_ld32(tmem + at + 64, v[0]);
+          csa::tmem_ld32(tmem + at + 96, v[1]);
         }
+        lines_out(out + 2 * at, 2 * kDim);
       }
     } else {
       float* part = K.parts + (static_cast<size_t>(blockIdx.x >> 1) * kParts + ordinal) * kPartFloats;
@@ -720,14 +743,15 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
         part[2 * kRows * kDim + at_row] = mc;
         part[2 * kRows * (kDim + 1) + at_row] = l;
       }
+      uint8_t* to = reinterpret_cast<uint8_t*>(part + static_cast<size_t>(kRows * rank + 32 * (warp & 1)) * kDim + 256 * half);
+      uint32_t v[32];
+      csa::tmem_ld32(tmem, v);
 #pragma unroll 1
       for (int at = 0; at < 256; at += 32) {
-        uint32_t v[32];
-        csa::tmem_ld32(tmem + at, v);
         csa::tmem_wait_ld();
-        if (there)
-#pragma unroll
-          for (int x = 0; x < 32; x += 8) csa::st_global_v8(part + static_cast<size_t>(at_row) * kDim + 256 * half + at + x, v + x, true);
+        lines_in(v);
+        if (at + 32 < 256) csa::tmem_ld32(tmem + at + 32, v);
+        lines_out(to + 4 * at, 4 * kDim);
       }
       ++ordinal;
     }
@@ -743,27 +767,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_
   Smem<kRope>& S = *reinterpret_cast<Smem<kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1, bars = smem_u32(S.bars);
-  if (threadIdx.x == 0) {
-    for (int k = 0; k < kSlots; ++k) {
-      csa::mbar_init(bars + 8 * (kBarFull + k), 2);  // a loader of each CTA
-      csa::mbar_init(bars + 8 * (kBarEmpty + k), 1);
-    }
-    csa::mbar_init(bars + 8 * kBarRopeFull, 2);
-    csa::mbar_init(bars + 8 * kBarRopeEmpty, 1);
-    for (int k = 0; k < 2; ++k) {
-      csa::mbar_init(bars + 8 * (kBarSFull + k), 1);
-      csa::mbar_init(bars + 8 * (kBarSEmpty + k), 2 * kSoftmaxWarps);
-    }
-    csa::mbar_init(bars + 8 * kBarPFull, 2 * kSoftmaxWarps);
-    csa::mbar_init(bars + 8 * kBarODone, 1);
-    csa::mbar_init(bars + 8 * kBarQFull, 2 * kQueryWarps);
-    csa::mbar_init(bars + 8 * kBarQEmpty, 1);
-    csa::mbar_init(bars + 8 * kBarOEmpty, 2 * kSoftmaxWarps);
-    csa::mbar_init(bars + 8 * kBarLand, 1);
-    csa::mbar_init(bars + 8 * kBarDrain, 1);
+  if (threadIdx.x < kBars) {  // a barrier's arrivals
+    const int k = threadIdx.x;
+    int n = 1;
+    if (k < kBarEmpty || k == kBarRopeFull) n = 2;  // a loader of each CTA
+    else if (k == kBarSEmpty || k == kBarSEmpty + 1 || k == kBarPFull || k == kBarOEmpty) n = 2 * kSoftmaxWarps;
+    else if (k == kBarQFull) n = 2 * kQueryWarps;
+    csa::mbar_init(bars + 8 * k, n);
     csa::mbar_init_fence();
-    S.abort = 0;
-    S.fills[0] = S.fills[1] = 0;
+  }
+  if (threadIdx.x == 0) S.abort = 0;
+  if (threadIdx.x < 2) S.fills[threadIdx.x] = 0;
+  if (threadIdx.x == 32 * kLoadWarp) {
+    csa::prefetch_tensormap(&M.two);
+    if (kRope != 0) csa::prefetch_tensormap(&M.one);
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(kTmemCols) : "memory");
@@ -785,33 +802,34 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_
     if (rank == 0 && warp == kQueryWarp && lane == 0) {  // what this run leaves for the join
       Part* parts = K.parts_of + (blockIdx.x >> 1) * kParts;
       int k = 0;
-      for (Walk W(K.A, S.plan); W.more(); W.next(K.A))
+      for (Walk W = S.walk; W.more(); W.next(K.A))
         if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), 0};
       while (k < kParts) parts[k++] = {0, 0, 0};
     }
     __syncwarp();
     role_query(K, S, rank);
   }
+  if (warp == kMmaWarp && rank == 1) csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);  // the last commit has told this CTA too
   csa::tc_fence_before();
   __syncthreads();
+  if (threadIdx.x < 3) st_peer_u32(csa::peer_smem(smem_u32(&S.theirs[threadIdx.x]), rank ^ 1), threadIdx.x < 2 ? S.fills[threadIdx.x] : static_cast<uint32_t>(S.abort));
   csa::cluster_arrive();
   csa::cluster_wait();
   // A wait that ran out may have left copies in flight, to be waited for before either CTA leaves. A slot's full barrier wants both
   // CTAs' arrival: the first CTA arrives for the one that did not fill the slot.
-  if (rank == 0 && threadIdx.x == 0) {
-    const uint32_t other = csa::peer_smem(smem_u32(S.fills), 1);
-    const uint32_t theirs[2] = {ld_peer_u32(other), ld_peer_u32(other + 4)};
-    if (S.abort || ld_peer_u32(csa::peer_smem(smem_u32(&S.abort), 1))) {
+  if (S.abort || S.theirs[2]) {
+    if (rank == 0 && threadIdx.x == 0) {
       auto drain = [&](int bar, uint32_t a, uint32_t b) {  // filled a and b times
         for (uint32_t k = min(a, b); k < max(a, b); ++k) csa::mbar_arrive(bars + 8 * bar);
         if (max(a, b) > 0) csa::mbar_wait_drain(bars + 8 * bar, (max(a, b) - 1) & 1);
       };
-      for (uint32_t k = 0; k < kSlots; ++k) drain(kBarFull + k, (S.fills[0] + kSlots - 1 - k) / kSlots, (theirs[0] + kSlots - 1 - k) / kSlots);
-      drain(kBarRopeFull, S.fills[1], theirs[1]);
+      for (uint32_t k = 0; k < kSlots; ++k) drain(kBarFull + k, (S.fills[0] + kSlots - 1 - k) / kSlots, (S.theirs[0] + kSlots - 1 - k) / kSlots);
+      drain(kBarRopeFull, S.fills[1], S.theirs[1]);
     }
+    __syncwarp();
+    csa::cluster_arrive();
+    csa::cluster_wait();
   }
-  csa::cluster_arrive();
-  csa::cluster_wait();
   if (warp == kMmaWarp) {
     csa::tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(S.tmem), "r"(kTmemCols));
@@ -827,58 +845,81 @@ __device__ __forceinline__ float weight(float x) {
   return h * h;
 }
 
-// Joins the units that are in parts. Block (k, y) takes 8 rows of the unit that entry k of the runs' parts is the first
-// part of; the unit's other parts come after it, in the order of its tiles, and are added in that order, so the result does not
-// depend on timing. A warp a row, 16 values a lane.
+// Joins the units that are in parts. Block (p, y) takes 8 rows of each unit whose first part is one of run p's; the unit's other
+// parts come after it, in the order of its tiles, and are added in that order, so the result does not depend on timing. A
+// warp a row, 16 values a lane.
 constexpr int kJoinWarps = 8;
 __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
   const csa_draft_attend_args& A = K.A;
-  __shared__ int32_t next[kMaxPairs * kParts], count;
-  const int tid = threadIdx.x, lane = tid & 31, row = blockIdx.y * kJoinWarps + (tid >> 5), all = K.pairs * kParts;
+  constexpr int kMost = kMaxPairs * kParts;
+  __shared__ Part parts[kMost];
+  __shared__ uint16_t list[kParts][kMost];  // of each of the run's parts that a unit begins with: the unit's
+  __shared__ int32_t count[kParts];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y * kJoinWarps + warp, all = K.pairs * kParts;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const Part mine = K.parts_of[blockIdx.x];
-  if (static_cast<int>(blockIdx.y) * kJoinWarps >= mine.rows) return;
-  bool before = false;
-  for (int k = tid; k < static_cast<int>(blockIdx.x); k += 32 * kJoinWarps) before |= K.parts_of[k].rows > 0 && K.parts_of[k].first == mine.first;
-  if (__syncthreads_or(before)) return;
-  if (tid < 32) {  // the unit's parts, in order
+  for (int k = tid; k < all; k += 32 * kJoinWarps) parts[k] = K.parts_of[k];
+  __syncthreads();
+  if (warp < kParts) {
+    const int mine = blockIdx.x * kParts + warp;
+    const Part P = parts[mine];
     int n = 0;
-    for (int k0 = blockIdx.x; k0 < all; k0 += 32) {
-      const int k = k0 + lane;
-      const bool is = k < all && K.parts_of[k].rows > 0 && K.parts_of[k].first == mine.first;
-      const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
-      if (is) next[n + __popc(who & ((1u << lane) - 1))] = k;
-      n += __popc(who);
+    if (static_cast<int>(blockIdx.y) * kJoinWarps < P.rows) {
+      bool before = false;
+      for (int k0 = 0; k0 < all; k0 += 32) {
+        const int k = k0 + lane;
+        const bool is = k < all && parts[k].first == P.first && parts[k].rows > 0;
+        before |= is && k < mine;
+        const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
+        if (is) list[warp][n + __popc(who & ((1u << lane) - 1))] = static_cast<uint16_t>(k);
+        n += __popc(who);
+      }
+      if (__any_sync(0xFFFFFFFFu, before)) n = 0;  // an earlier part's
     }
-    if (lane == 0) count = n;
+    if (lane == 0) count[warp] = n;
   }
   __syncthreads();
-  if (row >= mine.rows) return;
-  const int n = count;
-  float top = -INFINITY;
-  for (int i = lane; i < n; i += 32) top = fmaxf(top, K.parts[next[i] * kPartFloats + 2 * kRows * kDim + row]);
+  for (int i = 0; i < kParts; ++i) {
+    const int n = count[i];
+    const Part P = parts[blockIdx.x * kParts + i];
+    if (n == 0 || row >= P.rows) continue;
+    auto part_of = [&](int k) { return K.parts + static_cast<size_t>(list[i][k]) * kPartFloats; };
+    float top = -INFINITY;
+    for (int k = lane; k < n; k += 32) top = fmaxf(top, part_of(k)[2 * kRows * kDim + row]);
 #pragma unroll
-  for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-  const float ref = top == -INFINITY ? 0.f : top;
-  float l = 0.f;
-  float4 v[4] = {};
-#pragma unroll 4
-  for (int i = 0; i < n; ++i) {
-    const float* part = K.parts + next[i] * kPartFloats;
-    const float w = weight(part[2 * kRows * kDim + row] - ref);
-    const float4* x = reinterpret_cast<const float4*>(part + static_cast<size_t>(row) * kDim);
-    l = fmaf(part[2 * kRows * (kDim + 1) + row], w, l);
+    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
+    const float ref = top == -INFINITY ? 0.f : top;
+    float l = 0.f;
+    float4 v[4] = {};
+    auto add = [&](auto step, int k) {
+      constexpr int kStep = decltype(step)::value;
+      float w[kStep], s[kStep];
+      float4 x[kStep][4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 y = x[lane + 32 * k];
-      v[k] = make_float4(fmaf(y.x, w, v[k].x), fmaf(y.y, w, v[k].y), fmaf(y.z, w, v[k].z), fmaf(y.w, w, v[k].w));
-    }
+      for (int j = 0; j < kStep; ++j) {
+        const float* part = part_of(k + j);
+        w[j] = part[2 * kRows * kDim + row];
+        s[j] = part[2 * kRows * (kDim + 1) + row];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) x[j][c] = reinterpret_cast<const float4*>(part + static_cast<size_t>(row) * kDim)[lane + 32 * c];
+      }
+#pragma unroll
+      for (int j = 0; j < kStep; ++j) {
+        const float f = weight(w[j] - ref);
+        l = fmaf(s[j], f, l);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          v[c] = make_float4(fmaf(x[j][c].x, f, v[c].x), fmaf(x[j][c].y, f, v[c].y), fmaf(x[j][c].z, f, v[c].z), fmaf(x[j][c].w, f, v[c].w));
+      }
+    };
+    int k = 0;
+    for (; k + 4 <= n; k += 4) add(std::integral_constant<int, 4>(), k);
+    for (; k < n; ++k) add(std::integral_constant<int, 1>(), k);
+    const float inv = l > 0.f ? 1.f / l : l;
+    uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + (P.first + row) * kDim);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) out[lane + 32 * c] = make_uint2(pack_bf16(v[c].x * inv, v[c].y * inv), pack_bf16(v[c].z * inv, v[c].w * inv));
+    if (A.lse && lane == 0) A.lse[P.first + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
   }
-  const float inv = l > 0.f ? 1.f / l : l;
-  uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + (mine.first + row) * kDim);
-#pragma unroll
-  for (int k = 0; k < 4; ++k) out[lane + 32 * k] = make_uint2(pack_bf16(v[k].x * inv, v[k].y * inv), pack_bf16(v[k].z * inv, v[k].w * inv));
-  if (A.lse && lane == 0) A.lse[mine.first + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
 }
 
 // Pairs of the call: one for every two SMs, fewer when there cannot be as many tiles.
@@ -961,7 +1002,7 @@ extern "C" csa_status csa_draft_attend(const csa_draft_attend_args* a, void* ws,
   if (ls != CSA_OK || K.pairs == 1) return ls;
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = static_cast<int64_t>(a->num_q) * a->num_heads;
-  cfg.gridDim = dim3(K.pairs * kParts, static_cast<unsigned>(((rows < 2 * kRows ? rows : 2 * kRows) + kJoinWarps - 1) / kJoinWarps));
+  cfg.gridDim = dim3(K.pairs, static_cast<unsigned>(((rows < 2 * kRows ? rows : 2 * kRows) + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
