@@ -16,13 +16,20 @@ constexpr int kTile = 128;                     // records a tile: two pages, one
 constexpr int kRows = 64;                      // query rows (draft and head) of a CTA; a unit is the pair's 128
 constexpr int kSlots = 8;                      // of the ring: 64 records x 128 values each, two 8 KB columns of 64 values
 constexpr int kColBytes = kRows * 128, kSlotBytes = 2 * kColBytes;
-constexpr int kSoftmaxWarps = 4, kLoadWarp = 4, kMmaWarp = 5, kQueryWarp = 6, kQueryWarps = 2;
-constexpr int kThreads = 32 * (kQueryWarp + kQueryWarps);
+constexpr int kSoftmaxWarps = 8, kMmaWarp = kSoftmaxWarps;
+// The loaders: of bf16 records one warp, by TMA, and two for queries that TMA does not reach; of 4-bit records eight, through
+// registers, which take the queries too.
+template <bool kFp4>
+struct Warps {
+  static constexpr int kQuery = kMmaWarp + (kFp4 ? 1 : 2), kQueries = kFp4 ? 8 : 2, kThreads = 32 * (kQuery + kQueries);
+  static constexpr int kFills = kFp4 ? kQueries : 1;  // arrivals of a CTA that make a slot full
+};
+constexpr int kLoadWarp = kMmaWarp + 1;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O in columns 0 .. 255, S of even and odd tiles in 256 and 320
 constexpr float kGrow = 8.0f;                  // log2 of how far p may exceed 1
 constexpr int kMaxPairs = 80;                  // CTA pairs at most: sizes the workspace
 constexpr int kParts = 4;                      // cut pieces of a run at most, see Walk
-constexpr int kBarRows = 1;                    // named barriers 1, 2: the two warps of rows 0 .. 31, and of 32 .. 63
+constexpr int kBarRows = 1;                    // named barriers 1, 2: the four warps of rows 0 .. 31, and of 32 .. 63
 
 struct Request {
   int32_t row0, drafts, base, total;  // total: records that there are, history and drafts
@@ -42,85 +49,6 @@ __device__ __forceinline__ bool request_of(const csa_draft_attend_args& A, int r
   return true;
 }
 
-// Whether draft j (of row row0 + j) sees position p.
-__device__ __forceinline__ bool sees(const csa_draft_attend_args& A, const Request& R, int j, int32_t p) {
-  const int i = p - R.base;
-  if (i < 0) return true;
-  if (!A.mask) return i <= j;
-  return i < 64 * A.mask_words && (A.mask[(R.row0 + j) * A.mask_stride + i / 64] >> (i % 64) & 1);
-}
-
-// A block a query row and head: scores of 64 records, the running maximum and sum, 512 / 128 output values a thread.
-__global__ void __launch_bounds__(128) attend_simple(const csa_draft_attend_args A) {
-  __shared__ float q[kDim + 64], s[kPageRecs];
-  __shared__ int32_t found;
-  __shared__ Request R;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.x % A.num_heads, b = blockIdx.x / A.num_heads;
-  const bool fp4 = A.cache.record_format == CSA_LATENT_MXFP4;
-  const int rope = A.cache.rope_dim, rec_bytes = record_bytes(fp4, rope);
-  int32_t flags = 0;
-  if (tid == 0) found = -1;
-  __syncthreads();
-  for (int r = tid; r < A.num_req; r += 128) {
-    Request X;
-    if (request_of(A, r, &X, &flags) && b >= X.row0 && b < X.row0 + X.drafts) found = r;
-  }
-  __syncthreads();
-  if (flags && A.dev_status) atomicOr(A.dev_status, flags);
-  flags = 0;
-  const int r = found;
-  if (r < 0) return;
-  if (tid == 0) request_of(A, r, &R, &flags);
-  const __nv_bfloat16* qp = static_cast<const __nv_bfloat16*>(A.q) + b * A.q_row_stride + h * A.q_head_stride;
-  for (int i = tid; i < kDim + rope; i += 128) q[i] = __bfloat162float(qp[i]);
-  __syncthreads();
-  const int j = b - R.row0;
-  float m = -INFINITY, l = 0.f, o[4] = {};
-  auto value = [&](const uint8_t* rec, int i) {
-    if (!fp4) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec)[i]);
-    if (i >= kDim) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(rec + kCodeBytes + kScaleBytes)[i - kDim]);
-    const uint32_t code = rec[i / 2] >> (4 * (i & 1)) & 15, mag = code & 7;
-    const float v = mag < 2 ? 0.5f * mag : ldexpf(1.f + 0.5f * (mag & 1), (mag >> 1) - 1);
-    return (code & 8 ? -v : v) * ue8m0(rec[kCodeBytes + i / 32]);
-  };
-  for (int p0 = 0; p0 < R.total; p0 += kPageRecs) {
-    const int32_t page = A.page_table[static_cast<int64_t>(r) * A.pt_stride + p0 / kPageRecs];
-    if (page < 0 || page >= A.cache.num_pages) {
-      flags |= CSA_DEV_PAGE_OOB;
-      continue;
-    }
-    const uint8_t* recs = A.cache.pages + page * A.cache.page_stride_bytes;
-    for (int n = warp; n < kPageRecs; n += 4) {
-      float sum = 0.f;
-      const bool live = p0 + n < R.total && sees(A, R, j, p0 + n);
-      if (live)
-        for (int i = lane; i < kDim + rope; i += 32) sum = fmaf(q[i], value(recs + n * rec_bytes, i), sum);
-      for (int k = 16; k > 0; k >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, k);
-      if (lane == 0) s[n] = live ? sum * A.scale : -INFINITY;
-    }
-    __syncthreads();
-    float top = m;
-    for (int n = 0; n < kPageRecs; ++n) top = fmaxf(top, s[n]);
-    if (top > -INFINITY) {
-      const float keep = expf(m - top);
-      l *= keep;
-      for (int k = 0; k < 4; ++k) o[k] *= keep;
-      for (int n = 0; n < kPageRecs; ++n) {
-        if (s[n] == -INFINITY) continue;
-        const float p = expf(s[n] - top);
-        l += p;
-        for (int k = 0; k < 4; ++k) o[k] = fmaf(p, value(recs + n * rec_bytes, tid + 128 * k), o[k]);
-      }
-      m = top;
-    }
-    __syncthreads();
-  }
-  const int64_t row = static_cast<int64_t>(b) * A.num_heads + h;
-  for (int k = 0; k < 4; ++k) static_cast<__nv_bfloat16*>(A.out)[row * kDim + tid + 128 * k] = __float2bfloat16(l > 0.f ? o[k] / l : l);
-  if (tid == 0 && A.lse) A.lse[row] = l == 0.f ? -INFINITY : m + logf(l);
-  if (flags && A.dev_status) atomicOr(A.dev_status, flags);
-}
-
 // ------------------------------------------------------------- work
 //
 // A unit is 128 query rows (drafts times heads, in that order) of a request; its tiles are the request's. The tiles of
@@ -129,10 +57,11 @@ __global__ void __launch_bounds__(128) attend_simple(const csa_draft_attend_args
 // about the same time, so its records come from HBM once and from L2 for the others. What a run has of one unit's segment is
 // a piece; a unit that is not one whole piece leaves parts, which a second kernel joins in their order.
 
-// a / b of numbers that are not negative: most fit in 32 bits, whose division takes a fifth of the time.
-__host__ __device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+// a / b of numbers that are not negative: most fit in 32 bits, whose division takes a fifth of the time and little code.
+__device__ __noinline__ int64_t wide_quotient(int64_t a, int64_t b) { return a / b; }
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
   if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
-  return a / b;
+  return wide_quotient(a, b);
 }
 
 struct Work {
@@ -140,17 +69,21 @@ struct Work {
   int32_t units, tiles, segments;
 };
 
+__device__ __forceinline__ void set_segments(Work& w, int64_t run) {  // tiles / run, rounded
+  w.segments = run >= 2 * static_cast<int64_t>(w.tiles) ? 1 : max(1, static_cast<int32_t>(quotient(2 * static_cast<int64_t>(w.tiles) + run, 2 * run)));
+}
+
 // Request r's share; units 0 where it has no rows.
 __device__ __forceinline__ Work work_of(const csa_draft_attend_args& A, int r, int64_t run, int32_t* flags) {
   Work w = {{0, 0, 0, 0}, 0, 1, 1};
   if (!request_of(A, r, &w.R, flags) || w.R.drafts == 0) return w;
   w.units = static_cast<int32_t>((static_cast<int64_t>(w.R.drafts) * A.num_heads + 2 * kRows - 1) / (2 * kRows));
   w.tiles = (w.R.total + kTile - 1) / kTile;
-  w.segments = max(1, static_cast<int32_t>(quotient(2 * static_cast<int64_t>(w.tiles) + run, 2 * run)));  // tiles / run, rounded
+  set_segments(w, run);
   return w;
 }
 
-__host__ __device__ __forceinline__ int64_t run_start(int64_t total, int p, int pairs) { return quotient(total * p, pairs); }
+__device__ __forceinline__ int64_t run_start(int64_t total, int p, int pairs) { return quotient(total * p, pairs); }
 
 __device__ __forceinline__ int32_t segment_start(const Work& w, int s) { return static_cast<int32_t>(quotient(static_cast<int64_t>(w.tiles) * s, w.segments)); }
 
@@ -159,6 +92,7 @@ struct Kernel {
   struct Part* parts_of;  // [pairs][kParts]
   float* parts;
   int32_t pairs;
+  int32_t even;  // the rows of q (draft and head) are q_head_stride apart throughout
 };
 
 // A cut piece: where its rows begin among all rows (draft and head), and how many there are; 0 where there is no piece.
@@ -176,13 +110,13 @@ struct Walk {
   int64_t left, run;
   int32_t request, segment, unit, first, n;  // the piece: its first tile in the request, its tiles
   bool cut;
-  // The run of `tiles` tiles from tile x of request r's.
-  __device__ __forceinline__ void start(const csa_draft_attend_args& A, int32_t r, int64_t x, int64_t tiles, int64_t run_tiles) {
+  // The run of `tiles` tiles from tile x of request r's, whose work is `of`.
+  __device__ __forceinline__ void start(const Work& of, int32_t r, int64_t x, int64_t tiles, int64_t run_tiles) {
     left = tiles;
     run = run_tiles;
     request = r;
-    int32_t ignore = 0;
-    w = work_of(A, request, run, &ignore);
+    w = of;
+    set_segments(w, run);
     const int32_t t = static_cast<int32_t>(quotient(x, w.units));
     segment = static_cast<int32_t>(quotient((static_cast<int64_t>(t) + 1) * w.segments - 1, w.tiles));
     const int32_t s0 = segment_start(w, segment), len = segment_start(w, segment + 1) - s0;
@@ -221,19 +155,20 @@ struct Walk {
   }
 };
 
-template <int kRope>
+template <bool kFp4, int kRope>
 struct Smem {
+  using W = Warps<kFp4>;
   static constexpr int kCols = (kDim + kRope) / 64;
   uint8_t q[kCols * kColBytes];
   uint8_t ring[kSlots][kSlotBytes];
   uint8_t rope[kRope ? kColBytes : 16];
   alignas(1024) uint8_t p[2 * kColBytes];  // 64 rows x 128 keys, two columns of 64 keys
   uint64_t bars[32];
-  float top[2][kRows], sum[2][kRows];  // of the two halves of a row's keys
-  uint32_t fills[2];                   // slots and rope columns that this CTA filled
-  int64_t scan[kThreads / 32];
+  float quarter[4][kRows];             // maxima, or sums, of the quarters of a row's keys
+  uint32_t fills[3];                   // by TMA: slots and rope columns that this CTA filled, and Q
+  int64_t scan[W::kThreads / 32];
   Walk walk;  // at the run's first piece
-  uint32_t theirs[3];                  // the other CTA's fills, and whether a wait of its ran out
+  uint32_t theirs[4];                  // the other CTA's fills, and whether a wait of its ran out
   uint32_t tmem;
   int abort;
 };
@@ -242,14 +177,17 @@ enum { kBarFull = 0, kBarEmpty = kSlots, kBarRopeFull = 2 * kSlots, kBarRopeEmpt
 static_assert(kBars <= 32, "barriers");
 
 // The run of this pair: the requests' tiles are summed by the block.
-template <int kRope>
-__device__ void make_plan(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
+template <bool kFp4, int kRope>
+__device__ void make_plan(const Kernel& K, Smem<kFp4, kRope>& S, int32_t* flags) {
+  constexpr int kThreads = Warps<kFp4>::kThreads;
   const csa_draft_attend_args& A = K.A;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, pair = blockIdx.x >> 1;
   const int per = (A.num_req + kThreads - 1) / kThreads, r0 = min(tid * per, A.num_req), r1 = min(r0 + per, A.num_req);
+  constexpr int64_t kNoSegments = INT64_MAX / 4;
   int64_t mine = 0;
+  Work w;
   for (int r = r0; r < r1; ++r) {
-    const Work w = work_of(A, r, 1, flags);
+    w = work_of(A, r, kNoSegments, flags);
     mine += static_cast<int64_t>(w.units) * w.tiles;
   }
   int64_t incl = mine;
@@ -270,10 +208,10 @@ __device__ void make_plan(const Kernel& K, Smem<kRope>& S, int32_t* flags) {
   if (at < end && at >= before && at < before + mine) {
     int32_t ignore = 0;
     for (int r = r0; r < r1; ++r) {
-      const Work w = work_of(A, r, 1, &ignore);
+      if (per > 1) w = work_of(A, r, kNoSegments, &ignore);
       const int64_t all = static_cast<int64_t>(w.units) * w.tiles;
       if (at < before + all) {
-        S.walk.start(A, r, at - before, end - at, max(quotient(total, K.pairs), int64_t(1)));
+        S.walk.start(w, r, at - before, end - at, max(quotient(total, K.pairs), int64_t(1)));
         break;
       }
       before += all;
@@ -314,6 +252,13 @@ __device__ __forceinline__ void tma_pair_4d(uint32_t dst, const void* map, int32
       : "memory");
 }
 
+__device__ __forceinline__ void tma_pair_2d(uint32_t dst, const void* map, int32_t x, int32_t y, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(map), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+
 // D[tmem] (+)= A[smem] B[smem]^T over the pair: 128 rows of A, 64 in each CTA, and N columns, half of B in each. A CTA's D
 // are its 64 rows: the first CTA's columns in lanes 0 .. 63, the second one's in lanes 64 .. 127.
 __device__ __forceinline__ void mma_pair(uint32_t lead, uint32_t d, csa::Desc a, csa::Desc b, uint32_t idesc, bool accumulate) {
@@ -340,6 +285,7 @@ __device__ __forceinline__ void st_peer_u32(uint32_t addr, uint32_t v) {
 
 struct Maps {  // [page][column of 64 values][record][value]: boxes of a page's two columns, and of one
   CUtensorMap two, one;
+  CUtensorMap q;  // [row (draft and head)][value], boxes of a column of 64 rows
 };
 
 // ------------------------------------------------------------- roles
@@ -349,7 +295,7 @@ struct Maps {  // [page][column of 64 values][record][value]: boxes of a page's 
 // The values of a page with drafts or with an end in it are looked at before they are handed over: rows past the end
 // become 0, and so do values of drafts that are not finite (0 x NaN is not 0; a row that sees the draft has the NaN of its score).
 template <int kRope>
-__device__ void role_load(const Kernel& K, const Maps& M, Smem<kRope>& S, uint32_t rank, int32_t* flags) {
+__device__ void role_load(const Kernel& K, const Maps& M, Smem<false, kRope>& S, uint32_t rank, int32_t* flags) {
   const csa_draft_attend_args& A = K.A;
   const int lane = threadIdx.x & 31;
   volatile int* stop = &S.abort;
@@ -383,6 +329,7 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<kRope>& S, uint32
           }
         }
       }
+#pragma unroll 1
       for (int d = 0; d < kDim / 128; ++d) {
         if (!free_slot(q)) return;
         if (lane == 0) {
@@ -466,37 +413,184 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<kRope>& S, uint32
   }
 }
 
-// Q of a piece: row i of this CTA's 64 is row first + 64 rank + i of all (draft and head); zeros past the unit's last.
-template <int kRope>
-__device__ void role_query(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
-  constexpr int kCols = Smem<kRope>::kCols;
+// Q of a run's piece-th piece: row i of this CTA's 64 is row 64 rank + i of the unit. Past the unit's last lie zeros, or rows that
+// nothing comes of. By TMA where all rows lie evenly, else by the threads of the warps that call it.
+template <bool kFp4, int kRope>
+__device__ bool load_query(const Kernel& K, const Maps& M, Smem<kFp4, kRope>& S, const Walk& W, uint32_t piece, uint32_t rank) {
+  constexpr int kCols = Smem<kFp4, kRope>::kCols;
   const csa_draft_attend_args& A = K.A;
-  const int t = threadIdx.x - 32 * kQueryWarp, lane = t & 31;
-  volatile int* stop = &S.abort;
-  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0);
-  uint32_t piece = 0;
-  for (Walk W = S.walk; W.more(); W.next(A), ++piece) {
-    const int64_t first = static_cast<int64_t>(W.unit) * 2 * kRows + kRows * rank, draft = quotient(first, A.num_heads);  // of the request's rows
-    const int head = static_cast<int>(first - draft * A.num_heads), rows = W.rows(A) - kRows * static_cast<int>(rank);
-    if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, stop)) return;
-#pragma unroll 2
-    for (int i = t >> 3; i < kRows; i += 4 * kQueryWarps) {
-      const uint32_t x = head + i, j = x / static_cast<uint32_t>(A.num_heads), h = x - j * A.num_heads;
-      const uint8_t* q = static_cast<const uint8_t*>(A.q) + 16 * (t & 7);
-      if (i < rows) q += 2 * ((W.w.R.row0 + draft + j) * A.q_row_stride + h * A.q_head_stride);
-#pragma unroll
-      for (int c = 0; c < kCols; ++c) csa::cp_async16(smem_u32(S.q) + c * kColBytes + i * 128 + (((t & 7) ^ (i & 7)) << 4), i < rows ? q + 128 * c : A.q, i < rows);
+  const int t = threadIdx.x - 32 * Warps<kFp4>::kQuery, lane = t & 31;
+  const uint32_t bars = smem_u32(S.bars), full = csa::peer_smem(bars, 0) + 8 * kBarQFull;
+  if (K.even && t >= 32) return true;
+  if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, &S.abort)) return false;
+  if (K.even) {
+    if (t == 0) {
+      arrive_expect_at(full, sizeof(S.q));
+#pragma unroll 1
+      for (int c = 0; c < kCols; ++c)
+        tma_pair_2d(smem_u32(S.q) + c * kColBytes, &M.q, 64 * c, static_cast<int32_t>(W.first_row(A)) + kRows * static_cast<int32_t>(rank), full);
+      S.fills[2] = piece + 1;
     }
-    csa::cp_async_wait_all();
+    __syncwarp();
+    return true;
+  }
+  const int64_t first = static_cast<int64_t>(W.unit) * 2 * kRows + kRows * rank, draft = quotient(first, A.num_heads);  // of the request's rows
+  const int head = static_cast<int>(first - draft * A.num_heads), rows = W.rows(A) - kRows * static_cast<int>(rank);
+#pragma unroll 2
+  for (int i = t >> 3; i < kRows; i += 4 * Warps<kFp4>::kQueries) {
+    const uint32_t x = head + i, j = x / static_cast<uint32_t>(A.num_heads), h = x - j * A.num_heads;
+    const uint8_t* q = static_cast<const uint8_t*>(A.q) + 16 * (t & 7);
+    if (i < rows) q += 2 * ((W.w.R.row0 + draft + j) * A.q_row_stride + h * A.q_head_stride);
+#pragma unroll
+    for (int c = 0; c < kCols; ++c) csa::cp_async16(smem_u32(S.q) + c * kColBytes + i * 128 + (((t & 7) ^ (i & 7)) << 4), i < rows ? q + 128 * c : A.q, i < rows);
+  }
+  csa::cp_async_wait_all();
+  csa::fence_proxy_async_smem();
+  __syncwarp();
+  if (lane == 0) arrive_at(full);
+  return true;
+}
+
+// The queries of bf16 records' kernels, whose records come by another warp.
+template <int kRope>
+__device__ void role_query(const Kernel& K, const Maps& M, Smem<false, kRope>& S, uint32_t rank) {
+  uint32_t piece = 0;
+  for (Walk W = S.walk; W.more(); W.next(K.A), ++piece)
+    if (!load_query<false, kRope>(K, M, S, W, piece, rank)) return;
+}
+
+// 4-bit records: eight warps, four lanes a record. A slot is 128 values of 64 records, four blocks of 32 each: a block a thread
+// (16 code bytes and a scale byte become 64 bytes of bf16, exactly). What comes next is in registers already: the next tile's keys while
+// this one's values are stored, and the other way round. The order of the slots, and what becomes of rows past the end and of
+// drafts' values that are not finite, is as in role_load; the values of the CTA's own page are read and converted a second time,
+// because there is no room to keep them.
+template <int kRope>
+__device__ void role_load_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>& S, uint32_t rank, int32_t* flags) {
+  const csa_draft_attend_args& A = K.A;
+  const int t = threadIdx.x - 32 * Warps<true>::kQuery, lane = t & 31, r = t >> 2, s = t & 3;  // this thread's record and block
+  constexpr int kRec = record_bytes(true, kRope);
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0), ring = smem_u32(S.ring[0]);
+  const bool swap = s >= 2;  // lanes 2, 3 of a record store their words in another order: no two on one bank
+  csa::test_delay();
+  uint32_t q = 0, ropes = 0, piece = 0;
+  bool ok = true;
+  struct Codes {
+    uint4 code[4];
+    uint32_t scale[4];
+  };
+  auto convert_and_store = [&](uint4 c, uint32_t sb) {  // to slot q
+    const uint32_t bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7), two = bits | (bits << 16);
+    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
+    const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+    uint32_t v[16];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      mxfp4_four(word[j], s2, &v[4 * j], &v[4 * j + 1]);
+      mxfp4_four(word[j] >> 16, s2, &v[4 * j + 2], &v[4 * j + 3]);
+    }
+    ok = ok && warp_wait(bars + 8 * (kBarEmpty + q % kSlots), (q / kSlots & 1) ^ 1, stop);
+    if (!ok) return;
+    const uint32_t row = ring + q % kSlots * kSlotBytes + (s >> 1) * kColBytes + r * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int chunk = 4 * (s & 1) + (swap ? j ^ 2 : j);
+      csa::st_shared_v4(row + ((chunk ^ (r & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+    }
     csa::fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) arrive_at(lead_bars + 8 * kBarQFull);
+    if (lane == 0) arrive_at(lead_bars + 8 * (kBarFull + q % kSlots));
+    ++q;
+  };
+  for (Walk W = S.walk; ok && W.more(); W.next(A), ++piece) {
+    const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
+    const Request& R = W.w.R;
+    const int32_t past = W.first + W.n;  // of the piece's tiles
+    auto page_of = [&](int32_t tile, int half) { return tile < past && (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : -1; };
+    // this thread's record of a page of the tile, or null
+    auto record = [&](int32_t tile, int half, int32_t page) -> const uint8_t* {
+      const int32_t p0 = (2 * tile + half) * kPageRecs;
+      if (tile >= past || p0 >= R.total) return nullptr;
+      if (page < 0 || page >= A.cache.num_pages) {
+        *flags |= CSA_DEV_PAGE_OOB;
+        return nullptr;
+      }
+      return p0 + r < R.total ? A.cache.pages + page * A.cache.page_stride_bytes + static_cast<int64_t>(r) * kRec : nullptr;
+    };
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    Codes kc, vc;
+    uint4 rope[2];
+    auto fetch_keys = [&](int32_t tile, int32_t page) {
+      const uint8_t* rec = record(tile, static_cast<int>(rank), page);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        kc.code[c] = rec ? __ldg(reinterpret_cast<const uint4*>(rec) + 4 * c + s) : zero;
+        kc.scale[c] = rec ? __ldg(rec + kCodeBytes + 4 * c + s) : 0u;
+      }
+      if (kRope != 0)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) rope[k] = rec ? __ldg(reinterpret_cast<const uint4*>(rec + kCodeBytes + kScaleBytes) + 2 * s + k) : zero;
+    };
+    auto fetch_values = [&](int32_t tile, const int32_t (&page)[2]) {
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const uint8_t* rec = record(tile, c >> 1, page[c >> 1]);
+        const int block = 8 * static_cast<int>(rank) + 4 * (c & 1) + s;
+        vc.code[c] = rec ? __ldg(reinterpret_cast<const uint4*>(rec) + block) : zero;
+        vc.scale[c] = rec ? __ldg(rec + kCodeBytes + block) : 0u;
+        if (vc.scale[c] == 255 && (2 * tile + (c >> 1)) * kPageRecs + r >= R.base) vc.code[c] = zero, vc.scale[c] = 0;
+      }
+    };
+    auto keys = [&] {
+      if (kRope != 0) {
+        ok = ok && warp_wait(bars + 8 * kBarRopeEmpty, (ropes & 1) ^ 1, stop);
+        if (!ok) return;
+        ++ropes;
+        const uint32_t row = smem_u32(S.rope) + r * 128;
+#pragma unroll
+        for (int k = 0; k < 2; ++k) csa::st_shared_v4(row + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y, rope[k].z, rope[k].w);
+        csa::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) arrive_at(lead_bars + 8 * kBarRopeFull);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (ok) convert_and_store(kc.code[c], kc.scale[c]);
+    };
+    // pages of the tile whose values are next, of the one after it, and of the one after that
+    int32_t now[2], next[2], then[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      now[h] = page_of(W.first, h);
+      next[h] = page_of(W.first + 1, h);
+      then[h] = page_of(W.first + 2, h);
+    }
+    fetch_keys(W.first, rank ? now[1] : now[0]);
+    if (!load_query<true, kRope>(K, M, S, W, piece, rank)) ok = false;
+    fetch_values(W.first, now);
+    if (ok) keys();
+    fetch_keys(W.first + 1, rank ? next[1] : next[0]);
+    for (int32_t tile = W.first; ok && tile < past; ++tile) {
+      if (tile + 1 < past) {
+        keys();
+        fetch_keys(tile + 2, rank ? then[1] : then[0]);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (ok) convert_and_store(vc.code[c], vc.scale[c]);
+      fetch_values(tile + 1, next);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        next[h] = then[h];
+        then[h] = page_of(tile + 3, h);
+      }
+    }
   }
 }
 
 // One warp of the first CTA issues the pair's MMAs: S(0), then S(i + 1) and O(i) in turn.
-template <int kRope>
-__device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
+template <bool kFp4, int kRope>
+__device__ void role_mma(const Kernel& K, Smem<kFp4, kRope>& S) {
   const csa_draft_attend_args& A = K.A;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), tmem = csa::uniform(S.tmem), lead = csa::elect_lane();
@@ -521,39 +615,36 @@ __device__ void role_mma(const Kernel& K, Smem<kRope>& S) {
       for (int x = 0; x < 4; ++x) mma_pair(lead, d, q_desc.at(kDim / 64 * kColBytes + 32 * x), k_rope.at(32 * x), idesc_s, x > 0);
       commit_pair(lead, bars + 8 * kBarRopeEmpty);
     }
+    const uint32_t at_slot = q % kSlots, parity = q / kSlots & 1;  // four slots at a time: 0 .. 3 or 4 .. 7
+    const csa::Desc k = k_ring.at(at_slot * kSlotBytes);
 #pragma unroll
     for (int c = 0; c < kDim / 128; ++c) {
-      const uint32_t slot = q % kSlots;
-      if (!need(kBarFull + slot, q / kSlots & 1)) return;
-      const csa::Desc k = k_ring.at(slot * kSlotBytes);
+      if (!need(kBarFull + at_slot + c, parity)) return;
 #pragma unroll
       for (int x = 0; x < 8; ++x) {
-        const uint32_t at = x / 4 * kColBytes + x % 4 * 32;
-        mma_pair(lead, d, q_desc.at(c * kSlotBytes + at), k.at(at), idesc_s, kRope != 0 || c > 0 || x > 0);
+        const uint32_t at = c * kSlotBytes + x / 4 * kColBytes + x % 4 * 32;
+        mma_pair(lead, d, q_desc.at(at), k.at(at), idesc_s, kRope != 0 || c > 0 || x > 0);
       }
-      commit_pair(lead, bars + 8 * (kBarEmpty + slot));
-      ++q;
+      commit_pair(lead, bars + 8 * (kBarEmpty + at_slot + c));
     }
+    q += kDim / 128;
     commit_pair(lead, bars + 8 * (kBarSFull + (g & 1)));
     if (last) commit_pair(lead, bars + 8 * kBarQEmpty);
     ++g;
   };
   auto outputs = [&](bool begin) {
     if (!need(kBarPFull, done & 1)) return;
+    const uint32_t at_slot = q % kSlots, parity = q / kSlots & 1;
+    const csa::Desc v = v_ring.at(at_slot * kSlotBytes);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int c = 0; c < 4; ++c) {  // page c / 2, columns 128 (c % 2) .. of the CTAs' values
+      if (!need(kBarFull + at_slot + c, parity)) return;
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const uint32_t slot = q % kSlots;
-        if (!need(kBarFull + slot, q / kSlots & 1)) return;
-        const csa::Desc v = v_ring.at(slot * kSlotBytes);
-#pragma unroll
-        for (int x = 0; x < 4; ++x)
-          mma_pair(lead, tmem + 128 * b, p_desc.at(half * kColBytes + 32 * x), v.at(2048 * x), idesc_o, !begin || half > 0 || x > 0);
-        commit_pair(lead, bars + 8 * (kBarEmpty + slot));
-        ++q;
-      }
+      for (int x = 0; x < 4; ++x)
+        mma_pair(lead, tmem + 128 * (c & 1), p_desc.at(c / 2 * kColBytes + 32 * x), v.at(c * kSlotBytes + 2048 * x), idesc_o, !begin || c > 1 || x > 0);
+      commit_pair(lead, bars + 8 * (kBarEmpty + at_slot + c));
     }
+    q += 4;
     commit_pair(lead, bars + 8 * kBarODone);
     ++done;
   };
@@ -589,16 +680,18 @@ __device__ __forceinline__ uint64_t seen_bits(const csa_draft_attend_args& A, co
   return there & (history | drafts);
 }
 
-// A thread has a row and half of its tile's keys: warps 0, 1 the first page's (rows 0 .. 31, 32 .. 63), 2, 3 the second's.
-// For the output it has the row's values 0 .. 255 or 256 .. 511, its lane of TMEM. m is the row's reference, any: it
-// moves only when a tile exceeds it by 2^8, so that O is rarely scaled.
-template <int kRope>
-__device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
+// A thread has a row and a quarter of its tile's keys: warps 0, 1 half of the first page's (rows 0 .. 31, 32 .. 63), 2, 3 half of
+// the second's, 4 .. 7 the other halves. For the output it has 128 of the row's values, half of its lane of TMEM. m is the
+// row's reference, any: it moves only when a tile exceeds it by 2^8, so that O is rarely scaled.
+template <bool kFp4, int kRope>
+__device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t rank) {
   const csa_draft_attend_args& A = K.A;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, row = tid & (kRows - 1), half = tid >> 6, pair_bar = kBarRows + (warp & 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, row = threadIdx.x & (kRows - 1);
+  const int half = (warp >> 1) & 1, part = warp >> 2, mine = 2 * part + half, row_bar = kBarRows + (warp & 1);
+  constexpr int kRowThreads = 32 * kSoftmaxWarps / 2, kKeys = kTile / 4, kValues = kDim / 4;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0);
-  const uint32_t tmem = S.tmem + (static_cast<uint32_t>(32 * warp) << 16);
+  const uint32_t tmem = S.tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16), o_tmem = tmem + kValues * part;
   const float c = A.scale * 1.4426950408889634f;
   const float grow = fminf(kGrow / c, FLT_MAX);
   const uint32_t p_row = smem_u32(S.p) + half * kColBytes + row * 128;
@@ -614,41 +707,38 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
     const int32_t j = there ? static_cast<int32_t>(quotient(flat, A.num_heads)) - R.row0 : 0;
     auto page_at = [&](int32_t tile) { return (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : 0; };
     int32_t page = page_at(W.first);
-    float m = -INFINITY, l = 0.f;  // l: of this thread's half of the keys
+    float m = -INFINITY, l = 0.f;  // l: of this thread's quarter of the keys
     for (int i = 0; i < W.n; ++i, ++g) {
       const int32_t p0 = (2 * (W.first + i) + half) * kPageRecs;
       const bool good = page >= 0 && page < A.cache.num_pages;
       if (i + 1 < W.n) page = page_at(W.first + i + 1);
       ok = ok && warp_wait(bars + 8 * (kBarSFull + (g & 1)), g >> 1 & 1, stop);
       csa::tc_fence_after();
-      float s[64];
+      float s[kKeys];
       {
-        uint32_t raw[32];
+        uint32_t raw[kKeys];
+        csa::tmem_ld32(tmem + kTmemS + (g & 1) * (kTile / 2) + kKeys * part, raw);
+        csa::tmem_wait_ld();
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          csa::tmem_ld32(tmem + kTmemS + (g & 1) * (kTile / 2) + 32 * k, raw);
-          csa::tmem_wait_ld();
-#pragma unroll
-          for (int x = 0; x < 32; ++x) s[32 * k + x] = __uint_as_float(raw[x]);
-        }
+        for (int x = 0; x < kKeys; ++x) s[x] = __uint_as_float(raw[x]);
       }
       csa::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(lead_bars + 8 * (kBarSEmpty + (g & 1)));
       if (!(good && p0 + kPageRecs <= R.base && there)) {
-        const uint64_t seen = good && there ? seen_bits(A, R, j, p0) : 0;
+        const uint32_t seen = good && there ? static_cast<uint32_t>(seen_bits(A, R, j, p0) >> (kKeys * part)) : 0;
 #pragma unroll
-        for (int x = 0; x < 64; ++x)
+        for (int x = 0; x < kKeys; ++x)
           if (!(seen >> x & 1)) s[x] = -INFINITY;
       }
       float top = s[0];
 #pragma unroll
-      for (int x = 1; x < 64; ++x) top = fmaxf(top, s[x]);
-      if (csa::named_bar_any(pair_bar, 2 * 32, top > m + grow)) {  // also when there was nothing (-infinity), not where there is still nothing
-        S.top[half][row] = top;
-        csa::named_bar_sync(pair_bar, 2 * 32);
-        top = fmaxf(top, S.top[half ^ 1][row]);
-        csa::named_bar_sync(pair_bar, 2 * 32);
+      for (int x = 1; x < kKeys; ++x) top = fmaxf(top, s[x]);
+      if (csa::named_bar_any(row_bar, kRowThreads, top > m + grow)) {  // also when there was nothing (-infinity), not where there is still nothing
+        S.quarter[mine][row] = top;
+        csa::named_bar_sync(row_bar, kRowThreads);
+        top = fmaxf(fmaxf(S.quarter[0][row], S.quarter[1][row]), fmaxf(S.quarter[2][row], S.quarter[3][row]));
+        csa::named_bar_sync(row_bar, kRowThreads);
         float keep = 1.f;
         if (top > m + grow) {
           keep = csa::ex2((m - top) * c);  // 0 when there was nothing
@@ -659,13 +749,13 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
           ok = ok && o_done(g);
           csa::tc_fence_after();
 #pragma unroll 1
-          for (int at = 0; at < 256; at += 32) {
+          for (int at = 0; at < kValues; at += 32) {
             uint32_t v[32];
-            csa::tmem_ld32(tmem + at, v);
+            csa::tmem_ld32(o_tmem + at, v);
             csa::tmem_wait_ld();
 #pragma unroll
             for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
-            csa::tmem_st32(tmem + at, v);
+            csa::tmem_st32(o_tmem + at, v);
           }
           csa::tmem_wait_st();
           csa::tc_fence_before();
@@ -673,10 +763,10 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
       }
       // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
       const float mc = m == -INFINITY ? 0.f : m * c;
-      uint32_t w[32];
+      uint32_t w[kKeys / 2];
       float sum[2] = {0.f, 0.f};
 #pragma unroll
-      for (int x = 0; x < 32; ++x) {
+      for (int x = 0; x < kKeys / 2; ++x) {
         const float a = csa::ex2(fmaf(s[2 * x], c, -mc)), b = csa::ex2(fmaf(s[2 * x + 1], c, -mc));
         sum[x & 1] += a + b;
         w[x] = pack_bf16(a, b);
@@ -684,73 +774,71 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
       l += sum[0] + sum[1];
       ok = ok && o_done(g);  // the tile before has been read
 #pragma unroll
-      for (int x = 0; x < 8; ++x) csa::st_shared_v4(p_row + ((x ^ (row & 7)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
+      for (int x = 0; x < 4; ++x)
+        csa::st_shared_v4(p_row + (((4 * part + x) ^ (row & 7)) << 4), w[4 * x], w[4 * x + 1], w[4 * x + 2], w[4 * x + 3]);
       csa::fence_proxy_async_smem();
       csa::tc_fence_before();
       __syncwarp();
       if (lane == 0) arrive_at(lead_bars + 8 * kBarPFull);
     }
     // the piece's output
-    S.sum[half][row] = l;
-    csa::named_bar_sync(pair_bar, 2 * 32);
-    l = half == 0 ? l + S.sum[1][row] : S.sum[0][row] + l;  // the same for both halves
-    csa::named_bar_sync(pair_bar, 2 * 32);
+    S.quarter[mine][row] = l;
+    csa::named_bar_sync(row_bar, kRowThreads);
+    l = (S.quarter[0][row] + S.quarter[1][row]) + (S.quarter[2][row] + S.quarter[3][row]);
+    csa::named_bar_sync(row_bar, kRowThreads);
     ok = ok && o_done(g);
     csa::tc_fence_after();
     const float mc = m == -INFINITY ? -INFINITY : m * c;
-    // 128 bytes of each of the warp's 32 rows at a time go through its 4 KB of P (which is not in use between a piece's last
-    // O and the next one's first P) and out as whole lines: stores of 32 bytes a row took 7.8 k clocks a piece.
+    // 64 bytes of each of the warp's 32 rows at a time go through its 2 KB of P (which is not in use between a piece's last
+    // O and the next one's first P) and out in runs of them.
     const int rows_here = W.rows(A) - kRows * static_cast<int>(rank) - 32 * (warp & 1);  // of the warp's, that there are
-    const uint32_t stage = smem_u32(S.p) + 4096 * warp, r0 = lane >> 3, chunk = lane & 7;
-    auto lines_in = [&](const uint32_t (&v)[32]) {
+    const uint32_t stage = smem_u32(S.p) + 2048 * warp, r0 = lane >> 2, chunk = lane & 3;
+    auto lines_in = [&](const uint32_t (&v)[16]) {
       __syncwarp();
 #pragma unroll
-      for (int x = 0; x < 8; ++x) csa::st_shared_v4(p_row + ((x ^ (row & 7)) << 4), v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
+      for (int x = 0; x < 4; ++x) csa::st_shared_v4(stage + lane * 64 + ((x ^ ((lane >> 1) & 3)) << 4), v[4 * x], v[4 * x + 1], v[4 * x + 2], v[4 * x + 3]);
       __syncwarp();
     };
     auto lines_out = [&](uint8_t* to, int64_t row_bytes) {  // `to`: the warp's first row
-      uint4 y[8];
+      uint4 y[4];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) y[x] = csa::ld_shared_v4(stage + (r0 + 4 * x) * 128 + ((chunk ^ ((r0 + 4 * x) & 7)) << 4));
+      for (int x = 0; x < 4; ++x) y[x] = csa::ld_shared_v4(stage + (r0 + 8 * x) * 64 + ((chunk ^ (((r0 + 8 * x) >> 1) & 3)) << 4));
 #pragma unroll
-      for (int x = 0; x < 8; ++x)
-        if (static_cast<int>(r0) + 4 * x < rows_here) *reinterpret_cast<uint4*>(to + (r0 + 4 * x) * row_bytes + 16 * chunk) = y[x];
+      for (int x = 0; x < 4; ++x)
+        if (static_cast<int>(r0) + 8 * x < rows_here) *reinterpret_cast<uint4*>(to + (r0 + 8 * x) * row_bytes + 16 * chunk) = y[x];
     };
+    const int first_value = 256 * half + kValues * part;
     if (!W.cut) {
       const float inv = l > 0.f ? 1.f / l : l;  // 0 for an empty row; a NaN stays one
-      if (there && half == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
-      uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * ((W.first_row(A) + kRows * rank + 32 * (warp & 1)) * kDim + 256 * half);
-      uint32_t v[2][32];
-      csa::tmem_ld32(tmem, v[0]);
-      csa::tmem_ld32(tmem + 32, v[1]);
+      if (there && mine == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
+      uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * ((W.first_row(A) + kRows * rank + 32 * (warp & 1)) * kDim + first_value);
+      uint32_t v[32];
+      csa::tmem_ld32(o_tmem, v);
 #pragma unroll 1
-      for (int at = 0; at < 256; at += 64) {
-        uint32_t y[32];
+      for (int at = 0; at < kValues; at += 32) {
+        uint32_t y[16];
         csa::tmem_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) y[x] = pack_bf16(__uint_as_float(v[x >> 4][2 * (x & 15)]) * inv, __uint_as_float(v[x >> 4][2 * (x & 15) + 1]) * inv);
+        for (int x = 0; x < 16; ++x) y[x] = pack_bf16(__uint_as_float(v[2 * x]) * inv, __uint_as_float(v[2 * x + 1]) * inv);
         lines_in(y);
-        if (at + 64 < 256) {  // the next ones, while these go out
-          csa::tmem_ld32(tmem + at + 64, v[0]);
-          csa::tmem_ld32(tmem + at + 96, v[1]);
-        }
+        if (at + 32 < kValues) csa::tmem_ld32(o_tmem + at + 32, v);  // the next ones, while these go out
         lines_out(out + 2 * at, 2 * kDim);
       }
     } else {
-      float* part = K.parts + (static_cast<size_t>(blockIdx.x >> 1) * kParts + ordinal) * kPartFloats;
+      float* part_out = K.parts + (static_cast<size_t>(blockIdx.x >> 1) * kParts + ordinal) * kPartFloats;
       const int at_row = kRows * rank + row;
-      if (half == 0) {
-        part[2 * kRows * kDim + at_row] = mc;
-        part[2 * kRows * (kDim + 1) + at_row] = l;
+      if (mine == 0) {
+        part_out[2 * kRows * kDim + at_row] = mc;
+        part_out[2 * kRows * (kDim + 1) + at_row] = l;
       }
-      uint8_t* to = reinterpret_cast<uint8_t*>(part + static_cast<size_t>(kRows * rank + 32 * (warp & 1)) * kDim + 256 * half);
-      uint32_t v[32];
-      csa::tmem_ld32(tmem, v);
+      uint8_t* to = reinterpret_cast<uint8_t*>(part_out + static_cast<size_t>(kRows * rank + 32 * (warp & 1)) * kDim + first_value);
+      uint32_t v[16];
+      csa::tmem_ld16(o_tmem, v);
 #pragma unroll 1
-      for (int at = 0; at < 256; at += 32) {
+      for (int at = 0; at < kValues; at += 16) {
         csa::tmem_wait_ld();
         lines_in(v);
-        if (at + 32 < 256) csa::tmem_ld32(tmem + at + 32, v);
+        if (at + 16 < kValues) csa::tmem_ld16(o_tmem + at + 16, v);
         lines_out(to + 4 * at, 4 * kDim);
       }
       ++ordinal;
@@ -761,26 +849,27 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S, uint32_t rank) {
   }
 }
 
-template <int kRope>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Kernel K, const __grid_constant__ Maps M) {
+template <bool kFp4, int kRope>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kFp4>::kThreads, 1) attend_kernel(const __grid_constant__ Kernel K, const __grid_constant__ Maps M) {
   extern __shared__ uint8_t smem_raw[];
-  Smem<kRope>& S = *reinterpret_cast<Smem<kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Smem<kFp4, kRope>& S = *reinterpret_cast<Smem<kFp4, kRope>*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1, bars = smem_u32(S.bars);
   if (threadIdx.x < kBars) {  // a barrier's arrivals
     const int k = threadIdx.x;
     int n = 1;
-    if (k < kBarEmpty || k == kBarRopeFull) n = 2;  // a loader of each CTA
+    if (k < kBarEmpty || k == kBarRopeFull) n = 2 * Warps<kFp4>::kFills;
     else if (k == kBarSEmpty || k == kBarSEmpty + 1 || k == kBarPFull || k == kBarOEmpty) n = 2 * kSoftmaxWarps;
-    else if (k == kBarQFull) n = 2 * kQueryWarps;
+    else if (k == kBarQFull) n = 2 * (K.even ? 1 : Warps<kFp4>::kQueries);
     csa::mbar_init(bars + 8 * k, n);
     csa::mbar_init_fence();
   }
   if (threadIdx.x == 0) S.abort = 0;
-  if (threadIdx.x < 2) S.fills[threadIdx.x] = 0;
+  if (threadIdx.x < 3) S.fills[threadIdx.x] = 0;
   if (threadIdx.x == 32 * kLoadWarp) {
-    csa::prefetch_tensormap(&M.two);
-    if (kRope != 0) csa::prefetch_tensormap(&M.one);
+    if (!kFp4) csa::prefetch_tensormap(&M.two);
+    if (!kFp4 && kRope != 0) csa::prefetch_tensormap(&M.one);
+    if (K.even) csa::prefetch_tensormap(&M.q);
   }
   if (warp == kMmaWarp) {
     asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&S.tmem)), "r"(kTmemCols) : "memory");
@@ -788,36 +877,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_
   }
   int32_t flags = 0;
   csa::tc_fence_before();
-  make_plan(K, S, &flags);  // ends with a block barrier
   csa::cluster_arrive();
+  make_plan(K, S, &flags);  // ends with a block barrier
   csa::cluster_wait();  // the other CTA's barriers are there
   csa::tc_fence_after();
   if (warp < kSoftmaxWarps) {
-    role_softmax(K, S, rank);
-  } else if (warp == kLoadWarp) {
-    role_load(K, M, S, rank, &flags);
+    role_softmax<kFp4, kRope>(K, S, rank);
   } else if (warp == kMmaWarp) {
-    if (rank == 0) role_mma(K, S);
-  } else {
-    if (rank == 0 && warp == kQueryWarp && lane == 0) {  // what this run leaves for the join
-      Part* parts = K.parts_of + (blockIdx.x >> 1) * kParts;
-      int k = 0;
-      for (Walk W = S.walk; W.more(); W.next(K.A))
-        if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), 0};
-      while (k < kParts) parts[k++] = {0, 0, 0};
+    if (rank == 0) {
+      role_mma<kFp4, kRope>(K, S);
+    } else {  // what this run leaves for the join
+      if (lane == 0) {
+        Part* parts = K.parts_of + (blockIdx.x >> 1) * kParts;
+        int k = 0;
+        for (Walk W = S.walk; W.more(); W.next(K.A))
+          if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), 0};
+        while (k < kParts) parts[k++] = {0, 0, 0};
+      }
+      __syncwarp();
     }
-    __syncwarp();
-    role_query(K, S, rank);
+  } else {
+    if constexpr (kFp4) role_load_fp4<kRope>(K, M, S, rank, &flags);
+    else if (warp == kLoadWarp) role_load<kRope>(K, M, S, rank, &flags);
+    else role_query<kRope>(K, M, S, rank);
   }
   if (warp == kMmaWarp && rank == 1) csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);  // the last commit has told this CTA too
   csa::tc_fence_before();
   __syncthreads();
-  if (threadIdx.x < 3) st_peer_u32(csa::peer_smem(smem_u32(&S.theirs[threadIdx.x]), rank ^ 1), threadIdx.x < 2 ? S.fills[threadIdx.x] : static_cast<uint32_t>(S.abort));
+  if (threadIdx.x < 4) st_peer_u32(csa::peer_smem(smem_u32(&S.theirs[threadIdx.x]), rank ^ 1), threadIdx.x < 3 ? S.fills[threadIdx.x] : static_cast<uint32_t>(S.abort));
   csa::cluster_arrive();
   csa::cluster_wait();
   // A wait that ran out may have left copies in flight, to be waited for before either CTA leaves. A slot's full barrier wants both
   // CTAs' arrival: the first CTA arrives for the one that did not fill the slot.
-  if (S.abort || S.theirs[2]) {
+  if (S.abort || S.theirs[3]) {
     if (rank == 0 && threadIdx.x == 0) {
       auto drain = [&](int bar, uint32_t a, uint32_t b) {  // filled a and b times
         for (uint32_t k = min(a, b); k < max(a, b); ++k) csa::mbar_arrive(bars + 8 * bar);
@@ -825,6 +917,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) attend_
       };
       for (uint32_t k = 0; k < kSlots; ++k) drain(kBarFull + k, (S.fills[0] + kSlots - 1 - k) / kSlots, (S.theirs[0] + kSlots - 1 - k) / kSlots);
       drain(kBarRopeFull, S.fills[1], S.theirs[1]);
+      drain(kBarQFull, S.fills[2], S.theirs[2]);
     }
     __syncwarp();
     csa::cluster_arrive();
@@ -931,23 +1024,29 @@ int pairs_cap(const csa_draft_attend_args* a) {
 
 constexpr size_t kPartsOfBytes = (kMaxPairs * kParts * sizeof(Part) + 255) / 256 * 256;
 
-template <int kRope>
-csa_status launch_bf16(const Kernel& K, int dev, cudaStream_t stream) {
+template <bool kFp4, int kRope>
+csa_status launch(Kernel& K, int dev, cudaStream_t stream) {
   static Kept ready;  // the kernel's shared memory size is set on each device once
-  constexpr size_t smem = sizeof(Smem<kRope>) + 1024;
+  constexpr size_t smem = sizeof(Smem<kFp4, kRope>) + 1024;
   static_assert(smem <= 232448, "shared memory of one CTA");
-  const csa_latent_cache& cache = K.A.cache;
+  const csa_draft_attend_args& a = K.A;
   constexpr int64_t kRec = record_bytes(false, kRope);
   Maps M;
-  const cuuint64_t dims[4] = {64, kPageRecs, static_cast<cuuint64_t>(kRec / 128), static_cast<cuuint64_t>(cache.num_pages)};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kRec), 128, static_cast<cuuint64_t>(cache.page_stride_bytes)};
-  const cuuint32_t two[4] = {64, kPageRecs, 2, 1}, one[4] = {64, kPageRecs, 1, 1};
-  if (!encode_map(&M.two, cache.pages, 4, dims, strides, two) || !encode_map(&M.one, cache.pages, 4, dims, strides, one)) return CSA_ERR_INVALID_ARG;
+  if (!kFp4) {
+    const cuuint64_t dims[4] = {64, kPageRecs, static_cast<cuuint64_t>(kRec / 128), static_cast<cuuint64_t>(a.cache.num_pages)};
+    const cuuint64_t strides[3] = {static_cast<cuuint64_t>(kRec), 128, static_cast<cuuint64_t>(a.cache.page_stride_bytes)};
+    const cuuint32_t two[4] = {64, kPageRecs, 2, 1}, one[4] = {64, kPageRecs, 1, 1};
+    if (!encode_map(&M.two, a.cache.pages, 4, dims, strides, two) || !encode_map(&M.one, a.cache.pages, 4, dims, strides, one)) return CSA_ERR_INVALID_ARG;
+  }
+  const int64_t rows = static_cast<int64_t>(a.num_q) * a.num_heads, step = a.num_heads > 1 ? a.q_head_stride : a.q_row_stride;
+  K.even = rows <= INT32_MAX && (a.num_q == 1 || a.num_heads == 1 || a.q_row_stride == a.num_heads * a.q_head_stride) &&
+           encode_bf16(&M.q, a.q, kDim + kRope, 0, rows, 0, rows > 1 ? step : kDim + kRope, 0, kRows);
   if (!ready.get(dev)) {
-    if (cudaFuncSetAttribute(attend_kernel<kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess) return CSA_ERR_CUDA;
+    if (cudaFuncSetAttribute(attend_kernel<kFp4, kRope>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+      return CSA_ERR_CUDA;
     ready.set(dev, 1);
   }
-  attend_kernel<kRope><<<2 * K.pairs, kThreads, smem, stream>>>(K, M);
+  attend_kernel<kFp4, kRope><<<2 * K.pairs, Warps<kFp4>::kThreads, smem, stream>>>(K, M);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
@@ -986,11 +1085,6 @@ extern "C" csa_status csa_draft_attend(const csa_draft_attend_args* a, void* ws,
   if (!ws || ws_bytes < csa_draft_attend_workspace_bytes(a)) return CSA_ERR_WORKSPACE;
   if (!aligned(ws, 32)) return CSA_ERR_ALIGNMENT;
   const auto s = static_cast<cudaStream_t>(stream);
-  if (a->cache.record_format == CSA_LATENT_MXFP4) {
-    if (static_cast<int64_t>(a->num_q) * a->num_heads > INT32_MAX) return CSA_ERR_INVALID_ARG;
-    attend_simple<<<static_cast<unsigned>(a->num_q * a->num_heads), 128, 0, s>>>(*a);
-    return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
-  }
   int sms = 0, dev = 0;
   if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
   Kernel K;
@@ -998,7 +1092,8 @@ extern "C" csa_status csa_draft_attend(const csa_draft_attend_args* a, void* ws,
   K.pairs = pairs_cap(a) < sms / 2 ? pairs_cap(a) : sms / 2;
   K.parts_of = static_cast<Part*>(ws);
   K.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kPartsOfBytes);
-  const csa_status ls = a->cache.rope_dim ? launch_bf16<64>(K, dev, s) : launch_bf16<0>(K, dev, s);
+  const bool fp4 = a->cache.record_format == CSA_LATENT_MXFP4, rope = a->cache.rope_dim != 0;
+  const csa_status ls = fp4 ? (rope ? launch<true, 64>(K, dev, s) : launch<true, 0>(K, dev, s)) : (rope ? launch<false, 64>(K, dev, s) : launch<false, 0>(K, dev, s));
   if (ls != CSA_OK || K.pairs == 1) return ls;
   cudaLaunchConfig_t cfg = {};
   const int64_t rows = static_cast<int64_t>(a->num_q) * a->num_heads;

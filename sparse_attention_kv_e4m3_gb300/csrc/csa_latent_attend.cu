@@ -314,23 +314,6 @@ struct TileRegs<true, kRope> {
         rope[k] = kRope != 0 && p ? __ldg(p + (kCodeBytes + kScaleBytes) / 16 + 2 * (t & 3) + k) : zero;
     }
   }
-  // Four e2m1 codes (the low 16 bits of `sel`) as bf16 values times `s2`. The magnitudes
-  // 0 1/2 1 3/2 2 3 4 6 are looked up as the two bytes of their bf16 by byte permutes; a permute
-  // in its sign-replicating mode spreads the codes' sign bits. The product with a power of two is
-  // exact.
-  static __device__ __forceinline__ void four(uint32_t sel, __nv_bfloat162 s2, uint32_t* lo, uint32_t* hi) {
-    const uint32_t mag = sel & 0x7777u;
-    const uint32_t h = __byte_perm(0x3F3F3F00u, 0x40404040u, mag), l = __byte_perm(0xC0800000u, 0xC0804000u, mag);
-    // bytes 0x80 where the sign bit is clear, 0xFF where it is set: bit 6 is the sign
-    uint32_t sg;
-    asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(sel));
-    const uint32_t hs = h | ((sg << 1) & 0x80808080u);
-    uint32_t a = __byte_perm(l, hs, 0x5140), b = __byte_perm(l, hs, 0x7362);
-    const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), s2);
-    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), s2);
-    *lo = *reinterpret_cast<const uint32_t*>(&x);
-    *hi = *reinterpret_cast<const uint32_t*>(&y);
-  }
   static __device__ __forceinline__ void prefetch(const uint8_t* const (&rec)[kRecords], int t) {
     if (rec[0]) csa::prefetch_l2(rec[0] + min(128 * (t & 3), record_bytes(true, kRope) - 1));
   }
@@ -346,8 +329,8 @@ struct TileRegs<true, kRope> {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       uint32_t* v = value[pair & 1] + 4 * j;
-      four(word[j], s2, &v[0], &v[1]);
-      four(word[j] >> 16, s2, &v[2], &v[3]);
+      mxfp4_four(word[j], s2, &v[0], &v[1]);
+      mxfp4_four(word[j] >> 16, s2, &v[2], &v[3]);
     }
     if (kRope != 0 && pair == 0) {
       rope_now[0] = rope[0];

@@ -28,6 +28,24 @@ __device__ __forceinline__ float ue8m0(uint32_t b) {
   return __uint_as_float(b == 0 ? 0x00400000u : (b == 255 ? 0x7FC00000u : b << 23));
 }
 
+// Four e2m1 codes (the low 16 bits of `sel`) as bf16 values times `s2`. The magnitudes
+// 0 1/2 1 3/2 2 3 4 6 are looked up as the two bytes of their bf16 by byte permutes; a permute
+// in its sign-replicating mode spreads the codes' sign bits. The product with a power of two is
+// exact.
+__device__ __forceinline__ void mxfp4_four(uint32_t sel, __nv_bfloat162 s2, uint32_t* lo, uint32_t* hi) {
+  const uint32_t mag = sel & 0x7777u;
+  const uint32_t h = __byte_perm(0x3F3F3F00u, 0x40404040u, mag), l = __byte_perm(0xC0800000u, 0xC0804000u, mag);
+  // bytes 0x80 where the sign bit is clear, 0xFF where it is set: bit 6 is the sign
+  uint32_t sg;
+  asm("prmt.b32 %0, %1, %1, %2;" : "=r"(sg) : "r"(0x80808080u), "r"(sel));
+  const uint32_t hs = h | ((sg << 1) & 0x80808080u);
+  uint32_t a = __byte_perm(l, hs, 0x5140), b = __byte_perm(l, hs, 0x7362);
+  const __nv_bfloat162 x = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&a), s2);
+  const __nv_bfloat162 y = __hmul2(*reinterpret_cast<__nv_bfloat162*>(&b), s2);
+  *lo = *reinterpret_cast<const uint32_t*>(&x);
+  *hi = *reinterpret_cast<const uint32_t*>(&y);
+}
+
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
 // A softmax scale: the kernels multiply it by log2 e, which has to stay finite.
