@@ -17,12 +17,13 @@ constexpr int kRows = 64;                      // query rows (draft and head) of
 constexpr int kSlots = 8;                      // of the ring: 64 records x 128 values each, two 8 KB columns of 64 values
 constexpr int kColBytes = kRows * 128, kSlotBytes = 2 * kColBytes;
 constexpr int kSoftmaxWarps = 8, kMmaWarp = kSoftmaxWarps;
-// The loaders: of bf16 records one warp, by TMA, and two for queries that TMA does not reach; of 4-bit records eight, through
-// registers, which take the queries too.
+// The loaders: of bf16 records one warp, by TMA, and two for queries that TMA does not reach; of 4-bit records four for the keys
+// (and the queries) and four for the values, through registers.
 template <bool kFp4>
 struct Warps {
-  static constexpr int kQuery = kMmaWarp + (kFp4 ? 1 : 2), kQueries = kFp4 ? 8 : 2, kThreads = 32 * (kQuery + kQueries);
-  static constexpr int kFills = kFp4 ? kQueries : 1;  // arrivals of a CTA that make a slot full
+  static constexpr int kQuery = kMmaWarp + (kFp4 ? 1 : 2), kQueries = kFp4 ? 4 : 2, kValues = kQuery + kQueries;
+  static constexpr int kThreads = 32 * (kFp4 ? kValues + 4 : kValues);
+  static constexpr int kFills = kFp4 ? 4 : 1;  // arrivals of a CTA that make a slot full
 };
 constexpr int kLoadWarp = kMmaWarp + 1;
 constexpr uint32_t kTmemCols = 512, kTmemS = 256;  // O in columns 0 .. 255, S of even and odd tiles in 256 and 320
@@ -459,130 +460,174 @@ __device__ void role_query(const Kernel& K, const Maps& M, Smem<false, kRope>& S
     if (!load_query<false, kRope>(K, M, S, W, piece, rank)) return;
 }
 
-// 4-bit records: eight warps, four lanes a record. A slot is 128 values of 64 records, four blocks of 32 each: a block a thread
-// (16 code bytes and a scale byte become 64 bytes of bf16, exactly). What comes next is in registers already: the next tile's keys while
-// this one's values are stored, and the other way round. The order of the slots, and what becomes of rows past the end and of
-// drafts' values that are not finite, is as in role_load; the values of the CTA's own page are read and converted a second time,
-// because there is no room to keep them.
+// 4-bit records, four lanes a record. A slot is 128 values of 64 records, four blocks of 32 each: two blocks a thread (16 code
+// bytes and a scale byte become 64 bytes of bf16, exactly). The codes of the next two slots are on their way while one is
+// converted (of four, their registers and the code for them made it slower), and the page of the tile after the next one is
+// on its way to L2. Keys and values have four warps each, so that neither waits for the other's turn in the ring; the values of the
+// CTA's own page are read and converted a second time, because there is no room to keep them.
+struct Codes {
+  uint4 code[2];
+  uint32_t scale[2];
+};
+
+// To the slot at `slot`, as records t / 4 and t / 4 + 32, block t % 4.
+__device__ __forceinline__ void store_codes(const Codes& x, uint32_t slot, int t) {
+  const int s = t & 3;
+  const bool swap = s >= 2;  // lanes 2, 3 of a record store their words in another order: no two on one bank
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (t >> 2) + 32 * k;
+    const uint32_t sb = x.scale[k], bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7), two = bits | (bits << 16);
+    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
+    const uint4 c = x.code[k];
+    const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
+    const uint32_t row = slot + (s >> 1) * kColBytes + r * 128;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      uint32_t v[4];
+      mxfp4_four(word[j], s2, &v[0], &v[1]);
+      mxfp4_four(word[j] >> 16, s2, &v[2], &v[3]);
+      const int chunk = 4 * (s & 1) + (swap ? j ^ 2 : j);
+      csa::st_shared_v4(row + ((chunk ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
+    }
+  }
+}
+
+// A page of a piece, as the loaders of 4-bit records see it.
+struct PageView {
+  const uint8_t* records;  // null: none of it is there
+  int32_t rows;            // of its records, that there are
+};
+
+__device__ __forceinline__ PageView page_view(const csa_draft_attend_args& A, const Request& R, int32_t p, int32_t page, int32_t* flags) {
+  if (p * kPageRecs >= R.total) return {nullptr, 0};
+  if (page < 0 || page >= A.cache.num_pages) {
+    *flags |= CSA_DEV_PAGE_OOB;
+    return {nullptr, 0};
+  }
+  return {A.cache.pages + page * A.cache.page_stride_bytes, min(kPageRecs, R.total - p * kPageRecs)};
+}
+
 template <int kRope>
-__device__ void role_load_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>& S, uint32_t rank, int32_t* flags) {
-  const csa_draft_attend_args& A = K.A;
-  const int t = threadIdx.x - 32 * Warps<true>::kQuery, lane = t & 31, r = t >> 2, s = t & 3;  // this thread's record and block
+__device__ __forceinline__ void fetch_codes(Codes& x, const PageView& P, int block, int t) {
   constexpr int kRec = record_bytes(true, kRope);
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const int r = (t >> 2) + 32 * k;
+    const uint8_t* rec = P.records + r * kRec;
+    const bool there = r < P.rows;
+    x.code[k] = there ? __ldg(reinterpret_cast<const uint4*>(rec) + block) : make_uint4(0, 0, 0, 0);
+    x.scale[k] = there ? __ldg(rec + kCodeBytes + block) : 0u;
+  }
+}
+
+// Hands a slot, or the rope column, over.
+__device__ __forceinline__ void handed_over(uint32_t lead_bar) {
+  csa::fence_proxy_async_smem();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) arrive_at(lead_bar);
+}
+
+template <int kRope>
+__device__ void role_keys_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>& S, uint32_t rank, int32_t* flags) {
+  const csa_draft_attend_args& A = K.A;
+  const int t = threadIdx.x - 32 * Warps<true>::kQuery, s = t & 3;
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0), ring = smem_u32(S.ring[0]);
-  const bool swap = s >= 2;  // lanes 2, 3 of a record store their words in another order: no two on one bank
   csa::test_delay();
-  uint32_t q = 0, ropes = 0, piece = 0;
+  uint32_t q = 0, ropes = 0, piece = 0;  // q: slots of the pieces before
   bool ok = true;
-  struct Codes {
-    uint4 code[4];
-    uint32_t scale[4];
-  };
-  auto convert_and_store = [&](uint4 c, uint32_t sb) {  // to slot q
-    const uint32_t bits = sb == 0 ? 0x0040u : (sb == 255 ? 0x7FC0u : sb << 7), two = bits | (bits << 16);
-    const __nv_bfloat162 s2 = *reinterpret_cast<const __nv_bfloat162*>(&two);
-    const uint32_t word[4] = {swap ? c.z : c.x, swap ? c.w : c.y, swap ? c.x : c.z, swap ? c.y : c.w};
-    uint32_t v[16];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      mxfp4_four(word[j], s2, &v[4 * j], &v[4 * j + 1]);
-      mxfp4_four(word[j] >> 16, s2, &v[4 * j + 2], &v[4 * j + 3]);
-    }
-    ok = ok && warp_wait(bars + 8 * (kBarEmpty + q % kSlots), (q / kSlots & 1) ^ 1, stop);
-    if (!ok) return;
-    const uint32_t row = ring + q % kSlots * kSlotBytes + (s >> 1) * kColBytes + r * 128;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int chunk = 4 * (s & 1) + (swap ? j ^ 2 : j);
-      csa::st_shared_v4(row + ((chunk ^ (r & 7)) << 4), v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-    }
-    csa::fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) arrive_at(lead_bars + 8 * (kBarFull + q % kSlots));
-    ++q;
-  };
-  for (Walk W = S.walk; ok && W.more(); W.next(A), ++piece) {
+  for (Walk W = S.walk; ok && W.more(); q += 8 * W.n, W.next(A), ++piece) {
     const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
     const Request& R = W.w.R;
-    const int32_t past = W.first + W.n;  // of the piece's tiles
-    auto page_of = [&](int32_t tile, int half) { return tile < past && (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : -1; };
-    // this thread's record of a page of the tile, or null
-    auto record = [&](int32_t tile, int half, int32_t page) -> const uint8_t* {
-      const int32_t p0 = (2 * tile + half) * kPageRecs;
-      if (tile >= past || p0 >= R.total) return nullptr;
-      if (page < 0 || page >= A.cache.num_pages) {
-        *flags |= CSA_DEV_PAGE_OOB;
-        return nullptr;
-      }
-      return p0 + r < R.total ? A.cache.pages + page * A.cache.page_stride_bytes + static_cast<int64_t>(r) * kRec : nullptr;
-    };
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    Codes kc, vc;
-    uint4 rope[2];
-    auto fetch_keys = [&](int32_t tile, int32_t page) {
-      const uint8_t* rec = record(tile, static_cast<int>(rank), page);
+    const int32_t past = W.first + W.n;
+    auto page_at = [&](int32_t tile) { return tile < past && (2 * tile + static_cast<int>(rank)) * kPageRecs < R.total ? __ldg(table + 2 * tile + rank) : -1; };
+    auto view = [&](int32_t tile, int32_t page) { return tile < past ? page_view(A, R, 2 * tile + rank, page, flags) : PageView{nullptr, 0}; };
+    int32_t page = page_at(W.first + 1);
+    PageView now = view(W.first, page_at(W.first)), next;
+    Codes x[2];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        kc.code[c] = rec ? __ldg(reinterpret_cast<const uint4*>(rec) + 4 * c + s) : zero;
-        kc.scale[c] = rec ? __ldg(rec + kCodeBytes + 4 * c + s) : 0u;
-      }
-      if (kRope != 0)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) rope[k] = rec ? __ldg(reinterpret_cast<const uint4*>(rec + kCodeBytes + kScaleBytes) + 2 * s + k) : zero;
-    };
-    auto fetch_values = [&](int32_t tile, const int32_t (&page)[2]) {
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const uint8_t* rec = record(tile, c >> 1, page[c >> 1]);
-        const int block = 8 * static_cast<int>(rank) + 4 * (c & 1) + s;
-        vc.code[c] = rec ? __ldg(reinterpret_cast<const uint4*>(rec) + block) : zero;
-        vc.scale[c] = rec ? __ldg(rec + kCodeBytes + block) : 0u;
-        if (vc.scale[c] == 255 && (2 * tile + (c >> 1)) * kPageRecs + r >= R.base) vc.code[c] = zero, vc.scale[c] = 0;
-      }
-    };
-    auto keys = [&] {
-      if (kRope != 0) {
-        ok = ok && warp_wait(bars + 8 * kBarRopeEmpty, (ropes & 1) ^ 1, stop);
-        if (!ok) return;
+    for (int c = 0; c < 2; ++c) fetch_codes<kRope>(x[c], now, 4 * c + s, t);
+    ok = load_query<true, kRope>(K, M, S, W, piece, rank);
+    for (int i = 0; ok && i < W.n; ++i) {
+      next = view(W.first + i + 1, page);
+      page = page_at(W.first + i + 2);
+      if (kRope != 0) {  // the rope values go straight to shared memory, while the first codes are converted
+        if (!warp_wait(bars + 8 * kBarRopeEmpty, (ropes & 1) ^ 1, stop)) return;
         ++ropes;
-        const uint32_t row = smem_u32(S.rope) + r * 128;
 #pragma unroll
-        for (int k = 0; k < 2; ++k) csa::st_shared_v4(row + (((2 * s + k) ^ (r & 7)) << 4), rope[k].x, rope[k].y, rope[k].z, rope[k].w);
-        csa::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) arrive_at(lead_bars + 8 * kBarRopeFull);
+        for (int k = 0; k < 4; ++k) {
+          const int r = (t >> 3) + 16 * k;
+          csa::cp_async16(smem_u32(S.rope) + r * 128 + (((t & 7) ^ (r & 7)) << 4),
+                          r < now.rows ? now.records + r * record_bytes(true, kRope) + kCodeBytes + kScaleBytes + 16 * (t & 7) : A.cache.pages, r < now.rows);
+        }
       }
+      const uint32_t at = i == 0 ? q : q + 8 * i - 4;
+#pragma unroll 1
+      for (int c0 = 0; c0 < 4; c0 += 2) {
+        const PageView from = c0 == 0 ? now : next;
 #pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (ok) convert_and_store(kc.code[c], kc.scale[c]);
-    };
-    // pages of the tile whose values are next, of the one after it, and of the one after that
-    int32_t now[2], next[2], then[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      now[h] = page_of(W.first, h);
-      next[h] = page_of(W.first + 1, h);
-      then[h] = page_of(W.first + 2, h);
+        for (int c = 0; c < 2; ++c) {
+          const uint32_t slot = (at + c0 + c) % kSlots;
+          ok = ok && warp_wait(bars + 8 * (kBarEmpty + slot), (at / kSlots & 1) ^ 1, stop);
+          if (ok) store_codes(x[c], ring + slot * kSlotBytes, t);
+          if (kRope != 0 && c0 + c == 0) {
+            csa::cp_async_wait_all();
+            if (ok) handed_over(lead_bars + 8 * kBarRopeFull);
+          }
+          if (ok) handed_over(lead_bars + 8 * (kBarFull + slot));
+          fetch_codes<kRope>(x[c], from, 4 * (c0 == 0 ? c + 2 : c) + s, t);
+        }
+      }
+      now = next;
+      if (t == 0 && page >= 0 && page < A.cache.num_pages)
+        csa::bulk_prefetch_l2(A.cache.pages + page * A.cache.page_stride_bytes, kPageRecs * record_bytes(true, kRope));
     }
-    fetch_keys(W.first, rank ? now[1] : now[0]);
-    if (!load_query<true, kRope>(K, M, S, W, piece, rank)) ok = false;
-    fetch_values(W.first, now);
-    if (ok) keys();
-    fetch_keys(W.first + 1, rank ? next[1] : next[0]);
-    for (int32_t tile = W.first; ok && tile < past; ++tile) {
-      if (tile + 1 < past) {
-        keys();
-        fetch_keys(tile + 2, rank ? then[1] : then[0]);
-      }
-#pragma unroll
-      for (int c = 0; c < 4; ++c)
-        if (ok) convert_and_store(vc.code[c], vc.scale[c]);
-      fetch_values(tile + 1, next);
-#pragma unroll
+  }
+}
+
+// What becomes of rows past the end, and of drafts' values that are not finite, is as in role_load.
+template <int kRope>
+__device__ void role_values_fp4(const Kernel& K, Smem<true, kRope>& S, uint32_t rank, int32_t* flags) {
+  const csa_draft_attend_args& A = K.A;
+  const int t = threadIdx.x - 32 * Warps<true>::kValues, s = t & 3;
+  volatile int* stop = &S.abort;
+  const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0), ring = smem_u32(S.ring[0]);
+  csa::test_delay();
+  uint32_t q = 0;
+  for (Walk W = S.walk; W.more(); q += 8 * W.n, W.next(A)) {
+    const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
+    const Request& R = W.w.R;
+    const int32_t past = W.first + W.n;
+    auto page_at = [&](int32_t tile, int h) { return tile < past && (2 * tile + h) * kPageRecs < R.total ? __ldg(table + 2 * tile + h) : -1; };
+    auto view = [&](int32_t tile, int h, int32_t page) { return tile < past ? page_view(A, R, 2 * tile + h, page, flags) : PageView{nullptr, 0}; };
+    auto fetch = [&](Codes& x, const PageView& P, int b) { fetch_codes<kRope>(x, P, 8 * rank + 4 * b + s, t); };
+    PageView other = view(W.first, 1, page_at(W.first, 1));  // the page whose turn is next but one
+    int32_t page = page_at(W.first + 1, 0);                  // of the turn after it
+    Codes x[2];
+    {
+      const PageView first = view(W.first, 0, page_at(W.first, 0));
+      fetch(x[0], first, 0);
+      fetch(x[1], first, 1);
+    }
+    for (int i = 0; i < W.n; ++i) {
+      const uint32_t at = i + 1 < W.n ? q + 8 * i + 8 : q + 8 * W.n - 4;
+#pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        next[h] = then[h];
-        then[h] = page_of(tile + 3, h);
+        const int32_t drafts = R.base - (2 * (W.first + i) + h) * kPageRecs;  // the page's first draft
+#pragma unroll
+        for (int b = 0; b < 2; ++b) {
+          const uint32_t slot = (at + 2 * h + b) % kSlots;
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (x[b].scale[k] == 255 && (t >> 2) + 32 * k >= drafts) x[b].code[k] = make_uint4(0, 0, 0, 0), x[b].scale[k] = 0;
+          if (!warp_wait(bars + 8 * (kBarEmpty + slot), (at / kSlots & 1) ^ 1, stop)) return;
+          store_codes(x[b], ring + slot * kSlotBytes, t);
+          handed_over(lead_bars + 8 * (kBarFull + slot));
+          fetch(x[b], other, b);
+        }
+        other = view(W.first + i + 1, h, page);
+        page = page_at(W.first + i + 1 + h, h ^ 1);
       }
     }
   }
@@ -897,8 +942,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kFp4>::kThread
       __syncwarp();
     }
   } else {
-    if constexpr (kFp4) role_load_fp4<kRope>(K, M, S, rank, &flags);
-    else if (warp == kLoadWarp) role_load<kRope>(K, M, S, rank, &flags);
+    if constexpr (kFp4) {
+      if (warp < Warps<kFp4>::kValues) role_keys_fp4<kRope>(K, M, S, rank, &flags);
+      else role_values_fp4<kRope>(K, S, rank, &flags);
+    } else if (warp == kLoadWarp) role_load<kRope>(K, M, S, rank, &flags);
     else role_query<kRope>(K, M, S, rank);
   }
   if (warp == kMmaWarp && rank == 1) csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);  // the last commit has told this CTA too
