@@ -8,10 +8,12 @@ namespace {
 
 // ------------------------------------------------------------- norm and rotation of heads
 //
-// A group of 8, 16 or 32 lanes takes a head, a lane 8 values of each 256 (16 or 32 bytes a load). A head's values stay
-// in registers between the sum of squares and the store, so every value is read and written once; a rotated pair of halves
-// comes from another lane's values, which are loaded again (from L1) rather than exchanged, because where the rotated
-// part begins is free. The rows' cosines and sines are made once a block, in shared memory, for all heads of the row.
+// A group of 8, 16 or 32 lanes takes a head, a lane up to 4 pieces of 8 values of it (16 or 32 bytes a load): the fewest lanes with which
+// most of them have work. A head's values stay in registers between the sum of squares and the store, so every value is
+// read and written once; a rotated pair of halves comes from another lane's values, which are loaded again (from L1)
+// rather than exchanged, because where the rotated part begins is free. A block takes up to 32 rows at a time, whose cosines and
+// sines are made once, in shared memory, for all heads, as are the weights. 16384 rows of 17 heads of 192 (214 MB): 44 us, 4.9 TB/s; what
+// it takes beyond the bytes are instructions (72% of the issue slots when it took 49 us).
 
 constexpr int kRotThreads = 256;
 
@@ -52,165 +54,223 @@ struct Eight {  // eight values as they lie in memory
 
 struct RotateKernel {
   csa_rotate_args A;
-  int32_t q_blocks, q_items, k_items;  // blocks of the queries; heads a block, of each tensor
+  int32_t rows;              // a block's at a time
+  int32_t q_lanes, k_lanes;  // of a head
 };
 
-// Lanes of a head, and heads that a block takes at a time.
-__host__ __device__ constexpr int lanes_of(int dim) { return dim <= 64 ? 8 : (dim <= 128 ? 16 : 32); }
+constexpr int kMostRows = 32;
 
-template <bool kF32In, bool kF32Out, int kChunks, int kHeadsInFlight>
-__global__ void __launch_bounds__(kRotThreads) rotate_kernel(const RotateKernel K) {
-  extern __shared__ float2 turns[];  // [rows of the block][rope_dim / 2] cos, sin
-  __shared__ uint64_t per_token[CSA_ROTATE_MAX_ROPE / 2];
-  const csa_rotate_args& A = K.A;
-  const bool is_q = static_cast<int>(blockIdx.x) < K.q_blocks;
-  const csa_heads& T = is_q ? A.q : A.k;
-  const int64_t per = is_q ? K.q_items : K.k_items;
-  const int64_t first = per * (is_q ? blockIdx.x : blockIdx.x - K.q_blocks);
-  const int64_t last = min(first + per, A.n * T.heads);  // heads first .. last of all rows' heads
-  const int64_t row0 = first / T.heads;
-  const int half = A.rotation.rope_dim / 2;
-  int32_t flags = 0;
-  if (half > 0) {
-    for (int j = threadIdx.x; j < half; j += kRotThreads) per_token[j] = turns_per_token(A.rotation.freq[j]);
-    __syncthreads();
-    const int rows = static_cast<int>((last - 1) / T.heads - row0 + 1);
-    for (int i = threadIdx.x; i < rows * half; i += kRotThreads) turns[i] = cos_sin(per_token[i % half], A.pos[row0 + i / half], A.rotation.scale);
-    __syncthreads();
-  }
-  const int G = lanes_of(T.dim), lane = threadIdx.x & (G - 1), chunks = T.dim / 8;
-  const uint32_t mates = (G == 32 ? 0xFFFFFFFFu : (1u << G) - 1u) << (threadIdx.x & 31 & ~(G - 1));
+// Pieces of 8 values that a lane has of a head whose `lanes` share it.
+__host__ __device__ constexpr int pieces_of(int dim, int lanes) { return (dim / 8 + lanes - 1) / lanes; }
+
+// y r w of eight values; the weights lie as the first and the last four of each chunk of eight, apart.
+__device__ __forceinline__ void weighted(float (&y)[8], float r, const float4* w, int chunk, int chunks) {
+  const float4 a = w[chunk], b = w[chunks + chunk];
+  y[0] = y[0] * r * a.x, y[1] = y[1] * r * a.y, y[2] = y[2] * r * a.z, y[3] = y[3] * r * a.w;
+  y[4] = y[4] * r * b.x, y[5] = y[5] * r * b.y, y[6] = y[6] * r * b.z, y[7] = y[7] * r * b.w;
+}
+
+// Heads head0 .. head0 + heads of one tensor, of rows row0 .. row0 + rows. `weights` are the tensor's, in shared memory. Lanes
+// past a head's end, and groups past the last head, load what others load, and neither add nor store it.
+template <bool kF32In, int kPieces, bool kHalves>
+__device__ __forceinline__ void rotate_heads(const csa_rotate_args& A, const csa_heads& T, int G, int64_t row0, int rows, int head0, int heads,
+                                             const float4* turns, const int32_t* pos, const float4* weights) {
+  constexpr int kIn = kF32In ? 4 : 2;
+  const int lane = threadIdx.x & (G - 1), chunks = T.dim / 8, half = A.rotation.rope_dim / 2, groups = kRotThreads / G;
+  const float per_value = 1.f / static_cast<float>(T.dim);
   // of the head's chunks of 8 values, those that rotate, and how far apart halves lie
   const int turn0 = A.rope_first ? 0 : chunks - half / 4, turn1 = turn0 + half / 4, apart = half / 8;
-  const bool halves = A.rotation.pairing == CSA_PAIRS_HALVES;
-  constexpr int kIn = kF32In ? 4 : 2, kOut = kF32Out ? 4 : 2;
-  const int64_t step = kRotThreads / G;
-  for (int64_t at = first + threadIdx.x / G; at - threadIdx.x / G < last; at += kHeadsInFlight * step) {
-    Eight<kF32In> x[kHeadsInFlight][kChunks], other[kHeadsInFlight][kChunks];
-    int64_t row[kHeadsInFlight], head[kHeadsInFlight];
-    bool live[kHeadsInFlight];
+  // heads g, g + groups, ... of the rows' heads, row by row
+  const int step_rows = groups / heads, step_heads = groups - step_rows * heads;
+  int row = static_cast<int>(threadIdx.x) / G / heads, head = static_cast<int>(threadIdx.x) / G - row * heads;
+  const int most = (rows * heads + groups - 1) / groups;  // the same for all groups, whose lanes share warps
+  for (int i = 0; i < most; ++i) {
+    const int at_row = min(row, rows - 1), at_head = head0 + head;
+    const bool live = row < rows && pos[at_row] >= 0;
+    const uint8_t* src = static_cast<const uint8_t*>(T.x) + kIn * ((row0 + at_row) * T.x_row_stride + at_head * T.x_head_stride);
+    Eight<kF32In> x[kPieces], other[kHalves ? kPieces : 1];
 #pragma unroll
-    for (int i = 0; i < kHeadsInFlight; ++i) {
-      const int64_t item = at + i * step;
-      live[i] = item < last;
-      row[i] = live[i] ? item / T.heads : row0;
-      head[i] = live[i] ? item % T.heads : 0;
-      if (A.pos) {
-        const int32_t p = A.pos[row[i]];
-        if (live[i] && p < -1) flags |= CSA_DEV_LEN_OOB;
-        live[i] = live[i] && p >= 0;
+    for (int k = 0; k < kPieces; ++k) {
+      const int c = min(lane + G * k, chunks - 1);
+      x[k].load(src + 8 * kIn * c);
+      if (kHalves) other[k].load(src + 8 * kIn * (c >= turn0 && c < turn1 ? (c < turn0 + apart ? c + apart : c - apart) : c));
+    }
+    float r = 1.f;
+    if (T.norm) {
+      float part[2] = {0.f, 0.f};
+#pragma unroll
+      for (int k = 0; k < kPieces; ++k) {
+        float v[8];
+        x[k].get(v);
+        if (lane + G * k < chunks)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) part[j & 1] = fmaf(v[j], v[j], part[j & 1]);
       }
-      const uint8_t* src = static_cast<const uint8_t*>(T.x) + kIn * (row[i] * T.x_row_stride + head[i] * T.x_head_stride);
+      float sum = part[0] + part[1];
+      for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+      const float mean = fmaf(sum, per_value, A.eps);
+      r = rsqrtf(mean);
+      if (__any_sync(0xFFFFFFFFu, !plain_mean(mean))) {
+        double wide = 0.0;
+#pragma unroll 1
+        for (int c = lane; c < chunks; c += G) {
+          Eight<kF32In> again;
+          again.load(src + 8 * kIn * c);
+          float v[8];
+          again.get(v);
 #pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
-        const int c = lane + G * k;
-        if (!live[i] || c >= chunks) continue;
-        x[i][k].load(src + 8 * kIn * c);
-        if (halves && c >= turn0 && c < turn1) other[i][k].load(src + 8 * kIn * (c < turn0 + apart ? c + apart : c - apart));
+          for (int j = 0; j < 8; ++j) wide += static_cast<double>(v[j]) * v[j];
+        }
+        for (int o = G / 2; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
+        if (!plain_mean(mean)) r = static_cast<float>(1.0 / sqrt(wide / T.dim + A.eps));
       }
     }
     __syncwarp();  // in place: all of a head is read before any of it is written
+    if (live) {
+      const int64_t to = (row0 + at_row) * T.out_row_stride + at_head * T.out_head_stride;
 #pragma unroll
-    for (int i = 0; i < kHeadsInFlight; ++i) {
-      float r = 1.f;
-      if (T.norm) {
-        float sum = 0.f;
-#pragma unroll
-        for (int k = 0; k < kChunks; ++k) {
-          if (!live[i] || lane + G * k >= chunks) continue;
-          float v[8];
-          x[i][k].get(v);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) sum = fmaf(v[j], v[j], sum);
-        }
-        for (int o = G / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        const float mean = sum / static_cast<float>(T.dim) + A.eps;
-        r = 1.f / sqrtf(mean);
-        if (!plain_mean(mean)) {  // the same for all lanes of the head
-          double wide = 0.0;
-#pragma unroll
-          for (int k = 0; k < kChunks; ++k) {
-            if (!live[i] || lane + G * k >= chunks) continue;
-            float v[8];
-            x[i][k].get(v);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) wide += static_cast<double>(v[j]) * v[j];
-          }
-          for (int o = G / 2; o > 0; o >>= 1) wide += __shfl_xor_sync(mates, wide, o);
-          r = static_cast<float>(1.0 / sqrt(wide / T.dim + A.eps));
-        }
-      }
-      if (!live[i]) continue;
-      uint8_t* dst = static_cast<uint8_t*>(T.out) + kOut * (row[i] * T.out_row_stride + head[i] * T.out_head_stride);
-#pragma unroll
-      for (int k = 0; k < kChunks; ++k) {
+      for (int k = 0; k < kPieces; ++k) {
         const int c = lane + G * k;
-        if (c >= chunks) continue;
+        if (c >= chunks) break;
         float v[8];
-        x[i][k].get(v);
-        auto scale = [&](float (&y)[8], int chunk) {
-          if (!T.norm) return;
-          float w[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-          if (T.weight) {
-            const float4 a = __ldg(reinterpret_cast<const float4*>(T.weight) + 2 * chunk), b = __ldg(reinterpret_cast<const float4*>(T.weight) + 2 * chunk + 1);
-            w[0] = a.x, w[1] = a.y, w[2] = a.z, w[3] = a.w, w[4] = b.x, w[5] = b.y, w[6] = b.z, w[7] = b.w;
-          }
-#pragma unroll
-          for (int j = 0; j < 8; ++j) y[j] = y[j] * r * w[j];
-        };
-        scale(v, c);
+        x[k].get(v);
+        if (T.norm) weighted(v, r, weights, c, chunks);
         if (c >= turn0 && c < turn1) {
-          const float2* t = turns + (row[i] - row0) * half;
-          if (halves) {
+          const float4* t = turns + at_row * (half / 2);
+          if constexpr (kHalves) {
             const bool low = c < turn0 + apart;
             float u[8];
-            other[i][k].get(u);
-            scale(u, low ? c + apart : c - apart);
-            t += 8 * (low ? c - turn0 : c - turn0 - apart);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = low ? v[j] * t[j].x - u[j] * t[j].y : v[j] * t[j].x + u[j] * t[j].y;
-          } else {
-            t += 4 * (c - turn0);
+            other[k].get(u);
+            if (T.norm) weighted(u, r, weights, low ? c + apart : c - apart, chunks);
+            t += 4 * (low ? c - turn0 : c - turn0 - apart);
+            const float sign = low ? -1.f : 1.f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float a = v[2 * j], b = v[2 * j + 1];
-              v[2 * j] = a * t[j].x - b * t[j].y;
-              v[2 * j + 1] = b * t[j].x + a * t[j].y;
+              const float4 w = t[j];
+              v[2 * j] = v[2 * j] * w.x + sign * u[2 * j] * w.y;
+              v[2 * j + 1] = v[2 * j + 1] * w.z + sign * u[2 * j + 1] * w.w;
+            }
+          } else {
+            t += 2 * (c - turn0);
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float4 w = t[j];
+              float* y = v + 4 * j;
+              const float a0 = y[0], b0 = y[1], a1 = y[2], b1 = y[3];
+              y[0] = a0 * w.x - b0 * w.y, y[1] = b0 * w.x + a0 * w.y;
+              y[2] = a1 * w.z - b1 * w.w, y[3] = b1 * w.z + a1 * w.w;
             }
           }
         }
-        Eight<kF32Out> y;
-        y.put(v);
-        y.store(dst + 8 * kOut * c);
+        if (A.out_dtype == CSA_KEYS_F32) {
+          Eight<true> y;
+          y.put(v);
+          y.store(static_cast<float*>(T.out) + to + 8 * c);
+        } else {
+          Eight<false> y;
+          y.put(v);
+          y.store(static_cast<__nv_bfloat16*>(T.out) + to + 8 * c);
+        }
       }
     }
+    row += step_rows;
+    head += step_heads;
+    if (head >= heads) {
+      head -= heads;
+      ++row;
+    }
   }
-  flags = static_cast<int32_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(flags)));
-  if (flags && A.dev_status && (threadIdx.x & 31) == 0) atomicOr(A.dev_status, flags);
 }
 
-template <bool kF32In, bool kF32Out, int kChunks, int kHeadsInFlight>
-csa_status launch_rotate(RotateKernel& K, cudaStream_t stream) {
+template <bool kF32In, int kPieces, bool kHalves>
+__global__ void __launch_bounds__(kRotThreads, kF32In || kPieces > 3 ? 3 : 4) rotate_kernel(const RotateKernel K) {
+  extern __shared__ float4 rotate_smem[];  // the weights of q and of k, then [rows of the block][rope_dim / 2] cos, sin
+  __shared__ uint64_t per_token[CSA_ROTATE_MAX_ROPE / 2];
+  __shared__ int32_t pos[kMostRows];
+  const csa_rotate_args& A = K.A;
+  const int half = A.rotation.rope_dim / 2, tid = threadIdx.x;
+  const int q_dim = A.q.heads > 0 ? A.q.dim : 0, k_dim = A.k.heads > 0 ? A.k.dim : 0;
+  float* weights = reinterpret_cast<float*>(rotate_smem);
+  float2* turns = reinterpret_cast<float2*>(weights + q_dim + k_dim);
+  const float4 *q_weights = rotate_smem, *k_weights = rotate_smem + q_dim / 4, *row_turns = reinterpret_cast<const float4*>(turns);
+  int32_t flags = 0;
+  // this block's heads of each tensor: all of them, unless there are few rows
+  const int y = blockIdx.y, ys = gridDim.y;
+  const int q0 = A.q.heads * y / ys, q1 = A.q.heads * (y + 1) / ys, k0 = A.k.heads * y / ys, k1 = A.k.heads * (y + 1) / ys;
+  auto rows_at = [&](int64_t row0) { return static_cast<int>(min(static_cast<int64_t>(K.rows), A.n - row0)); };
+  const int64_t step = static_cast<int64_t>(gridDim.x) * K.rows;
+  for (int j = tid; j < half; j += kRotThreads) per_token[j] = turns_per_token(A.rotation.freq[j]);
+  for (int i = tid; i < q_dim + k_dim; i += kRotThreads) {
+    const float* w = i < q_dim ? A.q.weight : A.k.weight;
+    const int first = i < q_dim ? 0 : q_dim, n = i - first, dim = i < q_dim ? q_dim : k_dim;
+    weights[first + (n & 4) / 4 * (dim / 2) + n / 8 * 4 + (n & 3)] = w ? w[n] : 1.f;
+  }
+  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * K.rows; row0 < A.n; row0 += step) {
+    const int rows = rows_at(row0);
+    if (tid < rows) {  // every thread has taken what it needs of the last rows' positions: it has read their turns
+      const int32_t p = A.pos ? A.pos[row0 + tid] : 0;
+      if (p < -1) flags |= CSA_DEV_LEN_OOB;
+      pos[tid] = p;
+    }
+    __syncthreads();
+    for (int i = tid; i < rows * half; i += kRotThreads) turns[i] = cos_sin(per_token[i % half], pos[i / half], A.rotation.scale);
+    __syncthreads();
+    if (q1 > q0) rotate_heads<kF32In, kPieces, kHalves>(A, A.q, K.q_lanes, row0, rows, q0, q1 - q0, row_turns, pos, q_weights);
+    if (k1 > k0) rotate_heads<kF32In, kPieces, kHalves>(A, A.k, K.k_lanes, row0, rows, k0, k1 - k0, row_turns, pos, k_weights);
+    if (row0 + step < A.n) __syncthreads();
+  }
+  flags = static_cast<int32_t>(__reduce_or_sync(0xFFFFFFFFu, static_cast<uint32_t>(flags)));
+  if (flags && A.dev_status && (tid & 31) == 0) atomicOr(A.dev_status, flags);
+}
+
+template <bool kF32In, int kPieces, bool kHalves>
+csa_status launch_rotate(RotateKernel& K, int sms, int dev, cudaStream_t stream) {
   const csa_rotate_args& a = K.A;
-  auto items = [](const csa_heads& t) { return kHeadsInFlight * kRotThreads / lanes_of(t.dim); };
-  auto blocks = [&](const csa_heads& t) { return t.heads > 0 ? (a.n * t.heads + items(t) - 1) / items(t) : 0; };
-  auto rows = [&](const csa_heads& t) { return t.heads > 0 ? (items(t) - 1) / t.heads + 2 : 0; };  // that a block's heads can be of
-  K.q_items = a.q.heads > 0 ? items(a.q) : 0;
-  K.k_items = a.k.heads > 0 ? items(a.k) : 0;
-  const int64_t grid = blocks(a.q) + blocks(a.k);
-  if (grid > INT32_MAX) return CSA_ERR_INVALID_ARG;
-  K.q_blocks = static_cast<int32_t>(blocks(a.q));
-  const int most = rows(a.q) > rows(a.k) ? rows(a.q) : rows(a.k);
-  const size_t smem = sizeof(float2) * most * (a.rotation.rope_dim / 2);
-  rotate_kernel<kF32In, kF32Out, kChunks, kHeadsInFlight><<<static_cast<unsigned>(grid), kRotThreads, smem, stream>>>(K);
+  auto smem = [&](int rows) {
+    return sizeof(float) * ((a.q.heads > 0 ? a.q.dim : 0) + (a.k.heads > 0 ? a.k.dim : 0)) + sizeof(float2) * rows * (a.rotation.rope_dim / 2);
+  };
+  static Kept kept;  // resident blocks an SM, with the most shared memory
+  int per_sm = kept.get(dev);
+  if (per_sm == 0) {
+    constexpr size_t most = sizeof(float) * 2 * CSA_ROTATE_MAX_DIM + sizeof(float2) * kMostRows * (CSA_ROTATE_MAX_ROPE / 2);
+    static_assert(most <= 40 * 1024, "shared memory of a block");
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, rotate_kernel<kF32In, kPieces, kHalves>, kRotThreads, most) != cudaSuccess || per_sm < 1)
+      return CSA_ERR_CUDA;
+    kept.set(dev, per_sm);
+  }
+  // At most one wave; fewer rows a block where there are few, so that all SMs have some, and where there are fewer rows than SMs
+  // several blocks a row (64 rows of 65 heads: 8.6 us, with a block a row 10.5).
+  const int64_t cap = static_cast<int64_t>(sms) * per_sm, rounds = (a.n + cap * kMostRows - 1) / (cap * kMostRows);
+  K.rows = static_cast<int32_t>((a.n + cap * rounds - 1) / (cap * rounds));
+  const int64_t blocks = (a.n + K.rows - 1) / K.rows, heads = a.q.heads > a.k.heads ? a.q.heads : a.k.heads, share = 2 * sms / blocks;
+  const dim3 grid(static_cast<unsigned>(blocks < cap ? blocks : cap), static_cast<unsigned>(share < 1 ? 1 : (share < heads ? share : heads) < 16 ? (share < heads ? share : heads) : 16));
+  rotate_kernel<kF32In, kPieces, kHalves><<<grid, kRotThreads, smem(K.rows), stream>>>(K);
   return cudaGetLastError() == cudaSuccess ? CSA_OK : CSA_ERR_CUDA;
 }
 
-template <bool kF32In, bool kF32Out>
+template <bool kF32In, bool kHalves>
 csa_status launch_rotate_dim(RotateKernel& K, cudaStream_t stream) {
-  const int q = K.A.q.heads > 0 ? K.A.q.dim : 0, k = K.A.k.heads > 0 ? K.A.k.dim : 0, dim = q > k ? q : k;
-  if (dim <= 256) return launch_rotate<kF32In, kF32Out, 1, 2>(K, stream);
-  return dim <= 512 ? launch_rotate<kF32In, kF32Out, 2, 1>(K, stream) : launch_rotate<kF32In, kF32Out, 4, 1>(K, stream);
+  int sms = 0, dev = 0;
+  if (sm_count(&sms, &dev) != CSA_OK) return CSA_ERR_CUDA;
+  // lanes of a head: 8, 16 or 32, with the fewest idle, the fewest lanes first, and at most 3 pieces a lane where 32 are enough for that
+  auto lanes = [](const csa_heads& t) {
+    int best = 32;
+    for (int g = 16; g >= 8; g /= 2)
+      if (pieces_of(t.dim, g) <= 3 && g * pieces_of(t.dim, g) <= best * pieces_of(t.dim, best)) best = g;
+    return best;
+  };
+  int pieces = 1;
+  K.q_lanes = K.k_lanes = 32;
+  if (K.A.q.heads > 0) pieces = pieces_of(K.A.q.dim, K.q_lanes = lanes(K.A.q));
+  if (K.A.k.heads > 0) {
+    K.k_lanes = lanes(K.A.k);
+    const int k = pieces_of(K.A.k.dim, K.k_lanes);
+    pieces = k > pieces ? k : pieces;
+  }
+  if (pieces == 1) return launch_rotate<kF32In, 1, kHalves>(K, sms, dev, stream);
+  if (pieces == 2) return launch_rotate<kF32In, 2, kHalves>(K, sms, dev, stream);
+  if (pieces == 3) return launch_rotate<kF32In, 3, kHalves>(K, sms, dev, stream);
+  return launch_rotate<kF32In, 4, kHalves>(K, sms, dev, stream);
 }
 
 csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, bool f32_out) {
@@ -237,12 +297,23 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
 // twice, a little larger and a little smaller; where the two differ anywhere in the row (about one row in 100) the row is
 // computed again in fp64.
 
-// The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the division
-// and eps 2 x 2^-24, halved by the root; root, reciprocal and two products 4 x 2^-24 more. 2^-19 is more than twice that.
+// The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the mean and eps
+// 2 x 2^-24, halved by the root; rsqrtf (two units in the last place) 4 x 2^-24 and two products 2 x 2^-24 more: 18 x 2^-24.
+// 2^-19 is nearly twice that.
 constexpr float kNear = 0x1p-19f;
 
-// Codes and exponent of a lane's values in fp64: the exact norm's, next to a border too.
-__device__ __noinline__ void encode_exact(const float (&x)[16], const float (&w)[16], float eps, Coded<true>& c) {
+// Codes and exponent of a lane's values in fp64: the exact norm's, next to a border too. The row is read again, so that its values
+// need not have an address where they are not.
+template <bool kBf16In>
+__device__ __noinline__ Coded<true> encode_exact(const void* row, const float* weight, float eps) {
+  const int lane = threadIdx.x & 31;
+  RowIn<kBf16In> in;
+  in.load(row, lane, 0);
+  const float (&x)[16] = in.v;
+  float w[16];
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = weight ? __ldg(weight + 16 * lane + k) : 1.f;
+  Coded<true> c;
   double sum = 0.0;
 #pragma unroll
   for (int k = 0; k < 16; ++k) sum += static_cast<double>(x[k]) * x[k];
@@ -251,7 +322,7 @@ __device__ __noinline__ void encode_exact(const float (&x)[16], const float (&w)
   const double r = 1.0 / sqrt(sum / kDim + eps);
   double amax = 0.0;
   bool bad = false;
-#pragma unroll 1
+#pragma unroll
   for (int k = 0; k < 16; ++k) {
     const double y = fabs(x[k] * r * w[k]);
     bad |= !(y < 0x1.ffffffp127);  // what rounds to a finite fp32, and no NaN
@@ -262,21 +333,22 @@ __device__ __noinline__ void encode_exact(const float (&x)[16], const float (&w)
   // floor(log2 amax) - 2, held at -127 (a double that is subnormal lies far below)
   c.e = max(static_cast<int>(__double2hiint(amax) >> 20) - 1023 - 2, -127);
   const double up = __hiloint2double((1023 - c.e) << 20, 0);
-#pragma unroll 1
+#pragma unroll
   for (int h = 0; h < 2; ++h) {
     c.w[h] = 0;
-#pragma unroll 1
+#pragma unroll
     for (int k = 0; k < 8; ++k) {
       const double y = x[8 * h + k] * r * w[8 * h + k], t = fabs(y) * up;
       const uint32_t m = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
       c.w[h] |= (m | (signbit(y) ? 8u : 0u)) << (4 * k);
     }
   }
+  return c;
 }
 
 template <bool kBf16In, bool kFp4>
-__device__ __forceinline__ int32_t append_row(const csa_append_args& A, RowIn<kBf16In>& x, const float (&w)[16], const uint64_t (&per_token)[2],
-                                              int64_t slot, int32_t pos, int lane) {
+__device__ __forceinline__ int32_t append_row(const csa_append_args& A, const RowIn<kBf16In>& x, const void* row, const float (&w)[16],
+                                              const uint64_t (&per_token)[2], int64_t slot, int32_t pos, int lane) {
   if (slot == -1) return 0;
   if (slot < 0 || slot >= A.cache.num_pages * kPageRecs) return CSA_DEV_PAGE_OOB;
   const bool rope = A.cache.rope_dim != 0;
@@ -284,7 +356,7 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, RowIn<kB
   if (rope) {
     if (pos < 0) return CSA_DEV_LEN_OOB;
     const float2 t = cos_sin(per_token[0], pos, A.rotation.scale);
-    float a = x.r[0], b = x.r[1];
+    const float a = x.r[0], b = x.r[1];
     if (A.rotation.pairing == CSA_PAIRS_ADJACENT) {
       rope_word = pack_bf16(a * t.x - b * t.y, b * t.x + a * t.y);
     } else {  // values 2 l, 2 l + 1 of one half, the same of the other one 16 lanes away
@@ -302,8 +374,8 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, RowIn<kB
     for (int k = 0; k < 16; ++k) sum = fmaf(x.v[k], x.v[k], sum);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    const float mean = sum / kDim + A.eps;
-    float r = 1.f / sqrtf(mean);
+    const float mean = sum * (1.f / kDim) + A.eps;
+    float r = rsqrtf(mean);
     const bool plain = plain_mean(mean);
     if (!kFp4 && !plain) {
       double wide = 0.0;
@@ -316,27 +388,31 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, RowIn<kB
     float y[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) y[k] = x.v[k] * r * w[k];
-    c = encode<kFp4>(y);
-    if constexpr (kFp4) {
-      // the same codes and exponent a little further out and in
+    if constexpr (!kFp4) {
+      c = encode<false>(y);
+    } else {  // the codes and the exponent a little further out, and a little further in
       uint32_t amax = 0;
 #pragma unroll
       for (int k = 0; k < 16; ++k) amax = max(amax, __float_as_uint(y[k]) & 0x7FFFFFFFu);
       amax = max(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-      const float top = __uint_as_float(amax), out = 1.f + kNear, in = 1.f - kNear, up = block_up(c.e);
-      // below 2^-100 products and borders leave fp32's normal range
-      bool near = !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * out)) != c.e || block_exponent(__float_as_uint(top * in)) != c.e;
+      const float top = __uint_as_float(amax), far = 1.f + kNear, close = 1.f - kNear;
+      c.e = block_exponent(__float_as_uint(top * far));
+      c.bad = false;  // what is not finite is not plain, or near
+      const float up = block_up(c.e), up_far = up * far, up_close = up * close;
+      // outside of 2^-100 .. 2^100 products and borders may leave fp32's normal range
+      bool near = !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * close)) != c.e;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         uint32_t a = 0, b = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          a |= e2m1_pair(y[8 * h + 2 * k] * (up * out), y[8 * h + 2 * k + 1] * (up * out)) << (8 * k);
-          b |= e2m1_pair(y[8 * h + 2 * k] * (up * in), y[8 * h + 2 * k + 1] * (up * in)) << (8 * k);
+          a |= e2m1_pair(y[8 * h + 2 * k] * up_far, y[8 * h + 2 * k + 1] * up_far) << (8 * k);
+          b |= e2m1_pair(y[8 * h + 2 * k] * up_close, y[8 * h + 2 * k + 1] * up_close) << (8 * k);
         }
         near |= a != b;
+        c.w[h] = a;
       }
-      if (__any_sync(0xFFFFFFFFu, near)) encode_exact(x.v, w, A.eps, c);
+      if (__any_sync(0xFFFFFFFFu, near)) c = encode_exact<kBf16In>(row, A.weight, A.eps);
     }
   }
   if (__any_sync(0xFFFFFFFFu, c.bad || nonfinite_bf16x2(rope_word))) return CSA_DEV_RANGE;
@@ -345,8 +421,8 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, RowIn<kB
 }
 
 template <bool kBf16In, bool kFp4>
-__global__ void __launch_bounds__(kCopyThreads) append_kernel(const csa_append_args A) {
-  constexpr int kRowsInFlight = kBf16In ? 4 : 2;
+__global__ void __launch_bounds__(kCopyThreads, kFp4 ? 2 : 3) append_kernel(const csa_append_args A) {
+  constexpr int kRowsInFlight = 2;
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32);
   int32_t flags = 0;
@@ -362,6 +438,7 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(const csa_append_a
     per_token[0] = turns_per_token(A.rotation.freq[adjacent ? lane : 2 * lane & 31]);
     if (!adjacent) per_token[1] = turns_per_token(A.rotation.freq[(2 * lane & 31) + 1]);
   }
+  auto row_of = [&](int64_t i) { return static_cast<const uint8_t*>(A.x) + i * A.x_stride * (kBf16In ? 2 : 4); };
   for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; i < A.n; i += kRowsInFlight * warps) {
     int64_t slot[kRowsInFlight];
     int32_t pos[kRowsInFlight];
@@ -371,10 +448,10 @@ __global__ void __launch_bounds__(kCopyThreads) append_kernel(const csa_append_a
       const int64_t r = i + k * warps, at = r < A.n ? r : i;
       slot[k] = r < A.n ? A.slots[r] : -1;
       pos[k] = A.cache.rope_dim != 0 ? A.pos[at] : 0;
-      x[k].load(static_cast<const uint8_t*>(A.x) + at * A.x_stride * (kBf16In ? 2 : 4), lane, A.cache.rope_dim);
+      x[k].load(row_of(at), lane, A.cache.rope_dim);
     }
 #pragma unroll
-    for (int k = 0; k < kRowsInFlight; ++k) flags |= append_row<kBf16In, kFp4>(A, x[k], w, per_token, slot[k], pos[k], lane);
+    for (int k = 0; k < kRowsInFlight; ++k) flags |= append_row<kBf16In, kFp4>(A, x[k], row_of(i + k * warps), w, per_token, slot[k], pos[k], lane);
   }
   if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
 }
@@ -546,10 +623,11 @@ extern "C" csa_status csa_head_norm_rotate(const csa_rotate_args* a, void* strea
   for (const csa_heads* t : {&a->q, &a->k})
     if ((st = check_heads(*t, a->n, rope, f32_in, f32_out)) != CSA_OK) return st;
   if (!aligned(a->pos, 4) || !aligned(a->dev_status, 4)) return CSA_ERR_ALIGNMENT;
-  RotateKernel K = {*a, 0, 0, 0};
+  RotateKernel K = {*a, 1, 32, 32};
   const auto s = static_cast<cudaStream_t>(stream);
-  if (f32_in) return f32_out ? launch_rotate_dim<true, true>(K, s) : launch_rotate_dim<true, false>(K, s);
-  return f32_out ? launch_rotate_dim<false, true>(K, s) : launch_rotate_dim<false, false>(K, s);
+  const bool halves = rope > 0 && a->rotation.pairing == CSA_PAIRS_HALVES;
+  if (f32_in) return halves ? launch_rotate_dim<true, true>(K, s) : launch_rotate_dim<true, false>(K, s);
+  return halves ? launch_rotate_dim<false, true>(K, s) : launch_rotate_dim<false, false>(K, s);
 }
 
 extern "C" csa_status csa_latent_append(const csa_append_args* a, void* stream) {
