@@ -294,54 +294,65 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
 //
 // The cache's writer (a warp a row, its loads ahead of it) with the norm and the rotation between load and store. The codes of
 // a 4-bit record depend on which side of a border a value lies, so the fast result, whose error is known, is encoded
-// twice, a little larger and a little smaller; where the two differ anywhere in the row (about one row in 100) the row is
-// computed again in fp64.
+// twice, a little larger and a little smaller; where the two differ (a value or two of one row in 100) the row's factor
+// and those values are computed again in fp64. (All of the row in fp64 cost 65537 rows 20 us.)
 
 // The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the mean and eps
 // 2 x 2^-24, halved by the root; rsqrtf (two units in the last place) 4 x 2^-24 and two products 2 x 2^-24 more: 18 x 2^-24.
 // 2^-19 is nearly twice that.
 constexpr float kNear = 0x1p-19f;
 
-// Codes and exponent of a lane's values in fp64: the exact norm's, next to a border too. The row is read again, so that its values
-// need not have an address where they are not.
+// The norm's factor in fp64. Rows are read again where they are wanted exactly, so that their values need not have an
+// address where they are not.
 template <bool kBf16In>
-__device__ __noinline__ Coded<true> encode_exact(const void* row, const float* weight, float eps) {
-  const int lane = threadIdx.x & 31;
-  RowIn<kBf16In> in;
-  in.load(row, lane, 0);
-  const float (&x)[16] = in.v;
-  float w[16];
-#pragma unroll
-  for (int k = 0; k < 16; ++k) w[k] = weight ? __ldg(weight + 16 * lane + k) : 1.f;
-  Coded<true> c;
+__device__ __noinline__ double exact_factor(const void* row, float eps) {
+  RowIn<kBf16In> x;
+  x.load(row, threadIdx.x & 31, 0);
   double sum = 0.0;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) sum += static_cast<double>(x[k]) * x[k];
+  for (int k = 0; k < 16; ++k) sum += static_cast<double>(x.v[k]) * x.v[k];
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-  const double r = 1.0 / sqrt(sum / kDim + eps);
+  return 1.0 / sqrt(sum / kDim + eps);
+}
+
+// Value k of the lane's, normed by the factor r.
+template <bool kBf16In>
+__device__ __forceinline__ double exact_value(const void* row, const float* weight, double r, int k) {
+  const int at = 16 * (threadIdx.x & 31) + k;
+  const float x = kBf16In ? __bfloat162float(static_cast<const __nv_bfloat16*>(row)[at]) : static_cast<const float*>(row)[at];
+  return x * r * (weight ? __ldg(weight + at) : 1.f);
+}
+
+// The e2m1 code of y 2^-e: nearest, ties to the even code, saturating at 6.
+__device__ __forceinline__ uint32_t exact_code(double y, int e) {
+  const double t = fabs(y) * __hiloint2double((1023 - e) << 20, 0);
+  const uint32_t m = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
+  return m | (signbit(y) ? 8u : 0u);
+}
+
+// Codes and exponent of a lane's values, all of them in fp64.
+template <bool kBf16In>
+__device__ __noinline__ Coded<true> encode_exact(const void* row, const float* weight, float eps) {
+  const double r = exact_factor<kBf16In>(row, eps);
+  Coded<true> c;
   double amax = 0.0;
-  bool bad = false;
-#pragma unroll
+  c.bad = false;
+#pragma unroll 1
   for (int k = 0; k < 16; ++k) {
-    const double y = fabs(x[k] * r * w[k]);
-    bad |= !(y < 0x1.ffffffp127);  // what rounds to a finite fp32, and no NaN
+    const double y = fabs(exact_value<kBf16In>(row, weight, r, k));
+    c.bad |= !(y < 0x1.ffffffp127);  // what rounds to a finite fp32, and no NaN
     amax = fmax(amax, y);
   }
   amax = fmax(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, 1));
-  c.bad = bad;
   // floor(log2 amax) - 2, held at -127 (a double that is subnormal lies far below)
   c.e = max(static_cast<int>(__double2hiint(amax) >> 20) - 1023 - 2, -127);
-  const double up = __hiloint2double((1023 - c.e) << 20, 0);
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    c.w[h] = 0;
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const double y = x[8 * h + k] * r * w[8 * h + k], t = fabs(y) * up;
-      const uint32_t m = (t > 0.25) + (t >= 0.75) + (t > 1.25) + (t >= 1.75) + (t > 2.5) + (t >= 3.5) + (t > 5.0);
-      c.w[h] |= (m | (signbit(y) ? 8u : 0u)) << (4 * k);
-    }
+  c.w[0] = c.w[1] = 0;
+#pragma unroll 1
+  for (int k = 0; k < 16; ++k) {
+    const uint32_t code = exact_code(exact_value<kBf16In>(row, weight, r, k), c.e) << (4 * (k & 7));
+    if (k < 8) c.w[0] |= code;
+    else c.w[1] |= code;
   }
   return c;
 }
@@ -399,20 +410,32 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, const Ro
       c.e = block_exponent(__float_as_uint(top * far));
       c.bad = false;  // what is not finite is not plain, or near
       const float up = block_up(c.e), up_far = up * far, up_close = up * close;
-      // outside of 2^-100 .. 2^100 products and borders may leave fp32's normal range
-      bool near = !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * close)) != c.e;
+      uint32_t differ[2];
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        uint32_t a = 0, b = 0;
+        uint32_t b = 0;
+        c.w[h] = 0;
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          a |= e2m1_pair(y[8 * h + 2 * k] * up_far, y[8 * h + 2 * k + 1] * up_far) << (8 * k);
+          c.w[h] |= e2m1_pair(y[8 * h + 2 * k] * up_far, y[8 * h + 2 * k + 1] * up_far) << (8 * k);
           b |= e2m1_pair(y[8 * h + 2 * k] * up_close, y[8 * h + 2 * k + 1] * up_close) << (8 * k);
         }
-        near |= a != b;
-        c.w[h] = a;
+        differ[h] = c.w[h] ^ b;
       }
-      if (__any_sync(0xFFFFFFFFu, near)) c = encode_exact<kBf16In>(row, A.weight, A.eps);
+      // outside of 2^-100 .. 2^100 products and borders may leave fp32's normal range; next to a power of two the exponent is open
+      if (__any_sync(0xFFFFFFFFu, !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * close)) != c.e)) {
+        c = encode_exact<kBf16In>(row, A.weight, A.eps);
+      } else if (__any_sync(0xFFFFFFFFu, differ[0] | differ[1])) {
+        const double exact_r = exact_factor<kBf16In>(row, A.eps);
+        while (differ[0] | differ[1]) {  // the values whose code is open
+          const bool second = differ[0] == 0;
+          const int n = (__ffs(second ? differ[1] : differ[0]) - 1) / 4;
+          const uint32_t clear = ~(15u << (4 * n)), code = exact_code(exact_value<kBf16In>(row, A.weight, exact_r, 8 * second + n), c.e) << (4 * n);
+          if (second) c.w[1] = (c.w[1] & clear) | code, differ[1] &= clear;
+          else c.w[0] = (c.w[0] & clear) | code, differ[0] &= clear;
+        }
+        __syncwarp();
+      }
     }
   }
   if (__any_sync(0xFFFFFFFFu, c.bad || nonfinite_bf16x2(rope_word))) return CSA_DEV_RANGE;
@@ -421,8 +444,7 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, const Ro
 }
 
 template <bool kBf16In, bool kFp4>
-__global__ void __launch_bounds__(kCopyThreads, kFp4 ? 2 : 3) append_kernel(const csa_append_args A) {
-  constexpr int kRowsInFlight = 2;
+__global__ void __launch_bounds__(kCopyThreads, 2) append_kernel(const csa_append_args A) {
   const int lane = threadIdx.x & 31;
   const int64_t warps = static_cast<int64_t>(gridDim.x) * (kCopyThreads / 32);
   int32_t flags = 0;
@@ -439,19 +461,23 @@ __global__ void __launch_bounds__(kCopyThreads, kFp4 ? 2 : 3) append_kernel(cons
     if (!adjacent) per_token[1] = turns_per_token(A.rotation.freq[(2 * lane & 31) + 1]);
   }
   auto row_of = [&](int64_t i) { return static_cast<const uint8_t*>(A.x) + i * A.x_stride * (kBf16In ? 2 : 4); };
-  for (int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5; i < A.n; i += kRowsInFlight * warps) {
-    int64_t slot[kRowsInFlight];
-    int32_t pos[kRowsInFlight];
-    RowIn<kBf16In> x[kRowsInFlight];
-#pragma unroll
-    for (int k = 0; k < kRowsInFlight; ++k) {
-      const int64_t r = i + k * warps, at = r < A.n ? r : i;
-      slot[k] = r < A.n ? A.slots[r] : -1;
-      pos[k] = A.cache.rope_dim != 0 ? A.pos[at] : 0;
-      x[k].load(row_of(at), lane, A.cache.rope_dim);
-    }
-#pragma unroll
-    for (int k = 0; k < kRowsInFlight; ++k) flags |= append_row<kBf16In, kFp4>(A, x[k], row_of(i + k * warps), w, per_token, slot[k], pos[k], lane);
+  struct Row {
+    RowIn<kBf16In> x;
+    int64_t slot;
+    int32_t pos;
+  };
+  auto fetch = [&](Row& r, int64_t i) {
+    r.slot = i < A.n ? A.slots[i] : -1;
+    const int64_t at = i < A.n ? i : 0;
+    r.pos = A.cache.rope_dim != 0 ? A.pos[at] : 0;
+    r.x.load(row_of(at), lane, A.cache.rope_dim);
+  };
+  Row now, next;
+  int64_t i = (static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x) >> 5;
+  if (i < A.n) fetch(now, i);
+  for (; i < A.n; i += warps, now = next) {
+    fetch(next, i + warps);  // on its way while this one is normed and stored
+    flags |= append_row<kBf16In, kFp4>(A, now.x, row_of(i), w, per_token, now.slot, now.pos, lane);
   }
   if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
 }
