@@ -236,6 +236,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xFFFFFFFFu, csa::mbar_test(bar, parity)) || __all_sync(0xFFFFFFFFu, csa::mbar_wait(bar, parity, stop));
 }
 
+// The same, with a limit for each 2^18 tiles that others may be busy with meanwhile (they take about half of it).
+__device__ __forceinline__ bool patient_wait(uint32_t bar, uint32_t parity, volatile int* stop, int tiles) {
+  for (int k = tiles >> 18; k > 0 && !*stop; --k) {
+    volatile int over = 0;
+    if (warp_wait(bar, parity, &over)) return true;
+  }
+  return warp_wait(bar, parity, stop);
+}
+
 __device__ __forceinline__ void arrive_at(uint32_t remote) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(remote) : "memory");
 }
@@ -414,16 +423,16 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<false, kRope>& S,
   }
 }
 
-// Q of a run's piece-th piece: row i of this CTA's 64 is row 64 rank + i of the unit. Past the unit's last lie zeros, or rows that
+// Q of a run's piece-th piece (`tiles_before`: how much of the one before may still be to come): row i of this CTA's 64 is row 64 rank + i of the unit. Past the unit's last lie zeros, or rows that
 // nothing comes of. By TMA where all rows lie evenly, else by the threads of the warps that call it.
 template <bool kFp4, int kRope>
-__device__ bool load_query(const Kernel& K, const Maps& M, Smem<kFp4, kRope>& S, const Walk& W, uint32_t piece, uint32_t rank) {
+__device__ bool load_query(const Kernel& K, const Maps& M, Smem<kFp4, kRope>& S, const Walk& W, uint32_t piece, uint32_t rank, int tiles_before) {
   constexpr int kCols = Smem<kFp4, kRope>::kCols;
   const csa_draft_attend_args& A = K.A;
   const int t = threadIdx.x - 32 * Warps<kFp4>::kQuery, lane = t & 31;
   const uint32_t bars = smem_u32(S.bars), full = csa::peer_smem(bars, 0) + 8 * kBarQFull;
   if (K.even && t >= 32) return true;
-  if (!warp_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, &S.abort)) return false;
+  if (!patient_wait(bars + 8 * kBarQEmpty, (piece & 1) ^ 1, &S.abort, tiles_before)) return false;
   if (K.even) {
     if (t == 0) {
       arrive_expect_at(full, sizeof(S.q));
@@ -456,8 +465,9 @@ __device__ bool load_query(const Kernel& K, const Maps& M, Smem<kFp4, kRope>& S,
 template <int kRope>
 __device__ void role_query(const Kernel& K, const Maps& M, Smem<false, kRope>& S, uint32_t rank) {
   uint32_t piece = 0;
-  for (Walk W = S.walk; W.more(); W.next(K.A), ++piece)
-    if (!load_query<false, kRope>(K, M, S, W, piece, rank)) return;
+  int before = 0;  // tiles of the piece before
+  for (Walk W = S.walk; W.more(); before = W.n, W.next(K.A), ++piece)
+    if (!load_query<false, kRope>(K, M, S, W, piece, rank, before)) return;
 }
 
 // 4-bit records, four lanes a record. A slot is 128 values of 64 records, four blocks of 32 each: two blocks a thread (16 code
@@ -548,7 +558,7 @@ __device__ void role_keys_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>&
     Codes x[2];
 #pragma unroll
     for (int c = 0; c < 2; ++c) fetch_codes<kRope>(x[c], now, 4 * c + s, t);
-    ok = load_query<true, kRope>(K, M, S, W, piece, rank);
+    ok = load_query<true, kRope>(K, M, S, W, piece, rank, 0);
     for (int i = 0; ok && i < W.n; ++i) {
       next = view(W.first + i + 1, page);
       page = page_at(W.first + i + 2);
