@@ -31,6 +31,7 @@ constexpr float kGrow = 8.0f;                  // log2 of how far p may exceed 1
 constexpr int kMaxPairs = 80;                  // CTA pairs at most: sizes the workspace
 constexpr int kParts = 4;                      // cut pieces of a run at most, see Walk
 constexpr int kBarRows = 1;                    // named barriers 1, 2: the four warps of rows 0 .. 31, and of 32 .. 63
+constexpr int kBarAll = 3;                     // of all softmax warps
 
 struct Request {
   int32_t row0, drafts, base, total;  // total: records that there are, history and drafts
@@ -169,12 +170,14 @@ struct Smem {
   uint32_t fills[3];                   // by TMA: slots and rope columns that this CTA filled, and Q
   int64_t scan[W::kThreads / 32];
   Walk walk;  // at the run's first piece
+  Walk at;    // at the softmax warps' piece: theirs together, to spare their registers
   uint32_t theirs[4];                  // the other CTA's fills, and whether a wait of its ran out
   uint32_t tmem;
   int abort;
 };
 enum { kBarFull = 0, kBarEmpty = kSlots, kBarRopeFull = 2 * kSlots, kBarRopeEmpty, kBarSFull, kBarSEmpty = kBarSFull + 2,
-       kBarPFull = kBarSEmpty + 2, kBarODone, kBarQFull, kBarQEmpty, kBarOEmpty, kBarLand, kBarDrain, kBars };
+       kBarPFull = kBarSEmpty + 2, kBarODone, kBarQFull, kBarQEmpty, kBarOEmpty, kBarLand, kBarDrain,
+       kBarFirstKeys, kBarLastValues, kBars };
 static_assert(kBars <= 32, "barriers");
 
 // The run of this pair: the requests' tiles are summed by the block.
@@ -531,11 +534,15 @@ __device__ __forceinline__ void fetch_codes(Codes& x, const PageView& P, int blo
   }
 }
 
-// Hands a slot, or the rope column, over.
-__device__ __forceinline__ void handed_over(uint32_t lead_bar) {
+// Hands over four slots, whose barriers begin at `full`, and what else there is a barrier for. All at once: the fence to the
+// tensor cores' proxy holds a warp up longer than the slots' coming one by one gains (4-bit trees: a fence a slot 341 us, for
+// two 317, for four 304).
+__device__ __forceinline__ void handed_over(uint32_t full, uint32_t other) {
   csa::fence_proxy_async_smem();
   __syncwarp();
-  if ((threadIdx.x & 31) == 0) arrive_at(lead_bar);
+  if ((threadIdx.x & 31) != 0) return;
+  for (int k = 0; k < 4; ++k) arrive_at(full + 8 * k);
+  if (other) arrive_at(other);
 }
 
 template <int kRope>
@@ -573,6 +580,7 @@ __device__ void role_keys_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>&
         }
       }
       const uint32_t at = i == 0 ? q : q + 8 * i - 4;
+      if (i == 0 && piece > 0) ok = warp_wait(bars + 8 * kBarLastValues, (piece - 1) & 1, stop);
 #pragma unroll 1
       for (int c0 = 0; c0 < 4; c0 += 2) {
         const PageView from = c0 == 0 ? now : next;
@@ -581,11 +589,11 @@ __device__ void role_keys_fp4(const Kernel& K, const Maps& M, Smem<true, kRope>&
           const uint32_t slot = (at + c0 + c) % kSlots;
           ok = ok && warp_wait(bars + 8 * (kBarEmpty + slot), (at / kSlots & 1) ^ 1, stop);
           if (ok) store_codes(x[c], ring + slot * kSlotBytes, t);
-          if (kRope != 0 && c0 + c == 0) {
-            csa::cp_async_wait_all();
-            if (ok) handed_over(lead_bars + 8 * kBarRopeFull);
+          if (c == 1 && c0 == 2) {
+            if (kRope != 0) csa::cp_async_wait_all();
+            if (ok) handed_over(lead_bars + 8 * (kBarFull + slot - 3), kRope != 0 ? lead_bars + 8 * kBarRopeFull : 0);
+            if (ok && i == 0 && (t & 31) == 0) csa::mbar_arrive(bars + 8 * kBarFirstKeys);
           }
-          if (ok) handed_over(lead_bars + 8 * (kBarFull + slot));
           fetch_codes<kRope>(x[c], from, 4 * (c0 == 0 ? c + 2 : c) + s, t);
         }
       }
@@ -604,8 +612,8 @@ __device__ void role_values_fp4(const Kernel& K, Smem<true, kRope>& S, uint32_t 
   volatile int* stop = &S.abort;
   const uint32_t bars = smem_u32(S.bars), lead_bars = csa::peer_smem(bars, 0), ring = smem_u32(S.ring[0]);
   csa::test_delay();
-  uint32_t q = 0;
-  for (Walk W = S.walk; W.more(); q += 8 * W.n, W.next(A)) {
+  uint32_t q = 0, piece = 0;
+  for (Walk W = S.walk; W.more(); q += 8 * W.n, W.next(A), ++piece) {
     const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
     const Request& R = W.w.R;
     const int32_t past = W.first + W.n;
@@ -620,6 +628,7 @@ __device__ void role_values_fp4(const Kernel& K, Smem<true, kRope>& S, uint32_t 
       fetch(x[0], first, 0);
       fetch(x[1], first, 1);
     }
+    if (!warp_wait(bars + 8 * kBarFirstKeys, piece & 1, stop)) return;
     for (int i = 0; i < W.n; ++i) {
       const uint32_t at = i + 1 < W.n ? q + 8 * i + 8 : q + 8 * W.n - 4;
 #pragma unroll 1
@@ -633,13 +642,15 @@ __device__ void role_values_fp4(const Kernel& K, Smem<true, kRope>& S, uint32_t 
             if (x[b].scale[k] == 255 && (t >> 2) + 32 * k >= drafts) x[b].code[k] = make_uint4(0, 0, 0, 0), x[b].scale[k] = 0;
           if (!warp_wait(bars + 8 * (kBarEmpty + slot), (at / kSlots & 1) ^ 1, stop)) return;
           store_codes(x[b], ring + slot * kSlotBytes, t);
-          handed_over(lead_bars + 8 * (kBarFull + slot));
+          if (b == 1 && h == 1) handed_over(lead_bars + 8 * (kBarFull + slot - 3), 0);
           fetch(x[b], other, b);
         }
         other = view(W.first + i + 1, h, page);
         page = page_at(W.first + i + 1 + h, h ^ 1);
       }
     }
+    if ((t & 31) == 0) csa::mbar_arrive(bars + 8 * kBarLastValues);
+    __syncwarp();
   }
 }
 
@@ -754,19 +765,29 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
   bool ok = true;  // once a wait has run out, the rest runs through without waiting: the warps meet at every barrier
   auto o_done = [&](uint32_t tiles) { return tiles == 0 || warp_wait(bars + 8 * kBarODone, (tiles - 1) & 1, stop); };
   uint32_t ordinal = 0;  // of the run's cut pieces
-  for (Walk W = S.walk; W.more(); W.next(A)) {
+  const Walk& W = S.at;
+  auto step = [&](bool first) {
+    csa::named_bar_sync(kBarAll, 32 * kSoftmaxWarps);
+    if (threadIdx.x == 0) {
+      if (first) S.at = S.walk;
+      else S.at.next(A);
+    }
+    csa::named_bar_sync(kBarAll, 32 * kSoftmaxWarps);
+  };
+  for (step(true); W.more(); step(false)) {
     const Request R = W.w.R;
     const int32_t* table = A.page_table + static_cast<int64_t>(W.request) * A.pt_stride;
     const int64_t flat = W.first_row(A) + kRows * rank + row;
     const bool there = kRows * static_cast<int>(rank) + row < W.rows(A);
     const int32_t j = there ? static_cast<int32_t>(quotient(flat, A.num_heads)) - R.row0 : 0;
     auto page_at = [&](int32_t tile) { return (2 * tile + half) * kPageRecs < R.total ? __ldg(table + 2 * tile + half) : 0; };
-    int32_t page = page_at(W.first);
+    const int32_t first = W.first, n = W.n;
+    int32_t page = page_at(first);
     float m = -INFINITY, l = 0.f;  // l: of this thread's quarter of the keys
-    for (int i = 0; i < W.n; ++i, ++g) {
-      const int32_t p0 = (2 * (W.first + i) + half) * kPageRecs;
+    for (int i = 0; i < n; ++i, ++g) {
+      const int32_t p0 = (2 * (first + i) + half) * kPageRecs;
       const bool good = page >= 0 && page < A.cache.num_pages;
-      if (i + 1 < W.n) page = page_at(W.first + i + 1);
+      if (i + 1 < n) page = page_at(first + i + 1);
       ok = ok && warp_wait(bars + 8 * (kBarSFull + (g & 1)), g >> 1 & 1, stop);
       csa::tc_fence_after();
       float s[kKeys];
@@ -804,13 +825,13 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
           ok = ok && o_done(g);
           csa::tc_fence_after();
 #pragma unroll 1
-          for (int at = 0; at < kValues; at += 32) {
-            uint32_t v[32];
-            csa::tmem_ld32(o_tmem + at, v);
+          for (int at = 0; at < kValues; at += 16) {
+            uint32_t v[16];
+            csa::tmem_ld16(o_tmem + at, v);
             csa::tmem_wait_ld();
 #pragma unroll
-            for (int x = 0; x < 32; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
-            csa::tmem_st32(o_tmem + at, v);
+            for (int x = 0; x < 16; ++x) v[x] = __float_as_uint(__uint_as_float(v[x]) * keep);
+            csa::tmem_st16(o_tmem + at, v);
           }
           csa::tmem_wait_st();
           csa::tc_fence_before();
@@ -915,6 +936,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kFp4>::kThread
     int n = 1;
     if (k < kBarEmpty || k == kBarRopeFull) n = 2 * Warps<kFp4>::kFills;
     else if (k == kBarSEmpty || k == kBarSEmpty + 1 || k == kBarPFull || k == kBarOEmpty) n = 2 * kSoftmaxWarps;
+    else if (k == kBarFirstKeys || k == kBarLastValues) n = 4;
     else if (k == kBarQFull) n = 2 * (K.even ? 1 : Warps<kFp4>::kQueries);
     csa::mbar_init(bars + 8 * k, n);
     csa::mbar_init_fence();

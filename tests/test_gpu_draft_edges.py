@@ -130,6 +130,24 @@ def test_no_lse(draft, latent):  # noqa: F811
     assert torch.equal(out, want)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("base,drafts,heads", [([70000, 900, 1], [4, 2, 1], 64), ([200] * 400, [1] * 400, 128), ([300, 40, 700, 129] * 60, [2, 3, 1, 4] * 60, 64),
+                                               ([5000] * 40, [3] * 40, 64)])
+def test_the_same_bits_again_and_again(draft, latent, base, drafts, heads, fmt):  # noqa: F811
+    """Runs of pieces of one to many tiles, in which the loaders go from one piece to the next while the last one is still being read;
+    by both ways in which the queries come."""
+    c = Case(latent, base, drafts, heads, fmt=fmt, seed=20)
+    out, lse = c.call(draft)
+    c.check(out, lse, words=None, rows=[0]) if len(base) < 10 else None
+    swapped = c.q.transpose(0, 1).contiguous().transpose(0, 1)
+    busy = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    for k in range(25):
+        if k % 5 == 0:
+            busy.fill_(k)  # cold caches: other waits are the long ones
+        again, lse_again = c.call(draft, q=swapped if k % 2 else c.q)
+        assert torch.equal(again, out) and torch.equal(lse_again, lse), k
+
+
 # ------------------------------------------------------------------ graphs, streams, threads
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
