@@ -97,10 +97,11 @@ struct Kernel {
   int32_t even;  // the rows of q (draft and head) are q_head_stride apart throughout
 };
 
-// A cut piece: where its rows begin among all rows (draft and head), and how many there are; 0 where there is no piece.
+// A cut piece: where its rows begin among all rows (draft and head), how many there are (0 where there is no piece), and
+// whether it has the unit's first tile.
 struct Part {
   int64_t first;
-  int32_t rows, reserved;
+  int32_t rows, begins;
 };
 constexpr size_t kPartFloats = 2 * kRows * (static_cast<size_t>(kDim) + 2);  // O, then m c and l of its rows
 
@@ -968,7 +969,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kFp4>::kThread
         Part* parts = K.parts_of + (blockIdx.x >> 1) * kParts;
         int k = 0;
         for (Walk W = S.walk; W.more(); W.next(K.A))
-          if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), 0};
+          if (W.cut) parts[k++] = {W.first_row(K.A), W.rows(K.A), W.first == 0};
         while (k < kParts) parts[k++] = {0, 0, 0};
       }
       __syncwarp();
@@ -1028,31 +1029,33 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
   __shared__ uint16_t list[kParts][kMost];  // of each of the run's parts that a unit begins with: the unit's
   __shared__ int32_t count[kParts];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, row = blockIdx.y * kJoinWarps + warp, all = K.pairs * kParts;
+  const int from = blockIdx.x * kParts;  // the unit's other parts are behind its first
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (int k = tid; k < all; k += 32 * kJoinWarps) parts[k] = K.parts_of[k];
+  bool any = false;
+#pragma unroll
+  for (int k = 0; k < kParts; ++k) any |= K.parts_of[from + k].begins && static_cast<int>(blockIdx.y) * kJoinWarps < K.parts_of[from + k].rows;
+  if (!any) return;
+  for (int k = from + tid; k < all; k += 32 * kJoinWarps) parts[k] = K.parts_of[k];
   __syncthreads();
   if (warp < kParts) {
-    const int mine = blockIdx.x * kParts + warp;
+    const int mine = from + warp;
     const Part P = parts[mine];
     int n = 0;
-    if (static_cast<int>(blockIdx.y) * kJoinWarps < P.rows) {
-      bool before = false;
-      for (int k0 = 0; k0 < all; k0 += 32) {
+    if (P.begins && static_cast<int>(blockIdx.y) * kJoinWarps < P.rows) {
+      for (int k0 = mine; k0 < all; k0 += 32) {
         const int k = k0 + lane;
         const bool is = k < all && parts[k].first == P.first && parts[k].rows > 0;
-        before |= is && k < mine;
         const uint32_t who = __ballot_sync(0xFFFFFFFFu, is);
         if (is) list[warp][n + __popc(who & ((1u << lane) - 1))] = static_cast<uint16_t>(k);
         n += __popc(who);
       }
-      if (__any_sync(0xFFFFFFFFu, before)) n = 0;  // an earlier part's
     }
     if (lane == 0) count[warp] = n;
   }
   __syncthreads();
   for (int i = 0; i < kParts; ++i) {
     const int n = count[i];
-    const Part P = parts[blockIdx.x * kParts + i];
+    const Part P = parts[from + i];
     if (n == 0 || row >= P.rows) continue;
     auto part_of = [&](int k) { return K.parts + static_cast<size_t>(list[i][k]) * kPartFloats; };
     float top = -INFINITY;
