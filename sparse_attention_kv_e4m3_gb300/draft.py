@@ -101,12 +101,14 @@ def _dtype(t: torch.dtype, name: str) -> int:
 
 
 def _rotation(freq, pairing: str, scale: float, dev) -> RotationArgs:
-    if pairing not in PAIRINGS:
+    kind = PAIRINGS.get(pairing)
+    if kind is None:
         raise ValueError(f"pairing: one of {sorted(PAIRINGS)}, not {pairing!r}")
     if freq is None or freq.shape[0] == 0:
-        return RotationArgs(None, 0, PAIRINGS[pairing], float(scale), 0)
-    _same_device(dev, _want(freq, torch.float32, 1, "freq"))
-    return RotationArgs(freq.data_ptr(), 2 * freq.shape[0], PAIRINGS[pairing], float(scale), 0)
+        return RotationArgs(None, 0, kind, float(scale), 0)
+    if _want(freq, torch.float32, 1, "freq").device != dev:
+        raise ValueError(f"freq on {dev}, not on {freq.device}")
+    return RotationArgs(freq.data_ptr(), 2 * freq.shape[0], kind, float(scale), 0)
 
 
 def _weight(w, dim: int, dev, name: str):
@@ -126,15 +128,19 @@ def _ints(t: torch.Tensor, n: int, dev, name: str) -> int:
 def _heads(x: torch.Tensor, weight, norm: bool, out, out_dtype, name: str, stream):
     """One tensor's part of the call: its arguments and its output."""
     _want(x, x.dtype, 3, name)
-    dev, (n, heads, dim) = x.device, x.shape
+    dev, (n, heads, dim), (rows, step, _) = x.device, x.shape, x.stride()
+    width = heads * dim
+    if n == 1 or heads == 1:  # an axis of one element has no stride that matters
+        rows, step = (width if n == 1 else rows), (dim if heads == 1 else step)
     if out is None:
-        out = _new((n, heads, dim), out_dtype, dev, stream)
+        out, out_rows, out_step = _new((n, heads, dim), out_dtype, dev, stream), width, dim
     elif out.shape != x.shape or out.device != dev:
         raise ValueError(f"{name}_out: {tuple(x.shape)} on {dev}, not {tuple(out.shape)} on {out.device}")
     else:
         _want(out, out_dtype, 3, f"{name}_out")
-    return HeadsArgs(x.data_ptr(), out.data_ptr(), _weight(weight, dim, dev, f"{name}_weight"), _step(x, 0, heads * dim), _step(x, 1, dim),
-                     _step(out, 0, heads * dim), _step(out, 1, dim), heads, dim, 1 if norm else 0, 0), out
+        out_rows, out_step = _step(out, 0, width), _step(out, 1, dim)
+    return HeadsArgs(x.data_ptr(), out.data_ptr(), None if weight is None else _weight(weight, dim, dev, f"{name}_weight"), rows, step, out_rows, out_step,
+                     heads, dim, 1 if norm else 0, 0), out
 
 
 def csa_head_norm_rotate(q: torch.Tensor, pos: Optional[torch.Tensor], freq: Optional[torch.Tensor], *, k: Optional[torch.Tensor] = None,
@@ -147,23 +153,22 @@ def csa_head_norm_rotate(q: torch.Tensor, pos: Optional[torch.Tensor], freq: Opt
     freq None: the norm alone. q_out, k_out: the outputs' memory, or q, k themselves (in place).
     Returns (q_out, k_out), k_out None where k is."""
     dev, n = q.device, q.shape[0]
-    given = q_out if q_out is not None else k_out
-    if given is not None:
-        out_dtype = given.dtype
-    kinds = _dtype(q.dtype, "q"), _dtype(out_dtype, "the outputs' type")
+    if q_out is not None or k_out is not None:
+        out_dtype = (k_out if q_out is None else q_out).dtype
+    kind, out_kind = _dtype(q.dtype, "q"), _dtype(out_dtype, "the outputs' type")
     qa, q_out = _heads(q, q_weight, q_norm, q_out, out_dtype, "q", stream)
-    ka = HeadsArgs()
     if k is not None:
-        _same_device(dev, k)
-        if k.dtype != q.dtype or k.shape[0] != n:
-            raise ValueError(f"k: {n} rows of {q.dtype}, as q")
+        if k.dtype != q.dtype or k.shape[0] != n or k.device != dev:
+            raise ValueError(f"k: {n} rows of {q.dtype} on {dev}, as q")
         ka, k_out = _heads(k, k_weight, k_norm, k_out, out_dtype, "k", stream)
     elif k_out is not None:
         raise ValueError("k_out without k")
+    else:
+        ka = HeadsArgs()
     rotation = _rotation(freq, pairing, rope_scale, dev)
     if pos is None and rotation.rope_dim:
         raise ValueError("pos: a position for every row")
-    a = RotateArgs(qa, ka, n, None if pos is None else _ints(pos, n, dev, "pos"), rotation, *kinds, 1 if rope_first else 0, float(eps),
+    a = RotateArgs(qa, ka, n, None if pos is None else _ints(pos, n, dev, "pos"), rotation, kind, out_kind, 1 if rope_first else 0, float(eps),
                    _status(dev_status, dev))
     _done(load().csa_head_norm_rotate(ctypes.byref(a), _stream(stream, dev)), "csa_head_norm_rotate")
     return q_out, k_out
