@@ -12,6 +12,23 @@ namespace {
 
 using csa::smem_u32;
 
+// The kernel. Per query row i (a draft and a head) and record n that its draft sees, with S = q_i . c_n:
+//   p_n = 2^(S_n c - m c), c = scale log2 e,  O = sum p_n c_n[0:512],  l = sum p_n,  out = O / l, lse = ln 2 (m c + log2 l),
+// for any reference m a row (the running maximum, moved only when a tile exceeds it by 2^8).
+//
+// All rows of a request read the same records, so they are taken together, 128 rows (drafts times heads, whatever either is) over
+// tiles of 128 records, by a pair of CTAs. 128 rows of O, 512 values each, would fill one SM's TMEM and leave S no room; the pair
+// has 64 rows each, of S and of O, and the tensor cores of both work on all 128 (cta_group::2, M 128): a CTA's rows lie twice in
+// the 128 lanes, with half of the columns each, so O takes 256 columns and S 64 a tile. As operands a CTA has its 64 rows of Q
+// (72 KB) and of P (16 KB), the keys of one of the tile's two pages (all their values: half of S's columns) and 256 of the values of
+// both (half of O's columns), in a ring of eight slots of 16 KB: keys and values take four each, tile by tile.
+//
+// Shared memory is what bounds long histories: a tile's MMAs read 245 KB of operands at 128 bytes a clock and its copies write
+// 136 KB, 3.0 k clocks, where the tensor cores need 2.18 k (1152 for S, 1024 for O, which they reach with nothing else going on). The
+// values of a CTA's own page come in a second time because both CTAs' operands of an MMA lie at the same place. Two requests of 65536 and more records,
+// 16 drafts, 64 heads: 330 us, 1.34 PFLOP/s (the absorbed form's own kernel, 64 rows high, reaches 0.68). 32 requests of 8192 to
+// 32768, 16 heads, up to 8 drafts, whose records are 783 MB: 172 us, 4.6 TB/s. 4-bit records, 16 requests of 7001 to 16384, up to
+// 13 drafts: 310 us, 0.67 PFLOP/s, bound by the conversion to bf16: 10 k warp instructions a tile, at half of the issue rate.
 constexpr int kTile = 128;                     // records a tile: two pages, one for each CTA's keys
 constexpr int kRows = 64;                      // query rows (draft and head) of a CTA; a unit is the pair's 128
 constexpr int kSlots = 8;                      // of the ring: 64 records x 128 values each, two 8 KB columns of 64 values

@@ -295,7 +295,8 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
 // The cache's writer (a warp a row, its loads ahead of it) with the norm and the rotation between load and store. The codes of
 // a 4-bit record depend on which side of a border a value lies, so the fast result, whose error is known, is encoded
 // twice, a little larger and a little smaller; where the two differ (a value or two of one row in 100) the row's factor
-// and those values are computed again in fp64. (All of the row in fp64 cost 65537 rows 20 us.)
+// and those values are computed again in fp64. (All of the row in fp64 cost 65537 rows 5 us of 82.) 65537 fp32 rows to 4 bits: 50 us where the
+// bytes are 26, bound by 380 instructions a row at 61% of the issue rate; 16381 bf16 rows: 13.6 us, of which the bytes are 5.6.
 
 // The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the mean and eps
 // 2 x 2^-24, halved by the root; rsqrtf (two units in the last place) 4 x 2^-24 and two products 2 x 2^-24 more: 18 x 2^-24.
@@ -498,7 +499,7 @@ csa_status launch_append(const csa_append_args& a, cudaStream_t stream) {
 // layers as it has teams of threads, one a 16-byte column of a record. A column belongs to one thread, which takes the path
 // in order, kMoves loads and then their stores: as path[k] >= k and both ascend, no store falls on a record that a later load
 // wants, and none of the batch's loads is behind its stores. Every block checks the whole path of its request before it
-// moves anything.
+// moves anything. 48 requests, 24 layers (7 MB): 8.7 us, four loads each waiting on the one before.
 
 constexpr int kCommitThreads = 288, kMoves = 8;  // 4 layers of 72 columns, 11 of 25, 16 of 17
 constexpr int kPathBatch = 128;
