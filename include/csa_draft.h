@@ -24,7 +24,9 @@ extern "C" {
 
 #define CSA_ROTATE_MAX_DIM 1024   /* values of a head                                    */
 #define CSA_ROTATE_MAX_ROPE 256   /* rotated values of a head                            */
+#define CSA_ROTATE_MAX_HEADS 65536 /* heads of a tensor                                   */
 #define CSA_DRAFT_MAX_WORDS 16    /* 64-bit words of a draft's mask                      */
+#define CSA_DRAFT_MAX_REQ 65536   /* requests of one csa_draft_attend call               */
 #define CSA_COMMIT_MAX_REQ 16384  /* requests of one csa_draft_commit call               */
 
 #define CSA_PAIRS_ADJACENT 0 /* pairs of values (2 j, 2 j + 1)             */
@@ -53,10 +55,10 @@ typedef struct csa_rotation {
  * computed in fp32 (a head whose squares leave fp32's range in fp64), rounded once. NaN and infinities go
  * through the formula, within their own head. Rows whose position is -1 are left as they are.
  *
- * csa_heads: x [n, heads, dim] and out of the same shape; dim a multiple of 8, rope_dim .. CSA_ROTATE_MAX_DIM; heads 0:
- * none (nothing of it is looked at). The strides are in elements, multiples of 16 bytes; the addresses are on 16
- * bytes. out may be x itself, with the same strides and type (the operation is then in place), but must not overlap
- * it, or the other tensor, in another way. weight [dim] fp32, on 16 bytes, or NULL (all 1).
+ * csa_heads: x [n, heads, dim] and out of the same shape; dim a multiple of 8, rope_dim .. CSA_ROTATE_MAX_DIM; up to
+ * CSA_ROTATE_MAX_HEADS heads, 0: none (nothing of it is looked at). The strides are in elements, multiples of 16
+ * bytes; the addresses are on 16 bytes. out may be x itself, with the same strides and type (the operation is then in
+ * place), but must not overlap it, or the other tensor, in another way. weight [dim] fp32, on 16 bytes, or NULL (all 1).
  * rope_dim: 0, or a multiple of 16 up to CSA_ROTATE_MAX_ROPE.
  * pos [n] int32; NULL only where rope_dim is 0 (every row is there then). Device errors: a position below -1
  * CSA_DEV_LEN_OOB (the row is left as it is).
@@ -122,10 +124,12 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  *   with mask     those i whose bit i % 64 of word i / 64 of its mask is set (drafts past the words are not seen), or
  *   without       those i <= j (a chain).
  * A mask may leave out the draft itself, and all drafts. A row that sees nothing gets out 0 and lse -infinity. What
- * records hold that a row does not see (NaN, infinities) does not matter to it.
+ * records hold that a row does not see (NaN, infinities) does not matter to it; a record that it sees should be finite (one whose
+ * score becomes -infinity has weight 0).
  *
  * q          [num_q, num_heads, 512 + rope_dim] bf16, 16-byte aligned, the strides in elements
  *            and multiples of 8; num_heads 1 .. CSA_LATENT_MAX_HEADS
+ * page_table [num_req, pt_stride] int32; num_req up to CSA_DRAFT_MAX_REQ, 64 pt_stride up to 2^31 - 257
  * base_len   [num_req] int32
  * row_start  [num_req + 1] int32; rows of num_q that no request covers are left as they are
  * mask       [num_q, mask_words] 64-bit words, rows mask_stride words apart, or NULL (then mask_words is 0);
@@ -135,7 +139,8 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  * lse        [num_q, num_heads] fp32, or NULL
  * ws         csa_draft_attend_workspace_bytes(args) bytes, 32-byte aligned
  * Device errors: CSA_DEV_LEN_OOB (base_len below 0 or beyond the table: cut to it; drafts beyond the table are not
- * seen; bounds of rows that descend or leave [0, num_q]: that request's rows are left as they are), CSA_DEV_PAGE_OOB (the page's
+ * seen; bounds of rows that descend or leave [0, num_q]: that request's rows are left as they are, and rows that two requests claim, as only such
+ * bounds can, hold anything), CSA_DEV_PAGE_OOB (the page's
  * records are left out), CSA_DEV_TIMEOUT (an on-chip wait ran past its limit; output invalid).
  */
 typedef struct csa_draft_attend_args {
@@ -173,8 +178,9 @@ csa_status csa_draft_attend(const csa_draft_attend_args* args, void* ws, size_t 
  * freed in the order of the requests: n_freed of them, of which the first `room` are written; the entries of freed
  * behind them become -1. The table itself stays as it is.
  *
- * path [num_req, path_stride] int32 (contiguous: path_stride is its width); base_len, draft_len, path_len, new_len [num_req] int32; freed [room] int32;
- * n_freed [1] int32; num_req 0 .. CSA_COMMIT_MAX_REQ. What the call writes must not overlap what it reads: new_len is not base_len.
+ * path [num_req, path_stride] int32 (contiguous: path_stride is its width); base_len, draft_len, path_len, new_len
+ * [num_req] int32; freed [room] int32; n_freed [1] int32; num_req 0 .. CSA_COMMIT_MAX_REQ. A page with drafts' records is one
+ * entry of one request's table. What the call writes must not overlap what it reads: new_len is not base_len.
  * Device errors: CSA_DEV_LEN_OOB (a length below 0 or beyond the table; path_len above draft_len or the width of
  * path; a path that does not ascend within 0 .. draft_len - 1) and CSA_DEV_PAGE_OOB (a page that is moved from or to, or given
  * back, out of range): such a request is left as it is, new_len = base_len, and none of its pages are listed. CSA_DEV_ROWS:

@@ -444,8 +444,9 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<false, kRope>& S,
   }
 }
 
-// Q of a run's piece-th piece (`tiles_before`: how much of the one before may still be to come): row i of this CTA's 64 is row 64 rank + i of the unit. Past the unit's last lie zeros, or rows that
-// nothing comes of. By TMA where all rows lie evenly, else by the threads of the warps that call it.
+// Q of a run's piece-th piece (`tiles_before`: how much of the one before may still be to come): row i of this CTA's 64 is row
+// 64 rank + i of the unit. Past the unit's last lie zeros, or rows that nothing comes of. By TMA where all rows lie evenly, else by the
+// threads of the warps that call it.
 template <bool kFp4, int kRope>
 __device__ bool load_query(const Kernel& K, const Maps& M, Smem<kFp4, kRope>& S, const Walk& W, uint32_t piece, uint32_t rank, int tiles_before) {
   constexpr int kCols = Smem<kFp4, kRope>::kCols;
@@ -1151,14 +1152,15 @@ csa_status launch(Kernel& K, int dev, cudaStream_t stream) {
 
 csa_status check_args(const csa_draft_attend_args* a) {
   if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->mask_words < 0) return CSA_ERR_INVALID_ARG;
-  if (a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS || a->mask_words > CSA_DRAFT_MAX_WORDS) return CSA_ERR_UNSUPPORTED;
+  if (a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS || a->mask_words > CSA_DRAFT_MAX_WORDS || a->num_req > CSA_DRAFT_MAX_REQ)
+    return CSA_ERR_UNSUPPORTED;
   if (!good_scale(a->scale)) return CSA_ERR_INVALID_ARG;
   if (a->num_q == 0 || a->num_req == 0) return CSA_OK;
   const csa_status st = check_cache(a->cache);
   if (st != CSA_OK) return st;
   const int wide = kDim + a->cache.rope_dim;
   if (!a->q || !a->page_table || !a->base_len || !a->row_start || !a->out || a->pt_stride < 1) return CSA_ERR_INVALID_ARG;
-  if (static_cast<int64_t>(kPageRecs) * a->pt_stride > INT32_MAX) return CSA_ERR_INVALID_ARG;
+  if (static_cast<int64_t>(kPageRecs) * a->pt_stride > INT32_MAX - 2 * kTile) return CSA_ERR_INVALID_ARG;  // a tile's end is an int32 too
   if (a->mask ? (a->mask_words < 1 || (a->num_q > 1 && a->mask_stride < a->mask_words)) : a->mask_words != 0) return CSA_ERR_INVALID_ARG;
   if ((a->num_heads > 1 && a->q_head_stride < wide) || (a->num_q > 1 && a->q_row_stride < wide)) return CSA_ERR_INVALID_ARG;
   if (!aligned(a->q, 16) || a->q_row_stride % 8 != 0 || a->q_head_stride % 8 != 0 || !aligned(a->page_table, 4) || !aligned(a->base_len, 4) ||
@@ -1173,7 +1175,10 @@ csa_status check_args(const csa_draft_attend_args* a) {
 using namespace csa_latent;
 
 extern "C" size_t csa_draft_attend_workspace_bytes(const csa_draft_attend_args* a) {
-  if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS) return 0;
+  if (!a || a->num_q < 0 || a->num_req < 0 || a->pt_stride < 0 || a->num_heads < 1 || a->num_heads > CSA_LATENT_MAX_HEADS ||
+      a->num_req > CSA_DRAFT_MAX_REQ)
+    return 0;
+  if (a->num_q > 0 && a->num_req > 0 && (a->pt_stride < 1 || static_cast<int64_t>(kPageRecs) * a->pt_stride > INT32_MAX - 2 * kTile)) return 0;
   return kPartsOfBytes + kParts * static_cast<size_t>(pairs_cap(a)) * kPartFloats * sizeof(float);
 }
 

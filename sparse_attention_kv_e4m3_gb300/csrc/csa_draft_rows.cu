@@ -277,7 +277,7 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
   if (t.heads < 0) return CSA_ERR_INVALID_ARG;
   if (t.heads == 0) return CSA_OK;
   if (t.reserved0 != 0 || (t.norm != 0 && t.norm != 1)) return CSA_ERR_INVALID_ARG;
-  if (t.dim < 8 || t.dim > CSA_ROTATE_MAX_DIM || t.dim % 8 != 0) return CSA_ERR_UNSUPPORTED;
+  if (t.dim < 8 || t.dim > CSA_ROTATE_MAX_DIM || t.dim % 8 != 0 || t.heads > CSA_ROTATE_MAX_HEADS) return CSA_ERR_UNSUPPORTED;
   if (rope > t.dim || !t.x || !t.out) return CSA_ERR_INVALID_ARG;
   if ((t.heads > 1 && (t.x_head_stride < t.dim || t.out_head_stride < t.dim)) || (n > 1 && (t.x_row_stride < t.dim || t.out_row_stride < t.dim)))
     return CSA_ERR_INVALID_ARG;

@@ -19,7 +19,7 @@ from .latent import (LATENT_DIM, CacheArgs, LatentCache, _done, _pick, _same_dev
                      _workspace, record_bytes)
 from .native import _new
 
-ROTATE_MAX_DIM, ROTATE_MAX_ROPE, MAX_WORDS, COMMIT_MAX_REQ = 1024, 256, 16, 16384
+ROTATE_MAX_DIM, ROTATE_MAX_ROPE, ROTATE_MAX_HEADS, MAX_WORDS, MAX_REQ, COMMIT_MAX_REQ = 1024, 256, 65536, 16, 65536, 16384
 PAIRINGS = {"adjacent": 0, "halves": 1}
 
 _vp, _i32, _i64, _f32 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_float

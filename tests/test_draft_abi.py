@@ -34,7 +34,8 @@ def test_limits_match_header():
     text = open(HEADER).read()
     got = {k: int(v) for k, v in re.findall(r"#define CSA_(\w+) (\d+)", text)}
     assert got["ROTATE_MAX_DIM"] == draft.ROTATE_MAX_DIM and got["ROTATE_MAX_ROPE"] == draft.ROTATE_MAX_ROPE
-    assert got["DRAFT_MAX_WORDS"] == draft.MAX_WORDS and got["COMMIT_MAX_REQ"] == draft.COMMIT_MAX_REQ
+    assert got["ROTATE_MAX_HEADS"] == draft.ROTATE_MAX_HEADS
+    assert got["DRAFT_MAX_WORDS"] == draft.MAX_WORDS and got["DRAFT_MAX_REQ"] == draft.MAX_REQ and got["COMMIT_MAX_REQ"] == draft.COMMIT_MAX_REQ
     assert draft.PAIRINGS == {"adjacent": got["PAIRS_ADJACENT"], "halves": got["PAIRS_HALVES"]}
 
 
@@ -94,7 +95,7 @@ def _rotate(q=None, k=None, rotation=None, **kw):
 
 
 HEADS_REFUSALS = [
-    (dict(heads=-1), INVALID), (dict(dim=0), UNSUPPORTED), (dict(dim=132), UNSUPPORTED), (dict(dim=1032), UNSUPPORTED), (dict(dim=56), INVALID),
+    (dict(heads=-1), INVALID), (dict(heads=65537), UNSUPPORTED), (dict(dim=0), UNSUPPORTED), (dict(dim=132), UNSUPPORTED), (dict(dim=1032), UNSUPPORTED), (dict(dim=56), INVALID),
     (dict(norm=2), INVALID), (dict(reserved0=1), INVALID), (dict(weight=0x30008), ALIGNMENT)]
 
 
@@ -141,10 +142,10 @@ def _attend(cache=None, **kw):
 
 
 @pytest.mark.parametrize("change,want", [(dict(cache=c), w) for c, w in CACHE_REFUSALS] + [
-    (dict(num_heads=0), UNSUPPORTED), (dict(num_heads=129), UNSUPPORTED), (dict(mask_words=17, mask_stride=17), UNSUPPORTED), (dict(q=0), INVALID),
+    (dict(num_heads=0), UNSUPPORTED), (dict(num_heads=129), UNSUPPORTED), (dict(num_req=65537), UNSUPPORTED), (dict(mask_words=17, mask_stride=17), UNSUPPORTED), (dict(q=0), INVALID),
     (dict(q=0x20008), ALIGNMENT), (dict(q_row_stride=16 * 576 + 4), ALIGNMENT), (dict(q_head_stride=575), INVALID), (dict(q_head_stride=580), ALIGNMENT),
     (dict(q_row_stride=568), INVALID), (dict(num_q=-1), INVALID), (dict(num_req=-1), INVALID), (dict(page_table=0), INVALID), (dict(pt_stride=0), INVALID),
-    (dict(pt_stride=1 << 26), INVALID), (dict(base_len=0), INVALID), (dict(base_len=0x40002), ALIGNMENT), (dict(row_start=0), INVALID),
+    (dict(pt_stride=1 << 26), INVALID), (dict(pt_stride=(1 << 25) - 4), INVALID), (dict(base_len=0), INVALID), (dict(base_len=0x40002), ALIGNMENT), (dict(row_start=0), INVALID),
     (dict(row_start=0x50002), ALIGNMENT), (dict(mask=0x60004), ALIGNMENT), (dict(mask_words=0), INVALID), (dict(mask=0), INVALID),
     (dict(mask_words=2, mask_stride=1), INVALID), (dict(mask_words=-1), INVALID), (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID),
     (dict(scale=NAN), INVALID), (dict(scale=2.0 ** 127), INVALID), (dict(out=0), INVALID), (dict(out=0x70008), ALIGNMENT), (dict(lse=0x80002), ALIGNMENT),
@@ -163,7 +164,7 @@ def test_attend_workspace(lib):
     assert n == draft.draft_attend_workspace_bytes(4, 16, 4, 4)
     most = draft.draft_attend_workspace_bytes(1 << 20, 128, 1 << 10, 1 << 20)
     assert n <= most <= 90 << 20
-    for bad in (dict(num_heads=200), dict(num_heads=0), dict(num_q=-1), dict(num_req=-1), dict(pt_stride=-1)):
+    for bad in (dict(num_heads=200), dict(num_heads=0), dict(num_q=-1), dict(num_req=-1), dict(pt_stride=-1), dict(pt_stride=0), dict(pt_stride=1 << 26), dict(num_req=65537)):
         assert lib.csa_draft_attend_workspace_bytes(ctypes.byref(_attend(**bad))) == 0
     assert lib.csa_draft_attend_workspace_bytes(None) == 0
 
