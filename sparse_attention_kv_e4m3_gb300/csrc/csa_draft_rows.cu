@@ -300,8 +300,10 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
 
 // The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the mean and eps
 // 2 x 2^-24, halved by the root; rsqrtf (two units in the last place) 4 x 2^-24 and two products 2 x 2^-24 more: 18 x 2^-24.
-// 2^-19 is nearly twice that.
-constexpr float kNear = 0x1p-19f;
+// 2^-19 is nearly twice that. Where x r is subnormal it is off by 2^-150 instead: with weights up to 2^24 that is 2^-126 of a value, in a
+// block whose smallest border is 2^-104 or more (its largest value is above 2^-100), 2^-22 of it and still within 2^-19. Rows with
+// larger weights are computed in fp64 whole.
+constexpr float kNear = 0x1p-19f, kMostWeight = 0x1p24f;
 
 // The norm's factor in fp64. Rows are read again where they are wanted exactly, so that their values need not have an
 // address where they are not.
@@ -360,7 +362,7 @@ __device__ __noinline__ Coded<true> encode_exact(const void* row, const float* w
 
 template <bool kBf16In, bool kFp4>
 __device__ __forceinline__ int32_t append_row(const csa_append_args& A, const RowIn<kBf16In>& x, const void* row, const float (&w)[16],
-                                              const uint64_t (&per_token)[2], int64_t slot, int32_t pos, int lane) {
+                                              bool large, const uint64_t (&per_token)[2], int64_t slot, int32_t pos, int lane) {
   if (slot == -1) return 0;
   if (slot < 0 || slot >= A.cache.num_pages * kPageRecs) return CSA_DEV_PAGE_OOB;
   const bool rope = A.cache.rope_dim != 0;
@@ -424,7 +426,7 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, const Ro
         differ[h] = c.w[h] ^ b;
       }
       // outside of 2^-100 .. 2^100 products and borders may leave fp32's normal range; next to a power of two the exponent is open
-      if (__any_sync(0xFFFFFFFFu, !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * close)) != c.e)) {
+      if (__any_sync(0xFFFFFFFFu, large || !plain || !(top > 0x1p-100f && top < 0x1p100f) || block_exponent(__float_as_uint(top * close)) != c.e)) {
         c = encode_exact<kBf16In>(row, A.weight, A.eps);
       } else if (__any_sync(0xFFFFFFFFu, differ[0] | differ[1])) {
         const double exact_r = exact_factor<kBf16In>(row, A.eps);
@@ -455,6 +457,10 @@ __global__ void __launch_bounds__(kCopyThreads, 2) append_kernel(const csa_appen
     const float4 v = A.norm && A.weight ? __ldg(reinterpret_cast<const float4*>(A.weight) + 4 * lane + k) : make_float4(1.f, 1.f, 1.f, 1.f);
     w[4 * k] = v.x, w[4 * k + 1] = v.y, w[4 * k + 2] = v.z, w[4 * k + 3] = v.w;
   }
+  bool large = false;  // a weight of the lane's, or NaN
+  if (kFp4)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) large |= !(fabsf(w[k]) <= kMostWeight);
   uint64_t per_token[2] = {0, 0};
   if (A.cache.rope_dim != 0) {
     const bool adjacent = A.rotation.pairing == CSA_PAIRS_ADJACENT;
@@ -478,7 +484,7 @@ __global__ void __launch_bounds__(kCopyThreads, 2) append_kernel(const csa_appen
   if (i < A.n) fetch(now, i);
   for (; i < A.n; i += warps, now = next) {
     fetch(next, i + warps);  // on its way while this one is normed and stored
-    flags |= append_row<kBf16In, kFp4>(A, now.x, row_of(i), w, per_token, now.slot, now.pos, lane);
+    flags |= append_row<kBf16In, kFp4>(A, now.x, row_of(i), w, large, per_token, now.slot, now.pos, lane);
   }
   if (flags && A.dev_status && lane == 0) atomicOr(A.dev_status, flags);
 }

@@ -235,6 +235,21 @@ def test_four_bit_codes_next_to_their_borders(draft, latent):
     assert torch.equal(read_back(cache, slots, "mxfp4", 0), want)
 
 
+@pytest.mark.parametrize("top", [2.0 ** 20, 2.0 ** 40, 2.0 ** 126])
+def test_four_bit_codes_of_subnormal_values_with_large_weights(draft, latent, top):
+    """Values that become fp32's subnormal numbers, with few bits, when they are normed, and that their weights lift again."""
+    n = 256
+    g = gen(8)
+    x = randn(g, n, 512)
+    x[:, 32:] *= 2.0 ** -138
+    w = top * (1 + 0.5 * torch.rand(512, generator=g, device="cuda"))
+    w[:32] = 1
+    cache, slots, bad = latent.LatentCache.empty(n // 64, 0, "mxfp4"), torch.arange(n, device="cuda"), status()
+    draft.csa_latent_append(x, slots, None, cache, None, weight=w, eps=1e-6, dev_status=bad)
+    want, _ = D.appended(x, w, True, 1e-6, None, None, "adjacent", "mxfp4")
+    assert torch.equal(read_back(cache, slots, "mxfp4", 0), want) and int(bad) == 0
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
 @pytest.mark.parametrize("scale", [1e-38, 1e-25, 1e-12, 1e12, 1e25, 3e37])
 def test_append_squares_outside_fp32(draft, latent, scale, fmt):
