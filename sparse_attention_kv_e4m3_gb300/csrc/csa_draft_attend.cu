@@ -321,6 +321,14 @@ struct Maps {  // [page][column of 64 values][record][value]: boxes of a page's 
 
 // ------------------------------------------------------------- roles
 
+// Makes 0 of what is not finite in the 8 values at `addr` of shared memory.
+__device__ __forceinline__ void keep_finite(uint32_t addr) {
+  const uint4 v = csa::ld_shared_v4(addr);
+  if (!(nonfinite_bf16x2(v.x) | nonfinite_bf16x2(v.y) | nonfinite_bf16x2(v.z) | nonfinite_bf16x2(v.w))) return;
+  auto clean = [](uint32_t w) { return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u); };
+  csa::st_shared_v4(addr, clean(v.x), clean(v.y), clean(v.z), clean(v.w));
+}
+
 // The records, through the ring in the order in which the MMAs take them: the keys of tile 0, then keys of tile i + 1
 // and values of tile i. A CTA loads its page's 64 records whole as keys, and its 256 values' columns of both pages.
 // The values of a page with drafts or with an end in it are looked at before they are handed over: rows past the end
@@ -414,14 +422,8 @@ __device__ void role_load(const Kernel& K, const Maps& M, Smem<false, kRope>& S,
             const int row = at / 8 % kPageRecs;
             if (row < drafts) continue;
             const uint32_t addr = slot + 16 * at;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row < rows) {
-              v = csa::ld_shared_v4(addr);
-              if (!(nonfinite_bf16x2(v.x) | nonfinite_bf16x2(v.y) | nonfinite_bf16x2(v.z) | nonfinite_bf16x2(v.w))) continue;
-              auto clean = [](uint32_t w) { return ((w & 0x7F80u) == 0x7F80u ? 0u : w & 0xFFFFu) | ((w & 0x7F800000u) == 0x7F800000u ? 0u : w & 0xFFFF0000u); };
-              v = make_uint4(clean(v.x), clean(v.y), clean(v.z), clean(v.w));
-            }
-            csa::st_shared_v4(addr, v.x, v.y, v.z, v.w);
+            if (row < rows) keep_finite(addr);
+            else csa::st_shared_v4(addr, 0, 0, 0, 0);
           }
         }
         csa::fence_proxy_async_smem();
@@ -522,6 +524,17 @@ __device__ __forceinline__ void store_codes(const Codes& x, uint32_t slot, int t
       const int chunk = 4 * (s & 1) + (swap ? j ^ 2 : j);
       csa::st_shared_v4(row + ((chunk ^ (r & 7)) << 4), v[0], v[1], v[2], v[3]);
     }
+  }
+}
+
+// What a thread has stored of a tile's values (four slots, two of each page), in records `first` and after, without what is not finite: a
+// scale byte of 255 is NaN, and of 253 and 254 (2^126, 2^127; the writers' end at 252) the larger codes are infinite in bf16. Once a
+// tile that has drafts, out of the loop's way (4-bit trees 311 us; with a look at each slot 340, with a test of the codes 370).
+__device__ __noinline__ void keep_finite_codes(uint32_t slots, int first, int t) {
+#pragma unroll 1
+  for (int i = 0; i < 32; ++i) {
+    const int half = i >> 4, r = (t >> 2) + 32 * (i >> 2 & 1), chunk = 4 * (t & 1) + (i & 3);
+    if (kPageRecs * half + r >= first) keep_finite(slots + (i >> 3) * kSlotBytes + (t >> 1 & 1) * kColBytes + r * 128 + ((chunk ^ (r & 7)) << 4));
   }
 }
 
@@ -650,18 +663,18 @@ __device__ void role_values_fp4(const Kernel& K, Smem<true, kRope>& S, uint32_t 
     if (!warp_wait(bars + 8 * kBarFirstKeys, piece & 1, stop)) return;
     for (int i = 0; i < W.n; ++i) {
       const uint32_t at = i + 1 < W.n ? q + 8 * i + 8 : q + 8 * W.n - 4;
+      const int32_t drafts = R.base - (W.first + i) * kTile;  // the tile's first draft
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
-        const int32_t drafts = R.base - (2 * (W.first + i) + h) * kPageRecs;  // the page's first draft
 #pragma unroll
         for (int b = 0; b < 2; ++b) {
           const uint32_t slot = (at + 2 * h + b) % kSlots;
-#pragma unroll
-          for (int k = 0; k < 2; ++k)
-            if (x[b].scale[k] == 255 && (t >> 2) + 32 * k >= drafts) x[b].code[k] = make_uint4(0, 0, 0, 0), x[b].scale[k] = 0;
           if (!warp_wait(bars + 8 * (kBarEmpty + slot), (at / kSlots & 1) ^ 1, stop)) return;
           store_codes(x[b], ring + slot * kSlotBytes, t);
-          if (b == 1 && h == 1) handed_over(lead_bars + 8 * (kBarFull + slot - 3), 0);
+          if (b == 1 && h == 1) {
+            if (drafts < kTile) keep_finite_codes(ring + (slot - 3) * kSlotBytes, drafts, t);
+            handed_over(lead_bars + 8 * (kBarFull + slot - 3), 0);
+          }
           fetch(x[b], other, b);
         }
         other = view(W.first + i + 1, h, page);

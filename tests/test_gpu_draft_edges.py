@@ -55,6 +55,41 @@ def test_bad_4_bit_draft_beside_rows_that_do_not_see_it(draft, latent):  # noqa:
             assert torch.equal(out[j], clean[j]) and torch.equal(lse[j], clean_lse[j]), j
 
 
+@pytest.mark.parametrize("block", [0, 7, 8, 15, slice(0, 16)])
+@pytest.mark.parametrize("base", [60, 61, 70, 125, 130])
+@pytest.mark.parametrize("scale_byte,magnitudes", [(253, (6, 7)), (254, (4, 5, 6, 7)), (254, (0, 4)), (253, (5, 7))])
+def test_4_bit_draft_with_infinite_values_beside_rows_that_do_not_see_it(draft, latent, base, block, scale_byte, magnitudes):  # noqa: F811
+    """Scale bytes 253 and 254 are powers of two, but 4 x 2^126 and 2 x 2^127 are infinite in bf16. Draft 3 is in the first or the second page of a tile."""
+    masks = [0b1, 0b11, 0b111, 0b1000, 0b10111]
+    c = Case(latent, [base], [5], 9, fmt="mxfp4", seed=base)
+    clean, clean_lse = c.call(draft, masks)
+    page, at = int(c.table[0, (base + 3) // 64]), (base + 3) % 64
+    record = c.cache.pages[page][at * 400:(at + 1) * 400]
+    code = torch.tensor([m | s << 3 for m in magnitudes for s in (0, 1)], dtype=torch.uint8, device="cuda")
+    codes = code[torch.arange(32, device="cuda") % len(code)]
+    record[:256].view(16, 16)[block] = codes[::2] | codes[1::2] << 4
+    record[256:272][block] = scale_byte
+    out, lse = c.call(draft, masks)
+    for j, m in enumerate(masks):
+        if not m >> 3 & 1:
+            assert torch.equal(out[j], clean[j]) and torch.equal(lse[j], clean_lse[j]), j
+
+
+@pytest.mark.parametrize("base", [60, 70])
+@pytest.mark.parametrize("scale_byte,magnitude", [(252, 7), (253, 4), (253, 5), (254, 1), (254, 3)])
+def test_largest_finite_4_bit_values_of_a_draft(draft, latent, base, scale_byte, magnitude):  # noqa: F811
+    """Finite values stay beside infinite ones of their block, for the rows that see them; the queries have nothing there, so that scores stay."""
+    masks = [0b1, 0b11, 0b111, 0b1000, 0b11111]
+    c = Case(latent, [base], [5], 9, fmt="mxfp4", seed=base)
+    c.q[..., 224:256] = 0
+    at = int(c.table[0, (base + 3) // 64]) * 64 + (base + 3) % 64
+    c.records[at, 112:128], c.records[at, 256 + 7] = 0, scale_byte
+    c.records[at, 115] = magnitude | (magnitude | 8) << 4
+    c.cache.pages.copy_(c.records.reshape(c.cache.pages.shape))
+    out, lse = c.call(draft, masks)
+    c.check(out, lse, masks)
+
+
 def test_queries_that_are_not_finite_stay_in_their_row(draft, latent):  # noqa: F811
     c = Case(latent, [300], [5], 30, seed=4)
     clean, clean_lse = c.call(draft)
