@@ -46,6 +46,13 @@ struct Eight {  // eight values as they lie in memory
       w[0] = make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
     }
   }
+  __device__ __forceinline__ void times(float f) {
+    float v[8];
+    get(v);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] *= f;
+    put(v);
+  }
   __device__ __forceinline__ void store(void* p) const {
 #pragma unroll
     for (int k = 0; k < (kF32 ? 2 : 1); ++k) reinterpret_cast<uint4*>(p)[k] = w[k];
@@ -122,7 +129,18 @@ __device__ __forceinline__ void rotate_heads(const csa_rotate_args& A, const csa
           for (int j = 0; j < 8; ++j) wide += static_cast<double>(v[j]) * v[j];
         }
         for (int o = G / 2; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
-        if (!plain_mean(mean)) r = static_cast<float>(1.0 / sqrt(wide / T.dim + A.eps));
+        if (!plain_mean(mean)) {
+          // The factor may leave fp32's normal numbers where the normed values do not: these take a power of two of it first, which is exact
+          // (upwards always; downwards but for values that the factor makes 0).
+          const double all = 1.0 / sqrt(wide / T.dim + A.eps);
+          const float first = all > 0x1p100 ? 0x1p64f : (all < 0x1p-126 ? 0x1p-8f : 1.f);
+          r = static_cast<float>(all / first);
+#pragma unroll
+          for (int k = 0; k < kPieces; ++k) {
+            x[k].times(first);
+            if (kHalves) other[k].times(first);
+          }
+        }
       }
     }
     __syncwarp();  // in place: all of a head is read before any of it is written

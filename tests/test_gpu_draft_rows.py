@@ -149,6 +149,25 @@ def test_squares_outside_fp32(draft, dim, scale):
         near(got, D.norm_rotate(x, None, True, eps, None, None, "adjacent", half=D.F32))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("scale", [1e-39, 3e-40, 2.0 ** -126, 2.0 ** -120, 1e-34, 2.0 ** 125, 3e38])
+def test_factors_outside_fp32(draft, scale, pairing, dtype):
+    """Heads of subnormal values, whose factor is above fp32's largest number, and of the largest, whose factor is subnormal. The values are
+    rounded to the input's type before the 64-bit form sees them. One head has a single value that is not 0, the smallest of all."""
+    g = gen(12)
+    x = randn(g, 10, 3, 128)
+    x = ((torch.sign(x) if scale > 1e38 else x.clamp(-7, 7)) * scale).to(dtype)
+    x[:, 1] = 0
+    x[:, 1, 100] = 2.0 ** (-149 if dtype == torch.float32 else -133)
+    assert x.double().isfinite().all() and (x[:, 0] != 0).any(-1).all()
+    pos, freq, w = positions(g, 10, 1 << 17), D.freqs(64, device="cuda"), 1 + 0.2 * randn(g, 128)
+    got, _ = draft.csa_head_norm_rotate(x, pos, freq, q_weight=w, eps=0.0, pairing=pairing, out_dtype=torch.float32)
+    near(got, D.norm_rotate(x, w, True, 0.0, pos, freq, pairing, half=D.F32))
+    in_place, _ = draft.csa_head_norm_rotate(x, pos, freq, q_weight=w, eps=0.0, pairing=pairing, q_out=x)
+    assert in_place is x and torch.equal(x, got.to(dtype))
+
+
 def test_not_finite_and_zero_heads(draft):
     """A NaN stays in its head; an infinity makes its head's others 0; zeros are 0 with an eps and NaN without."""
     x = torch.ones(4, 3, 128, device="cuda")
