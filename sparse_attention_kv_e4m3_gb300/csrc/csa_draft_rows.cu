@@ -130,15 +130,12 @@ __device__ __forceinline__ void rotate_heads(const csa_rotate_args& A, const csa
         }
         for (int o = G / 2; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
         if (!plain_mean(mean)) {
-          // The factor may leave fp32's normal numbers where the normed values do not: these take a power of two of it first, which is exact
-          // (upwards always; downwards but for values that the factor makes 0).
-          const double all = 1.0 / sqrt(wide / T.dim + A.eps);
-          const float first = all > 0x1p100 ? 0x1p64f : (all < 0x1p-126 ? 0x1p-8f : 1.f);
-          r = static_cast<float>(all / first);
+          const Factor f = factor_of(1.0 / sqrt(wide / T.dim + A.eps));
+          r = f.rest;
 #pragma unroll
           for (int k = 0; k < kPieces; ++k) {
-            x[k].times(first);
-            if (kHalves) other[k].times(first);
+            x[k].times(f.first);
+            if (kHalves) other[k].times(f.first);
           }
         }
       }
@@ -409,17 +406,22 @@ __device__ __forceinline__ int32_t append_row(const csa_append_args& A, const Ro
     const float mean = sum * (1.f / kDim) + A.eps;
     float r = rsqrtf(mean);
     const bool plain = plain_mean(mean);
+    float y[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y[k] = x.v[k];
     if (!kFp4 && !plain) {
       double wide = 0.0;
 #pragma unroll
       for (int k = 0; k < 16; ++k) wide += static_cast<double>(x.v[k]) * x.v[k];
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) wide += __shfl_xor_sync(0xFFFFFFFFu, wide, o);
-      r = static_cast<float>(1.0 / sqrt(wide / kDim + A.eps));
-    }
-    float y[16];
+      const Factor f = factor_of(1.0 / sqrt(wide / kDim + A.eps));
+      r = f.rest;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) y[k] = x.v[k] * r * w[k];
+      for (int k = 0; k < 16; ++k) y[k] *= f.first;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) y[k] = y[k] * r * w[k];
     if constexpr (!kFp4) {
       c = encode<false>(y);
     } else {  // the codes and the exponent a little further out, and a little further in

@@ -33,6 +33,17 @@ __device__ __forceinline__ float2 cos_sin(uint64_t per_token, int32_t pos, float
 // not, the sum is taken again in fp64, which holds the square of any fp32 value.
 __device__ __forceinline__ bool plain_mean(float mean_eps) { return mean_eps > 1e-30f && mean_eps < 1e36f; }
 
+// A norm's factor in two steps. It may leave fp32's normal numbers where the normed values do not: these take a power of two of it first, which
+// is exact (upwards always; downwards but for values that the factor makes 0).
+struct Factor {
+  float first, rest;
+};
+
+__device__ __forceinline__ Factor factor_of(double all) {
+  const float first = all > 0x1p100 ? 0x1p64f : (all < 0x1p-126 ? 0x1p-8f : 1.f);
+  return {first, static_cast<float>(all / first)};
+}
+
 inline bool good_eps(float eps) { return eps >= 0.f && eps < INFINITY; }
 
 inline csa_status check_rotation(const csa_rotation& r) {

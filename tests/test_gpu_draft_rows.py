@@ -280,6 +280,23 @@ def test_append_squares_outside_fp32(draft, latent, scale, fmt):
         near(read_back(cache, slots, fmt, 0), D.appended(x, None, True, eps, None, None, "adjacent", fmt))
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("scale", [1e-39, 3e-40, 2.0 ** -126, 2.0 ** -120, 1e-34, 2.0 ** 125, 3e38])
+def test_append_factors_outside_fp32(draft, latent, scale, fmt, dtype):
+    """Rows of subnormal values without an eps, and of the largest; a row with a single value, the smallest of all."""
+    g = gen(13)
+    x = randn(g, 70, 512)
+    x = ((torch.sign(x) if scale > 1e38 else x.clamp(-7, 7)) * scale).to(dtype)
+    x[7] = 0
+    x[7, 300] = 2.0 ** (-149 if dtype == torch.float32 else -133)
+    slots, cache, bad, w = torch.arange(70, device="cuda"), latent.LatentCache.empty(2, 0, fmt), status(), 1 + 0.2 * randn(g, 512)
+    cache.pages.fill_(0x77)
+    draft.csa_latent_append(x, slots, None, cache, None, weight=w, eps=0.0, dev_status=bad)
+    near(read_back(cache, slots, fmt, 0), D.appended(x, w, True, 0.0, None, None, "adjacent", fmt))
+    assert int(bad) == 0
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
 def test_append_bad_rows_are_left_out(draft, latent, fmt):
     g = gen(6)
