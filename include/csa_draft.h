@@ -52,7 +52,8 @@ typedef struct csa_rotation {
  * Norm and rotation of every head's values, of queries and of keys in one pass:
  *   y_i = x_i / sqrt(mean(x^2) + eps) * weight_i   (where norm is 1, else y = x)
  *   out = y, its last rope_dim values (its first ones with rope_first) rotated to the row's position
- * computed in fp32 (a head whose squares leave fp32's range in fp64), rounded once. NaN and infinities go
+ * computed in fp32 (the squares of a head in fp64 where they leave fp32's range), rounded once; where x_i / sqrt(..)
+ * is below 2^-126 it is held to 2^-150, as fp32's subnormal numbers are, before its weight. NaN and infinities go
  * through the formula, within their own head. Rows whose position is -1 are left as they are.
  *
  * csa_heads: x [n, heads, dim] and out of the same shape; dim a multiple of 8, rope_dim .. CSA_ROTATE_MAX_DIM; up to
@@ -92,7 +93,7 @@ csa_status csa_head_norm_rotate(const csa_rotate_args* args, void* stream);
 /*
  * csa_latent_write with the norm and the rotation on the way: row i of x [n, 512 + rope_dim] becomes the
  * record at slot slots[i] (-1 skips the row), its 512 latent values normed as above (where norm is 1), its rope
- * values rotated to position pos[i], both rounded to the record's format from the unrounded result. In MXFP4 the
+ * values rotated to position pos[i], both rounded to the record's format from the result in fp32. In MXFP4 the
  * codes and scales are those of the exact norm: a value next to a border between two codes is decided in fp64.
  * Rows must target distinct records. Device errors (that row is not written): a slot outside the cache
  * CSA_DEV_PAGE_OOB; a position below 0 CSA_DEV_LEN_OOB; a result that is not finite CSA_DEV_RANGE.

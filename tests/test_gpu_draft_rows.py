@@ -168,6 +168,27 @@ def test_factors_outside_fp32(draft, scale, pairing, dtype):
     assert in_place is x and torch.equal(x, got.to(dtype))
 
 
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+@pytest.mark.parametrize("top", [2.0 ** 20, 2.0 ** 40, 2.0 ** 126])
+def test_subnormal_values_with_large_weights(draft, latent, top, pairing):
+    """Values that become fp32's subnormal numbers when they are normed, and that their weights lift again: 2^-150 of each is lost, times its
+    weight (below 1.5 top); a rotated value is made of two. In the heads and in records of bf16."""
+    g = gen(14)
+    x, pos, freq = randn(g, 128, 576), positions(g, 128, 1 << 17), D.freqs(64, device="cuda")
+    x[:, 32:512] *= 2.0 ** -138
+    w = top * (1 + 0.5 * torch.rand(512, generator=g, device="cuda"))
+    w[:32] = 1
+    lost = 2 * 2.0 ** -150 * 1.5 * top
+    got, _ = draft.csa_head_norm_rotate(x[:, None, :512], pos, freq, q_weight=w, eps=1e-6, pairing=pairing, out_dtype=torch.float32)
+    y, tol = D.norm_rotate(x[:, None, :512], w, True, 1e-6, pos, freq, pairing, half=D.F32)
+    near(got, (y, tol + lost))
+    cache, slots, bad = latent.LatentCache.empty(2, 64, "bf16"), torch.arange(128, device="cuda"), status()
+    draft.csa_latent_append(x, slots, pos, cache, freq, weight=w, eps=1e-6, pairing=pairing, dev_status=bad)
+    y, tol = D.appended(x, w, True, 1e-6, pos, freq, pairing, "bf16")
+    near(read_back(cache, slots, "bf16", 64), (y, tol + lost * (1 + L.BF16_HALF)))
+    assert int(bad) == 0
+
+
 def test_not_finite_and_zero_heads(draft):
     """A NaN stays in its head; an infinity makes its head's others 0; zeros are 0 with an eps and NaN without."""
     x = torch.ones(4, 3, 128, device="cuda")
