@@ -1012,9 +1012,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kFp4>::kThread
     } else if (warp == kLoadWarp) role_load<kRope>(K, M, S, rank, &flags);
     else role_query<kRope>(K, M, S, rank);
   }
-  if (warp == kMmaWarp && rank == 1) csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);  // the last commit has told this CTA too
   csa::tc_fence_before();
   __syncthreads();
+  // The last commit has told this CTA too. Behind the block's barrier, because the wait has a limit and this warp nothing else to do: from the
+  // start of a run it would end before runs of more than a second do.
+  if (warp == kMmaWarp && rank == 1) csa::mbar_wait_drain(bars + 8 * kBarDrain, 0);
+  __syncwarp();
   if (threadIdx.x < 4) st_peer_u32(csa::peer_smem(smem_u32(&S.theirs[threadIdx.x]), rank ^ 1), threadIdx.x < 3 ? S.fills[threadIdx.x] : static_cast<uint32_t>(S.abort));
   csa::cluster_arrive();
   csa::cluster_wait();

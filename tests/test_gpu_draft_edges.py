@@ -183,6 +183,30 @@ def test_the_same_bits_again_and_again(draft, latent, base, drafts, heads, fmt):
         assert torch.equal(again, out) and torch.equal(lse_again, lse), k
 
 
+def test_a_call_of_more_than_a_second(draft, latent):  # noqa: F811
+    """The waits' limit is a second: none may begin with a run and end with it. A history of 500000 records, whose pages are 40 in turn, and
+    16384 drafts of 128 heads: 2.3 x 10^15 operations."""
+    n, heads, base, distinct = 16384, 128, 500000, 40
+    c = Case(latent, [distinct * 64 - 64], [64], 1, seed=21)
+    pages = c.table[0, :distinct]
+    table = pages.repeat((base + n + 63) // 64 // distinct + 1)[None, :(base + n + 63) // 64].contiguous()
+    g = torch.Generator(device="cuda").manual_seed(22)
+    q = torch.empty(n, heads, 576, dtype=torch.bfloat16, device="cuda").normal_(generator=g)
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    begin.record()
+    out, lse = draft.csa_draft_attend(q, c.cache, table, c.ints([base]), c.ints([0, n]), scale=1.0, dev_status=bad)
+    end.record()
+    torch.cuda.synchronize()
+    assert int(bad) == 0 and begin.elapsed_time(end) > 1000
+    pos = torch.arange(base + n, device="cuda")
+    values = L.values(c.records[table[0].long()[pos // 64] * 64 + pos % 64], "bf16", 64)
+    for j in (0, 1, 8191, n - 1):
+        k = values[:base + j + 1]
+        for h in (0, 127):
+            L.hold(out[j, h:h + 1], lse[j, h:h + 1], L.softmax_out(q[j, h:h + 1].double(), k, k[:, :512], 1.0, 576))
+
+
 # ------------------------------------------------------------------ graphs, streams, threads
 
 @pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
