@@ -135,8 +135,9 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  * row_start  [num_req + 1] int32; rows of num_q that no request covers are left as they are
  * mask       [num_q, mask_words] 64-bit words, rows mask_stride words apart, or NULL (then mask_words is 0);
  *            mask_words up to CSA_DRAFT_MAX_WORDS
- * scale      above 0, below 2^127
- * out        [num_q, num_heads, 512] bf16, contiguous, 16-byte aligned
+ * scale      above 0, below 2^127; q . c has to stay below 2^127 in magnitude, whatever the scale
+ * out        [num_q, num_heads, 512] bf16, contiguous, 16-byte aligned. The softmax is fp32's; its weights are rounded to bf16 where
+ *            they meet the values (the tensor cores' operand type), their sum is not.
  * lse        [num_q, num_heads] fp32, or NULL
  * ws         csa_draft_attend_workspace_bytes(args) bytes, 32-byte aligned
  * Device errors: CSA_DEV_LEN_OOB (base_len below 0 or beyond the table: cut to it; drafts beyond the table are not

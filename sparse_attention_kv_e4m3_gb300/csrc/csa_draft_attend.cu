@@ -13,8 +13,9 @@ namespace {
 using csa::smem_u32;
 
 // The kernel. Per query row i (a draft and a head) and record n that its draft sees, with S = q_i . c_n:
-//   p_n = 2^(S_n c - m c), c = scale log2 e,  O = sum p_n c_n[0:512],  l = sum p_n,  out = O / l, lse = ln 2 (m c + log2 l),
-// for any reference m a row (the running maximum, moved only when a tile exceeds it by 2^8).
+//   p_n = 2^((S_n - m) c), c = scale log2 e,  O = sum p_n c_n[0:512],  l = sum p_n,  out = O / l, lse = scale m + ln l,
+// for any reference m a row (the running maximum, moved only when a tile exceeds it by 2^8). The difference comes before the product with c:
+// S c - m c is off by a rounding of m c, which from scores of 2^31 on is more than fp32's exponents hold.
 //
 // All rows of a request read the same records, so they are taken together, 128 rows (drafts times heads, whatever either is) over
 // tiles of 128 records, by a pair of CTAs. 128 rows of O, 512 values each, would fill one SM's TMEM and leave S no room; the pair
@@ -120,7 +121,7 @@ struct Part {
   int64_t first;
   int32_t rows, begins;
 };
-constexpr size_t kPartFloats = 2 * kRows * (static_cast<size_t>(kDim) + 2);  // O, then m c and l of its rows
+constexpr size_t kPartFloats = 2 * kRows * (static_cast<size_t>(kDim) + 2);  // O, then m and l of its rows
 
 // Walks a run piece by piece. A segment has at least 3/4 of a run's tiles (segments = tiles / run rounded, 2 at least), so a run
 // meets at most two whole ones, or one and the ends of two others: kParts are enough for its cut pieces. (A unit of a
@@ -870,12 +871,15 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
         }
       }
       // p is rounded to bf16 here, the tensor cores' operand type; l sums it unrounded
-      const float mc = m == -INFINITY ? 0.f : m * c;
+      const float ref = m == -INFINITY ? 0.f : m;
+      const csa::F2 minus_ref(-ref, -ref), c2(c, c), zero;
       uint32_t w[kKeys / 2];
       float sum[2] = {0.f, 0.f};
 #pragma unroll
       for (int x = 0; x < kKeys / 2; ++x) {
-        const float a = csa::ex2(fmaf(s[2 * x], c, -mc)), b = csa::ex2(fmaf(s[2 * x + 1], c, -mc));
+        float a, b;
+        csa::fma2(csa::add2(csa::F2(s[2 * x], s[2 * x + 1]), minus_ref), c2, zero).get(a, b);
+        a = csa::ex2(a), b = csa::ex2(b);
         sum[x & 1] += a + b;
         w[x] = pack_bf16(a, b);
       }
@@ -896,7 +900,6 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
     csa::named_bar_sync(row_bar, kRowThreads);
     ok = ok && o_done(g);
     csa::tc_fence_after();
-    const float mc = m == -INFINITY ? -INFINITY : m * c;
     // 64 bytes of each of the warp's 32 rows at a time go through its 2 KB of P (which is not in use between a piece's last
     // O and the next one's first P) and out in runs of them.
     const int rows_here = W.rows(A) - kRows * static_cast<int>(rank) - 32 * (warp & 1);  // of the warp's, that there are
@@ -918,7 +921,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
     const int first_value = 256 * half + kValues * part;
     if (!W.cut) {
       const float inv = l > 0.f ? 1.f / l : l;  // 0 for an empty row; a NaN stays one
-      if (there && mine == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : (mc + log2f(l)) * 0.6931471805599453f;
+      if (there && mine == 0 && A.lse) A.lse[flat] = l == 0.f ? -INFINITY : fmaf(m, A.scale, log2f(l) * 0.6931471805599453f);
       uint8_t* out = static_cast<uint8_t*>(A.out) + 2 * ((W.first_row(A) + kRows * rank + 32 * (warp & 1)) * kDim + first_value);
       uint32_t v[32];
       csa::tmem_ld32(o_tmem, v);
@@ -936,7 +939,7 @@ __device__ void role_softmax(const Kernel& K, Smem<kFp4, kRope>& S, uint32_t ran
       float* part_out = K.parts + (static_cast<size_t>(blockIdx.x >> 1) * kParts + ordinal) * kPartFloats;
       const int at_row = kRows * rank + row;
       if (mine == 0) {
-        part_out[2 * kRows * kDim + at_row] = mc;
+        part_out[2 * kRows * kDim + at_row] = m;
         part_out[2 * kRows * (kDim + 1) + at_row] = l;
       }
       uint8_t* to = reinterpret_cast<uint8_t*>(part_out + static_cast<size_t>(kRows * rank + 32 * (warp & 1)) * kDim + first_value);
@@ -1096,7 +1099,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
     for (int k = lane; k < n; k += 32) top = fmaxf(top, part_of(k)[2 * kRows * kDim + row]);
 #pragma unroll
     for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-    const float ref = top == -INFINITY ? 0.f : top;
+    const float ref = top == -INFINITY ? 0.f : top, exponent = A.scale * 1.4426950408889634f;
     float l = 0.f;
     float4 v[4] = {};
     auto add = [&](auto step, int k) {
@@ -1113,7 +1116,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
       }
 #pragma unroll
       for (int j = 0; j < kStep; ++j) {
-        const float f = weight(w[j] - ref);
+        const float f = weight((w[j] - ref) * exponent);
         l = fmaf(s[j], f, l);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -1127,7 +1130,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) join_kernel(const Kernel K) {
     uint2* out = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(A.out) + (P.first + row) * kDim);
 #pragma unroll
     for (int c = 0; c < 4; ++c) out[lane + 32 * c] = make_uint2(pack_bf16(v[c].x * inv, v[c].y * inv), pack_bf16(v[c].z * inv, v[c].w * inv));
-    if (A.lse && lane == 0) A.lse[P.first + row] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+    if (A.lse && lane == 0) A.lse[P.first + row] = l == 0.f ? -INFINITY : fmaf(top, A.scale, log2f(l) * 0.6931471805599453f);
   }
 }
 

@@ -291,3 +291,59 @@ def test_offsets_past_32_bits(draft, latent):
     cache = latent.LatentCache(pool, 64, "bf16")
     out, lse = draft.csa_draft_attend(c.q, cache, t, c.ints([300]), c.ints([0, 4]), scale=c.scale)
     c.check(out, lse, words=None)
+
+
+def test_bounds_that_descend_beside_rows_of_their_own(draft, latent):
+    """Request 0's bounds descend: it writes nothing. Rows 0 and 1 belong to nobody; request 1 has rows 2 to 7."""
+    c = Case(latent, [64, 200], [4, 6], 6, seed=12)
+    c.q = c.q[:8].contiguous()
+    out, lse, bad = torch.full((8, 6, 512), 7.0, dtype=torch.bfloat16, device="cuda"), torch.full((8, 6), 7.0, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    draft.csa_draft_attend(c.q, c.cache, c.table, c.ints(c.base), c.ints([4, 2, 8]), scale=c.scale, out=out, lse=lse, dev_status=bad)
+    assert int(bad) == 32 and (out[:2] == 7).all() and (lse[:2] == 7).all()
+    values = c.values(1)
+    for j in range(6):
+        L.hold(out[2 + j], lse[2 + j], D.attend_row(c.q[2 + j], values, 200, range(j + 1), c.scale, 64))
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+def test_scores_of_the_largest_range(draft, latent, fmt):
+    """Scores q . c up to 2^125 in magnitude, both signs in a row: the softmax of a tiny scale, and with scale 1 the one record of the largest."""
+    c = Case(latent, [300], [4], 5, fmt=fmt, seed=13)
+    c.q[:] = 0
+    c.q[..., 3] = 2.0 ** 123
+    c.scale = 2.0 ** -124
+    out, lse = c.call(draft)
+    c.check(out, lse, words=None)
+    v = c.values(0)[:, 3]
+    if fmt == "bf16":  # 4-bit values tie
+        c.scale = 1.0
+        out, lse = c.call(draft)
+        for j in range(4):
+            best = int(v[:301 + j].argmax())
+            second = float(v[:301 + j].sort(descending=True).values[1])
+            if second < float(v[best]):
+                assert torch.equal(out[j].double(), c.values(0)[best, :512].expand(5, 512))
+                assert torch.allclose(lse[j].double(), v[best] * 2.0 ** 123, rtol=2 ** -20)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("base", [300, 30000])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("logit", [2.0 ** 27, 2.0 ** 30, 2.0 ** 33, 2.0 ** 36, 2.0 ** 60, 2.0 ** 126])
+def test_scores_above_what_an_exponent_holds(draft, latent, logit, sign, base, fmt):
+    """Scaled scores of 2^27 and more, which a tile's products with scale log2 e round by more than a softmax bears, also in requests whose parts
+    are joined. The next score is 2^-8 of them less at least: the weights are 1 or 0, equal for the records of the largest."""
+    c = Case(latent, [base], [3], 5, fmt=fmt, seed=14)
+    c.q[:] = 0
+    c.q[..., 3] = sign * 2.0 ** 100
+    c.scale = logit * 2.0 ** -103  # values are below 2^3
+    out, lse = c.call(draft)
+    values = c.values(0)
+    assert float(values[:, 3].abs().max()) < 8
+    for j in range(3):
+        seen = values[:base + j + 1]
+        score = sign * seen[:, 3]
+        best = seen[score == score.max(), :512]
+        assert ((out[j].double() - best.mean(0)).abs() <= 2.1 * L.BF16_HALF * best.abs().mean(0) + 1e-30).all(), j
+        want = float(score.max()) * 2.0 ** 100 * c.scale
+        assert (lse[j].double() - want).abs().max() <= 2 ** -22 * abs(want)

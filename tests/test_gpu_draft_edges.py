@@ -183,6 +183,21 @@ def test_the_same_bits_again_and_again(draft, latent, base, drafts, heads, fmt):
         assert torch.equal(again, out) and torch.equal(lse_again, lse), k
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("base,drafts,heads", [([200] * 400, [1] * 400, 128), ([300, 40, 700, 129] * 60, [2, 3, 1, 4] * 60, 64), ([5000] * 40, [3] * 40, 64)])
+def test_runs_of_several_pieces_against_the_64_bit_form(draft, latent, base, drafts, heads, fmt):  # noqa: F811
+    """The shapes above whose runs go through several pieces: the first and last requests and a sample, each draft of them, by both ways of the queries."""
+    c = Case(latent, base, drafts, heads, fmt=fmt, seed=23)
+    rows = sorted(set(random.Random(24).sample(range(len(base)), 20)) | {0, 1, len(base) - 2, len(base) - 1})
+    for q in (c.q, c.q.transpose(0, 1).contiguous().transpose(0, 1)):
+        out, lse = c.call(draft, q=q)
+        for r in rows:
+            values = c.values(r)
+            for j in range(drafts[r]):
+                row = c.start[r] + j
+                L.hold(out[row], lse[row], D.attend_row(c.q[row], values, base[r], range(j + 1), c.scale, 64))
+
+
 def test_a_call_of_more_than_a_second(draft, latent):  # noqa: F811
     """The waits' limit is a second: none may begin with a run and end with it. A history of 500000 records, whose pages are 40 in turn, and
     16384 drafts of 128 heads: 2.3 x 10^15 operations."""

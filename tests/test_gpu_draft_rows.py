@@ -1,5 +1,7 @@
 """Norms with rotation, the rotating writer and the move of accepted drafts on the GPU, against their 64-bit forms."""
+import math
 import random
+from fractions import Fraction
 
 import pytest
 import torch
@@ -135,6 +137,39 @@ def test_far_positions(draft, pairing):
     out, _ = draft.csa_head_norm_rotate(q, pos, freq, q_norm=False, pairing=pairing, out_dtype=torch.float32)
     y, tol = D.norm_rotate(q, None, False, 0.0, pos, freq, pairing, half=D.F32)
     near(out, (y, tol + 1e-6 * 2 ** -1))
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459")
+
+
+def exact_turn(pos, freq):
+    """cos and sin of pos * freq from whole numbers: the angle's turns modulo 1 before anything is rounded."""
+    turns = Fraction(pos) * Fraction(freq) / (2 * PI) % 1
+    return math.cos(2 * math.pi * float(turns)), math.sin(2 * math.pi * float(turns))
+
+
+@pytest.mark.parametrize("pairing", ["adjacent", "halves"])
+def test_large_frequencies(draft, latent, pairing):
+    """Up to 2^10 radians a token, at positions up to 2^31 - 1; in the heads, and in the writer's records."""
+    g = gen(16)
+    at = [0, 1, 3, 4097, (1 << 24) + 1, (1 << 31) - 2, (1 << 31) - 1]
+    f = [1024.0, -1024.0, 1023.9999, 777.125, -100.7, 6.2831855, 2.0 ** -140, 0.5] * 4
+    pos, freq = torch.tensor(at, dtype=torch.int32, device="cuda"), torch.tensor(f, dtype=torch.float32, device="cuda")
+    q = randn(g, len(at), 2, 64)
+    turned, size = torch.empty_like(q, dtype=torch.float64), torch.empty_like(q, dtype=torch.float64)
+    for j in range(32):
+        ia, ib = (2 * j, 2 * j + 1) if pairing == "adjacent" else (j, j + 32)
+        a, b = q[..., ia].double(), q[..., ib].double()
+        turn = torch.tensor([exact_turn(p, float(freq[j])) for p in at], dtype=torch.float64, device="cuda")[:, None]
+        turned[..., ia], turned[..., ib] = a * turn[..., 0] - b * turn[..., 1], b * turn[..., 0] + a * turn[..., 1]
+        size[..., ia] = size[..., ib] = a.abs() + b.abs()
+    tol = D.TURN * size
+    out, _ = draft.csa_head_norm_rotate(q, pos, freq, q_norm=False, pairing=pairing, out_dtype=torch.float32)
+    near(out, (turned, tol + D.F32 * (turned.abs() + tol) + 1e-37))
+    x = torch.cat([torch.ones(len(at), 512, device="cuda"), q[:, 0]], 1)
+    cache, slots = latent.LatentCache.empty(1, 64, "bf16"), torch.arange(len(at), device="cuda")
+    draft.csa_latent_append(x, slots, pos, cache, freq, norm=False, pairing=pairing)
+    near(read_back(cache, slots, "bf16", 64)[:, 512:], (turned[:, 0], (tol + L.BF16_HALF * (turned.abs() + tol) + 1e-37)[:, 0]))
 
 
 @pytest.mark.parametrize("scale", [1e-30, 1e-18, 1e18, 1e30, 3e37])
@@ -383,6 +418,45 @@ def test_commit_of_one_cache_and_padded_pages(draft, latent):
     r = draft.csa_draft_commit(cache, ints(table), ints(base), ints(drafts), ints([p + [0] * (wide - len(p)) for p in paths]), ints([len(p) for p in paths]))
     assert torch.equal(padded[:, :64 * rec].cpu(), pool[0]) and not padded[:, 64 * rec:].any()
     assert r.new_len.tolist() == new and r.freed[:len(freed)].tolist() == freed and (r.freed[len(freed):] == -1).all()
+
+
+@pytest.mark.parametrize("fmt,rope", [("bf16", 64), ("mxfp4", 0)])
+def test_commit_of_layers_within_each_page(draft, fmt, rope):
+    """A pool whose pages hold every layer's records one after the other: layers are closer together than pages."""
+    rng = random.Random(6)
+    base, drafts, paths, table, pool, rec = commit_case(rng, 9, 12, 4, fmt, rope)
+    pages = pool.transpose(0, 1).contiguous().cuda().transpose(0, 1)
+    cache = draft.LayeredCache(pages, rope, fmt)
+    assert cache.layer_stride == 64 * rec and cache.args.page_stride_bytes == 4 * 64 * rec
+    new, freed = D.commit(pool, table, base, drafts, paths, rec)
+    wide = max(1, max(len(p) for p in paths))
+    r = draft.csa_draft_commit(cache, ints(table), ints(base), ints(drafts), ints([p + [0] * (wide - len(p)) for p in paths]), ints([len(p) for p in paths]))
+    assert torch.equal(pages.cpu(), pool) and r.new_len.tolist() == new and r.freed[:len(freed)].tolist() == freed
+
+
+def test_commit_of_the_most_requests(draft):
+    """16384 of them, one layer, every eleventh refused."""
+    n, rng = draft.COMMIT_MAX_REQ, random.Random(7)
+    base, drafts = [rng.randint(0, 100) for _ in range(n)], [rng.randint(0, 4) for _ in range(n)]
+    paths = [sorted(rng.sample(range(d), rng.randint(0, d))) for d in drafts]
+    table = [[2 * r, 2 * r + 1] for r in range(n)]
+    pool = torch.randint(0, 256, (1, 2 * n, 64 * 272), dtype=torch.uint8, generator=torch.Generator().manual_seed(8))
+    lens = [len(p) for p in paths]
+    for r in range(0, n, 11):
+        lens[r] = drafts[r] + 1
+    cache, bad = draft.LayeredCache(pool.cuda(), 0, "mxfp4"), status()
+    r = draft.csa_draft_commit(cache, ints(table), ints(base), ints(drafts), ints([p + [0] * (5 - len(p)) for p in paths]), ints(lens), dev_status=bad)
+    freed, new = [], []
+    for i in range(n):
+        ok = i % 11 != 0
+        new.append(base[i] + (len(paths[i]) if ok else 0))
+        if ok:
+            freed += table[i][-(-new[-1] // 64):-(-(base[i] + drafts[i]) // 64)]
+            for k, d in enumerate(paths[i]):  # ascending, and never behind its place: in order, in place
+                to, by = base[i] + k, base[i] + d
+                pool[0, table[i][to // 64], to % 64 * 272:(to % 64 + 1) * 272] = pool[0, table[i][by // 64], by % 64 * 272:(by % 64 + 1) * 272]
+    assert int(bad) == 32 and r.new_len.tolist() == new and r.n_freed.tolist() == [len(freed)] and r.freed[:len(freed)].tolist() == freed
+    assert torch.equal(cache.pages.cpu(), pool)
 
 
 def test_commit_bad_requests_are_left_as_they_are(draft):
