@@ -165,7 +165,7 @@ csa_status csa_latent_read(const csa_latent_read_args* args, void* stream);
  * row_req    [num_q] int32, or NULL for row b -> request b
  * row_len    [num_q] int32
  * idx        [num_q, top] int32 rows idx_stride apart, or NULL (then top is 0)
- * scale      above 0, below 2^127
+ * scale      above 0, below 2^127; s_n has to stay below 2^126 in magnitude, q . c below 2^127
  * out        [num_q, num_heads, 512] bf16, contiguous, 16-byte aligned
  * lse        [num_q, num_heads] fp32, or NULL
  * ws         csa_latent_attend_workspace_bytes(args) bytes, 16-byte aligned

@@ -815,11 +815,11 @@ __device__ void role_softmax(const Kernel& K, Smem<kRope>& S) {
       uint32_t w[2][8];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float mc = m[r] == -INFINITY ? 0.f : m[r] * c;
+        const float ref = m[r] == -INFINITY ? 0.f : m[r], factor = exponent_factor(ref * c, c), mc = ref * factor;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 16; j += 2) {
-          const float p0 = csa::ex2(fmaf(s[r][j], c, -mc)), p1 = csa::ex2(fmaf(s[r][j + 1], c, -mc));
+          const float p0 = csa::ex2(fmaf(s[r][j], factor, -mc)), p1 = csa::ex2(fmaf(s[r][j + 1], factor, -mc));
           sum += p0 + p1;
           const __nv_bfloat162 two = __floats2bfloat162_rn(p0, p1);
           w[r][j >> 1] = *reinterpret_cast<const uint32_t*>(&two);

@@ -51,6 +51,13 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 // A softmax scale: the kernels multiply it by log2 e, which has to stay finite.
 inline bool good_scale(float scale) { return scale > 0.f && scale < 0x1p127f; }
 
+// The factor c (the scale, times log2 e) of a row's exponents S c - m c, for its reference m. The rounding of m c that is left in them is 2^-25 of it:
+// above 2^30 it could be more than an exponent holds. Scores that differ at all differ by 2^-24 of theirs, though, so that weights there are 1
+// or 0 as well with the power of two below c, whose product with m is exact.
+__device__ __forceinline__ float exponent_factor(float mc, float c) {
+  return fabsf(mc) > 0x1p30f ? __uint_as_float(__float_as_uint(c) & 0x7F800000u) : c;
+}
+
 inline csa_status check_cache(const csa_latent_cache& c) {
   if (!c.pages || c.num_pages < 1 || c.num_pages > INT32_MAX) return CSA_ERR_INVALID_ARG;
   const int64_t rec = csa_latent_record_bytes(c.record_format, c.rope_dim);

@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+import _latent as L
 from sparse_attention_kv_e4m3_gb300 import latent
 from test_gpu_latent import DEV, Attend, Prefill, _lib  # noqa: F401
 
@@ -27,6 +28,30 @@ def test_prefill_scales_down_to_subnormal(scale):
     p = Prefill([300, 7], [500, 7], 2, seed=18)
     p.scale = scale
     p.check()
+
+
+@pytest.mark.parametrize("logit", [2.0 ** 27, 2.0 ** 33, 2.0 ** 36, 2.0 ** 60, 2.0 ** 125])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("lens,top", [([700, 1, 64], 0), ([30000, 7], 0), ([900] * 20, 300)])
+def test_attend_scores_above_what_an_exponent_holds(lens, top, fmt, sign, logit):
+    """Scaled scores of 2^27 and more, which a tile's products with scale log2 e round by more than a softmax bears. The next score is 2^-8 of
+    them less at least: the weights are 1 or 0, equal for the records of the largest."""
+    a = Attend(lens, 16, 64, fmt, top=top, req=[0] * len(lens) if top else None, seed=20)
+    a.q[:] = 0
+    a.q[..., 3] = sign * 2.0 ** 100
+    a.scale = logit * 2.0 ** -103  # values are below 2^3
+    out, lse = a.run()
+    for b, (n, r) in enumerate(a.rows):
+        pos = torch.arange(n, device=DEV) if a.idx is None else a.idx[b].long()
+        pos = pos[(pos >= 0) & (pos < n)]
+        seen = a.values[a.table[r].long()[pos // 64] * 64 + pos % 64]
+        score = sign * seen[:, 3]
+        assert float(score.abs().max()) < 8
+        best = seen[score == score.max(), :512]
+        assert ((out[b].double() - best.mean(0)).abs() <= 2.1 * L.BF16_HALF * best.abs().mean(0) + 1e-30).all(), b
+        want = float(score.max()) * 2.0 ** 100 * a.scale
+        assert (lse[b].double() - want).abs().max() <= 2 ** -22 * abs(want)
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
