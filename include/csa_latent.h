@@ -209,7 +209,8 @@ csa_status csa_latent_attend(const csa_latent_attend_args* args, void* ws, size_
  *   out_ih = sum_j softmax_j(s_ij) v_jh,  lse_ih = log sum_j exp(s_ij)
  * A row that sees no key gets out 0 and lse -infinity. What keys and values of other requests
  * hold does not matter. Within a request a value v_jh that is not finite may reach rows that do
- * not see key j too (as 0 times it); rows that see no key stay 0.
+ * not see key j too (as 0 times it); rows that see no key stay 0. s_ij has to stay within 2^30 in magnitude (exponents
+ * are differences of rounded products: beyond, a rounding is more than an exponent holds).
  *
  * q        [total_q, num_heads, 192] bf16; k_nope, v [total_k, num_heads, 128] bf16; k_rope
  *          [total_k, 64] bf16: 16-byte aligned, strides in elements and multiples of 8 (k_nope and

@@ -54,6 +54,28 @@ def test_attend_scores_above_what_an_exponent_holds(lens, top, fmt, sign, logit)
         assert (lse[b].double() - want).abs().max() <= 2 ** -22 * abs(want)
 
 
+@pytest.mark.parametrize("logit", [2.0 ** 27, 2.0 ** 30])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_prefill_scores_of_the_largest_range(sign, logit):
+    p = Prefill([300, 7], [500, 900], 2, seed=21)
+    p.q[:] = 0
+    p.q[..., 3] = sign * 2.0 ** 100
+    p.scale = logit * 2.0 ** -103
+    out, lse = p.run()
+    assert int(p.st) == 0
+    for r in range(2):
+        (q0, q1), (k0, k1) = p.qs[r:r + 2], p.ks[r:r + 2]
+        for h in range(2):
+            score, v = sign * p.kn[k0:k1, h, 3].double(), p.v[k0:k1, h].double()
+            assert float(score.abs().max()) < 8
+            for i in range(0, q1 - q0, 13):
+                seen = score[:k1 - k0 - (q1 - q0) + i + 1]
+                best = v[:len(seen)][seen == seen.max()]
+                assert ((out[q0 + i, h].double() - best.mean(0)).abs() <= 2.1 * L.BF16_HALF * best.abs().mean(0) + 1e-30).all(), (r, h, i)
+                want = float(seen.max()) * 2.0 ** 100 * p.scale
+                assert abs(float(lse[q0 + i, h]) - want) <= 2 ** -22 * abs(want)
+
+
 @pytest.mark.parametrize("bad", [math.nan, math.inf])
 def test_prefill_rows_without_keys_beside_values_that_are_not_finite(bad):
     """More queries than keys: the first rows see none, in a tile whose other rows see a NaN or infinite value."""
