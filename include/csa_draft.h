@@ -124,6 +124,7 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  * records makes these tables). A draft's row sees the history and, of its request's drafts,
  *   with mask     those i whose bit i % 64 of word i / 64 of its mask is set (drafts past the words are not seen), or
  *   without       those i <= j (a chain).
+ * (One draft a request may go to csa_latent_attend as well, the faster one up to 64 heads and for few requests.)
  * A mask may leave out the draft itself, and all drafts. A row that sees nothing gets out 0 and lse -infinity. What
  * records hold that a row does not see (NaN, infinities) does not matter to it; a record that it sees should be finite (one whose
  * score becomes -infinity has weight 0).

@@ -29,7 +29,7 @@ using csa::smem_u32;
 // values of a CTA's own page come in a second time because both CTAs' operands of an MMA lie at the same place. Two requests of 65536 and more records,
 // 16 drafts, 64 heads: 330 us, 1.34 PFLOP/s (the absorbed form's own kernel, 64 rows high, reaches 0.68). 32 requests of 8192 to
 // 32768, 16 heads, up to 8 drafts, whose records are 783 MB: 172 us, 4.6 TB/s. 4-bit records, 16 requests of 7001 to 16384, up to
-// 13 drafts: 310 us, 0.67 PFLOP/s, bound by the conversion to bf16: 10 k warp instructions a tile, at half of the issue rate.
+// 13 drafts: 308 us, 0.68 PFLOP/s, bound by the conversion to bf16: 10 k warp instructions a tile, at half of the issue rate.
 constexpr int kTile = 128;                     // records a tile: two pages, one for each CTA's keys
 constexpr int kRows = 64;                      // query rows (draft and head) of a CTA; a unit is the pair's 128
 constexpr int kSlots = 8;                      // of the ring: 64 records x 128 values each, two 8 KB columns of 64 values

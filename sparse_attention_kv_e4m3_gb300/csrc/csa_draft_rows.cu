@@ -311,7 +311,8 @@ csa_status check_heads(const csa_heads& t, int64_t n, int rope, bool f32_in, boo
 // a 4-bit record depend on which side of a border a value lies, so the fast result, whose error is known, is encoded
 // twice, a little larger and a little smaller; where the two differ (a value or two of one row in 100) the row's factor
 // and those values are computed again in fp64. (All of the row in fp64 cost 65537 rows 5 us of 82.) 65537 fp32 rows to 4 bits: 50 us where the
-// bytes are 26, bound by 380 instructions a row at 61% of the issue rate; 16381 bf16 rows: 13.6 us, of which the bytes are 5.6.
+// bytes are 26, 380 instructions a row and 61% of the issue slots: with 16 warps an SM neither is full; 16381 bf16 rows: 13.6 us, of which the bytes
+// are 5.6, 44% of the issue slots.
 
 // The relative error of x r w in fp32: the sum of 16 squares a lane and 5 steps over the lanes, (16 + 5) 2^-24, the mean and eps
 // 2 x 2^-24, halved by the root; rsqrtf (two units in the last place) 4 x 2^-24 and two products 2 x 2^-24 more: 18 x 2^-24.
