@@ -126,8 +126,8 @@ csa_status csa_latent_append(const csa_append_args* args, void* stream);
  *   without       those i <= j (a chain).
  * (One draft a request may go to csa_latent_attend as well, the faster one up to 64 heads and for few requests.)
  * A mask may leave out the draft itself, and all drafts. A row that sees nothing gets out 0 and lse -infinity. What
- * records hold that a row does not see (NaN, infinities) does not matter to it; a record that it sees should be finite (one whose
- * score becomes -infinity has weight 0).
+ * records hold that a row does not see (NaN, infinities) does not matter to it; a record that it sees should be finite. (A draft's
+ * whose score becomes -infinity is as one that is not seen.)
  *
  * q          [num_q, num_heads, 512 + rope_dim] bf16, 16-byte aligned, the strides in elements
  *            and multiples of 8; num_heads 1 .. CSA_LATENT_MAX_HEADS

@@ -90,6 +90,27 @@ def test_largest_finite_4_bit_values_of_a_draft(draft, latent, base, scale_byte,
     c.check(out, lse, masks)
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("base", [0, 61, 70])
+def test_draft_whose_score_is_minus_infinity(draft, latent, base, fmt):  # noqa: F811
+    """Draft 3 has an infinite value where every query is positive: the rows that see it are what they are without it, or empty where it is all."""
+    masks = [0b1, 0b11, 0b111, 0b1000, 0b11111]
+    c = Case(latent, [base], [5], 9, fmt=fmt, seed=base)
+    c.q[..., 7] = c.q[..., 7].abs() + 0.1
+    want, want_lse = c.call(draft, [m & ~0b1000 for m in masks])
+    page, at, rec = int(c.table[0, (base + 3) // 64]), (base + 3) % 64, c.cache.record_bytes
+    record = c.cache.pages[page][at * rec:(at + 1) * rec]
+    if fmt == "bf16":
+        record.view(torch.bfloat16)[7] = -math.inf
+    else:
+        record[:16] = 0
+        record[3], record[256] = 15 << 4, 254
+    out, lse = c.call(draft, masks)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+    if base == 0:
+        assert not out[3].any() and torch.isneginf(lse[3]).all()
+
+
 def test_queries_that_are_not_finite_stay_in_their_row(draft, latent):  # noqa: F811
     c = Case(latent, [300], [5], 30, seed=4)
     clean, clean_lse = c.call(draft)
